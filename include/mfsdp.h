@@ -323,6 +323,137 @@ mfsdp_status_t mfsdp_shampoo_stats(const mfsdp_stats_matrix_t* mats, int64_t n_m
                                    void* workspace, size_t workspace_bytes,
                                    hipStream_t stream);
 
+/*
+ * The gradients that the step takes.  Two kinds of tensors of a model have
+ * gradients that are not one plain matrix product: the matrices of a mixture of
+ * experts (a list of small whole matrices, each with the rows that were routed
+ * to it), and the embedding table (a tail tensor under Muon's convention, in
+ * the packed fp32 buffer of mfsdp_adamw_tail).  The calls below make them, with
+ * the forward products they belong to and 8-bit copies of the activations that
+ * the backward pass needs.
+ *   - All of them are asynchronous on `stream`, allocate nothing, read offsets
+ *     and tokens on the device, and can be captured into a graph (a graph
+ *     keeps the workspace it was captured with: two graphs that may run at the
+ *     same time need one each).
+ *   - Results do not depend on timing: no atomics on sums.
+ *   - Sums are fp32 throughout and rounded once, to the output's type.
+ *   - Outputs must not overlap inputs, the workspace or each other
+ *     (MFSDP_ERR_ALIAS); inputs may overlap inputs.
+ *   - Buffers are aligned to their elements.  Rows that start on 16 bytes and
+ *     widths of whole 16-byte groups take the fast kernels.
+ *
+ * Products grouped by expert.  Source: arxivlens Abstract (the owner holds
+ * whole 2D weights and their whole gradients); gist.science "Contributions
+ * cles" (matrix-wise optimizers on models with many small expert matrices).
+ * The pages give no product: these are the linear layer and its derivatives.
+ *   weight   device, n_experts x n x k, contiguous: W_e is the n x k row-major
+ *            (out x in) matrix at weight + e*n*k, as mfsdp_muon_step takes it
+ *   offsets  device int32, n_experts + 1, non-decreasing, in [0, rows]: rows
+ *            offsets[e] <= r < offsets[e+1] of the activations go to expert e.
+ *            An expert may have none.  Rows before offsets[0] and from
+ *            offsets[n_experts] on belong to nobody: they are not read, and
+ *            their output rows are left as they were.  Offsets are not checked
+ *            on the host; the kernels clamp them to [0, rows] and take a
+ *            decreasing pair as empty, so wrong ones give wrong results but no
+ *            access outside the buffers.
+ *   rows     rows of the activation buffers; ld_* row strides in elements
+ * forward          y[r]  = x[r] W_e^T     (x: rows x k, y: rows x n)
+ * input gradient   dx[r] = dy[r] W_e      (dy: rows x n, dx: rows x k)
+ * weight gradient  dw_e  = beta*dw_e + sum_r dy[r]^T x[r], contiguous n_experts
+ *                  x n x k in `dtype` or fp32 (dw_dtype).  beta == 0 does not
+ *                  read dw; an expert without rows gets beta*dw_e.
+ * The checkpoint form takes x as codes and scales of mfsdp_ckpt_quantize
+ * (contiguous, rows x k).  With dtype BF16 it multiplies them exactly; the
+ * result is that of the weight gradient with the restored x.
+ * n_experts == 0, and rows == 0 for the first two, return MFSDP_OK, no work.
+ * Errors: MFSDP_ERR_INVALID_ARGUMENT (negative counts, widths < 1, strides
+ * smaller than rows, null or misaligned pointers, non-finite beta),
+ * MFSDP_ERR_UNSUPPORTED (dtypes; n, k or strides above 2^24, rows above 2^30,
+ * n_experts above 2^20, more than 2^31 tiles), MFSDP_ERR_ALIAS, MFSDP_ERR_HIP.
+ */
+mfsdp_status_t mfsdp_grouped_linear(const void* x, int64_t ld_x, const void* weight,
+                                    const int32_t* offsets, int64_t n_experts, int64_t rows,
+                                    int64_t n, int64_t k, mfsdp_dtype_t dtype, void* y,
+                                    int64_t ld_y, hipStream_t stream);
+
+mfsdp_status_t mfsdp_grouped_linear_dgrad(const void* dy, int64_t ld_dy, const void* weight,
+                                          const int32_t* offsets, int64_t n_experts, int64_t rows,
+                                          int64_t n, int64_t k, mfsdp_dtype_t dtype, void* dx,
+                                          int64_t ld_dx, hipStream_t stream);
+
+mfsdp_status_t mfsdp_grouped_linear_wgrad(const void* dy, int64_t ld_dy, const void* x,
+                                          int64_t ld_x, const int32_t* offsets, int64_t n_experts,
+                                          int64_t rows, int64_t n, int64_t k, mfsdp_dtype_t dtype,
+                                          void* dw, mfsdp_dtype_t dw_dtype, float beta,
+                                          hipStream_t stream);
+
+mfsdp_status_t mfsdp_grouped_linear_wgrad_ckpt(const void* dy, int64_t ld_dy, const int8_t* codes,
+                                               const uint8_t* scales, const int32_t* offsets,
+                                               int64_t n_experts, int64_t rows, int64_t n,
+                                               int64_t k, mfsdp_dtype_t dtype, void* dw,
+                                               mfsdp_dtype_t dw_dtype, float beta,
+                                               hipStream_t stream);
+
+/*
+ * Activation checkpoints in 8 bits: a copy of an activation, half (bf16) or a
+ * quarter (fp32) of its size, kept from the forward to the backward pass.
+ * Each row is cut into blocks of MFSDP_CKPT_BLOCK columns (the last may be
+ * shorter); a block is held as whole numbers q in [-127, 127] and one power of
+ * two 2^e, the smallest e >= -126 with max|x| <= 127 * 2^e, but 121 at most so
+ * that q * 2^e stays finite:
+ *   q = x / 2^e to the nearest, ties to even;   restored: q * 2^e
+ * The error is at most 2^(e-1) (below 2^121 for |x| above 127.5 * 2^121, where
+ * q stops at 127).  q * 2^e is exact in bf16 and fp32.
+ *   x       device, rows x k, row stride ld_x, bf16 or fp32
+ *   codes   device int8, rows x k, contiguous
+ *   scales  device uint8, rows x ceil(k / MFSDP_CKPT_BLOCK): e + 127; 255 marks
+ *           a block with an infinity or a NaN, which restores as NaN
+ * rows == 0 returns MFSDP_OK, no work.  Errors as above.
+ */
+#define MFSDP_CKPT_BLOCK 128
+
+mfsdp_status_t mfsdp_ckpt_quantize(const void* x, int64_t ld_x, int64_t rows, int64_t k,
+                                   mfsdp_dtype_t dtype, int8_t* codes, uint8_t* scales,
+                                   hipStream_t stream);
+
+mfsdp_status_t mfsdp_ckpt_restore(const int8_t* codes, const uint8_t* scales, int64_t rows,
+                                  int64_t k, mfsdp_dtype_t dtype, void* x, int64_t ld_x,
+                                  hipStream_t stream);
+
+/*
+ * Embedding: out[i] = scale * table[token_i], in fp32 and rounded once.
+ *   table   device, vocab x d, contiguous, bf16 or fp32 (a packed tail segment)
+ *   tokens  device, n_tokens, int32 or int64 (token_bytes 4 or 8).  A token
+ *           outside [0, vocab) stands for padding: its row is zero.
+ *   out     device, n_tokens x d, row stride ld_out, bf16 or fp32
+ * Its gradient, into the dense fp32 gradient of the table:
+ *   grad[v] = beta*grad[v] + scale * sum_{i: token_i = v} dy[i]
+ *   dy      device, n_tokens x d, row stride ld_dy, bf16 or fp32; the rows of
+ *           padding tokens are not read
+ *   grad    device fp32, vocab x d, contiguous.  beta == 0 does not read it
+ *           (rows without a token become zero); beta == 1 leaves the rows
+ *           without a token untouched.
+ * Each row is summed over its tokens in the order of the list, in chunks of 64
+ * of the sorted list when it has more than 64: the result depends on the
+ * inputs alone.
+ * workspace  device, >= mfsdp_embedding_grad_workspace_size bytes, 256-byte
+ *            aligned, scratch; none is needed for n_tokens == 0.
+ * Errors: as above, MFSDP_ERR_WORKSPACE, and MFSDP_ERR_UNSUPPORTED for vocab
+ * above 2^31 - 1, n_tokens above 2^28, d or strides above 2^24.
+ */
+mfsdp_status_t mfsdp_embedding(const void* table, mfsdp_dtype_t table_dtype, int64_t vocab,
+                               int64_t d, const void* tokens, int token_bytes, int64_t n_tokens,
+                               float scale, void* out, int64_t ld_out, mfsdp_dtype_t out_dtype,
+                               hipStream_t stream);
+
+mfsdp_status_t mfsdp_embedding_grad_workspace_size(int64_t n_tokens, int64_t vocab, int64_t d,
+                                                   size_t* out_bytes);
+
+mfsdp_status_t mfsdp_embedding_grad(const void* dy, int64_t ld_dy, mfsdp_dtype_t dtype,
+                                    const void* tokens, int token_bytes, int64_t n_tokens,
+                                    int64_t vocab, int64_t d, float scale, float beta, float* grad,
+                                    void* workspace, size_t workspace_bytes, hipStream_t stream);
+
 /* Static, human-readable name of a status code. */
 const char* mfsdp_status_string(mfsdp_status_t status);
 
@@ -350,7 +481,11 @@ typedef enum mfsdp_kernel_kind {
   MFSDP_KERNEL_STATS_PREP = 8,/* gradient copies for the statistics   */
   MFSDP_KERNEL_SYRK = 9,      /* L, R statistics products            */
   MFSDP_KERNEL_SMALL = 10,    /* whole NS chain + apply of small matrices */
-  MFSDP_KERNEL_KINDS = 11
+  MFSDP_KERNEL_GROUPED = 11,  /* products grouped by expert          */
+  MFSDP_KERNEL_CKPT = 12,     /* 8-bit checkpoints                   */
+  MFSDP_KERNEL_EMBED = 13,    /* embedding lookup                    */
+  MFSDP_KERNEL_EMBED_GRAD = 14, /* embedding gradient (all launches) */
+  MFSDP_KERNEL_KINDS = 15
 } mfsdp_kernel_kind_t;
 
 mfsdp_status_t mfsdp_timing_enable(int enable);

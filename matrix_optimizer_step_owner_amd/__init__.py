@@ -22,10 +22,15 @@ import torch
 
 from . import _lib
 from ._lib import MfsdpError, NOALLOC_SCRATCH_BYTES, NS_EPS
+from .grads import (CKPT_BLOCK, ckpt_quantize, ckpt_restore, embedding, embedding_grad,
+                    grouped_linear, grouped_linear_dgrad, grouped_linear_wgrad,
+                    grouped_linear_wgrad_ckpt)
 
 __all__ = ["muon_step", "muon_step_noalloc", "MuonStep", "adamw_tail", "muon_workspace_size",
            "default_scale", "plan_owners", "tail_layout", "tail_pack", "tail_unpack",
-           "shampoo_stats", "mfma_probe", "timing", "MfsdpError", "NS_EPS", "NOALLOC_SCRATCH_BYTES",
+           "shampoo_stats", "grouped_linear", "grouped_linear_dgrad", "grouped_linear_wgrad",
+           "grouped_linear_wgrad_ckpt", "ckpt_quantize", "ckpt_restore", "embedding",
+           "embedding_grad", "CKPT_BLOCK", "mfma_probe", "timing", "MfsdpError", "NS_EPS", "NOALLOC_SCRATCH_BYTES",
            "library_path"]
 
 library_path = _lib.LIB_PATH

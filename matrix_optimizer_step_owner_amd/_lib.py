@@ -20,13 +20,16 @@ NS_EPS = 1e-7
 NOALLOC_SCRATCH_BYTES = 256 << 20
 KERNEL_KINDS = {"momentum": 0, "norm": 1, "gram": 2, "poly": 3, "update": 4,
                 "apply": 5, "adamw": 6, "final": 7, "stats_prep": 8, "syrk": 9,
-                "small": 10}
+                "small": 10, "grouped": 11, "ckpt": 12, "embed": 13, "embed_grad": 14}
 
 #: Every symbol include/mfsdp.h declares.
 EXPORTED = ("mfsdp_muon_workspace_size", "mfsdp_muon_step", "mfsdp_muon_step_noalloc",
             "mfsdp_adamw_tail",
             "mfsdp_plan_owners", "mfsdp_tail_layout", "mfsdp_tail_pack",
             "mfsdp_tail_unpack", "mfsdp_stats_workspace_size", "mfsdp_shampoo_stats",
+            "mfsdp_grouped_linear", "mfsdp_grouped_linear_dgrad", "mfsdp_grouped_linear_wgrad",
+            "mfsdp_grouped_linear_wgrad_ckpt", "mfsdp_ckpt_quantize", "mfsdp_ckpt_restore",
+            "mfsdp_embedding", "mfsdp_embedding_grad_workspace_size", "mfsdp_embedding_grad",
             "mfsdp_status_string", "mfsdp_last_error",
             "mfsdp_timing_enable", "mfsdp_timing_reset", "mfsdp_timing_read",
             "mfsdp_mfma_probe")
@@ -113,6 +116,30 @@ def load() -> ctypes.CDLL:
             c.POINTER(MfsdpStatsMatrix), c.c_int64, c.c_int, c.c_float, c.c_float,
             c.c_void_p, c.c_size_t, c.c_void_p]
         lib.mfsdp_shampoo_stats.restype = c.c_int
+        ptr, i64, f32 = c.c_void_p, c.c_int64, c.c_float
+        lib.mfsdp_grouped_linear.argtypes = [ptr, i64, ptr, ptr, i64, i64, i64, i64, c.c_int,
+                                             ptr, i64, ptr]
+        lib.mfsdp_grouped_linear.restype = c.c_int
+        lib.mfsdp_grouped_linear_dgrad.argtypes = lib.mfsdp_grouped_linear.argtypes
+        lib.mfsdp_grouped_linear_dgrad.restype = c.c_int
+        lib.mfsdp_grouped_linear_wgrad.argtypes = [ptr, i64, ptr, i64, ptr, i64, i64, i64, i64,
+                                                   c.c_int, ptr, c.c_int, f32, ptr]
+        lib.mfsdp_grouped_linear_wgrad.restype = c.c_int
+        lib.mfsdp_grouped_linear_wgrad_ckpt.argtypes = [ptr, i64, ptr, ptr, ptr, i64, i64, i64,
+                                                        i64, c.c_int, ptr, c.c_int, f32, ptr]
+        lib.mfsdp_grouped_linear_wgrad_ckpt.restype = c.c_int
+        lib.mfsdp_ckpt_quantize.argtypes = [ptr, i64, i64, i64, c.c_int, ptr, ptr, ptr]
+        lib.mfsdp_ckpt_quantize.restype = c.c_int
+        lib.mfsdp_ckpt_restore.argtypes = [ptr, ptr, i64, i64, c.c_int, ptr, i64, ptr]
+        lib.mfsdp_ckpt_restore.restype = c.c_int
+        lib.mfsdp_embedding.argtypes = [ptr, c.c_int, i64, i64, ptr, c.c_int, i64, f32, ptr, i64,
+                                        c.c_int, ptr]
+        lib.mfsdp_embedding.restype = c.c_int
+        lib.mfsdp_embedding_grad_workspace_size.argtypes = [i64, i64, i64, c.POINTER(c.c_size_t)]
+        lib.mfsdp_embedding_grad_workspace_size.restype = c.c_int
+        lib.mfsdp_embedding_grad.argtypes = [ptr, i64, c.c_int, ptr, c.c_int, i64, i64, i64, f32,
+                                             f32, ptr, ptr, c.c_size_t, ptr]
+        lib.mfsdp_embedding_grad.restype = c.c_int
         lib.mfsdp_status_string.argtypes = [c.c_int]
         lib.mfsdp_status_string.restype = c.c_char_p
         lib.mfsdp_last_error.argtypes = []

@@ -1,0 +1,159 @@
+// Activation checkpoints in 8 bits (gfx950).
+//
+// Each row of an activation is cut into blocks of kCkptBlock columns.  A block
+// is held as whole numbers q in [-127, 127] and one power of two 2^e, the
+// smallest e >= -126 with max |x| <= 127 * 2^e:
+//   q = x / 2^e rounded to the nearest, ties to even;  x is held as q * 2^e.
+// The error is at most 2^(e-1), half a step, under max|x| / 126.  e stops at
+// 121, above which q * 2^e could pass the largest float, and q at 127: only
+// values beyond 127.5 * 2^121 are then off by more (by under one step).  A power of
+// two makes the division exact and q * 2^e a bf16 number (seven bits of
+// magnitude), so the checkpoint restores without a second rounding and the
+// weight gradient can multiply it in bf16 as it stands.  e is stored as the
+// byte e + 127; 255 marks a block with an infinity or a NaN, which restores as
+// NaN throughout.
+//
+// Bound by HBM: x is read once and one byte and 1/128 written per value.
+// Sixteen lanes take one block, eight values each (16-byte loads in bf16,
+// 8-byte code stores), and find its maximum with four lane exchanges.
+#pragma once
+
+#include "common.hpp"
+#include "grouped_kernels.hpp"
+
+namespace mfsdp {
+
+constexpr int kCkptUnits = 4;   // blocks per 16-lane group, loads of all in flight
+
+struct CkptArgs {
+  void* x;             // rows x k, row stride ld (read by quantize, written by restore)
+  int8_t* codes;       // rows x k, contiguous
+  uint8_t* scales;     // rows x nb
+  int64_t ld;
+  int64_t units;       // rows * nb
+  int32_t k, nb;
+  int32_t vec;         // rows of x start on 16 bytes and k is a multiple of 8
+};
+
+// Column of value j (0..7) of lane l16 in its block: eight consecutive ones on
+// the vector path, sixteen apart otherwise.
+__device__ __forceinline__ int ckpt_col(bool vec, int l16, int j) {
+  return vec ? l16 * 8 + j : j * 16 + l16;
+}
+
+template <class E>
+__global__ __launch_bounds__(256) void ckpt_quantize_kernel(CkptArgs a) {
+  using S = typename E::storage_t;
+  const int l16 = threadIdx.x & 15;
+  const int64_t unit0 = static_cast<int64_t>(blockIdx.x) * (16 * kCkptUnits) + (threadIdx.x >> 4);
+  const bool vec = a.vec != 0;
+  const S* x = static_cast<const S*>(a.x);
+  float v[kCkptUnits][8];
+#pragma unroll
+  for (int i = 0; i < kCkptUnits; ++i) {
+    const int64_t u = unit0 + 16 * i;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[i][j] = 0.f;
+    if (u >= a.units) continue;
+    const int64_t row = u / a.nb;
+    const int c0 = static_cast<int>(u - row * a.nb) * kCkptBlock;
+    const S* src = x + row * a.ld + c0;
+    if (vec) {
+      if (c0 + l16 * 8 < a.k) load8<E>(src + l16 * 8, v[i]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (c0 + j * 16 + l16 < a.k) v[i][j] = E::to_f32(src[j * 16 + l16]);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kCkptUnits; ++i) {
+    const int64_t u = unit0 + 16 * i;
+    if (u >= a.units) continue;   // whole 16-lane groups leave together
+    // largest magnitude by its bits: infinities and NaN come out on top
+    uint32_t top = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(v[i][j]) & 0x7fffffffu);
+#pragma unroll
+    for (int d = 8; d > 0; d >>= 1) top = max(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), d, 16)));
+    // max = m 2^p, 1 <= m < 2: e = p - 6 while m <= 127/64, else p - 5; the
+    // biased exponent is clamped to [1, 248] (e = -126 .. 121)
+    int be = static_cast<int>(top >> 23) - 6 + ((top & 0x7fffffu) > 0x7e0000u ? 1 : 0);
+    be = min(max(be, 1), 248);
+    const bool bad = top >= 0x7f800000u;
+    const float inv = __uint_as_float(static_cast<uint32_t>(254 - be) << 23);   // 2^-e
+    const int64_t row = u / a.nb;
+    const int blk = static_cast<int>(u - row * a.nb);
+    const int c0 = blk * kCkptBlock;
+    int8_t* dst = a.codes + row * a.k + c0;
+    uint32_t w[2] = {0, 0};
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int q = bad ? 0 : static_cast<int>(fminf(fmaxf(rintf(v[i][j] * inv), -127.f), 127.f));
+      w[j >> 2] |= static_cast<uint32_t>(q & 0xff) << (8 * (j & 3));
+    }
+    if (vec) {
+      if (c0 + l16 * 8 < a.k) *reinterpret_cast<uint2*>(dst + l16 * 8) = make_uint2(w[0], w[1]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (c0 + j * 16 + l16 < a.k) dst[j * 16 + l16] = static_cast<int8_t>(w[j >> 2] >> (8 * (j & 3)));
+    }
+    if (l16 == 0) a.scales[u] = static_cast<uint8_t>(bad ? 255 : be);
+  }
+}
+
+template <class E>
+__global__ __launch_bounds__(256) void ckpt_restore_kernel(CkptArgs a) {
+  using S = typename E::storage_t;
+  const int l16 = threadIdx.x & 15;
+  const int64_t unit0 = static_cast<int64_t>(blockIdx.x) * (16 * kCkptUnits) + (threadIdx.x >> 4);
+  const bool vec = a.vec != 0;
+  S* x = static_cast<S*>(a.x);
+  uint32_t w[kCkptUnits][2];
+  uint32_t b[kCkptUnits];
+#pragma unroll
+  for (int i = 0; i < kCkptUnits; ++i) {
+    const int64_t u = unit0 + 16 * i;
+    w[i][0] = w[i][1] = b[i] = 0;
+    if (u >= a.units) continue;
+    const int64_t row = u / a.nb;
+    const int c0 = static_cast<int>(u - row * a.nb) * kCkptBlock;
+    const int8_t* src = a.codes + row * a.k + c0;
+    b[i] = a.scales[u];
+    if (vec) {
+      if (c0 + l16 * 8 < a.k) {
+        const uint2 t = *reinterpret_cast<const uint2*>(src + l16 * 8);
+        w[i][0] = t.x;
+        w[i][1] = t.y;
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (c0 + j * 16 + l16 < a.k)
+          w[i][j >> 2] |= static_cast<uint32_t>(static_cast<uint8_t>(src[j * 16 + l16])) << (8 * (j & 3));
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kCkptUnits; ++i) {
+    const int64_t u = unit0 + 16 * i;
+    if (u >= a.units) continue;
+    const int64_t row = u / a.nb;
+    const int c0 = static_cast<int>(u - row * a.nb) * kCkptBlock;
+    S* dst = x + row * a.ld + c0;
+    const float s = ckpt_scale(b[i]);
+    float v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      v[j] = static_cast<float>(static_cast<int8_t>(w[i][j >> 2] >> (8 * (j & 3)))) * s;
+    if (vec) {
+      if (c0 + l16 * 8 < a.k) store8<E>(dst + l16 * 8, v);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (c0 + j * 16 + l16 < a.k) dst[j * 16 + l16] = E::from_f32(v[j]);
+    }
+  }
+}
+
+}  // namespace mfsdp

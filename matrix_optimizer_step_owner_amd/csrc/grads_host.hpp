@@ -1,0 +1,555 @@
+// Host side of the operators that make the gradients of the owner-local step:
+// products grouped by expert, 8-bit activation checkpoints and the embedding
+// with its gradient.  Included once, by mfsdp.hip, after its helpers (fail,
+// launch, check_aliasing); every launch takes its sizes from the arguments
+// alone and its offsets and tokens from device memory, so all of these calls
+// can be captured into a graph.
+#pragma once
+
+namespace {
+
+// Extent in bytes of `rows` rows of `cols` elements, `ld` elements apart.
+size_t strided_bytes(int64_t rows, int64_t cols, int64_t ld, size_t es) {
+  return rows < 1 || cols < 1 ? 0 : (static_cast<size_t>(rows - 1) * ld + cols) * es;
+}
+
+void add_range(std::vector<Range>* rs, const void* p, size_t nb, const char* what) {
+  const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
+  if (nb) rs->push_back({lo, lo + nb, what, 0});
+}
+
+// The outputs must be disjoint from the inputs and from each other; inputs may
+// overlap one another.
+mfsdp_status_t check_outputs(const std::vector<Range>& outs, const std::vector<Range>& ins) {
+  for (size_t i = 0; i < outs.size(); ++i) {
+    for (size_t j = i + 1; j < outs.size(); ++j)
+      if (outs[i].lo < outs[j].hi && outs[j].lo < outs[i].hi)
+        return fail(MFSDP_ERR_ALIAS, "%s overlaps %s", outs[i].what, outs[j].what);
+    for (const Range& in : ins)
+      if (outs[i].lo < in.hi && in.lo < outs[i].hi)
+        return fail(MFSDP_ERR_ALIAS, "%s overlaps %s", outs[i].what, in.what);
+  }
+  return MFSDP_OK;
+}
+
+// ---------------------------------------------------------------------------
+// Products grouped by expert
+// ---------------------------------------------------------------------------
+constexpr int64_t kGroupDimMax = int64_t(1) << 24;      // n, k
+constexpr int64_t kGroupRowsMax = int64_t(1) << 30;
+constexpr int64_t kGroupExpertsMax = int64_t(1) << 20;
+
+// Upper bound of the row tiles of height bp: every expert with rows adds at
+// most one that is not full.
+int64_t group_tiles_max(int64_t rows, int64_t experts, int64_t bp) {
+  return (rows + std::min(rows, experts) * (bp - 1)) / bp;
+}
+
+template <class E, int MODE, bool CKPT>
+hipError_t launch_grouped(const GroupArgs& g, int64_t blocks, hipStream_t stream) {
+  return launch(MFSDP_KERNEL_GROUPED, stream, [&] {
+    grouped_any_kernel<E, MODE, CKPT>
+        <<<dim3(static_cast<unsigned>(blocks)), dim3(256), 0, stream>>>(g);
+  });
+}
+
+// rows x np = P's extent per row etc. are checked by the callers; this checks
+// what the three products share and launches.
+mfsdp_status_t grouped_impl(int mode, const void* p, int64_t ldp, const void* q, int64_t ldq,
+                            const uint8_t* qs, const int32_t* offsets, int64_t experts,
+                            int64_t rows, int64_t n, int64_t k, mfsdp_dtype_t dtype, void* out,
+                            int64_t ldo, mfsdp_dtype_t out_dtype, float beta,
+                            hipStream_t stream) {
+  g_last_error.clear();
+  if (dtype != MFSDP_DTYPE_F32 && dtype != MFSDP_DTYPE_BF16)
+    return fail(MFSDP_ERR_UNSUPPORTED, "unsupported dtype %d", (int)dtype);
+  if (out_dtype != dtype && out_dtype != MFSDP_DTYPE_F32)
+    return fail(MFSDP_ERR_UNSUPPORTED, "unsupported gradient dtype %d", (int)out_dtype);
+  if (experts < 0 || rows < 0 || n < 1 || k < 1)
+    return fail(MFSDP_ERR_INVALID_ARGUMENT,
+                "experts=%lld rows=%lld n=%lld k=%lld: counts must be >= 0, widths >= 1",
+                (long long)experts, (long long)rows, (long long)n, (long long)k);
+  if (!finite(beta)) return fail(MFSDP_ERR_INVALID_ARGUMENT, "non-finite beta");
+  const int64_t np = mode == kGroupFwd ? k : n;                           // width of P's rows
+  const int64_t no = mode == kGroupFwd ? n : k;                           // width of the output's
+  if (ldp < np || (mode == kGroupWgrad ? ldq < k : ldo < no))
+    return fail(MFSDP_ERR_INVALID_ARGUMENT, "a row stride is smaller than the row");
+  if (experts > kGroupExpertsMax || rows > kGroupRowsMax || n > kGroupDimMax || k > kGroupDimMax ||
+      ldp > kGroupDimMax || ldq > kGroupDimMax || ldo > kGroupDimMax)
+    return fail(MFSDP_ERR_UNSUPPORTED, "a size exceeds the kernels' indexing");
+  if (experts == 0 || (rows == 0 && mode != kGroupWgrad)) return MFSDP_OK;
+  if (!out || !offsets || (rows > 0 && (!p || !q)) || (mode != kGroupWgrad && !q))
+    return fail(MFSDP_ERR_INVALID_ARGUMENT, "null pointer");
+  const size_t es = elem_size(dtype), eo = elem_size(out_dtype);
+  if (!aligned(p, es) || (!qs && !aligned(q, es)) || !aligned(out, eo) || !aligned(offsets, 4))
+    return fail(MFSDP_ERR_INVALID_ARGUMENT, "a buffer is not aligned to its elements");
+  {
+    std::vector<Range> ins, outs;
+    const size_t wb = static_cast<size_t>(experts) * n * k;
+    add_range(&ins, offsets, static_cast<size_t>(experts + 1) * 4, "offsets");
+    add_range(&ins, p, strided_bytes(rows, np, ldp, es), mode == kGroupFwd ? "x" : "dy");
+    if (mode == kGroupWgrad) {
+      add_range(&ins, q, strided_bytes(rows, k, ldq, qs ? 1 : es), qs ? "codes" : "x");
+      if (qs)
+        add_range(&ins, qs, static_cast<size_t>(rows) * ((k + kCkptBlock - 1) / kCkptBlock),
+                  "scales");
+      add_range(&outs, out, wb * eo, "dw");
+    } else {
+      add_range(&ins, q, wb * es, "weight");
+      add_range(&outs, out, strided_bytes(rows, no, ldo, es), mode == kGroupFwd ? "y" : "dx");
+    }
+    const mfsdp_status_t st = check_outputs(outs, ins);
+    if (st != MFSDP_OK) return st;
+  }
+
+  GroupArgs g{};
+  g.p = p;
+  g.q = q;
+  g.qs = qs;
+  g.out = out;
+  g.off = offsets;
+  g.ldp = ldp;
+  g.ldq = ldq;
+  g.ldo = ldo;
+  g.experts = static_cast<int32_t>(experts);
+  g.rows = static_cast<int32_t>(rows);
+  g.n = static_cast<int32_t>(n);
+  g.k = static_cast<int32_t>(k);
+  g.beta = beta;
+  g.out_f32 = out_dtype == MFSDP_DTYPE_F32 ? 1 : 0;
+
+  auto div = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
+  const int64_t blocks = mode == kGroupWgrad ? experts * div(n, 64) * div(k, 64)
+                                             : group_tiles_max(rows, experts, 64) * div(no, 64);
+  if (blocks >= (int64_t(1) << 31)) return fail(MFSDP_ERR_UNSUPPORTED, "too many tiles");
+  hipError_t e;
+  const bool bf = dtype == MFSDP_DTYPE_BF16;
+  if (mode == kGroupFwd)
+    e = bf ? launch_grouped<ElemBF16, kGroupFwd, false>(g, blocks, stream)
+           : launch_grouped<ElemF32, kGroupFwd, false>(g, blocks, stream);
+  else if (mode == kGroupDgrad)
+    e = bf ? launch_grouped<ElemBF16, kGroupDgrad, false>(g, blocks, stream)
+           : launch_grouped<ElemF32, kGroupDgrad, false>(g, blocks, stream);
+  else if (!qs)
+    e = bf ? launch_grouped<ElemBF16, kGroupWgrad, false>(g, blocks, stream)
+           : launch_grouped<ElemF32, kGroupWgrad, false>(g, blocks, stream);
+  else
+    e = bf ? launch_grouped<ElemBF16, kGroupWgrad, true>(g, blocks, stream)
+           : launch_grouped<ElemF32, kGroupWgrad, true>(g, blocks, stream);
+  if (e != hipSuccess) return fail(MFSDP_ERR_HIP, "grouped launch: %s", hipGetErrorString(e));
+  return MFSDP_OK;
+}
+
+// ---------------------------------------------------------------------------
+// 8-bit activation checkpoints
+// ---------------------------------------------------------------------------
+mfsdp_status_t ckpt_impl(bool quantize, void* x, int64_t ld, int8_t* codes, uint8_t* scales,
+                         int64_t rows, int64_t k, mfsdp_dtype_t dtype, hipStream_t stream) {
+  g_last_error.clear();
+  if (dtype != MFSDP_DTYPE_F32 && dtype != MFSDP_DTYPE_BF16)
+    return fail(MFSDP_ERR_UNSUPPORTED, "unsupported dtype %d", (int)dtype);
+  if (rows < 0 || k < 1 || ld < k)
+    return fail(MFSDP_ERR_INVALID_ARGUMENT, "rows=%lld k=%lld ld=%lld", (long long)rows,
+                (long long)k, (long long)ld);
+  if (rows > kGroupRowsMax || k > kGroupDimMax || ld > kGroupDimMax)
+    return fail(MFSDP_ERR_UNSUPPORTED, "a size exceeds the kernels' indexing");
+  if (rows == 0) return MFSDP_OK;
+  if (!x || !codes || !scales) return fail(MFSDP_ERR_INVALID_ARGUMENT, "null pointer");
+  const size_t es = elem_size(dtype);
+  if (!aligned(x, es))
+    return fail(MFSDP_ERR_INVALID_ARGUMENT, "a buffer is not aligned to its elements");
+  CkptArgs a{};
+  a.x = x;
+  a.codes = codes;
+  a.scales = scales;
+  a.ld = ld;
+  a.k = static_cast<int32_t>(k);
+  a.nb = static_cast<int32_t>((k + kCkptBlock - 1) / kCkptBlock);
+  a.units = rows * a.nb;
+  a.vec = aligned(x, 16) && (ld * static_cast<int64_t>(es)) % 16 == 0 && k % 8 == 0 &&
+          aligned(codes, 8);
+  {
+    std::vector<Range> xs, cs;
+    add_range(&xs, x, strided_bytes(rows, k, ld, es), "x");
+    add_range(&cs, codes, static_cast<size_t>(rows) * k, "codes");
+    add_range(&cs, scales, static_cast<size_t>(a.units), "scales");
+    const mfsdp_status_t st = quantize ? check_outputs(cs, xs) : check_outputs(xs, cs);
+    if (st != MFSDP_OK) return st;
+  }
+  const int64_t blocks = (a.units + 16 * kCkptUnits - 1) / (16 * kCkptUnits);
+  if (blocks >= (int64_t(1) << 31)) return fail(MFSDP_ERR_UNSUPPORTED, "too many blocks");
+  const dim3 grid(static_cast<unsigned>(blocks)), wg(256);
+  const hipError_t e = launch(MFSDP_KERNEL_CKPT, stream, [&] {
+    if (quantize) {
+      if (dtype == MFSDP_DTYPE_BF16) ckpt_quantize_kernel<ElemBF16><<<grid, wg, 0, stream>>>(a);
+      else ckpt_quantize_kernel<ElemF32><<<grid, wg, 0, stream>>>(a);
+    } else {
+      if (dtype == MFSDP_DTYPE_BF16) ckpt_restore_kernel<ElemBF16><<<grid, wg, 0, stream>>>(a);
+      else ckpt_restore_kernel<ElemF32><<<grid, wg, 0, stream>>>(a);
+    }
+  });
+  if (e != hipSuccess) return fail(MFSDP_ERR_HIP, "checkpoint launch: %s", hipGetErrorString(e));
+  return MFSDP_OK;
+}
+
+// ---------------------------------------------------------------------------
+// Embedding
+// ---------------------------------------------------------------------------
+constexpr int64_t kEmbVocabMax = (int64_t(1) << 31) - 1;
+constexpr int64_t kEmbTokensMax = int64_t(1) << 28;
+
+template <class ET, class EO>
+hipError_t launch_embedding(const EmbArgs& a, bool vec, int64_t blocks, hipStream_t stream) {
+  return launch(MFSDP_KERNEL_EMBED, stream, [&] {
+    const dim3 grid(static_cast<unsigned>(blocks)), wg(256);
+    if (vec) embedding_kernel<ET, EO, true><<<grid, wg, 0, stream>>>(a);
+    else embedding_kernel<ET, EO, false><<<grid, wg, 0, stream>>>(a);
+  });
+}
+
+mfsdp_status_t embedding_impl(const void* table, mfsdp_dtype_t table_dtype, int64_t vocab,
+                              int64_t d, const void* tokens, int token_bytes, int64_t n_tokens,
+                              float scale, void* out, int64_t ldo, mfsdp_dtype_t out_dtype,
+                              hipStream_t stream) {
+  g_last_error.clear();
+  for (mfsdp_dtype_t dt : {table_dtype, out_dtype})
+    if (dt != MFSDP_DTYPE_F32 && dt != MFSDP_DTYPE_BF16)
+      return fail(MFSDP_ERR_UNSUPPORTED, "unsupported dtype %d", (int)dt);
+  if (token_bytes != 4 && token_bytes != 8)
+    return fail(MFSDP_ERR_UNSUPPORTED, "tokens of %d bytes: 4 or 8 are taken", token_bytes);
+  if (vocab < 1 || d < 1 || n_tokens < 0 || ldo < d)
+    return fail(MFSDP_ERR_INVALID_ARGUMENT, "vocab=%lld d=%lld tokens=%lld ldo=%lld",
+                (long long)vocab, (long long)d, (long long)n_tokens, (long long)ldo);
+  if (!finite(scale)) return fail(MFSDP_ERR_INVALID_ARGUMENT, "non-finite scale");
+  if (vocab > kEmbVocabMax || d > kGroupDimMax || ldo > kGroupDimMax || n_tokens > kEmbTokensMax)
+    return fail(MFSDP_ERR_UNSUPPORTED, "a size exceeds the kernels' indexing");
+  if (n_tokens == 0) return MFSDP_OK;
+  if (!table || !tokens || !out) return fail(MFSDP_ERR_INVALID_ARGUMENT, "null pointer");
+  const size_t et = elem_size(table_dtype), eo = elem_size(out_dtype);
+  if (!aligned(table, et) || !aligned(out, eo) || !aligned(tokens, token_bytes))
+    return fail(MFSDP_ERR_INVALID_ARGUMENT, "a buffer is not aligned to its elements");
+  {
+    std::vector<Range> ins, outs;
+    add_range(&ins, table, static_cast<size_t>(vocab) * d * et, "table");
+    add_range(&ins, tokens, static_cast<size_t>(n_tokens) * token_bytes, "tokens");
+    add_range(&outs, out, strided_bytes(n_tokens, d, ldo, eo), "out");
+    const mfsdp_status_t st = check_outputs(outs, ins);
+    if (st != MFSDP_OK) return st;
+  }
+  EmbArgs a{};
+  a.table = table;
+  a.tokens = tokens;
+  a.out = out;
+  a.n_tokens = n_tokens;
+  a.vocab = vocab;
+  a.ldo = ldo;
+  a.d = static_cast<int32_t>(d);
+  a.tok64 = token_bytes == 8;
+  a.scale = scale;
+  const bool vec = d % 8 == 0 && aligned(table, 16) && aligned(out, 16) &&
+                   (ldo * static_cast<int64_t>(eo)) % 16 == 0;
+  const int64_t units = vec ? d / 8 : d;
+  int64_t blocks;
+  if (units > 128) {
+    a.chunks = static_cast<int32_t>((units + 255) / 256);
+    blocks = n_tokens * a.chunks;
+  } else {
+    a.per_wg = static_cast<int32_t>(256 / units);
+    blocks = (n_tokens + a.per_wg - 1) / a.per_wg;
+  }
+  if (blocks >= (int64_t(1) << 31)) return fail(MFSDP_ERR_UNSUPPORTED, "too many rows");
+  const bool tb = table_dtype == MFSDP_DTYPE_BF16, ob = out_dtype == MFSDP_DTYPE_BF16;
+  const hipError_t e = tb ? (ob ? launch_embedding<ElemBF16, ElemBF16>(a, vec, blocks, stream)
+                                : launch_embedding<ElemBF16, ElemF32>(a, vec, blocks, stream))
+                          : (ob ? launch_embedding<ElemF32, ElemBF16>(a, vec, blocks, stream)
+                                : launch_embedding<ElemF32, ElemF32>(a, vec, blocks, stream));
+  if (e != hipSuccess) return fail(MFSDP_ERR_HIP, "embedding launch: %s", hipGetErrorString(e));
+  return MFSDP_OK;
+}
+
+// Workspace of an embedding gradient: two (key, position) lists, the digit
+// counts of the sort and the partial rows of long runs.
+struct EmbPlan {
+  size_t key0, pos0, key1, pos1, hist, part, total;
+  int32_t key_bits, bits, passes, per_block, blocks;
+};
+
+// Lists up to this length are sorted by one workgroup in one launch.
+constexpr int64_t kSortSmall = 4096;
+
+EmbPlan emb_plan(int64_t n, int64_t vocab, int64_t d) {
+  EmbPlan p{};
+  p.key_bits = 1;
+  while ((int64_t(1) << p.key_bits) <= vocab) ++p.key_bits;    // keys are 0..vocab
+  p.passes = (p.key_bits + kSortBitsMax - 1) / kSortBitsMax;
+  p.bits = (p.key_bits + p.passes - 1) / p.passes;
+  // at most 512 workgroups: each reads the digit counts of all of them
+  const int64_t per = std::max<int64_t>(2048, (n + 511) / 512);
+  p.per_block = static_cast<int32_t>(round_up(per, kSortThreads));
+  p.blocks = n <= kSortSmall ? 1 : static_cast<int32_t>((n + p.per_block - 1) / p.per_block);
+  size_t off = 0;
+  auto take = [&](size_t nb) {
+    const size_t at = off;
+    off = align_up(off + nb, kWsAlign);
+    return at;
+  };
+  const size_t list = static_cast<size_t>(n) * 4;
+  p.key0 = take(list);
+  p.pos0 = take(list);
+  p.key1 = take(list);
+  p.pos1 = take(list);
+  p.hist = take(p.blocks > 1 ? (static_cast<size_t>(p.blocks) << p.bits) * 4 : 0);
+  p.part = take(n > kEmbRun ? static_cast<size_t>((n + kEmbRun - 1) / kEmbRun) * 2 * d * 4 : 0);
+  p.total = off;
+  return p;
+}
+
+mfsdp_status_t emb_grad_sizes(int64_t n_tokens, int64_t vocab, int64_t d) {
+  if (vocab < 1 || d < 1 || n_tokens < 0)
+    return fail(MFSDP_ERR_INVALID_ARGUMENT, "vocab=%lld d=%lld tokens=%lld", (long long)vocab,
+                (long long)d, (long long)n_tokens);
+  if (vocab > kEmbVocabMax || d > kGroupDimMax || n_tokens > kEmbTokensMax)
+    return fail(MFSDP_ERR_UNSUPPORTED, "a size exceeds the kernels' indexing");
+  return MFSDP_OK;
+}
+
+template <class E, int W>
+hipError_t launch_emb_sums(const EmbGradArgs& a, hipStream_t stream) {
+  const int64_t col_wgs = (a.d / W + 255) / 256;
+  hipError_t e = hipSuccess;
+  if (a.n > kEmbRun) {
+    const int64_t blocks = (a.n + kEmbRun - 1) / kEmbRun * col_wgs;
+    e = launch(MFSDP_KERNEL_EMBED_GRAD, stream, [&] {
+      emb_partial_kernel<E, W><<<dim3(static_cast<unsigned>(blocks)), dim3(256), 0, stream>>>(
+          a, static_cast<int>(col_wgs));
+    });
+    if (e != hipSuccess) return e;
+  }
+  const int64_t blocks = (a.vocab + kEmbRows - 1) / kEmbRows * col_wgs;
+  return launch(MFSDP_KERNEL_EMBED_GRAD, stream, [&] {
+    emb_rows_kernel<E, W><<<dim3(static_cast<unsigned>(blocks)), dim3(256), 0, stream>>>(
+        a, static_cast<int>(col_wgs));
+  });
+}
+
+mfsdp_status_t embedding_grad_impl(const void* dy, int64_t ld, mfsdp_dtype_t dtype,
+                                   const void* tokens, int token_bytes, int64_t n_tokens,
+                                   int64_t vocab, int64_t d, float scale, float beta, float* grad,
+                                   void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  g_last_error.clear();
+  if (dtype != MFSDP_DTYPE_F32 && dtype != MFSDP_DTYPE_BF16)
+    return fail(MFSDP_ERR_UNSUPPORTED, "unsupported dtype %d", (int)dtype);
+  if (token_bytes != 4 && token_bytes != 8)
+    return fail(MFSDP_ERR_UNSUPPORTED, "tokens of %d bytes: 4 or 8 are taken", token_bytes);
+  mfsdp_status_t st = emb_grad_sizes(n_tokens, vocab, d);
+  if (st != MFSDP_OK) return st;
+  if (ld < d) return fail(MFSDP_ERR_INVALID_ARGUMENT, "a row stride is smaller than the row");
+  if (ld > kGroupDimMax) return fail(MFSDP_ERR_UNSUPPORTED, "a size exceeds the kernels' indexing");
+  if (!finite(scale) || !finite(beta))
+    return fail(MFSDP_ERR_INVALID_ARGUMENT, "non-finite scale or beta");
+  if (!grad || (n_tokens > 0 && (!dy || !tokens)))
+    return fail(MFSDP_ERR_INVALID_ARGUMENT, "null pointer");
+  const size_t es = elem_size(dtype);
+  if ((n_tokens > 0 && (!aligned(dy, es) || !aligned(tokens, token_bytes))) || !aligned(grad, 4))
+    return fail(MFSDP_ERR_INVALID_ARGUMENT, "a buffer is not aligned to its elements");
+  const EmbPlan p = emb_plan(n_tokens, vocab, d);
+  if (n_tokens > 0) {
+    if (!workspace) return fail(MFSDP_ERR_WORKSPACE, "workspace is null");
+    if (!aligned(workspace, kWsAlign))
+      return fail(MFSDP_ERR_WORKSPACE, "workspace must be %zu-byte aligned", kWsAlign);
+    if (workspace_bytes < p.total)
+      return fail(MFSDP_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", workspace_bytes,
+                  p.total);
+  }
+  {
+    std::vector<Range> ins, outs;
+    add_range(&ins, dy, strided_bytes(n_tokens, d, ld, es), "dy");
+    add_range(&ins, tokens, static_cast<size_t>(n_tokens) * token_bytes, "tokens");
+    add_range(&outs, grad, static_cast<size_t>(vocab) * d * 4, "grad");
+    if (n_tokens > 0) add_range(&outs, workspace, p.total, "workspace");
+    st = check_outputs(outs, ins);
+    if (st != MFSDP_OK) return st;
+  }
+  const bool vec = d % 8 == 0 && aligned(grad, 16) && aligned(dy, 16) &&
+                   (ld * static_cast<int64_t>(es)) % 16 == 0;
+  const int64_t col_wgs = ((vec ? d / 8 : d) + 255) / 256;
+  if ((vocab + kEmbRows - 1) / kEmbRows * col_wgs >= (int64_t(1) << 31) ||
+      (n_tokens + kEmbRun - 1) / kEmbRun * col_wgs >= (int64_t(1) << 31))
+    return fail(MFSDP_ERR_UNSUPPORTED, "too many rows");
+
+  char* ws = static_cast<char*>(workspace);
+  EmbGradArgs a{};
+  a.dy = dy;
+  a.grad = grad;
+  a.vocab = vocab;
+  a.ld = ld;
+  a.n = static_cast<int32_t>(n_tokens);
+  a.d = static_cast<int32_t>(d);
+  a.scale = scale;
+  a.beta = beta;
+  hipError_t e = hipSuccess;
+  if (n_tokens > 0) {
+    uint32_t* key[2] = {reinterpret_cast<uint32_t*>(ws + p.key0), reinterpret_cast<uint32_t*>(ws + p.key1)};
+    uint32_t* pos[2] = {reinterpret_cast<uint32_t*>(ws + p.pos0), reinterpret_cast<uint32_t*>(ws + p.pos1)};
+    SortArgs s{};
+    s.tokens = tokens;
+    s.hist = reinterpret_cast<uint32_t*>(ws + p.hist);
+    s.vocab = vocab;
+    s.n = a.n;
+    s.tok64 = token_bytes == 8;
+    s.per_block = p.per_block;
+    s.bits = p.bits;
+    int at = 0;   // list that holds the result
+    if (p.blocks == 1) {
+      SortSmallArgs sm{};
+      sm.s = s;
+      sm.s.key_out = key[0];
+      sm.s.pos_out = pos[0];
+      sm.key_tmp = key[1];
+      sm.pos_tmp = pos[1];
+      sm.key_bits = p.key_bits;
+      sm.passes = p.passes;
+      e = launch(MFSDP_KERNEL_EMBED_GRAD, stream, [&] {
+        sort_small_kernel<<<dim3(1), dim3(kSortThreads), 0, stream>>>(sm);
+      });
+    } else {
+      for (int q = 0; q < p.passes && e == hipSuccess; ++q) {
+        s.first = q == 0;
+        s.shift = q * p.bits;
+        s.key_in = key[at];
+        s.pos_in = pos[at];
+        at ^= 1;
+        s.key_out = key[at];
+        s.pos_out = pos[at];
+        const dim3 grid(static_cast<unsigned>(p.blocks)), wg(kSortThreads);
+        e = launch(MFSDP_KERNEL_EMBED_GRAD, stream,
+                   [&] { sort_hist_kernel<<<grid, wg, 0, stream>>>(s); });
+        if (e == hipSuccess)
+          e = launch(MFSDP_KERNEL_EMBED_GRAD, stream,
+                     [&] { sort_scatter_kernel<<<grid, wg, 0, stream>>>(s); });
+      }
+    }
+    if (e != hipSuccess) return fail(MFSDP_ERR_HIP, "sort launch: %s", hipGetErrorString(e));
+    a.key = key[at];
+    a.pos = pos[at];
+    a.part = reinterpret_cast<float*>(ws + p.part);
+  }
+  if (dtype == MFSDP_DTYPE_BF16)
+    e = vec ? launch_emb_sums<ElemBF16, 8>(a, stream) : launch_emb_sums<ElemBF16, 1>(a, stream);
+  else
+    e = vec ? launch_emb_sums<ElemF32, 8>(a, stream) : launch_emb_sums<ElemF32, 1>(a, stream);
+  if (e != hipSuccess)
+    return fail(MFSDP_ERR_HIP, "embedding gradient launch: %s", hipGetErrorString(e));
+  return MFSDP_OK;
+}
+
+// No C++ exception crosses the ABI.
+template <class F>
+mfsdp_status_t guarded(F&& f) {
+  try {
+    return f();
+  } catch (const std::exception& ex) {
+    return fail(MFSDP_ERR_UNSUPPORTED, "host exception: %s", ex.what());
+  }
+}
+
+}  // namespace
+
+extern "C" {
+
+mfsdp_status_t mfsdp_grouped_linear(const void* x, int64_t ld_x, const void* weight,
+                                    const int32_t* offsets, int64_t n_experts, int64_t rows,
+                                    int64_t n, int64_t k, mfsdp_dtype_t dtype, void* y,
+                                    int64_t ld_y, hipStream_t stream) {
+  return guarded([&] {
+    return grouped_impl(kGroupFwd, x, ld_x, weight, 0, nullptr, offsets, n_experts, rows, n, k,
+                        dtype, y, ld_y, dtype, 0.f, stream);
+  });
+}
+
+mfsdp_status_t mfsdp_grouped_linear_dgrad(const void* dy, int64_t ld_dy, const void* weight,
+                                          const int32_t* offsets, int64_t n_experts, int64_t rows,
+                                          int64_t n, int64_t k, mfsdp_dtype_t dtype, void* dx,
+                                          int64_t ld_dx, hipStream_t stream) {
+  return guarded([&] {
+    return grouped_impl(kGroupDgrad, dy, ld_dy, weight, 0, nullptr, offsets, n_experts, rows, n, k,
+                        dtype, dx, ld_dx, dtype, 0.f, stream);
+  });
+}
+
+mfsdp_status_t mfsdp_grouped_linear_wgrad(const void* dy, int64_t ld_dy, const void* x,
+                                          int64_t ld_x, const int32_t* offsets, int64_t n_experts,
+                                          int64_t rows, int64_t n, int64_t k, mfsdp_dtype_t dtype,
+                                          void* dw, mfsdp_dtype_t dw_dtype, float beta,
+                                          hipStream_t stream) {
+  return guarded([&] {
+    return grouped_impl(kGroupWgrad, dy, ld_dy, x, ld_x, nullptr, offsets, n_experts, rows, n, k,
+                        dtype, dw, 0, dw_dtype, beta, stream);
+  });
+}
+
+mfsdp_status_t mfsdp_grouped_linear_wgrad_ckpt(const void* dy, int64_t ld_dy, const int8_t* codes,
+                                               const uint8_t* scales, const int32_t* offsets,
+                                               int64_t n_experts, int64_t rows, int64_t n,
+                                               int64_t k, mfsdp_dtype_t dtype, void* dw,
+                                               mfsdp_dtype_t dw_dtype, float beta,
+                                               hipStream_t stream) {
+  return guarded([&]() -> mfsdp_status_t {
+    if (!scales && rows > 0 && n_experts > 0) {
+      g_last_error.clear();
+      return fail(MFSDP_ERR_INVALID_ARGUMENT, "null pointer");
+    }
+    return grouped_impl(kGroupWgrad, dy, ld_dy, codes, k, scales, offsets, n_experts, rows, n, k,
+                        dtype, dw, 0, dw_dtype, beta, stream);
+  });
+}
+
+mfsdp_status_t mfsdp_ckpt_quantize(const void* x, int64_t ld_x, int64_t rows, int64_t k,
+                                   mfsdp_dtype_t dtype, int8_t* codes, uint8_t* scales,
+                                   hipStream_t stream) {
+  return guarded([&] {
+    return ckpt_impl(true, const_cast<void*>(x), ld_x, codes, scales, rows, k, dtype, stream);
+  });
+}
+
+mfsdp_status_t mfsdp_ckpt_restore(const int8_t* codes, const uint8_t* scales, int64_t rows,
+                                  int64_t k, mfsdp_dtype_t dtype, void* x, int64_t ld_x,
+                                  hipStream_t stream) {
+  return guarded([&] {
+    return ckpt_impl(false, x, ld_x, const_cast<int8_t*>(codes), const_cast<uint8_t*>(scales),
+                     rows, k, dtype, stream);
+  });
+}
+
+mfsdp_status_t mfsdp_embedding(const void* table, mfsdp_dtype_t table_dtype, int64_t vocab,
+                               int64_t d, const void* tokens, int token_bytes, int64_t n_tokens,
+                               float scale, void* out, int64_t ld_out, mfsdp_dtype_t out_dtype,
+                               hipStream_t stream) {
+  return guarded([&] {
+    return embedding_impl(table, table_dtype, vocab, d, tokens, token_bytes, n_tokens, scale, out,
+                          ld_out, out_dtype, stream);
+  });
+}
+
+mfsdp_status_t mfsdp_embedding_grad_workspace_size(int64_t n_tokens, int64_t vocab, int64_t d,
+                                                   size_t* out_bytes) {
+  return guarded([&]() -> mfsdp_status_t {
+    g_last_error.clear();
+    if (!out_bytes) return fail(MFSDP_ERR_INVALID_ARGUMENT, "out_bytes is null");
+    const mfsdp_status_t st = emb_grad_sizes(n_tokens, vocab, d);
+    if (st == MFSDP_OK) *out_bytes = n_tokens > 0 ? emb_plan(n_tokens, vocab, d).total : 0;
+    return st;
+  });
+}
+
+mfsdp_status_t mfsdp_embedding_grad(const void* dy, int64_t ld_dy, mfsdp_dtype_t dtype,
+                                    const void* tokens, int token_bytes, int64_t n_tokens,
+                                    int64_t vocab, int64_t d, float scale, float beta, float* grad,
+                                    void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  return guarded([&] {
+    return embedding_grad_impl(dy, ld_dy, dtype, tokens, token_bytes, n_tokens, vocab, d, scale,
+                               beta, grad, workspace, workspace_bytes, stream);
+  });
+}
+
+}  // extern "C"

@@ -24,8 +24,11 @@
 #include <vector>
 
 #include "../../include/mfsdp.h"
+#include "ckpt_kernels.hpp"
 #include "common.hpp"
+#include "embedding_kernels.hpp"
 #include "ew_kernels.hpp"
+#include "grouped_kernels.hpp"
 #include "ns_gemm.hpp"
 #include "ns_small.hpp"
 #include "planner.hpp"
@@ -110,7 +113,13 @@ hipError_t launch(int kind, hipStream_t stream, F&& f) {
     if (a) g_timing.free_events.push_back(a);
     if (b) g_timing.free_events.push_back(b);
   };
-  if (g_timing.enabled) {
+  bool timed = g_timing.enabled;
+  if (timed) {   // an event recorded into a graph has no time of its own
+    hipStreamCaptureStatus cs = hipStreamCaptureStatusNone;
+    if (hipStreamIsCapturing(stream, &cs) == hipSuccess && cs != hipStreamCaptureStatusNone)
+      timed = false;
+  }
+  if (timed) {
     hipError_t e = take_event(&a);
     if (e == hipSuccess) e = take_event(&b);
     if (e == hipSuccess) e = hipEventRecord(a, stream);
@@ -121,12 +130,12 @@ hipError_t launch(int kind, hipStream_t stream, F&& f) {
   }
   f();
   hipError_t e = hipGetLastError();
-  if (e == hipSuccess && g_timing.enabled) e = hipEventRecord(b, stream);
+  if (e == hipSuccess && timed) e = hipEventRecord(b, stream);
   if (e != hipSuccess) {
     give_back();
     return e;
   }
-  if (g_timing.enabled) g_timing.pending.push_back({kind, a, b});
+  if (timed) g_timing.pending.push_back({kind, a, b});
   return hipSuccess;
 }
 
@@ -1373,3 +1382,5 @@ mfsdp_status_t mfsdp_timing_read(mfsdp_kernel_kind_t kind, double* total_ms, int
 }
 
 }  // extern "C"
+
+#include "grads_host.hpp"

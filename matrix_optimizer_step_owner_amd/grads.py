@@ -1,0 +1,298 @@
+"""The gradients that the owner-local step takes, where they are more than one
+plain matrix product: experts' matrices (``grouped_linear`` and its gradients),
+8-bit activation checkpoints, and the embedding table.
+
+Argument checks and marshalling only (C ABI in ``include/mfsdp.h``); every call
+runs on torch's current stream of its tensors' device, waits for nothing and
+can be captured into a graph.  None of them records an autograd graph: the
+gradients are calls of their own, and write where the step reads them --
+``grouped_linear_wgrad`` into the stacked ``(experts, n, k)`` gradient whose
+views ``grad[e]`` a ``MuonStep`` takes, ``embedding_grad`` into the table's
+segment of the packed gradient of ``adamw_tail``.
+
+Source of the setting: arxivlens page, Abstract (the owner holds whole 2D
+weights with their whole gradients; the other tensors are packed for AdamW).
+"""
+
+from __future__ import annotations
+
+import ctypes
+from typing import Optional, Tuple
+
+import torch
+
+from . import _lib
+
+#: columns of an activation row that share one checkpoint scale
+CKPT_BLOCK = 128
+
+_DTYPES = {torch.float32: _lib.DTYPE_F32, torch.bfloat16: _lib.DTYPE_BF16}
+
+
+def _check(t: torch.Tensor, name: str, device, dtypes, dim: int) -> None:
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a tensor")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {' or '.join(map(str, dtypes))}")
+    if t.dim() != dim:
+        raise ValueError(f"{name} must be {dim}D")
+
+
+def _contiguous(t: torch.Tensor, name: str, shape=None) -> None:
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+
+
+def _rows(t: torch.Tensor, name: str, shape=None) -> int:
+    """Row stride of a matrix whose rows are contiguous (any stride between rows)."""
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.size(1) > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    if t.size(0) <= 1:
+        return max(t.size(1), 1)
+    if t.stride(0) < t.size(1):
+        raise ValueError(f"rows of {name} overlap")
+    return t.stride(0)
+
+
+def _gpu(t: torch.Tensor, name: str) -> torch.device:
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a tensor")
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} must be a GPU tensor")
+    return t.device
+
+
+def _call(device: torch.device, fn, *args) -> None:
+    """fn(*args, stream) with `device` current, on its current stream."""
+    with torch.cuda.device(device):
+        _lib.check(fn(*args, torch.cuda.current_stream(device).cuda_stream))
+
+
+def _scratch(device: torch.device, nbytes: int, given: Optional[torch.Tensor]) -> torch.Tensor:
+    """The caller's workspace; else one kept per (device, stream), which calls
+    on that stream share in order; else, under capture, one that belongs to the
+    graph (a kept one could be replayed by two graphs at once)."""
+    if given is not None:
+        _check(given, "workspace", device, (given.dtype,), given.dim())
+        _contiguous(given, "workspace")
+        return given
+    with torch.cuda.device(device):
+        if torch.cuda.is_current_stream_capturing():
+            return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
+    from . import _workspace
+    return _workspace(device, torch.cuda.current_stream(device).cuda_stream, nbytes)
+
+
+def _grouped_args(act: torch.Tensor, name: str, weight: torch.Tensor, wname: str,
+                  offsets: torch.Tensor):
+    device = _gpu(act, name)
+    _check(act, name, device, tuple(_DTYPES), 2)
+    _check(offsets, "offsets", device, (torch.int32,), 1)
+    _check(weight, wname, device, tuple(_DTYPES), 3)
+    _contiguous(weight, wname)
+    _contiguous(offsets, "offsets", (weight.size(0) + 1,))
+    return device
+
+
+def grouped_linear(x: torch.Tensor, weight: torch.Tensor, offsets: torch.Tensor,
+                   out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """``out[r] = x[r] @ weight[e].T`` for the rows offsets[e] <= r < offsets[e+1]
+    of every expert e (mfsdp_grouped_linear).
+
+    x: (rows, k) bf16 or fp32, rows contiguous at any stride, sorted by expert;
+    weight: (experts, n, k) contiguous, x's dtype; offsets: (experts + 1,) int32
+    on the GPU, non-decreasing, read there.  Rows of no expert are left as they
+    are in ``out`` (and undefined in an ``out`` made here)."""
+    device = _grouped_args(x, "x", weight, "weight", offsets)
+    experts, n, k = weight.shape
+    if weight.dtype != x.dtype:
+        raise TypeError(f"weight has dtype {weight.dtype}, expected {x.dtype}")
+    ldx = _rows(x, "x", (x.size(0), k))
+    if out is None:
+        out = torch.empty(x.size(0), n, dtype=x.dtype, device=device)
+    _check(out, "out", device, (x.dtype,), 2)
+    _call(device, _lib.load().mfsdp_grouped_linear, x.data_ptr(), ldx, weight.data_ptr(),
+          offsets.data_ptr(), experts, x.size(0), n, k, _DTYPES[x.dtype], out.data_ptr(),
+          _rows(out, "out", (x.size(0), n)))
+    return out
+
+
+def grouped_linear_dgrad(dy: torch.Tensor, weight: torch.Tensor, offsets: torch.Tensor,
+                         out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Gradient of ``grouped_linear``'s input: ``out[r] = dy[r] @ weight[e]``
+    (mfsdp_grouped_linear_dgrad).  dy: (rows, n); out: (rows, k); the rest as
+    there."""
+    device = _grouped_args(dy, "dy", weight, "weight", offsets)
+    experts, n, k = weight.shape
+    if weight.dtype != dy.dtype:
+        raise TypeError(f"weight has dtype {weight.dtype}, expected {dy.dtype}")
+    lddy = _rows(dy, "dy", (dy.size(0), n))
+    if out is None:
+        out = torch.empty(dy.size(0), k, dtype=dy.dtype, device=device)
+    _check(out, "out", device, (dy.dtype,), 2)
+    _call(device, _lib.load().mfsdp_grouped_linear_dgrad, dy.data_ptr(), lddy, weight.data_ptr(),
+          offsets.data_ptr(), experts, dy.size(0), n, k, _DTYPES[dy.dtype], out.data_ptr(),
+          _rows(out, "out", (dy.size(0), k)))
+    return out
+
+
+def grouped_linear_wgrad(dy: torch.Tensor, x: torch.Tensor, offsets: torch.Tensor,
+                         grad: torch.Tensor, beta: float = 0.0) -> torch.Tensor:
+    """Gradients of the experts' matrices, in place:
+    ``grad[e] = beta * grad[e] + dy[rows of e].T @ x[rows of e]``
+    (mfsdp_grouped_linear_wgrad).
+
+    dy: (rows, n), x: (rows, k), one dtype; grad: (experts, n, k) contiguous in
+    that dtype or fp32, each ``grad[e]`` as ``muon_step`` takes it.  beta = 1
+    adds a micro-batch to what is there; beta = 0 does not read it.  An expert
+    without rows gets ``beta * grad[e]``.  Returns grad."""
+    device = _grouped_args(dy, "dy", grad, "grad", offsets)
+    experts, n, k = grad.shape
+    if grad.dtype not in (dy.dtype, torch.float32):
+        raise TypeError(f"grad has dtype {grad.dtype}, expected {dy.dtype} or torch.float32")
+    _check(x, "x", device, (dy.dtype,), 2)
+    _call(device, _lib.load().mfsdp_grouped_linear_wgrad, dy.data_ptr(),
+          _rows(dy, "dy", (dy.size(0), n)), x.data_ptr(), _rows(x, "x", (dy.size(0), k)),
+          offsets.data_ptr(), experts, dy.size(0), n, k, _DTYPES[dy.dtype], grad.data_ptr(),
+          _DTYPES[grad.dtype], beta)
+    return grad
+
+
+def _check_ckpt(codes: torch.Tensor, scales: torch.Tensor, device, rows: int, k: int) -> None:
+    _check(codes, "codes", device, (torch.int8,), 2)
+    _check(scales, "scales", device, (torch.uint8,), 2)
+    _contiguous(codes, "codes", (rows, k))
+    _contiguous(scales, "scales", (rows, -(-k // CKPT_BLOCK)))
+
+
+def grouped_linear_wgrad_ckpt(dy: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor,
+                              offsets: torch.Tensor, grad: torch.Tensor,
+                              beta: float = 0.0) -> torch.Tensor:
+    """``grouped_linear_wgrad`` with x as its 8-bit checkpoint, (codes, scales)
+    of ``ckpt_quantize`` (mfsdp_grouped_linear_wgrad_ckpt): the gradient for the
+    restored x, which is never written out."""
+    device = _grouped_args(dy, "dy", grad, "grad", offsets)
+    experts, n, k = grad.shape
+    if grad.dtype not in (dy.dtype, torch.float32):
+        raise TypeError(f"grad has dtype {grad.dtype}, expected {dy.dtype} or torch.float32")
+    _check_ckpt(codes, scales, device, dy.size(0), k)
+    _call(device, _lib.load().mfsdp_grouped_linear_wgrad_ckpt, dy.data_ptr(),
+          _rows(dy, "dy", (dy.size(0), n)), codes.data_ptr(), scales.data_ptr(),
+          offsets.data_ptr(), experts, dy.size(0), n, k, _DTYPES[dy.dtype], grad.data_ptr(),
+          _DTYPES[grad.dtype], beta)
+    return grad
+
+
+def ckpt_quantize(x: torch.Tensor, codes: Optional[torch.Tensor] = None,
+                  scales: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """8-bit checkpoint of an activation (mfsdp_ckpt_quantize): int8 codes
+    (rows, k) and uint8 scales (rows, ceil(k / 128)).
+
+    Each block of 128 columns of a row is held as whole numbers q and one power
+    of two 2^e (scale byte e + 127), the smallest with max|x| <= 127 * 2^e;
+    x is held as q * 2^e, off by at most half of 2^e.  x: (rows, k) bf16 or
+    fp32, rows contiguous at any stride."""
+    device = _gpu(x, "x")
+    _check(x, "x", device, tuple(_DTYPES), 2)
+    rows, k = x.shape
+    if codes is None:
+        codes = torch.empty(rows, k, dtype=torch.int8, device=device)
+    if scales is None:
+        scales = torch.empty(rows, -(-k // CKPT_BLOCK), dtype=torch.uint8, device=device)
+    _check_ckpt(codes, scales, device, rows, k)
+    _call(device, _lib.load().mfsdp_ckpt_quantize, x.data_ptr(), _rows(x, "x"), rows, k,
+          _DTYPES[x.dtype], codes.data_ptr(), scales.data_ptr())
+    return codes, scales
+
+
+def ckpt_restore(codes: torch.Tensor, scales: torch.Tensor, dtype: torch.dtype = torch.bfloat16,
+                 out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The activation that a checkpoint holds, in bf16 or fp32 (exact in both;
+    mfsdp_ckpt_restore).  With ``out`` its dtype is taken."""
+    device = _gpu(codes, "codes")
+    _check(codes, "codes", device, (torch.int8,), 2)
+    rows, k = codes.shape
+    _check_ckpt(codes, scales, device, rows, k)
+    if out is None:
+        if dtype not in _DTYPES:
+            raise TypeError(f"unsupported dtype {dtype}")
+        out = torch.empty(rows, k, dtype=dtype, device=device)
+    _check(out, "out", device, tuple(_DTYPES), 2)
+    _call(device, _lib.load().mfsdp_ckpt_restore, codes.data_ptr(), scales.data_ptr(), rows, k,
+          _DTYPES[out.dtype], out.data_ptr(), _rows(out, "out", (rows, k)))
+    return out
+
+
+def _check_tokens(tokens: torch.Tensor, device) -> int:
+    _check(tokens, "tokens", device, (torch.int32, torch.int64), tokens.dim())
+    _contiguous(tokens, "tokens")
+    return tokens.element_size()
+
+
+def embedding(table: torch.Tensor, tokens: torch.Tensor, *, scale: float = 1.0,
+              dtype: Optional[torch.dtype] = None,
+              out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """``scale * table[token]`` for a list of tokens, computed in fp32 and
+    rounded once (mfsdp_embedding).
+
+    table: (vocab, d) contiguous, bf16 or fp32; tokens: int32 or int64 of any
+    shape, contiguous; a token outside [0, vocab) stands for padding and gives
+    a row of zeros.  Returns tokens.shape + (d,) in ``dtype`` (default the
+    table's), or writes ``out``, (number of tokens, d) with rows at any
+    stride."""
+    device = _gpu(table, "table")
+    _check(table, "table", device, tuple(_DTYPES), 2)
+    _contiguous(table, "table")
+    size = _check_tokens(tokens, device)
+    vocab, d = table.shape
+    n = tokens.numel()
+    shape = None
+    if out is None:
+        dtype = table.dtype if dtype is None else dtype
+        if dtype not in _DTYPES:
+            raise TypeError(f"unsupported dtype {dtype}")
+        out = torch.empty(n, d, dtype=dtype, device=device)
+        shape = tuple(tokens.shape) + (d,)
+    elif dtype is not None and dtype != out.dtype:
+        raise TypeError(f"out has dtype {out.dtype}, expected {dtype}")
+    _check(out, "out", device, tuple(_DTYPES), 2)
+    _call(device, _lib.load().mfsdp_embedding, table.data_ptr(), _DTYPES[table.dtype], vocab, d,
+          tokens.data_ptr(), size, n, scale, out.data_ptr(), _rows(out, "out", (n, d)),
+          _DTYPES[out.dtype])
+    return out if shape is None else out.view(shape)
+
+
+def embedding_grad(dy: torch.Tensor, tokens: torch.Tensor, grad: torch.Tensor, *,
+                   scale: float = 1.0, beta: float = 0.0,
+                   workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Gradient of ``embedding``'s table, in place:
+    ``grad[v] = beta * grad[v] + scale * sum of dy over the tokens equal to v``
+    (mfsdp_embedding_grad).
+
+    dy: (number of tokens, d) bf16 or fp32, rows contiguous at any stride;
+    grad: (vocab, d) fp32 contiguous, for example the table's segment of the
+    packed gradient that ``adamw_tail`` takes.  The sums run over the tokens in
+    sorted order and depend on the inputs alone.  beta = 1 adds a micro-batch
+    and leaves the rows without a token untouched.  Returns grad."""
+    device = _gpu(dy, "dy")
+    _check(dy, "dy", device, tuple(_DTYPES), 2)
+    _check(grad, "grad", device, (torch.float32,), 2)
+    _contiguous(grad, "grad")
+    size = _check_tokens(tokens, device)
+    vocab, d = grad.shape
+    n = tokens.numel()
+    ld = _rows(dy, "dy", (n, d))
+    lib = _lib.load()
+    need = ctypes.c_size_t(0)
+    _lib.check(lib.mfsdp_embedding_grad_workspace_size(n, vocab, d, ctypes.byref(need)))
+    ws = _scratch(device, need.value, workspace)
+    _call(device, lib.mfsdp_embedding_grad, dy.data_ptr(), ld, _DTYPES[dy.dtype],
+          tokens.data_ptr(), size, n, vocab, d, scale, beta, grad.data_ptr(), ws.data_ptr(),
+          ws.numel() * ws.element_size())
+    return grad
