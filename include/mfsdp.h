@@ -362,6 +362,10 @@ mfsdp_status_t mfsdp_shampoo_stats(const mfsdp_stats_matrix_t* mats, int64_t n_m
  * weight gradient  dw_e  = beta*dw_e + sum_r dy[r]^T x[r], contiguous n_experts
  *                  x n x k in `dtype` or fp32 (dw_dtype).  beta == 0 does not
  *                  read dw; an expert without rows gets beta*dw_e.
+ *                  Few or small matrices with many rows are summed in parts:
+ *                  workspace (device, 256-byte aligned, scratch) then holds
+ *                  mfsdp_grouped_linear_wgrad_workspace_size bytes; that may
+ *                  be 0, and workspace NULL.
  * The checkpoint form takes x as codes and scales of mfsdp_ckpt_quantize
  * (contiguous, rows x k).  With dtype BF16 it multiplies them exactly; the
  * result is that of the weight gradient with the restored x.
@@ -369,7 +373,8 @@ mfsdp_status_t mfsdp_shampoo_stats(const mfsdp_stats_matrix_t* mats, int64_t n_m
  * Errors: MFSDP_ERR_INVALID_ARGUMENT (negative counts, widths < 1, strides
  * smaller than rows, null or misaligned pointers, non-finite beta),
  * MFSDP_ERR_UNSUPPORTED (dtypes; n, k or strides above 2^24, rows above 2^30,
- * n_experts above 2^20, more than 2^31 tiles), MFSDP_ERR_ALIAS, MFSDP_ERR_HIP.
+ * n_experts above 2^20, more than 2^31 tiles), MFSDP_ERR_WORKSPACE,
+ * MFSDP_ERR_ALIAS, MFSDP_ERR_HIP.
  */
 mfsdp_status_t mfsdp_grouped_linear(const void* x, int64_t ld_x, const void* weight,
                                     const int32_t* offsets, int64_t n_experts, int64_t rows,
@@ -381,10 +386,15 @@ mfsdp_status_t mfsdp_grouped_linear_dgrad(const void* dy, int64_t ld_dy, const v
                                           int64_t n, int64_t k, mfsdp_dtype_t dtype, void* dx,
                                           int64_t ld_dx, hipStream_t stream);
 
+mfsdp_status_t mfsdp_grouped_linear_wgrad_workspace_size(int64_t n_experts, int64_t rows,
+                                                         int64_t n, int64_t k,
+                                                         mfsdp_dtype_t dtype, size_t* out_bytes);
+
 mfsdp_status_t mfsdp_grouped_linear_wgrad(const void* dy, int64_t ld_dy, const void* x,
                                           int64_t ld_x, const int32_t* offsets, int64_t n_experts,
                                           int64_t rows, int64_t n, int64_t k, mfsdp_dtype_t dtype,
                                           void* dw, mfsdp_dtype_t dw_dtype, float beta,
+                                          void* workspace, size_t workspace_bytes,
                                           hipStream_t stream);
 
 mfsdp_status_t mfsdp_grouped_linear_wgrad_ckpt(const void* dy, int64_t ld_dy, const int8_t* codes,
@@ -392,6 +402,7 @@ mfsdp_status_t mfsdp_grouped_linear_wgrad_ckpt(const void* dy, int64_t ld_dy, co
                                                int64_t n_experts, int64_t rows, int64_t n,
                                                int64_t k, mfsdp_dtype_t dtype, void* dw,
                                                mfsdp_dtype_t dw_dtype, float beta,
+                                               void* workspace, size_t workspace_bytes,
                                                hipStream_t stream);
 
 /*

@@ -28,6 +28,7 @@ EXPORTED = ("mfsdp_muon_workspace_size", "mfsdp_muon_step", "mfsdp_muon_step_noa
             "mfsdp_plan_owners", "mfsdp_tail_layout", "mfsdp_tail_pack",
             "mfsdp_tail_unpack", "mfsdp_stats_workspace_size", "mfsdp_shampoo_stats",
             "mfsdp_grouped_linear", "mfsdp_grouped_linear_dgrad", "mfsdp_grouped_linear_wgrad",
+            "mfsdp_grouped_linear_wgrad_workspace_size",
             "mfsdp_grouped_linear_wgrad_ckpt", "mfsdp_ckpt_quantize", "mfsdp_ckpt_restore",
             "mfsdp_embedding", "mfsdp_embedding_grad_workspace_size", "mfsdp_embedding_grad",
             "mfsdp_status_string", "mfsdp_last_error",
@@ -123,11 +124,16 @@ def load() -> ctypes.CDLL:
         lib.mfsdp_grouped_linear_dgrad.argtypes = lib.mfsdp_grouped_linear.argtypes
         lib.mfsdp_grouped_linear_dgrad.restype = c.c_int
         lib.mfsdp_grouped_linear_wgrad.argtypes = [ptr, i64, ptr, i64, ptr, i64, i64, i64, i64,
-                                                   c.c_int, ptr, c.c_int, f32, ptr]
+                                                   c.c_int, ptr, c.c_int, f32, ptr, c.c_size_t,
+                                                   ptr]
         lib.mfsdp_grouped_linear_wgrad.restype = c.c_int
         lib.mfsdp_grouped_linear_wgrad_ckpt.argtypes = [ptr, i64, ptr, ptr, ptr, i64, i64, i64,
-                                                        i64, c.c_int, ptr, c.c_int, f32, ptr]
+                                                        i64, c.c_int, ptr, c.c_int, f32, ptr,
+                                                        c.c_size_t, ptr]
         lib.mfsdp_grouped_linear_wgrad_ckpt.restype = c.c_int
+        lib.mfsdp_grouped_linear_wgrad_workspace_size.argtypes = [i64, i64, i64, i64, c.c_int,
+                                                                  c.POINTER(c.c_size_t)]
+        lib.mfsdp_grouped_linear_wgrad_workspace_size.restype = c.c_int
         lib.mfsdp_ckpt_quantize.argtypes = [ptr, i64, i64, i64, c.c_int, ptr, ptr, ptr]
         lib.mfsdp_ckpt_quantize.restype = c.c_int
         lib.mfsdp_ckpt_restore.argtypes = [ptr, ptr, i64, i64, c.c_int, ptr, i64, ptr]

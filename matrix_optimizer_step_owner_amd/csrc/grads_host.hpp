@@ -45,37 +45,136 @@ int64_t group_tiles_max(int64_t rows, int64_t experts, int64_t bp) {
   return (rows + std::min(rows, experts) * (bp - 1)) / bp;
 }
 
+constexpr int64_t kGroupBlocksMax = (int64_t(1) << 31) - 1;
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// Workgroups of one launch with tiles of bp x bq.
+int64_t group_blocks(const GroupArgs& g, int mode, int bp, int bq) {
+  if (mode == kGroupWgrad) return WgradOrder(g.n, g.k, bp, bq).blocks(g.experts);
+  return group_tiles_max(g.rows, g.experts, bp) * ceil_div(mode == kGroupFwd ? g.n : g.k, bq);
+}
+
 template <class E, int MODE, bool CKPT>
-hipError_t launch_grouped(const GroupArgs& g, int64_t blocks, hipStream_t stream) {
+hipError_t launch_any(const GroupArgs& g, hipStream_t stream) {
+  const int64_t blocks = MODE == kGroupWgrad ? g.experts * ceil_div(g.n, 64) * ceil_div(g.k, 64)
+                                             : group_blocks(g, MODE, 64, 64);
   return launch(MFSDP_KERNEL_GROUPED, stream, [&] {
     grouped_any_kernel<E, MODE, CKPT>
         <<<dim3(static_cast<unsigned>(blocks)), dim3(256), 0, stream>>>(g);
   });
 }
 
-// rows x np = P's extent per row etc. are checked by the callers; this checks
-// what the three products share and launches.
-mfsdp_status_t grouped_impl(int mode, const void* p, int64_t ldp, const void* q, int64_t ldq,
-                            const uint8_t* qs, const int32_t* offsets, int64_t experts,
-                            int64_t rows, int64_t n, int64_t k, mfsdp_dtype_t dtype, void* out,
-                            int64_t ldo, mfsdp_dtype_t out_dtype, float beta,
-                            hipStream_t stream) {
-  g_last_error.clear();
+template <class E, int MODE, class C, bool CKPT = false>
+hipError_t launch_tile(const GroupArgs& g, hipStream_t stream) {
+  const dim3 grid(static_cast<unsigned>(group_blocks(g, MODE, C::BP, C::BQ)),
+                  MODE == kGroupWgrad ? g.splits : 1);
+  return launch(MFSDP_KERNEL_GROUPED, stream, [&] {
+    grouped_tile_kernel<E, MODE, C, CKPT><<<grid, dim3(C::THREADS), 0, stream>>>(g);
+  });
+}
+
+using TileWgrad = GroupTile<256, 256, 2, 4, 1, 4>;        // both panels read along t: whole lines
+using TileWgradSquare = GroupTile<128, 128, 2, 2, 1, 4>;  // two workgroups per CU
+using TileLarge = GroupTile<256, 256, 2, 4, 2, 2>;
+using TileWide = GroupTile<128, 256, 2, 4, 2, 3>;
+using TilePair = GroupTile<128, 256, 2, 2, 1, 3>;         // two workgroups per CU
+using TileSquare = GroupTile<128, 128, 2, 2, 2, 2>;       // two workgroups per CU
+using TileSmall = GroupTile<64, 256, 1, 4, 1, 4>;         // two workgroups per CU
+using TileF32 = GroupTile<128, 128, 2, 2, 1, 4>;
+
+// Weight gradients with too few 256 x 256 tiles for the 256 CUs take 128 x 128
+// ones, and where those are too few for two per CU each segment is cut into
+// parts of 256 rows or more that a second kernel sums.
+bool wgrad_large(int64_t experts, int64_t n, int64_t k) {
+  return experts * ceil_div(n, 256) * ceil_div(k, 256) >= 192;
+}
+
+int wgrad_splits(int64_t experts, int64_t rows, int64_t n, int64_t k, bool bf) {
+  if (experts == 0 || (bf && wgrad_large(experts, n, k))) return 1;
+  const int64_t tiles = experts * ceil_div(n, 128) * ceil_div(k, 128);
+  return static_cast<int>(
+      std::max<int64_t>(1, std::min<int64_t>({512 / tiles, rows / experts / 256, 16})));
+}
+
+template <int MODE>
+hipError_t launch_grouped(const GroupArgs& g, bool bf, bool dma, hipStream_t stream) {
+  if (!dma) {
+    if constexpr (MODE == kGroupWgrad)
+      if (g.qs)
+        return bf ? launch_any<ElemBF16, MODE, true>(g, stream)
+                  : launch_any<ElemF32, MODE, true>(g, stream);
+    return bf ? launch_any<ElemBF16, MODE, false>(g, stream)
+              : launch_any<ElemF32, MODE, false>(g, stream);
+  }
+  if constexpr (MODE == kGroupWgrad) {
+    hipError_t e;
+    const bool large = wgrad_large(g.experts, g.n, g.k);
+    if (!bf)
+      e = launch_tile<ElemF32, MODE, TileF32>(g, stream);
+    else if (g.qs)
+      e = large ? launch_tile<ElemBF16, MODE, TileWgrad, true>(g, stream)
+                : launch_tile<ElemBF16, MODE, TileWgradSquare, true>(g, stream);
+    else
+      e = large ? launch_tile<ElemBF16, MODE, TileWgrad>(g, stream)
+                : launch_tile<ElemBF16, MODE, TileWgradSquare>(g, stream);
+    if (e != hipSuccess || g.splits <= 1) return e;
+    const int64_t per = ceil_div(static_cast<int64_t>(g.n) * g.k, 2048);
+    const dim3 grid(static_cast<unsigned>(g.experts * per));
+    return launch(MFSDP_KERNEL_GROUPED, stream, [&] {
+      if (bf && !g.out_f32)
+        grouped_sum_kernel<ElemBF16><<<grid, dim3(256), 0, stream>>>(g, static_cast<int>(per));
+      else
+        grouped_sum_kernel<ElemF32><<<grid, dim3(256), 0, stream>>>(g, static_cast<int>(per));
+    });
+  } else {
+    if (!bf) return launch_tile<ElemF32, MODE, TileF32>(g, stream);
+    // rows per expert decide the tile's height, and the number of tiles
+    // whether there are enough of that size for the 256 CUs
+    const int64_t experts = std::min<int64_t>(g.experts, g.rows);
+    const int64_t per = g.rows / experts;
+    const int64_t width = MODE == kGroupFwd ? g.n : g.k, depth = MODE == kGroupFwd ? g.k : g.n;
+    auto tiles = [&](int64_t bp, int64_t bq) {
+      return (g.rows / bp + experts / 2 + 1) * ceil_div(width, bq);
+    };
+    if (per <= 48) return launch_tile<ElemBF16, MODE, TileSmall>(g, stream);
+    if (tiles(128, 256) < 256) return launch_tile<ElemBF16, MODE, TileSquare>(g, stream);
+    if (per >= 320 && tiles(256, 256) >= 256) return launch_tile<ElemBF16, MODE, TileLarge>(g, stream);
+    return depth >= 1024 ? launch_tile<ElemBF16, MODE, TileWide>(g, stream)
+                         : launch_tile<ElemBF16, MODE, TilePair>(g, stream);
+  }
+}
+
+mfsdp_status_t grouped_sizes(int64_t experts, int64_t rows, int64_t n, int64_t k,
+                             mfsdp_dtype_t dtype) {
   if (dtype != MFSDP_DTYPE_F32 && dtype != MFSDP_DTYPE_BF16)
     return fail(MFSDP_ERR_UNSUPPORTED, "unsupported dtype %d", (int)dtype);
-  if (out_dtype != dtype && out_dtype != MFSDP_DTYPE_F32)
-    return fail(MFSDP_ERR_UNSUPPORTED, "unsupported gradient dtype %d", (int)out_dtype);
   if (experts < 0 || rows < 0 || n < 1 || k < 1)
     return fail(MFSDP_ERR_INVALID_ARGUMENT,
                 "experts=%lld rows=%lld n=%lld k=%lld: counts must be >= 0, widths >= 1",
                 (long long)experts, (long long)rows, (long long)n, (long long)k);
+  if (experts > kGroupExpertsMax || rows > kGroupRowsMax || n > kGroupDimMax || k > kGroupDimMax)
+    return fail(MFSDP_ERR_UNSUPPORTED, "a size exceeds the kernels' indexing");
+  return MFSDP_OK;
+}
+
+// Checks what the three products share, chooses the kernel and launches.
+mfsdp_status_t grouped_impl(int mode, const void* p, int64_t ldp, const void* q, int64_t ldq,
+                            const uint8_t* qs, const int32_t* offsets, int64_t experts,
+                            int64_t rows, int64_t n, int64_t k, mfsdp_dtype_t dtype, void* out,
+                            int64_t ldo, mfsdp_dtype_t out_dtype, float beta, void* workspace,
+                            size_t workspace_bytes, hipStream_t stream) {
+  g_last_error.clear();
+  mfsdp_status_t st = grouped_sizes(experts, rows, n, k, dtype);
+  if (st != MFSDP_OK) return st;
+  if (out_dtype != dtype && out_dtype != MFSDP_DTYPE_F32)
+    return fail(MFSDP_ERR_UNSUPPORTED, "unsupported gradient dtype %d", (int)out_dtype);
   if (!finite(beta)) return fail(MFSDP_ERR_INVALID_ARGUMENT, "non-finite beta");
   const int64_t np = mode == kGroupFwd ? k : n;                           // width of P's rows
   const int64_t no = mode == kGroupFwd ? n : k;                           // width of the output's
   if (ldp < np || (mode == kGroupWgrad ? ldq < k : ldo < no))
     return fail(MFSDP_ERR_INVALID_ARGUMENT, "a row stride is smaller than the row");
-  if (experts > kGroupExpertsMax || rows > kGroupRowsMax || n > kGroupDimMax || k > kGroupDimMax ||
-      ldp > kGroupDimMax || ldq > kGroupDimMax || ldo > kGroupDimMax)
+  if (ldp > kGroupDimMax || ldq > kGroupDimMax || ldo > kGroupDimMax)
     return fail(MFSDP_ERR_UNSUPPORTED, "a size exceeds the kernels' indexing");
   if (experts == 0 || (rows == 0 && mode != kGroupWgrad)) return MFSDP_OK;
   if (!out || !offsets || (rows > 0 && (!p || !q)) || (mode != kGroupWgrad && !q))
@@ -83,9 +182,20 @@ mfsdp_status_t grouped_impl(int mode, const void* p, int64_t ldp, const void* q,
   const size_t es = elem_size(dtype), eo = elem_size(out_dtype);
   if (!aligned(p, es) || (!qs && !aligned(q, es)) || !aligned(out, eo) || !aligned(offsets, 4))
     return fail(MFSDP_ERR_INVALID_ARGUMENT, "a buffer is not aligned to its elements");
+  const bool bf = dtype == MFSDP_DTYPE_BF16;
+  const int splits = mode == kGroupWgrad ? wgrad_splits(experts, rows, n, k, bf) : 1;
+  const size_t need = splits > 1 ? static_cast<size_t>(splits) * experts * n * k * 4 : 0;
+  if (need) {
+    if (!workspace) return fail(MFSDP_ERR_WORKSPACE, "workspace is null");
+    if (!aligned(workspace, kWsAlign))
+      return fail(MFSDP_ERR_WORKSPACE, "workspace must be %zu-byte aligned", kWsAlign);
+    if (workspace_bytes < need)
+      return fail(MFSDP_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", workspace_bytes, need);
+  }
   {
     std::vector<Range> ins, outs;
     const size_t wb = static_cast<size_t>(experts) * n * k;
+    if (need) add_range(&outs, workspace, need, "workspace");
     add_range(&ins, offsets, static_cast<size_t>(experts + 1) * 4, "offsets");
     add_range(&ins, p, strided_bytes(rows, np, ldp, es), mode == kGroupFwd ? "x" : "dy");
     if (mode == kGroupWgrad) {
@@ -98,7 +208,7 @@ mfsdp_status_t grouped_impl(int mode, const void* p, int64_t ldp, const void* q,
       add_range(&ins, q, wb * es, "weight");
       add_range(&outs, out, strided_bytes(rows, no, ldo, es), mode == kGroupFwd ? "y" : "dx");
     }
-    const mfsdp_status_t st = check_outputs(outs, ins);
+    st = check_outputs(outs, ins);
     if (st != MFSDP_OK) return st;
   }
 
@@ -117,25 +227,24 @@ mfsdp_status_t grouped_impl(int mode, const void* p, int64_t ldp, const void* q,
   g.k = static_cast<int32_t>(k);
   g.beta = beta;
   g.out_f32 = out_dtype == MFSDP_DTYPE_F32 ? 1 : 0;
+  g.splits = splits;
+  g.part = static_cast<float*>(workspace);
 
-  auto div = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
-  const int64_t blocks = mode == kGroupWgrad ? experts * div(n, 64) * div(k, 64)
-                                             : group_tiles_max(rows, experts, 64) * div(no, 64);
-  if (blocks >= (int64_t(1) << 31)) return fail(MFSDP_ERR_UNSUPPORTED, "too many tiles");
-  hipError_t e;
-  const bool bf = dtype == MFSDP_DTYPE_BF16;
-  if (mode == kGroupFwd)
-    e = bf ? launch_grouped<ElemBF16, kGroupFwd, false>(g, blocks, stream)
-           : launch_grouped<ElemF32, kGroupFwd, false>(g, blocks, stream);
-  else if (mode == kGroupDgrad)
-    e = bf ? launch_grouped<ElemBF16, kGroupDgrad, false>(g, blocks, stream)
-           : launch_grouped<ElemF32, kGroupDgrad, false>(g, blocks, stream);
-  else if (!qs)
-    e = bf ? launch_grouped<ElemBF16, kGroupWgrad, false>(g, blocks, stream)
-           : launch_grouped<ElemF32, kGroupWgrad, false>(g, blocks, stream);
-  else
-    e = bf ? launch_grouped<ElemBF16, kGroupWgrad, true>(g, blocks, stream)
-           : launch_grouped<ElemF32, kGroupWgrad, true>(g, blocks, stream);
+  // 64 x 64 is the smallest tile: what it can count, all can
+  if (group_blocks(g, mode, 64, 64) > kGroupBlocksMax ||
+      experts * ceil_div(n, 64) * ceil_div(k, 64) > kGroupBlocksMax)
+    return fail(MFSDP_ERR_UNSUPPORTED, "too many tiles");
+  // 16-byte loads: every operand row starts on 16 bytes and has a whole number
+  // of 16-byte pieces, and 256 rows of it lie within 2^31 bytes
+  const int64_t v = 16 / static_cast<int64_t>(es);
+  const bool dma = (!qs || (bf && k % 16 == 0)) && aligned(p, 16) && aligned(q, 16) && k % v == 0 &&
+                   (n % v == 0 || mode == kGroupFwd) && ldp % v == 0 && ldq % v == 0 &&
+                   std::max({n, k, ldp, ldq}) * static_cast<int64_t>(es) < (int64_t(1) << 23);
+  const int64_t ldout = mode == kGroupWgrad ? k : ldo;
+  g.vec_out = aligned(out, 16) && ldout * static_cast<int64_t>(eo) % 16 == 0;
+  const hipError_t e = mode == kGroupFwd     ? launch_grouped<kGroupFwd>(g, bf, dma, stream)
+                       : mode == kGroupDgrad ? launch_grouped<kGroupDgrad>(g, bf, dma, stream)
+                                             : launch_grouped<kGroupWgrad>(g, bf, dma, stream);
   if (e != hipSuccess) return fail(MFSDP_ERR_HIP, "grouped launch: %s", hipGetErrorString(e));
   return MFSDP_OK;
 }
@@ -463,7 +572,7 @@ mfsdp_status_t mfsdp_grouped_linear(const void* x, int64_t ld_x, const void* wei
                                     int64_t ld_y, hipStream_t stream) {
   return guarded([&] {
     return grouped_impl(kGroupFwd, x, ld_x, weight, 0, nullptr, offsets, n_experts, rows, n, k,
-                        dtype, y, ld_y, dtype, 0.f, stream);
+                        dtype, y, ld_y, dtype, 0.f, nullptr, 0, stream);
   });
 }
 
@@ -473,7 +582,21 @@ mfsdp_status_t mfsdp_grouped_linear_dgrad(const void* dy, int64_t ld_dy, const v
                                           int64_t ld_dx, hipStream_t stream) {
   return guarded([&] {
     return grouped_impl(kGroupDgrad, dy, ld_dy, weight, 0, nullptr, offsets, n_experts, rows, n, k,
-                        dtype, dx, ld_dx, dtype, 0.f, stream);
+                        dtype, dx, ld_dx, dtype, 0.f, nullptr, 0, stream);
+  });
+}
+
+mfsdp_status_t mfsdp_grouped_linear_wgrad_workspace_size(int64_t n_experts, int64_t rows,
+                                                         int64_t n, int64_t k,
+                                                         mfsdp_dtype_t dtype, size_t* out_bytes) {
+  return guarded([&]() -> mfsdp_status_t {
+    g_last_error.clear();
+    if (!out_bytes) return fail(MFSDP_ERR_INVALID_ARGUMENT, "out_bytes is null");
+    const mfsdp_status_t st = grouped_sizes(n_experts, rows, n, k, dtype);
+    if (st != MFSDP_OK) return st;
+    const int splits = wgrad_splits(n_experts, rows, n, k, dtype == MFSDP_DTYPE_BF16);
+    *out_bytes = splits > 1 ? static_cast<size_t>(splits) * n_experts * n * k * 4 : 0;
+    return MFSDP_OK;
   });
 }
 
@@ -481,10 +604,11 @@ mfsdp_status_t mfsdp_grouped_linear_wgrad(const void* dy, int64_t ld_dy, const v
                                           int64_t ld_x, const int32_t* offsets, int64_t n_experts,
                                           int64_t rows, int64_t n, int64_t k, mfsdp_dtype_t dtype,
                                           void* dw, mfsdp_dtype_t dw_dtype, float beta,
+                                          void* workspace, size_t workspace_bytes,
                                           hipStream_t stream) {
   return guarded([&] {
     return grouped_impl(kGroupWgrad, dy, ld_dy, x, ld_x, nullptr, offsets, n_experts, rows, n, k,
-                        dtype, dw, 0, dw_dtype, beta, stream);
+                        dtype, dw, 0, dw_dtype, beta, workspace, workspace_bytes, stream);
   });
 }
 
@@ -493,6 +617,7 @@ mfsdp_status_t mfsdp_grouped_linear_wgrad_ckpt(const void* dy, int64_t ld_dy, co
                                                int64_t n_experts, int64_t rows, int64_t n,
                                                int64_t k, mfsdp_dtype_t dtype, void* dw,
                                                mfsdp_dtype_t dw_dtype, float beta,
+                                               void* workspace, size_t workspace_bytes,
                                                hipStream_t stream) {
   return guarded([&]() -> mfsdp_status_t {
     if (!scales && rows > 0 && n_experts > 0) {
@@ -500,7 +625,7 @@ mfsdp_status_t mfsdp_grouped_linear_wgrad_ckpt(const void* dy, int64_t ld_dy, co
       return fail(MFSDP_ERR_INVALID_ARGUMENT, "null pointer");
     }
     return grouped_impl(kGroupWgrad, dy, ld_dy, codes, k, scales, offsets, n_experts, rows, n, k,
-                        dtype, dw, 0, dw_dtype, beta, stream);
+                        dtype, dw, 0, dw_dtype, beta, workspace, workspace_bytes, stream);
   });
 }
 

@@ -30,6 +30,9 @@ struct GroupArgs {
   int32_t n, k;
   float beta;            // wgrad
   int32_t out_f32;       // wgrad: dW is fp32 whatever the operands' type
+  int32_t vec_out;       // output rows start on 16 bytes
+  int32_t splits;        // wgrad: parts of each segment (blockIdx.y), summed by a second kernel
+  float* part;           // wgrad with splits > 1: [splits][experts][n][k]
 };
 
 // Columns of an activation row that share one checkpoint scale.
@@ -232,6 +235,584 @@ __global__ __launch_bounds__(256) void grouped_any_kernel(GroupArgs g) {
       }
     } else {
       static_cast<S*>(g.out)[(lo + p) * g.ldo + q] = E::from_f32(acc[r]);
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// The MFMA kernel for rows that start on 16 bytes
+// ---------------------------------------------------------------------------
+// Tile BP x BQ of C by WP x WQ waves, each TP x TQ MFMA blocks of 32 x 32.  A
+// step is 64 * U bytes of t per row (32 U bf16, 16 U fp32), 2 U sub-steps of
+// one MFMA depth, kept in STAGES LDS buffers that are filled by DMA.
+template <int BP_, int BQ_, int WP_, int WQ_, int U_, int STAGES_>
+struct GroupTile {
+  static constexpr int BP = BP_, BQ = BQ_, WP = WP_, WQ = WQ_, U = U_, STAGES = STAGES_;
+  static constexpr int WAVES = WP * WQ, THREADS = 64 * WAVES;
+  static constexpr int TP = BP / WP / 32, TQ = BQ / WQ / 32;
+  static constexpr int SLOTS = TP * TQ;              // MFMA blocks per wave and sub-step
+  static constexpr int SUBS = 2 * U;
+  static constexpr int PP = BP * U / 16 / WAVES;     // 1 KB DMA pieces per wave and step, P panel
+  static constexpr int QP = BQ * U / 16 / WAVES;     // ... Q panel
+  static constexpr int STAGE_BYTES = (BP + BQ) * 64 * U;
+  static_assert(PP * 16 * WAVES == BP * U && QP * 16 * WAVES == BQ * U, "whole pieces");
+  static_assert(TP * 32 * WP == BP && TQ * 32 * WQ == BQ, "whole blocks");
+  static_assert(STAGES >= 2, "one buffer fills while another is read");
+  // A buffer's refill is issued over the SUBS * SLOTS MFMA slots that follow
+  // the barrier behind its last read: slots 0 .. SLOTS - 1 are the last
+  // sub-step of that step, the others the next step up to its barrier.
+  // slot_of(q) spreads the pieces, so that requests do not queue up in front of
+  // the MFMAs; with two buffers they have to arrive by that next barrier and
+  // go out in the first half.
+  static constexpr int WINDOW = STAGES == 2 ? SUBS * SLOTS / 2 : SUBS * SLOTS;
+  template <int N>
+  static constexpr int slot_of(int q) { return q * WINDOW / N; }
+  template <int N>
+  static constexpr int early() {                      // pieces of the last sub-step
+    int n = 0;
+    for (int q = 0; q < N; ++q) n += slot_of<N>(q) < SLOTS ? 1 : 0;
+    return n;
+  }
+};
+
+// One wave-wide global -> LDS copy of 64 x 16 bytes: lane l's bytes at
+// base + voff land at lds + 16 * l.  The buffer's range check turns the
+// offset kDmaNone into zeros, which is how rows and columns outside the
+// operand are filled.  Inline assembly for the reason given at lds_dma16; no
+// output register, and the kernel waits with vmcnt before the barrier that
+// publishes the data.
+typedef uint32_t u32x4s_t __attribute__((ext_vector_type(4)));
+constexpr uint32_t kDmaNone = 0x80000000u;
+
+__device__ __forceinline__ u32x4s_t dma_buffer(const char* base) {
+  const uint64_t b = reinterpret_cast<uintptr_t>(base);
+  u32x4s_t r;
+  r[0] = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(b));
+  r[1] = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(b >> 32)) & 0xffffu;   // stride 0
+  r[2] = 0x7fffffffu;    // bytes: every valid offset is below (checked on the host)
+  r[3] = 0x00020000u;    // untyped 32-bit data
+  return r;
+}
+
+__device__ __forceinline__ void lds_dma16_buf(uint32_t lds, uint32_t voff, u32x4s_t buf) {
+  const uint32_t ulds = static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(lds));
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+               :: "s"(ulds), "v"(voff), "s"(buf) : "memory", "m0");
+}
+
+// 16-byte chunk swizzle of a K-contiguous panel row of 64 * U bytes: the 16 rows
+// that a fragment read touches at one chunk cover all 16 chunks of the 256-byte
+// bank row.
+template <int U>
+__device__ __forceinline__ int rswz(int row) {
+  return U == 1 ? (row >> 2) & 3 : (row >> 1) & 7;
+}
+
+// 16-byte chunk swizzle of a panel read along t (row of B elements per t): the
+// four rows that one transposing read touches land in four 64-byte windows of
+// the 256-byte bank row.
+template <int B>
+__device__ __forceinline__ int tswz(int kk) {
+  return B >= 128 ? 4 * (kk & 3) : 4 * ((kk >> 1) & 1);
+}
+
+// Rows of one part of a split segment of R rows: whole 64-row groups.
+__device__ __forceinline__ int split_rows(int R, int splits) {
+  return ((R + splits - 1) / splits + 63) & ~63;
+}
+
+// Which (expert, row tile, column tile) workgroup b of a weight gradient takes.
+// Tiles of one expert go in chunks of up to 32 (a band of eight by four, which
+// share panels) to the XCDs in turn: experts differ in length, and an XCD
+// that held whole experts would finish long after another.  False if b is one
+// of the places that the last chunks leave empty.
+struct WgradOrder {
+  int tp, tq, per, chunks, size;   // tiles, chunks per expert, tiles per chunk
+  __host__ __device__ WgradOrder(int n, int k, int bp, int bq) {
+    tp = (n + bp - 1) / bp;
+    tq = (k + bq - 1) / bq;
+    per = tp * tq;
+    chunks = (per + 31) / 32;
+    size = (per + chunks - 1) / chunks;
+  }
+  __host__ __device__ int64_t blocks(int64_t experts) const {
+    return (experts * chunks + kXcds - 1) / kXcds * kXcds * size;
+  }
+};
+
+__device__ __forceinline__ bool wgrad_find(const GroupArgs& g, int b, int bp, int bq, int& expert,
+                                           int& ti, int& tj) {
+  const WgradOrder o(g.n, g.k, bp, bq);
+  const int x = b % kXcds, i = b / kXcds;
+  const int j = i / o.size;
+  const int chunk = j * kXcds + x;
+  expert = chunk / o.chunks;
+  const int local = (chunk - expert * o.chunks) * o.size + i - j * o.size;
+  if (expert >= g.experts || local >= o.per) return false;
+  const int band = local / (kGroupBand * o.tq), r = local - band * (kGroupBand * o.tq);
+  const int in_band = min(kGroupBand, o.tp - band * kGroupBand);
+  ti = band * kGroupBand + r % in_band;
+  tj = r / in_band;
+  return true;
+}
+
+// CKPT: Q is the int8 checkpoint of X.  Its codes arrive by DMA one step ahead
+// of P, 32 rows of BQ bytes per step, and while step t is multiplied every
+// thread turns 16 codes of step t + 1 into bf16 (exact: seven bits of
+// magnitude and a power of two) in one of two panels that the fragments are
+// then read from as from X itself: each code is converted once, where a
+// conversion of the fragments would do it for every wave row.  The scales of
+// kCkptSteps steps at a time wait in LDS as floats, two such groups in turn.
+constexpr int kCkptSteps = 16;
+
+template <class E, int MODE, class C, bool CKPT = false>
+__global__ __launch_bounds__(C::THREADS, 2) void grouped_tile_kernel(GroupArgs g) {
+  static_assert(!CKPT || (MODE == kGroupWgrad && E::kVec == 8 && C::U == 1), "checkpoint form");
+  using S = typename E::storage_t;
+  constexpr int V = E::kVec;
+  constexpr int BK = 4 * V * C::U;
+  constexpr int ROW = 64 * C::U;               // bytes of a K-contiguous panel row
+  constexpr bool kPT = MODE == kGroupWgrad;    // P, Q read along t
+  constexpr bool kQT = MODE != kGroupFwd;
+  constexpr int TP = C::TP, TQ = C::TQ;
+  // Stages: P panel, then Q panel; with CKPT P panel, then codes, and behind
+  // the stages two Q panels and two groups of scales.
+  constexpr int kQCodes = C::BQ * 32;                       // bytes of one step's codes
+  constexpr int kStage = CKPT ? C::BP * ROW + kQCodes : C::STAGE_BYTES;
+  constexpr int kStagesEnd = C::STAGES * kStage;
+  constexpr int kQPanel = C::BQ * ROW;
+  constexpr int kScaleCols = C::BQ / kCkptBlock;
+  constexpr int kScaleGroup = kCkptSteps * 32 * kScaleCols;  // floats
+  constexpr int kLds = CKPT ? kStagesEnd + 2 * kQPanel + 2 * kScaleGroup * 4 : kStagesEnd;
+  constexpr int QPW = CKPT ? kQCodes / 1024 / C::WAVES : C::QP;   // DMA pieces per wave
+  constexpr int PIECES = C::PP + QPW;
+  static_assert(!CKPT || (QPW * 1024 * C::WAVES == kQCodes && kQCodes == 16 * C::THREADS),
+                "16 codes per thread and step");
+  __shared__ __align__(16) char lds[kLds];
+
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wp = wave / C::WQ, wq = wave % C::WQ;
+  const int lrow = lane & 31, lhalf = lane >> 5;
+
+  // ---- tile and operands ----------------------------------------------------
+  int e, ti, tj, lo, hi;
+  if (MODE == kGroupWgrad) {
+    if (!wgrad_find(g, blockIdx.x, C::BP, C::BQ, e, ti, tj)) return;
+  } else {
+    const int nq = ((MODE == kGroupFwd ? g.n : g.k) + C::BQ - 1) / C::BQ;
+    if (!group_find(g, blockIdx.x, C::BP, nq, e, ti, tj)) return;
+  }
+  group_segment(g, e, lo, hi);
+  const size_t wsize = static_cast<size_t>(g.n) * g.k;
+  const bool split = MODE == kGroupWgrad && g.splits > 1;
+  if (split) {   // this workgroup's part of the segment; the sum skips empty parts
+    const int len = split_rows(hi - lo, g.splits);
+    const int64_t at = static_cast<int64_t>(lo) + static_cast<int64_t>(len) * blockIdx.y;
+    if (at >= hi) return;
+    lo = static_cast<int>(at);
+    hi = min(lo + len, hi);
+  }
+  const int p0 = ti * C::BP, q0 = tj * C::BQ;
+  const S* P = static_cast<const S*>(g.p) + lo * g.ldp;
+  const S* Q = static_cast<const S*>(g.q);
+  int64_t ldq;
+  int np, nq, R;
+  if (MODE == kGroupWgrad) {
+    if (!CKPT) Q += lo * g.ldq;
+    ldq = g.ldq;
+    np = g.n; nq = g.k; R = hi - lo;
+  } else {
+    Q += e * wsize;
+    ldq = g.k;
+    np = hi - lo;
+    nq = MODE == kGroupFwd ? g.n : g.k;
+    R = MODE == kGroupFwd ? g.k : g.n;
+  }
+  P += kPT ? p0 : p0 * g.ldp;
+  Q += kQT ? q0 : q0 * ldq;
+  const int prem = np - p0, qrem = nq - q0;    // rows / columns of the tile that exist
+
+  // ---- DMA: this wave's pieces of a step -------------------------------------
+  // K-contiguous panel: 16 / U rows x 64 U bytes per piece, chunk c of row r at
+  // r * 64 U + (c ^ rswz(r)) * 16.  Panel read along t: BK rows of B elements,
+  // chunk c of row kk at kk * B * size + (c ^ tswz(kk)) * 16.  voff is the
+  // lane's byte offset from the step's base, klim the first t (from the step's
+  // own) that the chunk holds: at or past the end of t it loads zeros, as do
+  // chunks outside the tile's rows and columns.
+  uint32_t voff[PIECES];
+  int klim[PIECES];
+  auto setup = [&](int q, int piece, bool along, int64_t ld, int rem, int width) {
+    if (!along) {
+      const int row = piece * (16 / C::U) + lane / (4 * C::U), c = (lane & (4 * C::U - 1)) ^ rswz<C::U>(row);
+      voff[q] = static_cast<uint32_t>((row * ld + c * V) * static_cast<int64_t>(sizeof(S)));
+      klim[q] = row < rem ? c * V : 0x7fffffff;
+    } else {
+      const int pitch = width * static_cast<int>(sizeof(S));
+      const int at = piece * 1024 + lane * 16;
+      const int kk = at / pitch, pc = at % pitch / 16;
+      const int c = V == 8 ? pc ^ (width >= 128 ? 4 * (kk & 3) : 4 * ((kk >> 1) & 1)) : pc;
+      voff[q] = static_cast<uint32_t>((kk * ld + c * V) * static_cast<int64_t>(sizeof(S)));
+      klim[q] = c * V < rem ? kk : 0x7fffffff;
+    }
+  };
+#pragma unroll
+  for (int q = 0; q < C::PP; ++q) setup(q, wave * C::PP + q, kPT, g.ldp, prem, C::BP);
+#pragma unroll
+  for (int q = 0; q < QPW; ++q) {
+    if constexpr (CKPT) {   // codes: rows of BQ bytes, 16 columns per lane
+      const int at = (wave * QPW + q) * 1024 + lane * 16;
+      const int kk = at / C::BQ, col = at % C::BQ;
+      voff[C::PP + q] = static_cast<uint32_t>(kk * ldq + col);
+      klim[C::PP + q] = col < qrem ? kk : 0x7fffffff;
+    } else {
+      setup(C::PP + q, wave * QPW + q, kQT, ldq, qrem, C::BQ);
+    }
+  }
+  const char* pbase = reinterpret_cast<const char*>(P);
+  const char* qbase = CKPT ? static_cast<const char*>(g.q) + lo * g.ldq + q0
+                           : reinterpret_cast<const char*>(Q);
+  const int64_t pstep = (kPT ? g.ldp : 1) * static_cast<int64_t>(BK * sizeof(S));
+  const int64_t qstep = (kQT ? ldq : 1) * static_cast<int64_t>(BK * (CKPT ? 1 : sizeof(S)));
+  const uint32_t lds0 = lds_addr(lds);
+  // Next step to fetch: pbase / qbase point at it, `left` values of t remain
+  // from it on.  With CKPT qbase and qleft are one step further on.
+  int left = R, qleft = R;
+  auto dma_piece = [&](uint32_t stage, int q) {
+    const bool is_p = q < C::PP;
+    uint32_t at = lds0 + stage;
+    if (CKPT && !is_p) at = lds0 + (stage + kStage == kStagesEnd ? 0 : stage + kStage);
+    at += is_p ? (wave * C::PP + q) * 1024 : C::BP * ROW + (wave * QPW + q - C::PP) * 1024;
+    lds_dma16_buf(at, klim[q] < (is_p ? left : qleft) ? voff[q] : kDmaNone,
+                  dma_buffer(is_p ? pbase : qbase));
+  };
+  auto dma_next = [&] {
+    pbase += pstep;
+    qbase += qstep;
+    left -= BK;
+    qleft -= BK;
+  };
+
+  // ---- fragments ---------------------------------------------------------------
+  // Lane l holds, for sub-step s, the 16-byte slice 2s + l/32 of t of row l%32
+  // of each 32-row block.
+  constexpr int kPR = kPT && V == 8 ? 2 : 1, kQR = kQT && V == 8 ? 2 : 1;   // reads per fragment
+  constexpr int kReads = TP * kPR + TQ * kQR;
+  auto frag = [&](const char* panel, auto along_c, auto width_c, int s, int base, int half, uint4& f) {
+    constexpr bool along = decltype(along_c)::value;
+    constexpr int width = decltype(width_c)::value;
+    if constexpr (!along) {
+      const int row = base + lrow, c = 2 * s + lhalf;
+      f = *reinterpret_cast<const uint4*>(panel + row * ROW + ((c ^ rswz<C::U>(row)) << 4));
+    } else if constexpr (V == 8) {
+      // transposing read: in each group of 16 lanes, lane i points at row
+      // kk + i/4, columns n + 4 (i%4) .. + 4, and receives column i at rows
+      // kk .. kk + 3
+      const int il = lane & 15;
+      const int n = base + 16 * ((lane >> 4) & 1) + 4 * (il & 3);
+      const int kk = 16 * s + 8 * lhalf + 4 * half + (il >> 2);
+      const int byte = kk * (width * 2) + (((n >> 3) ^ tswz<width>(kk)) << 4) + ((n & 7) << 1);
+      const v4i16_t t = __builtin_amdgcn_ds_read_tr16_b64_v4i16((MFSDP_LDS v4i16_t*)(panel + byte));
+      const uint2 w = __builtin_bit_cast(uint2, t);
+      if (half == 0) {
+        f.x = w.x;
+        f.y = w.y;
+      } else {
+        f.z = w.x;
+        f.w = w.y;
+      }
+    } else {
+      const float* pf = reinterpret_cast<const float*>(panel);
+      const int kk = 4 * (2 * s + lhalf), n = base + lrow;
+      f = make_uint4(__float_as_uint(pf[(kk + 0) * width + n]), __float_as_uint(pf[(kk + 1) * width + n]),
+                     __float_as_uint(pf[(kk + 2) * width + n]), __float_as_uint(pf[(kk + 3) * width + n]));
+    }
+  };
+  uint4 fp[2][TP], fq[2][TQ];
+  using PT_c = std::integral_constant<bool, kPT>;
+  using QT_c = std::integral_constant<bool, kQT>;
+  using PW_c = std::integral_constant<int, C::BP>;
+  using QW_c = std::integral_constant<int, C::BQ>;
+  auto read_piece = [&](uint32_t stage, uint32_t qpanel, int s, int r, uint4 (&a)[TP], uint4 (&b)[TQ]) {
+    const char* base = lds + stage;
+    if (r < TP * kPR) {
+      frag(base, PT_c{}, PW_c{}, s, (wp * TP + r / kPR) * 32, r % kPR, a[r / kPR]);
+    } else {
+      const int j = r - TP * kPR;
+      frag(CKPT ? lds + kStagesEnd + qpanel : base + C::BP * ROW, QT_c{}, QW_c{}, s, (wq * TQ + j / kQR) * 32, j % kQR, b[j / kQR]);
+    }
+  };
+
+  f32x16_t acc[TP][TQ];
+#pragma unroll
+  for (int i = 0; i < TP; ++i)
+#pragma unroll
+    for (int j = 0; j < TQ; ++j) acc[i][j] = f32x16_t{};
+
+  // ---- main loop ------------------------------------------------------------------
+  // Step t computes on stage t % STAGES.  Each sub-step reads the fragments of
+  // the next one; before the last, whose fragments have then been read, the
+  // waves wait until step t + 1 has landed (only later steps' pieces may be in
+  // flight) and until their own reads are done (lgkmcnt), and meet a barrier:
+  // behind it the last sub-step reads step t + 1's first fragments, and the
+  // stage of step t is free for the DMA of step t + STAGES.  Steps past the end
+  // load zeros and are never multiplied.
+  const int nk = (R + BK - 1) / BK;
+
+  // CKPT: this thread's 16 codes of a step are row crow, columns ccol..; the
+  // scales of group j (steps kCkptSteps * j on) go to half j & 1.
+  const int crow = tid * 16 / C::BQ, ccol = tid * 16 % C::BQ;
+  float* const scale_lds = reinterpret_cast<float*>(lds + kStagesEnd + 2 * kQPanel);
+  constexpr int kScaleLd = CKPT ? kScaleGroup / C::THREADS : 1;
+  float sc[kScaleLd];
+  auto scales_load = [&](int j) {
+    const int nb = (g.k + kCkptBlock - 1) / kCkptBlock;
+#pragma unroll
+    for (int i = 0; i < kScaleLd; ++i) {
+      const int u = tid + i * C::THREADS;
+      const int row = j * (kCkptSteps * 32) + u / kScaleCols, blk = q0 / kCkptBlock + u % kScaleCols;
+      sc[i] = row < R && blk < nb
+                  ? ckpt_scale(gld<uint8_t>(g.qs + static_cast<size_t>(lo + row) * nb + blk)) : 0.f;
+    }
+  };
+  auto scales_store = [&](int j) {
+#pragma unroll
+    for (int i = 0; i < kScaleLd; ++i) scale_lds[(j & 1) * kScaleGroup + tid + i * C::THREADS] = sc[i];
+  };
+  auto convert = [&](uint32_t stage, int t) {   // codes of step t, kept in `stage`
+    const uint4 c = *reinterpret_cast<const uint4*>(lds + stage + C::BP * ROW + tid * 16);
+    const float s = scale_lds[((t / kCkptSteps) & 1) * kScaleGroup +
+                              (t % kCkptSteps * 32 + crow) * kScaleCols + ccol / kCkptBlock];
+    const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+    char* panel = lds + kStagesEnd + (t & 1) * kQPanel + crow * (C::BQ * 2);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float v[8];
+#pragma unroll
+      for (int b = 0; b < 8; ++b)
+        v[b] = static_cast<float>(static_cast<int8_t>(w[2 * h + (b >> 2)] >> (8 * (b & 3)))) * s;
+      *reinterpret_cast<uint4*>(panel + (((ccol / 8 + h) ^ tswz<C::BQ>(crow)) << 4)) =
+          make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                     pack_bf16x2(v[6], v[7]));
+    }
+  };
+
+  if (nk > 0) {
+    if constexpr (CKPT) {   // codes of step 0, then one step ahead of P
+      scales_load(0);
+      scales_store(0);
+#pragma unroll
+      for (int q = C::PP; q < PIECES; ++q) dma_piece(kStagesEnd - kStage, q);
+      qbase += qstep;
+      qleft -= BK;
+    }
+#pragma unroll
+    for (int s = 0; s < C::STAGES - 1; ++s) {
+#pragma unroll
+      for (int q = 0; q < PIECES; ++q) dma_piece(s * kStage, q);
+      dma_next();
+    }
+    uint32_t cur = 0, fill = kStagesEnd - kStage;
+    constexpr int kEarly = C::template early<PIECES>();
+    static_assert(!CKPT || kEarly <= C::PP, "the codes behind step 0's may only follow their conversion");
+#pragma unroll
+    for (int q = 0; q < kEarly; ++q) dma_piece(fill, q);
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier"
+                 :: "n"((C::STAGES - 2) * PIECES + kEarly) : "memory");
+    if constexpr (CKPT) {
+      convert(0, 0);
+      asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    }
+    uint32_t qcur = 0;
+#pragma unroll
+    for (int r = 0; r < kReads; ++r) read_piece(0, 0, 0, r, fp[0], fq[0]);
+#pragma unroll 1
+    for (int t = 0; t < nk; ++t) {
+      const uint32_t nxt = cur + kStage == kStagesEnd ? 0 : cur + kStage;
+      if constexpr (CKPT) {
+        // the next group's scales: loaded at the start of a group, stored half
+        // way, read from the last conversion of the group on
+        if (t % kCkptSteps == 0) scales_load(t / kCkptSteps + 1);
+        if (t % kCkptSteps == kCkptSteps / 2) scales_store(t / kCkptSteps + 1);
+      }
+#pragma unroll
+      for (int sub = 0; sub < C::SUBS; ++sub) {
+        constexpr int kLast = C::SUBS - 1;
+#pragma unroll
+        for (int x = 0; x < C::SLOTS; ++x) {
+          Mma<E>::run(acc[x / TQ][x % TQ], fq[sub & 1][x % TQ], fp[sub & 1][x / TQ]);
+#pragma unroll
+          for (int r = x; r < kReads; r += C::SLOTS) {
+            if (sub < kLast) read_piece(cur, qcur, sub + 1, r, fp[(sub + 1) & 1], fq[(sub + 1) & 1]);
+            else read_piece(nxt, qcur ^ kQPanel, 0, r, fp[0], fq[0]);
+          }
+#pragma unroll
+          for (int q = 0; q < PIECES; ++q)
+            if (C::template slot_of<PIECES>(q) == (sub == kLast ? x : (sub + 1) * C::SLOTS + x))
+              dma_piece(sub == kLast ? cur : fill, q);
+          if constexpr (CKPT) {
+            if (sub == 0 && x == C::SLOTS / 4) convert(nxt, t + 1);
+          }
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        if (sub == kLast - 1) {
+          dma_next();
+          asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier"
+                       :: "n"((C::STAGES - 2) * PIECES) : "memory");
+        }
+      }
+      fill = cur;
+      cur = nxt;
+      qcur ^= kQPanel;
+    }
+  }
+  // every DMA has landed and every fragment is read before the stages are reused
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+
+  // ---- epilogue -------------------------------------------------------------------
+  // Each wave turns its blocks through its own part of LDS, 32 rows at a time
+  // (no barrier), so that a store writes whole row pieces: lane l holds row
+  // l % 32 and four consecutive columns per four registers.
+  constexpr int COLS = TQ * 32;
+  const float beta = split ? 0.f : g.beta;
+  const bool out_f32 = V == 4 || (MODE == kGroupWgrad && (split || g.out_f32));
+  const bool f32 = out_f32 || (MODE == kGroupWgrad && beta != 0.f);
+  const int prow0 = wp * TP * 32, qcol0 = wq * COLS;
+  char* out;
+  int64_t ldo;
+  if (MODE == kGroupWgrad) {
+    ldo = g.k;
+    out = split ? reinterpret_cast<char*>(g.part + blockIdx.y * (g.experts * wsize)) : static_cast<char*>(g.out);
+    out += (e * wsize + p0 * ldo + q0) * (out_f32 ? 4 : 2);
+  } else {
+    ldo = g.ldo;
+    out = static_cast<char*>(g.out) + ((lo + p0) * ldo + q0) * static_cast<int64_t>(sizeof(S));
+  }
+  const bool vec = split ? g.k % 4 == 0 : g.vec_out != 0;   // parts start on 256 bytes
+  constexpr int GROUPS = COLS / 8;          // 8-column groups per row
+  constexpr int RPP = 64 / GROUPS;          // rows per pass of a wave
+  if (!f32) {
+    constexpr int PITCH = COLS * 2 + 16;
+    char* mine = lds + wave * (32 * PITCH);
+    static_assert(C::WAVES * 32 * PITCH <= kLds, "staging fits");
+#pragma unroll
+    for (int i = 0; i < TP; ++i) {
+#pragma unroll
+      for (int j = 0; j < TQ; ++j)
+#pragma unroll
+        for (int r = 0; r < 16; r += 4)
+          *reinterpret_cast<uint2*>(mine + lrow * PITCH + (j * 32 + acc_q(r, lhalf)) * 2) =
+              make_uint2(pack_bf16x2(acc[i][j][r], acc[i][j][r + 1]), pack_bf16x2(acc[i][j][r + 2], acc[i][j][r + 3]));
+#pragma unroll
+      for (int r0 = 0; r0 < 32; r0 += RPP) {
+        const int row = r0 + lane / GROUPS, col = lane % GROUPS * 8;
+        const uint4 v = *reinterpret_cast<const uint4*>(mine + row * PITCH + col * 2);
+        const int p = prow0 + i * 32 + row, q = qcol0 + col;
+        if (p < prem && q < qrem) {
+          uint16_t* o = reinterpret_cast<uint16_t*>(out) + p * ldo + q;
+          if (vec && q + 8 <= qrem) {
+            gst<uint4>(o, v);
+          } else {
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              if (q + k < qrem) o[k] = static_cast<uint16_t>(w[k >> 1] >> (16 * (k & 1)));
+          }
+        }
+      }
+    }
+  } else {
+    constexpr int PITCH = COLS * 4 + 16;
+    char* mine = lds + wave * (32 * PITCH);
+    static_assert(C::WAVES * 32 * PITCH <= kLds, "staging fits");
+#pragma unroll
+    for (int i = 0; i < TP; ++i) {
+#pragma unroll
+      for (int j = 0; j < TQ; ++j)
+#pragma unroll
+        for (int r = 0; r < 16; r += 4)
+          *reinterpret_cast<float4*>(mine + lrow * PITCH + (j * 32 + acc_q(r, lhalf)) * 4) =
+              make_float4(acc[i][j][r], acc[i][j][r + 1], acc[i][j][r + 2], acc[i][j][r + 3]);
+#pragma unroll
+      for (int r0 = 0; r0 < 32; r0 += RPP) {
+        const int row = r0 + lane / GROUPS, col = lane % GROUPS * 8;
+        const float4 a = *reinterpret_cast<const float4*>(mine + row * PITCH + col * 4);
+        const float4 b = *reinterpret_cast<const float4*>(mine + row * PITCH + col * 4 + 16);
+        float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+        const int p = prow0 + i * 32 + row, q = qcol0 + col;
+        if (p >= prem || q >= qrem) continue;
+        const bool whole = vec && q + 8 <= qrem;
+        if (out_f32) {
+          float* o = reinterpret_cast<float*>(out) + p * ldo + q;
+          if (whole) {
+            if (MODE == kGroupWgrad && beta != 0.f) {
+              float old[8];
+              load8<ElemF32>(o, old);
+#pragma unroll
+              for (int k = 0; k < 8; ++k) v[k] = fmaf(beta, old[k], v[k]);
+            }
+            store8<ElemF32>(o, v);
+          } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              if (q + k < qrem) o[k] = MODE == kGroupWgrad && beta != 0.f ? fmaf(beta, o[k], v[k]) : v[k];
+          }
+        } else {
+          uint16_t* o = reinterpret_cast<uint16_t*>(out) + p * ldo + q;
+          if (whole) {
+            float old[8];
+            load8<ElemBF16>(o, old);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[k] = fmaf(beta, old[k], v[k]);
+            store8<ElemBF16>(o, v);
+          } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              if (q + k < qrem) o[k] = f32_to_bf16_rne(fmaf(beta, bf16_to_f32(o[k]), v[k]));
+          }
+        }
+      }
+    }
+  }
+}
+
+// Sum of the parts of a split weight gradient, in their order:
+// dW = beta dW + sum_s part[s].  One workgroup takes 2048 elements of one
+// expert; a part past the end of the segment was not written and is not read.
+template <class EO>
+__global__ __launch_bounds__(256) void grouped_sum_kernel(GroupArgs g, int per_expert) {
+  using O = typename EO::storage_t;
+  const int e = blockIdx.x / per_expert;
+  const size_t wsize = static_cast<size_t>(g.n) * g.k;
+  int lo, hi;
+  group_segment(g, e, lo, hi);
+  const int len = split_rows(hi - lo, g.splits);
+  const int parts = len > 0 ? (hi - lo + len - 1) / len : 0;
+  const size_t i = static_cast<size_t>(blockIdx.x % per_expert) * 2048 + threadIdx.x * 8;
+  if (i >= wsize) return;
+  const size_t at = e * wsize + i, stride = g.experts * wsize;
+  O* out = static_cast<O*>(g.out) + at;
+  const float* part = g.part + at;
+  float v[8] = {};
+  if (g.vec_out && wsize % 8 == 0) {
+    for (int s = 0; s < parts; ++s) {
+      float p[8];
+      load8<ElemF32>(part + s * stride, p);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] += p[k];
+    }
+    if (g.beta != 0.f) {
+      float old[8];
+      load8<EO>(out, old);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] = fmaf(g.beta, old[k], v[k]);
+    }
+    store8<EO>(out, v);
+  } else {
+    for (int k = 0; k < 8 && i + k < wsize; ++k) {
+      float x = 0.f;
+      for (int s = 0; s < parts; ++s) x += part[s * stride + k];
+      out[k] = EO::from_f32(g.beta != 0.f ? fmaf(g.beta, EO::to_f32(out[k]), x) : x);
     }
   }
 }

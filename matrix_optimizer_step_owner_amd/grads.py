@@ -142,8 +142,21 @@ def grouped_linear_dgrad(dy: torch.Tensor, weight: torch.Tensor, offsets: torch.
     return out
 
 
+def _wgrad_scratch(dy: torch.Tensor, grad: torch.Tensor, given: Optional[torch.Tensor]):
+    """(address, bytes) of the workspace of a weight gradient, (None, 0) if it needs none."""
+    lib = _lib.load()
+    need = ctypes.c_size_t(0)
+    _lib.check(lib.mfsdp_grouped_linear_wgrad_workspace_size(
+        grad.size(0), dy.size(0), grad.size(1), grad.size(2), _DTYPES[dy.dtype], ctypes.byref(need)))
+    if need.value == 0 and given is None:
+        return None, 0
+    ws = _scratch(dy.device, need.value, given)
+    return ws.data_ptr(), ws.numel() * ws.element_size()
+
+
 def grouped_linear_wgrad(dy: torch.Tensor, x: torch.Tensor, offsets: torch.Tensor,
-                         grad: torch.Tensor, beta: float = 0.0) -> torch.Tensor:
+                         grad: torch.Tensor, beta: float = 0.0,
+                         workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Gradients of the experts' matrices, in place:
     ``grad[e] = beta * grad[e] + dy[rows of e].T @ x[rows of e]``
     (mfsdp_grouped_linear_wgrad).
@@ -160,7 +173,7 @@ def grouped_linear_wgrad(dy: torch.Tensor, x: torch.Tensor, offsets: torch.Tenso
     _call(device, _lib.load().mfsdp_grouped_linear_wgrad, dy.data_ptr(),
           _rows(dy, "dy", (dy.size(0), n)), x.data_ptr(), _rows(x, "x", (dy.size(0), k)),
           offsets.data_ptr(), experts, dy.size(0), n, k, _DTYPES[dy.dtype], grad.data_ptr(),
-          _DTYPES[grad.dtype], beta)
+          _DTYPES[grad.dtype], beta, *_wgrad_scratch(dy, grad, workspace))
     return grad
 
 
@@ -172,8 +185,8 @@ def _check_ckpt(codes: torch.Tensor, scales: torch.Tensor, device, rows: int, k:
 
 
 def grouped_linear_wgrad_ckpt(dy: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor,
-                              offsets: torch.Tensor, grad: torch.Tensor,
-                              beta: float = 0.0) -> torch.Tensor:
+                              offsets: torch.Tensor, grad: torch.Tensor, beta: float = 0.0,
+                              workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
     """``grouped_linear_wgrad`` with x as its 8-bit checkpoint, (codes, scales)
     of ``ckpt_quantize`` (mfsdp_grouped_linear_wgrad_ckpt): the gradient for the
     restored x, which is never written out."""
@@ -185,7 +198,7 @@ def grouped_linear_wgrad_ckpt(dy: torch.Tensor, codes: torch.Tensor, scales: tor
     _call(device, _lib.load().mfsdp_grouped_linear_wgrad_ckpt, dy.data_ptr(),
           _rows(dy, "dy", (dy.size(0), n)), codes.data_ptr(), scales.data_ptr(),
           offsets.data_ptr(), experts, dy.size(0), n, k, _DTYPES[dy.dtype], grad.data_ptr(),
-          _DTYPES[grad.dtype], beta)
+          _DTYPES[grad.dtype], beta, *_wgrad_scratch(dy, grad, workspace))
     return grad
 
 

@@ -53,6 +53,9 @@ ROUTES = {
     "tiny": ([1, 2, 0, 1, 1, 3, 1, 0, 1], 0, 0),
     "mixed": ([33, 127, 0, 128, 129, 255, 256, 257, 31, 32], 0, 5),
     "skewed": ([1500, 3, 0, 40], 1, 0),
+    "parts": ([1300, 0, 900, 37], 0, 3),           # weight gradients summed in parts
+    "long one": ([5003], 2, 0),
+    "five": ([300, 0, 70, 513, 40], 0, 0),
     "many": ([(7 * i * i) % 23 for i in range(200)], 0, 0),
 }
 # n, k, columns before and after each activation row (strides)
@@ -65,11 +68,13 @@ WIDTHS = {
     "one": (1, 1, 0),
     "short": (8, 40, 0),
     "long": (40, 1032, 8),
+    "big": (1496, 2000, 8),                        # several tiles each way
 }
 GROUPED = [("one row", "whole"), ("one expert", "whole"), ("empty ones", "ragged"), ("none", "whole"), ("tiny", "whole"),
            ("tiny", "odd"), ("mixed", "whole"), ("mixed", "ragged"), ("mixed", "odd"), ("mixed", "odd stride"), ("skewed", "ragged"),
            ("skewed", "long"), ("many", "narrow"), ("many", "odd"), ("empty ones", "one"), ("mixed", "short"), ("one row", "long"),
-           ("tiny", "long")]
+           ("tiny", "long"), ("parts", "whole"), ("parts", "narrow"), ("parts", "odd"), ("long one", "narrow"), ("long one", "ragged"),
+           ("five", "big"), ("many", "ragged")]
 
 
 def setup(route, width, dtype, seed=0):

@@ -26,12 +26,12 @@ def fwd(x=X, ldx=64, w=W, off=OFF, e=4, rows=100, n=32, k=64, dt=BF, y=Y, ldy=32
     return getattr(_lib.load(), name)(x, ldx, w, off, e, rows, n, k, dt, y, ldy, None)
 
 
-def wgrad(dy=X, lddy=32, x=W, ldx=64, off=OFF, e=4, rows=100, n=32, k=64, dt=BF, dw=Y, dwt=BF, beta=0.0):
-    return _lib.load().mfsdp_grouped_linear_wgrad(dy, lddy, x, ldx, off, e, rows, n, k, dt, dw, dwt, beta, None)
+def wgrad(dy=X, lddy=32, x=W, ldx=64, off=OFF, e=4, rows=100, n=32, k=64, dt=BF, dw=Y, dwt=BF, beta=0.0, ws=None, wsb=0):
+    return _lib.load().mfsdp_grouped_linear_wgrad(dy, lddy, x, ldx, off, e, rows, n, k, dt, dw, dwt, beta, ws, wsb, None)
 
 
 def wgrad_ckpt(codes=W, scales=WS, rows=100, e=4, dt=BF, dwt=BF, beta=0.0, dw=Y):
-    return _lib.load().mfsdp_grouped_linear_wgrad_ckpt(X, 32, codes, scales, OFF, e, rows, 32, 64, dt, dw, dwt, beta, None)
+    return _lib.load().mfsdp_grouped_linear_wgrad_ckpt(X, 32, codes, scales, OFF, e, rows, 32, 64, dt, dw, dwt, beta, None, 0, None)
 
 
 @pytest.mark.parametrize("over,want", [
@@ -101,6 +101,23 @@ def test_embedding_refusals(over, want):
     a = {**dict(table=X, tdt=BF, vocab=50, d=8, tokens=W, tb=8, nt=20, scale=1.0, out=Y, ldo=8, odt=BF), **over}
     assert _lib.load().mfsdp_embedding(a["table"], a["tdt"], a["vocab"], a["d"], a["tokens"], a["tb"], a["nt"], a["scale"],
                                        a["out"], a["ldo"], a["odt"], None) == want
+
+
+def wgrad_ws(e, rows, n, k, dt=BF):
+    out = ctypes.c_size_t(7)
+    return _lib.load().mfsdp_grouped_linear_wgrad_workspace_size(e, rows, n, k, dt, ctypes.byref(out)), out.value
+
+
+def test_wgrad_workspace():
+    assert wgrad_ws(0, 0, 1, 1) == (OK, 0) and wgrad_ws(256, 32768, 512, 1536) == (OK, 0) and wgrad_ws(4, 100, 32, 64) == (OK, 0)
+    assert wgrad_ws(-1, 0, 1, 1)[0] == INVALID and wgrad_ws(1, 1, 0, 1)[0] == INVALID and wgrad_ws(1, 1, 1, 1, 5)[0] == UNSUPPORTED
+    assert _lib.load().mfsdp_grouped_linear_wgrad_workspace_size(1, 1, 1, 1, BF, None) == INVALID
+    # two small matrices with many rows are summed in parts
+    st, need = wgrad_ws(2, 10000, 32, 64)
+    assert st == OK and need > 0 and need % (2 * 32 * 64 * 4) == 0
+    args = dict(e=2, rows=10000, dw=A + 8 * GB)
+    assert wgrad(**args) == WORKSPACE and wgrad(**args, ws=WS + 16, wsb=need) == WORKSPACE and wgrad(**args, ws=WS, wsb=need - 1) == WORKSPACE
+    assert wgrad(**args, ws=X, wsb=need) == ALIAS and wgrad(**args, ws=args["dw"], wsb=need) == ALIAS
 
 
 def emb_ws(nt, vocab, d):
