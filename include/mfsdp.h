@@ -372,7 +372,7 @@ mfsdp_status_t mfsdp_shampoo_stats(const mfsdp_stats_matrix_t* mats, int64_t n_m
  * n_experts == 0, and rows == 0 for the first two, return MFSDP_OK, no work.
  * Errors: MFSDP_ERR_INVALID_ARGUMENT (negative counts, widths < 1, strides
  * smaller than rows, null or misaligned pointers, non-finite beta),
- * MFSDP_ERR_UNSUPPORTED (dtypes; n, k or strides above 2^24, rows above 2^30,
+ * MFSDP_ERR_UNSUPPORTED (dtypes; n, k or strides above 2^22, rows above 2^30,
  * n_experts above 2^20, more than 2^31 tiles), MFSDP_ERR_WORKSPACE,
  * MFSDP_ERR_ALIAS, MFSDP_ERR_HIP.
  */
@@ -450,7 +450,7 @@ mfsdp_status_t mfsdp_ckpt_restore(const int8_t* codes, const uint8_t* scales, in
  * workspace  device, >= mfsdp_embedding_grad_workspace_size bytes, 256-byte
  *            aligned, scratch; none is needed for n_tokens == 0.
  * Errors: as above, MFSDP_ERR_WORKSPACE, and MFSDP_ERR_UNSUPPORTED for vocab
- * above 2^31 - 1, n_tokens above 2^28, d or strides above 2^24.
+ * above 2^31 - 1, n_tokens above 2^28, d or strides above 2^22.
  */
 mfsdp_status_t mfsdp_embedding(const void* table, mfsdp_dtype_t table_dtype, int64_t vocab,
                                int64_t d, const void* tokens, int token_bytes, int64_t n_tokens,

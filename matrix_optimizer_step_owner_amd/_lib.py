@@ -68,6 +68,8 @@ _lock = threading.Lock()
 def load() -> ctypes.CDLL:
     """Load libmfsdp.so; raise if it has not been built (no fallback)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib

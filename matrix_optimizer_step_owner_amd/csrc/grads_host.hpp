@@ -35,7 +35,8 @@ mfsdp_status_t check_outputs(const std::vector<Range>& outs, const std::vector<R
 // ---------------------------------------------------------------------------
 // Products grouped by expert
 // ---------------------------------------------------------------------------
-constexpr int64_t kGroupDimMax = int64_t(1) << 24;      // n, k
+// n, k and strides: 128 rows of fp32 lie within the kernels' 32-bit byte offsets
+constexpr int64_t kGroupDimMax = int64_t(1) << 22;
 constexpr int64_t kGroupRowsMax = int64_t(1) << 30;
 constexpr int64_t kGroupExpertsMax = int64_t(1) << 20;
 
@@ -55,22 +56,12 @@ int64_t group_blocks(const GroupArgs& g, int mode, int bp, int bq) {
   return group_tiles_max(g.rows, g.experts, bp) * ceil_div(mode == kGroupFwd ? g.n : g.k, bq);
 }
 
-template <class E, int MODE, bool CKPT>
-hipError_t launch_any(const GroupArgs& g, hipStream_t stream) {
-  const int64_t blocks = MODE == kGroupWgrad ? g.experts * ceil_div(g.n, 64) * ceil_div(g.k, 64)
-                                             : group_blocks(g, MODE, 64, 64);
-  return launch(MFSDP_KERNEL_GROUPED, stream, [&] {
-    grouped_any_kernel<E, MODE, CKPT>
-        <<<dim3(static_cast<unsigned>(blocks)), dim3(256), 0, stream>>>(g);
-  });
-}
-
-template <class E, int MODE, class C, bool CKPT = false>
+template <class E, int MODE, class C, int LOAD>
 hipError_t launch_tile(const GroupArgs& g, hipStream_t stream) {
   const dim3 grid(static_cast<unsigned>(group_blocks(g, MODE, C::BP, C::BQ)),
                   MODE == kGroupWgrad ? g.splits : 1);
   return launch(MFSDP_KERNEL_GROUPED, stream, [&] {
-    grouped_tile_kernel<E, MODE, C, CKPT><<<grid, dim3(C::THREADS), 0, stream>>>(g);
+    grouped_tile_kernel<E, MODE, C, LOAD><<<grid, dim3(C::THREADS), 0, stream>>>(g);
   });
 }
 
@@ -81,6 +72,8 @@ using TileWide = GroupTile<128, 256, 2, 4, 2, 3>;
 using TilePair = GroupTile<128, 256, 2, 2, 1, 3>;         // two workgroups per CU
 using TileSquare = GroupTile<128, 128, 2, 2, 2, 2>;       // two workgroups per CU
 using TileSmall = GroupTile<64, 256, 1, 4, 1, 4>;         // two workgroups per CU
+using TileRows = GroupTile<32, 64, 1, 2, 4, 3, 4>;        // two workgroups per CU
+using TileRowsReg = GroupTile<32, 64, 1, 2, 4, 2, 4>;
 using TileF32 = GroupTile<128, 128, 2, 2, 1, 4>;
 
 // Weight gradients with too few 256 x 256 tiles for the 256 CUs take 128 x 128
@@ -97,52 +90,68 @@ int wgrad_splits(int64_t experts, int64_t rows, int64_t n, int64_t k, bool bf) {
       std::max<int64_t>(1, std::min<int64_t>({512 / tiles, rows / experts / 256, 16})));
 }
 
-template <int MODE>
-hipError_t launch_grouped(const GroupArgs& g, bool bf, bool dma, hipStream_t stream) {
-  if (!dma) {
-    if constexpr (MODE == kGroupWgrad)
-      if (g.qs)
-        return bf ? launch_any<ElemBF16, MODE, true>(g, stream)
-                  : launch_any<ElemF32, MODE, true>(g, stream);
-    return bf ? launch_any<ElemBF16, MODE, false>(g, stream)
-              : launch_any<ElemF32, MODE, false>(g, stream);
-  }
-  if constexpr (MODE == kGroupWgrad) {
-    hipError_t e;
-    const bool large = wgrad_large(g.experts, g.n, g.k);
-    if (!bf)
-      e = launch_tile<ElemF32, MODE, TileF32>(g, stream);
-    else if (g.qs)
-      e = large ? launch_tile<ElemBF16, MODE, TileWgrad, true>(g, stream)
-                : launch_tile<ElemBF16, MODE, TileWgradSquare, true>(g, stream);
+template <class E, int LOAD>
+hipError_t launch_wgrad(const GroupArgs& g, hipStream_t stream) {
+  hipError_t e;
+  if constexpr (LOAD == kLoadReg || LOAD == kLoadRegCkpt)
+    e = launch_tile<E, kGroupWgrad, TileSquare, LOAD>(g, stream);
+  else if constexpr (E::kVec == 4)
+    e = launch_tile<E, kGroupWgrad, TileF32, LOAD>(g, stream);
+  else
+    e = wgrad_large(g.experts, g.n, g.k)
+            ? launch_tile<E, kGroupWgrad, TileWgrad, LOAD>(g, stream)
+            : launch_tile<E, kGroupWgrad, TileWgradSquare, LOAD>(g, stream);
+  if (e != hipSuccess || g.splits <= 1) return e;
+  const int64_t per = ceil_div(static_cast<int64_t>(g.n) * g.k, 2048);
+  const dim3 grid(static_cast<unsigned>(g.experts * per));
+  return launch(MFSDP_KERNEL_GROUPED, stream, [&] {
+    if (E::kVec == 8 && !g.out_f32)
+      grouped_sum_kernel<ElemBF16><<<grid, dim3(256), 0, stream>>>(g, static_cast<int>(per));
     else
-      e = large ? launch_tile<ElemBF16, MODE, TileWgrad>(g, stream)
-                : launch_tile<ElemBF16, MODE, TileWgradSquare>(g, stream);
-    if (e != hipSuccess || g.splits <= 1) return e;
-    const int64_t per = ceil_div(static_cast<int64_t>(g.n) * g.k, 2048);
-    const dim3 grid(static_cast<unsigned>(g.experts * per));
-    return launch(MFSDP_KERNEL_GROUPED, stream, [&] {
-      if (bf && !g.out_f32)
-        grouped_sum_kernel<ElemBF16><<<grid, dim3(256), 0, stream>>>(g, static_cast<int>(per));
-      else
-        grouped_sum_kernel<ElemF32><<<grid, dim3(256), 0, stream>>>(g, static_cast<int>(per));
-    });
+      grouped_sum_kernel<ElemF32><<<grid, dim3(256), 0, stream>>>(g, static_cast<int>(per));
+  });
+}
+
+template <class E, int MODE>
+hipError_t launch_rows(const GroupArgs& g, bool dma, hipStream_t stream) {
+  // rows per expert decide the tile's height, and the number of tiles whether
+  // there are enough of that size for the 256 CUs
+  const int64_t experts = std::min<int64_t>(g.experts, g.rows);
+  const int64_t per = g.rows / experts;
+  const int64_t width = MODE == kGroupFwd ? g.n : g.k, depth = MODE == kGroupFwd ? g.k : g.n;
+  auto tiles = [&](int64_t bp, int64_t bq) {   // an expert with few rows has one row tile
+    const int64_t high = per < bp / 2 ? experts : g.rows / bp + experts / 2 + 1;
+    return high * ceil_div(width, bq);
+  };
+  if (!dma)
+    return per <= 48 || tiles(128, 128) < 128
+               ? launch_tile<E, MODE, TileRowsReg, kLoadReg>(g, stream)
+               : launch_tile<E, MODE, TileSquare, kLoadReg>(g, stream);
+  if constexpr (E::kVec == 4) {
+    return per <= 96 || tiles(128, 128) < 192
+               ? launch_tile<E, MODE, TileRows, kLoadDma>(g, stream)
+               : launch_tile<E, MODE, TileF32, kLoadDma>(g, stream);
   } else {
-    if (!bf) return launch_tile<ElemF32, MODE, TileF32>(g, stream);
-    // rows per expert decide the tile's height, and the number of tiles
-    // whether there are enough of that size for the 256 CUs
-    const int64_t experts = std::min<int64_t>(g.experts, g.rows);
-    const int64_t per = g.rows / experts;
-    const int64_t width = MODE == kGroupFwd ? g.n : g.k, depth = MODE == kGroupFwd ? g.k : g.n;
-    auto tiles = [&](int64_t bp, int64_t bq) {
-      return (g.rows / bp + experts / 2 + 1) * ceil_div(width, bq);
-    };
-    if (per <= 48) return launch_tile<ElemBF16, MODE, TileSmall>(g, stream);
-    if (tiles(128, 256) < 256) return launch_tile<ElemBF16, MODE, TileSquare>(g, stream);
-    if (per >= 320 && tiles(256, 256) >= 256) return launch_tile<ElemBF16, MODE, TileLarge>(g, stream);
-    return depth >= 1024 ? launch_tile<ElemBF16, MODE, TileWide>(g, stream)
-                         : launch_tile<ElemBF16, MODE, TilePair>(g, stream);
+    if ((MODE == kGroupFwd && per <= 40) || tiles(64, 256) < 128)
+      return launch_tile<E, MODE, TileRows, kLoadDma>(g, stream);
+    if (per <= 24 || tiles(128, 256) < 100)
+      return launch_tile<E, MODE, TileSmall, kLoadDma>(g, stream);
+    if (per >= 320 && tiles(256, 256) >= 256)
+      return launch_tile<E, MODE, TileLarge, kLoadDma>(g, stream);
+    return depth < 1024 && tiles(128, 256) >= 512
+               ? launch_tile<E, MODE, TilePair, kLoadDma>(g, stream)
+               : launch_tile<E, MODE, TileWide, kLoadDma>(g, stream);
   }
+}
+
+template <class E>
+hipError_t launch_grouped(int mode, const GroupArgs& g, bool dma, hipStream_t stream) {
+  if (mode == kGroupFwd) return launch_rows<E, kGroupFwd>(g, dma, stream);
+  if (mode == kGroupDgrad) return launch_rows<E, kGroupDgrad>(g, dma, stream);
+  if (!g.qs) return dma ? launch_wgrad<E, kLoadDma>(g, stream) : launch_wgrad<E, kLoadReg>(g, stream);
+  if constexpr (E::kVec == 8)
+    if (dma) return launch_wgrad<E, kLoadDmaCkpt>(g, stream);
+  return launch_wgrad<E, kLoadRegCkpt>(g, stream);
 }
 
 mfsdp_status_t grouped_sizes(int64_t experts, int64_t rows, int64_t n, int64_t k,
@@ -230,21 +239,18 @@ mfsdp_status_t grouped_impl(int mode, const void* p, int64_t ldp, const void* q,
   g.splits = splits;
   g.part = static_cast<float*>(workspace);
 
-  // 64 x 64 is the smallest tile: what it can count, all can
-  if (group_blocks(g, mode, 64, 64) > kGroupBlocksMax ||
-      experts * ceil_div(n, 64) * ceil_div(k, 64) > kGroupBlocksMax)
-    return fail(MFSDP_ERR_UNSUPPORTED, "too many tiles");
+  // the smallest tiles
+  const int64_t blocks = mode == kGroupWgrad ? group_blocks(g, mode, 128, 128)
+                                             : group_blocks(g, mode, 32, 64);
+  if (blocks > kGroupBlocksMax) return fail(MFSDP_ERR_UNSUPPORTED, "too many tiles");
   // 16-byte loads: every operand row starts on 16 bytes and has a whole number
   // of 16-byte pieces, and 256 rows of it lie within 2^31 bytes
   const int64_t v = 16 / static_cast<int64_t>(es);
   const bool dma = (!qs || (bf && k % 16 == 0)) && aligned(p, 16) && aligned(q, 16) && k % v == 0 &&
                    (n % v == 0 || mode == kGroupFwd) && ldp % v == 0 && ldq % v == 0 &&
                    std::max({n, k, ldp, ldq}) * static_cast<int64_t>(es) < (int64_t(1) << 23);
-  const int64_t ldout = mode == kGroupWgrad ? k : ldo;
-  g.vec_out = aligned(out, 16) && ldout * static_cast<int64_t>(eo) % 16 == 0;
-  const hipError_t e = mode == kGroupFwd     ? launch_grouped<kGroupFwd>(g, bf, dma, stream)
-                       : mode == kGroupDgrad ? launch_grouped<kGroupDgrad>(g, bf, dma, stream)
-                                             : launch_grouped<kGroupWgrad>(g, bf, dma, stream);
+  const hipError_t e = bf ? launch_grouped<ElemBF16>(mode, g, dma, stream)
+                          : launch_grouped<ElemF32>(mode, g, dma, stream);
   if (e != hipSuccess) return fail(MFSDP_ERR_HIP, "grouped launch: %s", hipGetErrorString(e));
   return MFSDP_OK;
 }

@@ -30,7 +30,6 @@ struct GroupArgs {
   int32_t n, k;
   float beta;            // wgrad
   int32_t out_f32;       // wgrad: dW is fp32 whatever the operands' type
-  int32_t vec_out;       // output rows start on 16 bytes
   int32_t splits;        // wgrad: parts of each segment (blockIdx.y), summed by a second kernel
   float* part;           // wgrad with splits > 1: [splits][experts][n][k]
 };
@@ -115,148 +114,22 @@ __device__ __forceinline__ bool group_find(const GroupArgs& g, int b, int bp, in
 // r % 4, four consecutive q per four registers.
 __device__ __forceinline__ int acc_q(int r, int lhalf) { return (r >> 2) * 8 + lhalf * 4 + (r & 3); }
 
-// The kernel for every alignment, stride and width: 64 x 64 tiles, four waves
-// of one 32 x 32 MFMA block each, operands loaded element by element (lanes
-// along whichever axis is contiguous) and stored to LDS with t contiguous.
-// It takes the shapes that the 16-byte DMA kernel cannot (rows that do not
-// start on 16 bytes, widths off a multiple of 16 bytes).
-template <class E, int MODE, bool CKPT>
-__global__ __launch_bounds__(256) void grouped_any_kernel(GroupArgs g) {
-  using S = typename E::storage_t;
-  constexpr int V = E::kVec;
-  constexpr int BK = 4 * V;          // 32 bf16 or 16 fp32 per step: 64 bytes
-  constexpr int PITCH = BK + V;      // 80 bytes: 16-byte aligned, spreads the banks
-  constexpr int B = 64;
-  constexpr int N_LD = B * BK / 256;
-  __shared__ __align__(16) S sp[B * PITCH];
-  __shared__ __align__(16) S sq[B * PITCH];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int lrow = lane & 31, lhalf = lane >> 5;
-
-  int e, ti, tj, lo, hi;
-  if (MODE == kGroupWgrad) {
-    const int tq = (g.k + B - 1) / B, tp = (g.n + B - 1) / B;
-    const int t = xcd_remap(blockIdx.x, gridDim.x);
-    e = t / (tp * tq);
-    ti = t / tq % tp;
-    tj = t % tq;
-  } else {
-    const int nq = ((MODE == kGroupFwd ? g.n : g.k) + B - 1) / B;
-    if (!group_find(g, blockIdx.x, B, nq, e, ti, tj)) return;
-  }
-  group_segment(g, e, lo, hi);
-  const size_t wsize = static_cast<size_t>(g.n) * g.k;
-  // strides of P and Q along p / q (s?) and along t (t?)
-  const S* P = static_cast<const S*>(g.p);
-  const S* Q = static_cast<const S*>(g.q);
-  const int8_t* Qc = static_cast<const int8_t*>(g.q);
-  int64_t ps, pt, qs, qt;
-  int np, nq, R;
-  if (MODE == kGroupWgrad) {
-    P += lo * g.ldp;
-    Q += lo * g.ldq;
-    Qc += lo * g.ldq;
-    ps = 1; pt = g.ldp; qs = 1; qt = g.ldq;
-    np = g.n; nq = g.k; R = hi - lo;
-  } else {
-    P += lo * g.ldp;
-    Q += e * wsize;
-    ps = g.ldp; pt = 1;
-    np = hi - lo;
-    if (MODE == kGroupFwd) {
-      qs = g.k; qt = 1; nq = g.n; R = g.k;
-    } else {
-      qs = 1; qt = g.k; nq = g.k; R = g.n;
-    }
-  }
-  const int p0 = ti * B, q0 = tj * B;
-  f32x16_t acc = f32x16_t{};
-  const int wp = (wave >> 1) * 32, wq = (wave & 1) * 32;
-  S rp[N_LD], rq[N_LD];
-  constexpr bool kPT = MODE == kGroupWgrad, kQT = MODE != kGroupFwd;
-  auto coord = [&](int j, bool along_t, int& i, int& t) {
-    const int u = tid + 256 * j;
-    if (along_t) { t = u % BK; i = u / BK; } else { i = u % B; t = u / B; }
-  };
-  auto load = [&](int t0) {
-#pragma unroll
-    for (int j = 0; j < N_LD; ++j) {
-      int i, t;
-      coord(j, !kPT, i, t);
-      rp[j] = p0 + i < np && t0 + t < R ? P[(p0 + i) * ps + (t0 + t) * pt] : S(0);
-      coord(j, !kQT, i, t);
-      const bool in = q0 + i < nq && t0 + t < R;
-      if constexpr (CKPT) {
-        const int col = q0 + i;
-        const int nb = (g.k + kCkptBlock - 1) / kCkptBlock;
-        rq[j] = in ? E::from_f32(Qc[col + (t0 + t) * qt] *
-                                 ckpt_scale(g.qs[static_cast<size_t>(lo + t0 + t) * nb + col / kCkptBlock]))
-                   : S(0);
-      } else {
-        rq[j] = in ? Q[(q0 + i) * qs + (t0 + t) * qt] : S(0);
-      }
-    }
-  };
-  if (R > 0) load(0);
-  for (int t0 = 0; t0 < R; t0 += BK) {
-    __syncthreads();
-#pragma unroll
-    for (int j = 0; j < N_LD; ++j) {
-      int i, t;
-      coord(j, !kPT, i, t);
-      sp[i * PITCH + t] = rp[j];
-      coord(j, !kQT, i, t);
-      sq[i * PITCH + t] = rq[j];
-    }
-    __syncthreads();
-    if (t0 + BK < R) load(t0 + BK);
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      const int c = (2 * s + lhalf) * V;
-      const uint4 fp = *reinterpret_cast<const uint4*>(sp + (wp + lrow) * PITCH + c);
-      const uint4 fq = *reinterpret_cast<const uint4*>(sq + (wq + lrow) * PITCH + c);
-      Mma<E>::run(acc, fq, fp);
-    }
-  }
-  const int p = p0 + wp + lrow;
-  if (p >= np) return;
-#pragma unroll
-  for (int r = 0; r < 16; ++r) {
-    const int q = q0 + wq + acc_q(r, lhalf);
-    if (q >= nq) continue;
-    if (MODE == kGroupWgrad) {
-      const size_t at = e * wsize + static_cast<size_t>(p) * g.k + q;
-      if (g.out_f32) {
-        float* o = static_cast<float*>(g.out) + at;
-        *o = g.beta == 0.f ? acc[r] : fmaf(g.beta, *o, acc[r]);
-      } else {
-        S* o = static_cast<S*>(g.out) + at;
-        *o = E::from_f32(g.beta == 0.f ? acc[r] : fmaf(g.beta, E::to_f32(*o), acc[r]));
-      }
-    } else {
-      static_cast<S*>(g.out)[(lo + p) * g.ldo + q] = E::from_f32(acc[r]);
-    }
-  }
-}
-
-// ---------------------------------------------------------------------------
-// The MFMA kernel for rows that start on 16 bytes
-// ---------------------------------------------------------------------------
 // Tile BP x BQ of C by WP x WQ waves, each TP x TQ MFMA blocks of 32 x 32.  A
 // step is 64 * U bytes of t per row (32 U bf16, 16 U fp32), 2 U sub-steps of
-// one MFMA depth, kept in STAGES LDS buffers that are filled by DMA.
-template <int BP_, int BQ_, int WP_, int WQ_, int U_, int STAGES_>
+// one MFMA depth, kept in STAGES LDS buffers.  KS > 1: KS such sets of waves
+// share a step's sub-steps, and their sums are added at the end.
+template <int BP_, int BQ_, int WP_, int WQ_, int U_, int STAGES_, int KS_ = 1>
 struct GroupTile {
-  static constexpr int BP = BP_, BQ = BQ_, WP = WP_, WQ = WQ_, U = U_, STAGES = STAGES_;
-  static constexpr int WAVES = WP * WQ, THREADS = 64 * WAVES;
+  static constexpr int BP = BP_, BQ = BQ_, WP = WP_, WQ = WQ_, U = U_, STAGES = STAGES_, KS = KS_;
+  static constexpr int WAVES = WP * WQ * KS, THREADS = 64 * WAVES;
   static constexpr int TP = BP / WP / 32, TQ = BQ / WQ / 32;
   static constexpr int SLOTS = TP * TQ;              // MFMA blocks per wave and sub-step
   static constexpr int SUBS = 2 * U;
-  static constexpr int PP = BP * U / 16 / WAVES;     // 1 KB DMA pieces per wave and step, P panel
+  static constexpr int PP = BP * U / 16 / WAVES;     // 1 KB pieces per wave and step, P panel
   static constexpr int QP = BQ * U / 16 / WAVES;     // ... Q panel
   static constexpr int STAGE_BYTES = (BP + BQ) * 64 * U;
   static_assert(PP * 16 * WAVES == BP * U && QP * 16 * WAVES == BQ * U, "whole pieces");
-  static_assert(TP * 32 * WP == BP && TQ * 32 * WQ == BQ, "whole blocks");
+  static_assert(TP * 32 * WP == BP && TQ * 32 * WQ == BQ && SUBS % KS == 0, "whole blocks");
   static_assert(STAGES >= 2, "one buffer fills while another is read");
   // A buffer's refill is issued over the SUBS * SLOTS MFMA slots that follow
   // the barrier behind its last read: slots 0 .. SLOTS - 1 are the last
@@ -274,6 +147,49 @@ struct GroupTile {
     return n;
   }
 };
+
+// How a tile's operands reach LDS.
+enum GroupLoad {
+  kLoadDma = 0,      // 16-byte DMA: rows start on 16 bytes, widths are whole 16-byte pieces
+  kLoadDmaCkpt = 1,  // the same, Q as int8 codes (k a multiple of 16, bf16)
+  kLoadReg = 2,      // through registers, any alignment and width
+  kLoadRegCkpt = 3   // the same, Q as int8 codes
+};
+
+// 16 bytes of bf16 or fp32 elements, 8 and 4 bytes of codes, at any element.
+typedef u32x4_t u32x4_el_t __attribute__((aligned(2)));
+typedef unsigned int u32x2_t __attribute__((ext_vector_type(2)));
+typedef u32x2_t u32x2_b_t __attribute__((aligned(1)));
+typedef uint32_t u32_b_t __attribute__((aligned(1)));
+
+__device__ __forceinline__ uint4 load16_any(const void* p) {
+  const u32x4_t v = *(const MFSDP_GLOBAL u32x4_el_t*)(p);
+  return make_uint4(v.x, v.y, v.z, v.w);
+}
+
+__device__ __forceinline__ void store16_any(void* p, const uint4& v) {
+  *(MFSDP_GLOBAL u32x4_el_t*)(p) = u32x4_t{v.x, v.y, v.z, v.w};
+}
+
+// load8 / store8 at any element.
+template <class E>
+__device__ __forceinline__ void load8_any(const typename E::storage_t* p, float (&v)[8]) {
+  Raw8 r;
+  r.a = load16_any(p);
+  r.b = E::kVec == 4 ? load16_any(p + 4) : make_uint4(0, 0, 0, 0);
+  unpack_raw8<E>(r, v);
+}
+
+template <class E>
+__device__ __forceinline__ void store8_any(typename E::storage_t* p, const float (&v)[8]) {
+  if constexpr (E::kVec == 8) {
+    store16_any(p, Vec16<E>::pack(v));
+  } else {
+    const float a[4] = {v[0], v[1], v[2], v[3]}, b[4] = {v[4], v[5], v[6], v[7]};
+    store16_any(p, Vec16<E>::pack(a));
+    store16_any(p + 4, Vec16<E>::pack(b));
+  }
+}
 
 // One wave-wide global -> LDS copy of 64 x 16 bytes: lane l's bytes at
 // base + voff land at lds + 16 * l.  The buffer's range check turns the
@@ -305,7 +221,7 @@ __device__ __forceinline__ void lds_dma16_buf(uint32_t lds, uint32_t voff, u32x4
 // bank row.
 template <int U>
 __device__ __forceinline__ int rswz(int row) {
-  return U == 1 ? (row >> 2) & 3 : (row >> 1) & 7;
+  return U == 1 ? (row >> 2) & 3 : U == 2 ? (row >> 1) & 7 : row & 15;
 }
 
 // 16-byte chunk swizzle of a panel read along t (row of B elements per t): the
@@ -365,9 +281,13 @@ __device__ __forceinline__ bool wgrad_find(const GroupArgs& g, int b, int bp, in
 // kCkptSteps steps at a time wait in LDS as floats, two such groups in turn.
 constexpr int kCkptSteps = 16;
 
-template <class E, int MODE, class C, bool CKPT = false>
+template <class E, int MODE, class C, int LOAD>
 __global__ __launch_bounds__(C::THREADS, 2) void grouped_tile_kernel(GroupArgs g) {
-  static_assert(!CKPT || (MODE == kGroupWgrad && E::kVec == 8 && C::U == 1), "checkpoint form");
+  constexpr bool CKPT = LOAD == kLoadDmaCkpt;
+  constexpr bool kReg = LOAD == kLoadReg || LOAD == kLoadRegCkpt;
+  constexpr bool kCodes = LOAD == kLoadDmaCkpt || LOAD == kLoadRegCkpt;
+  static_assert(!kCodes || MODE == kGroupWgrad, "checkpoint form");
+  static_assert(!CKPT || (E::kVec == 8 && C::U == 1 && C::KS == 1), "checkpoint form");
   using S = typename E::storage_t;
   constexpr int V = E::kVec;
   constexpr int BK = 4 * V * C::U;
@@ -392,7 +312,9 @@ __global__ __launch_bounds__(C::THREADS, 2) void grouped_tile_kernel(GroupArgs g
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wp = wave / C::WQ, wq = wave % C::WQ;
+  constexpr int kTileWaves = C::WP * C::WQ;
+  const int tw = wave % kTileWaves, ks = wave / kTileWaves;   // wave of the tile, set of waves
+  const int wp = tw / C::WQ, wq = tw % C::WQ;
   const int lrow = lane & 31, lhalf = lane >> 5;
 
   // ---- tile and operands ----------------------------------------------------
@@ -419,7 +341,7 @@ __global__ __launch_bounds__(C::THREADS, 2) void grouped_tile_kernel(GroupArgs g
   int64_t ldq;
   int np, nq, R;
   if (MODE == kGroupWgrad) {
-    if (!CKPT) Q += lo * g.ldq;
+    if (!kCodes) Q += lo * g.ldq;
     ldq = g.ldq;
     np = g.n; nq = g.k; R = hi - lo;
   } else {
@@ -440,13 +362,16 @@ __global__ __launch_bounds__(C::THREADS, 2) void grouped_tile_kernel(GroupArgs g
   // lane's byte offset from the step's base, klim the first t (from the step's
   // own) that the chunk holds: at or past the end of t it loads zeros, as do
   // chunks outside the tile's rows and columns.
+  // kLoadReg: the columns of a chunk that exist are counted too (cnt), and a
+  // chunk that reaches past the row loads them one by one.
   uint32_t voff[PIECES];
-  int klim[PIECES];
+  int klim[PIECES], cnt[PIECES];
   auto setup = [&](int q, int piece, bool along, int64_t ld, int rem, int width) {
     if (!along) {
       const int row = piece * (16 / C::U) + lane / (4 * C::U), c = (lane & (4 * C::U - 1)) ^ rswz<C::U>(row);
       voff[q] = static_cast<uint32_t>((row * ld + c * V) * static_cast<int64_t>(sizeof(S)));
       klim[q] = row < rem ? c * V : 0x7fffffff;
+      cnt[q] = V;
     } else {
       const int pitch = width * static_cast<int>(sizeof(S));
       const int at = piece * 1024 + lane * 16;
@@ -454,6 +379,8 @@ __global__ __launch_bounds__(C::THREADS, 2) void grouped_tile_kernel(GroupArgs g
       const int c = V == 8 ? pc ^ (width >= 128 ? 4 * (kk & 3) : 4 * ((kk >> 1) & 1)) : pc;
       voff[q] = static_cast<uint32_t>((kk * ld + c * V) * static_cast<int64_t>(sizeof(S)));
       klim[q] = c * V < rem ? kk : 0x7fffffff;
+      cnt[q] = min(V, rem - c * V);
+      if (LOAD == kLoadRegCkpt && q >= C::PP) voff[q] = static_cast<uint32_t>(kk * ld + c * V);
     }
   };
 #pragma unroll
@@ -470,10 +397,10 @@ __global__ __launch_bounds__(C::THREADS, 2) void grouped_tile_kernel(GroupArgs g
     }
   }
   const char* pbase = reinterpret_cast<const char*>(P);
-  const char* qbase = CKPT ? static_cast<const char*>(g.q) + lo * g.ldq + q0
+  const char* qbase = kCodes ? static_cast<const char*>(g.q) + lo * g.ldq + q0
                            : reinterpret_cast<const char*>(Q);
   const int64_t pstep = (kPT ? g.ldp : 1) * static_cast<int64_t>(BK * sizeof(S));
-  const int64_t qstep = (kQT ? ldq : 1) * static_cast<int64_t>(BK * (CKPT ? 1 : sizeof(S)));
+  const int64_t qstep = (kQT ? ldq : 1) * static_cast<int64_t>(BK * (kCodes ? 1 : sizeof(S)));
   const uint32_t lds0 = lds_addr(lds);
   // Next step to fetch: pbase / qbase point at it, `left` values of t remain
   // from it on.  With CKPT qbase and qleft are one step further on.
@@ -491,6 +418,59 @@ __global__ __launch_bounds__(C::THREADS, 2) void grouped_tile_kernel(GroupArgs g
     qbase += qstep;
     left -= BK;
     qleft -= BK;
+  };
+
+  // kLoadReg: this thread's chunks of the next step, in registers (codes are
+  // converted on the way).
+  uint4 stash[kReg ? PIECES : 1];
+  auto reg_load = [&] {
+#pragma unroll
+    for (int q = 0; q < PIECES; ++q) {
+      const bool is_p = q < C::PP;
+      const bool along = is_p ? kPT : kQT;
+      int n = along ? (klim[q] < left ? cnt[q] : 0) : min(max(left - klim[q], 0), V);
+      const char* src = (is_p ? pbase : qbase) + voff[q];
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (LOAD == kLoadRegCkpt && !is_p) {
+        uint32_t w[2] = {0, 0};
+        float s = 0.f;
+        if (n > 0) {
+          const int nb = (g.k + kCkptBlock - 1) / kCkptBlock;
+          const int row = R - left + klim[q], col = q0 + static_cast<int>(voff[q] - klim[q] * ldq);
+          s = ckpt_scale(gld<uint8_t>(g.qs + static_cast<size_t>(lo + row) * nb + col / kCkptBlock));
+        }
+        if (n == V && V == 8) {
+          const u32x2_t t = *(const MFSDP_GLOBAL u32x2_b_t*)(src);
+          w[0] = t.x;
+          w[1] = t.y;
+        } else if (n == V) {
+          w[0] = *(const MFSDP_GLOBAL u32_b_t*)(src);
+        } else {
+          for (int i = 0; i < n; ++i)
+            w[i >> 2] |= static_cast<uint32_t>(gld<uint8_t>(src + i)) << (8 * (i & 3));
+        }
+        float f[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+          f[i] = static_cast<float>(static_cast<int8_t>(w[i >> 2] >> (8 * (i & 3)))) * (i < n ? s : 0.f);
+        v = Vec16<E>::pack(f);
+      } else if (n == V) {
+        v = load16_any(src);
+      } else if (n > 0) {
+        S x[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) x[i] = i < n ? gld<S>(src + i * sizeof(S)) : S(0);
+        __builtin_memcpy(&v, x, 16);
+      }
+      stash[q] = v;
+    }
+  };
+  auto reg_store = [&](uint32_t stage) {
+#pragma unroll
+    for (int q = 0; q < PIECES; ++q) {
+      const int piece = q < C::PP ? wave * C::PP + q : wave * QPW + q - C::PP;
+      *reinterpret_cast<uint4*>(lds + stage + (q < C::PP ? 0 : C::BP * ROW) + piece * 1024 + lane * 16) = stash[q];
+    }
   };
 
   // ---- fragments ---------------------------------------------------------------
@@ -549,6 +529,31 @@ __global__ __launch_bounds__(C::THREADS, 2) void grouped_tile_kernel(GroupArgs g
 #pragma unroll
     for (int j = 0; j < TQ; ++j) acc[i][j] = f32x16_t{};
 
+  // fp32: the blocks' sums are moved to a second set every kFlush steps, so that
+  // a long sum is a sum of sums of 512 values and its rounding does not grow
+  // with its whole length.
+  constexpr int kFlush = 512 / BK;
+  constexpr bool kTwoSums = V == 4 && C::KS == 1;
+  f32x16_t acc2[kTwoSums ? TP : 1][kTwoSums ? TQ : 1];
+  if constexpr (kTwoSums) {
+#pragma unroll
+    for (int i = 0; i < TP; ++i)
+#pragma unroll
+      for (int j = 0; j < TQ; ++j) acc2[i][j] = f32x16_t{};
+  }
+  auto flush = [&](int t) {
+    if constexpr (kTwoSums) {
+      if (t % kFlush != kFlush - 1) return;
+#pragma unroll
+      for (int i = 0; i < TP; ++i)
+#pragma unroll
+        for (int j = 0; j < TQ; ++j) {
+          acc2[i][j] += acc[i][j];
+          acc[i][j] = f32x16_t{};
+        }
+    }
+  };
+
   // ---- main loop ------------------------------------------------------------------
   // Step t computes on stage t % STAGES.  Each sub-step reads the fragments of
   // the next one; before the last, whose fragments have then been read, the
@@ -597,7 +602,60 @@ __global__ __launch_bounds__(C::THREADS, 2) void grouped_tile_kernel(GroupArgs g
     }
   };
 
-  if (nk > 0) {
+  if constexpr (kReg || C::KS > 1) {
+    // One barrier per step: behind it every wave has read the step before, whose
+    // buffer the loads refill, and this step is there.
+    constexpr int kSubs = C::SUBS / C::KS;      // of this set of waves
+    auto multiply = [&](uint32_t stage) {
+#pragma unroll
+      for (int i = 0; i < kSubs; ++i) {
+#pragma unroll
+        for (int r = 0; r < kReads; ++r) read_piece(stage, 0, ks * kSubs + i, r, fp[i & 1], fq[i & 1]);
+#pragma unroll
+        for (int x = 0; x < C::SLOTS; ++x)
+          Mma<E>::run(acc[x / TQ][x % TQ], fq[i & 1][x % TQ], fp[i & 1][x / TQ]);
+      }
+    };
+    if constexpr (kReg) {
+      static_assert(C::STAGES == 2, "two buffers behind the registers");
+      if (nk > 0) {
+        reg_load();
+        reg_store(0);
+        dma_next();
+      }
+      uint32_t cur = 0;
+#pragma unroll 1
+      for (int t = 0; t < nk; ++t) {
+        if (t + 1 < nk) reg_load();
+        __syncthreads();
+        multiply(cur);
+        flush(t);
+        cur ^= kStage;
+        if (t + 1 < nk) reg_store(cur);
+        dma_next();
+      }
+    } else if (nk > 0) {
+#pragma unroll
+      for (int s = 0; s < C::STAGES - 1; ++s) {
+#pragma unroll
+        for (int q = 0; q < PIECES; ++q) dma_piece(s * kStage, q);
+        dma_next();
+      }
+      uint32_t cur = 0, fill = kStagesEnd - kStage;
+#pragma unroll 1
+      for (int t = 0; t < nk; ++t) {
+        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier"
+                     :: "n"((C::STAGES - 2) * PIECES) : "memory");
+#pragma unroll
+        for (int q = 0; q < PIECES; ++q) dma_piece(fill, q);
+        dma_next();
+        multiply(cur);
+        flush(t);
+        fill = cur;
+        cur = cur + kStage == kStagesEnd ? 0 : cur + kStage;
+      }
+    }
+  } else if (nk > 0) {
     if constexpr (CKPT) {   // codes of step 0, then one step ahead of P
       scales_load(0);
       scales_store(0);
@@ -661,6 +719,7 @@ __global__ __launch_bounds__(C::THREADS, 2) void grouped_tile_kernel(GroupArgs g
                        :: "n"((C::STAGES - 2) * PIECES) : "memory");
         }
       }
+      flush(t);
       fill = cur;
       cur = nxt;
       qcur ^= kQPanel;
@@ -668,6 +727,39 @@ __global__ __launch_bounds__(C::THREADS, 2) void grouped_tile_kernel(GroupArgs g
   }
   // every DMA has landed and every fragment is read before the stages are reused
   asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+
+  if constexpr (kTwoSums) {
+#pragma unroll
+    for (int i = 0; i < TP; ++i)
+#pragma unroll
+      for (int j = 0; j < TQ; ++j) acc[i][j] += acc2[i][j];
+  }
+  if constexpr (C::KS > 1) {   // the other sets' sums, in their order
+    constexpr int kBlock = 64 * 16;   // floats of one MFMA block
+    float* sums = reinterpret_cast<float*>(lds);
+    static_assert((C::KS - 1) * kTileWaves * C::SLOTS * kBlock * 4 <= kLds, "sums fit");
+    auto at = [&](int set, int x, int r) {
+      return ((set * kTileWaves + tw) * C::SLOTS + x) * kBlock + r * 64 + lane;
+    };
+    if (ks > 0) {
+#pragma unroll
+      for (int x = 0; x < C::SLOTS; ++x)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) sums[at(ks - 1, x, r)] = acc[x / TQ][x % TQ][r];
+    }
+    __syncthreads();
+    if (ks > 0) return;
+#pragma unroll
+    for (int s = 0; s < C::KS - 1; ++s)
+#pragma unroll
+      for (int x = 0; x < C::SLOTS; ++x)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) acc[x / TQ][x % TQ][r] += sums[at(s, x, r)];
+    // this wave's staging below may overlap sums that another wave still reads
+    static_assert(kTileWaves * 32 * (TQ * 32 * 4 + 16) <= kLds / 2 &&
+                      (C::KS - 1) * kTileWaves * C::SLOTS * kBlock * 4 <= kLds / 2,
+                  "staging behind the sums");
+  }
 
   // ---- epilogue -------------------------------------------------------------------
   // Each wave turns its blocks through its own part of LDS, 32 rows at a time
@@ -688,13 +780,12 @@ __global__ __launch_bounds__(C::THREADS, 2) void grouped_tile_kernel(GroupArgs g
     ldo = g.ldo;
     out = static_cast<char*>(g.out) + ((lo + p0) * ldo + q0) * static_cast<int64_t>(sizeof(S));
   }
-  const bool vec = split ? g.k % 4 == 0 : g.vec_out != 0;   // parts start on 256 bytes
   constexpr int GROUPS = COLS / 8;          // 8-column groups per row
   constexpr int RPP = 64 / GROUPS;          // rows per pass of a wave
   if (!f32) {
     constexpr int PITCH = COLS * 2 + 16;
-    char* mine = lds + wave * (32 * PITCH);
-    static_assert(C::WAVES * 32 * PITCH <= kLds, "staging fits");
+    char* mine = lds + (C::KS > 1 ? kLds / 2 : 0) + tw * (32 * PITCH);
+    static_assert(kTileWaves * 32 * PITCH <= kLds, "staging fits");
 #pragma unroll
     for (int i = 0; i < TP; ++i) {
 #pragma unroll
@@ -710,8 +801,8 @@ __global__ __launch_bounds__(C::THREADS, 2) void grouped_tile_kernel(GroupArgs g
         const int p = prow0 + i * 32 + row, q = qcol0 + col;
         if (p < prem && q < qrem) {
           uint16_t* o = reinterpret_cast<uint16_t*>(out) + p * ldo + q;
-          if (vec && q + 8 <= qrem) {
-            gst<uint4>(o, v);
+          if (q + 8 <= qrem) {
+            store16_any(o, v);
           } else {
             const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -723,8 +814,8 @@ __global__ __launch_bounds__(C::THREADS, 2) void grouped_tile_kernel(GroupArgs g
     }
   } else {
     constexpr int PITCH = COLS * 4 + 16;
-    char* mine = lds + wave * (32 * PITCH);
-    static_assert(C::WAVES * 32 * PITCH <= kLds, "staging fits");
+    char* mine = lds + (C::KS > 1 ? kLds / 2 : 0) + tw * (32 * PITCH);
+    static_assert(kTileWaves * 32 * PITCH <= kLds, "staging fits");
 #pragma unroll
     for (int i = 0; i < TP; ++i) {
 #pragma unroll
@@ -741,17 +832,17 @@ __global__ __launch_bounds__(C::THREADS, 2) void grouped_tile_kernel(GroupArgs g
         float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
         const int p = prow0 + i * 32 + row, q = qcol0 + col;
         if (p >= prem || q >= qrem) continue;
-        const bool whole = vec && q + 8 <= qrem;
+        const bool whole = q + 8 <= qrem;
         if (out_f32) {
           float* o = reinterpret_cast<float*>(out) + p * ldo + q;
           if (whole) {
             if (MODE == kGroupWgrad && beta != 0.f) {
               float old[8];
-              load8<ElemF32>(o, old);
+              load8_any<ElemF32>(o, old);
 #pragma unroll
               for (int k = 0; k < 8; ++k) v[k] = fmaf(beta, old[k], v[k]);
             }
-            store8<ElemF32>(o, v);
+            store8_any<ElemF32>(o, v);
           } else {
 #pragma unroll
             for (int k = 0; k < 8; ++k)
@@ -761,10 +852,10 @@ __global__ __launch_bounds__(C::THREADS, 2) void grouped_tile_kernel(GroupArgs g
           uint16_t* o = reinterpret_cast<uint16_t*>(out) + p * ldo + q;
           if (whole) {
             float old[8];
-            load8<ElemBF16>(o, old);
+            load8_any<ElemBF16>(o, old);
 #pragma unroll
             for (int k = 0; k < 8; ++k) v[k] = fmaf(beta, old[k], v[k]);
-            store8<ElemBF16>(o, v);
+            store8_any<ElemBF16>(o, v);
           } else {
 #pragma unroll
             for (int k = 0; k < 8; ++k)
@@ -794,20 +885,20 @@ __global__ __launch_bounds__(256) void grouped_sum_kernel(GroupArgs g, int per_e
   O* out = static_cast<O*>(g.out) + at;
   const float* part = g.part + at;
   float v[8] = {};
-  if (g.vec_out && wsize % 8 == 0) {
+  if (i + 8 <= wsize) {
     for (int s = 0; s < parts; ++s) {
       float p[8];
-      load8<ElemF32>(part + s * stride, p);
+      load8_any<ElemF32>(part + s * stride, p);
 #pragma unroll
       for (int k = 0; k < 8; ++k) v[k] += p[k];
     }
     if (g.beta != 0.f) {
       float old[8];
-      load8<EO>(out, old);
+      load8_any<EO>(out, old);
 #pragma unroll
       for (int k = 0; k < 8; ++k) v[k] = fmaf(g.beta, old[k], v[k]);
     }
-    store8<EO>(out, v);
+    store8_any<EO>(out, v);
   } else {
     for (int k = 0; k < 8 && i + k < wsize; ++k) {
       float x = 0.f;

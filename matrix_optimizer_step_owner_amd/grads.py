@@ -27,6 +27,12 @@ from . import _lib
 CKPT_BLOCK = 128
 
 _DTYPES = {torch.float32: _lib.DTYPE_F32, torch.bfloat16: _lib.DTYPE_BF16}
+_FLOATS = tuple(_DTYPES)
+
+
+# The handle of a device's current stream, without the Stream object that
+# torch.cuda.current_stream makes around it (over a microsecond a call).
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 def _check(t: torch.Tensor, name: str, device, dtypes, dim: int) -> None:
@@ -36,42 +42,51 @@ def _check(t: torch.Tensor, name: str, device, dtypes, dim: int) -> None:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
     if t.dtype not in dtypes:
         raise TypeError(f"{name} has dtype {t.dtype}, expected {' or '.join(map(str, dtypes))}")
-    if t.dim() != dim:
+    if t.ndim != dim:
         raise ValueError(f"{name} must be {dim}D")
 
 
 def _contiguous(t: torch.Tensor, name: str, shape=None) -> None:
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
 
 
 def _rows(t: torch.Tensor, name: str, shape=None) -> int:
     """Row stride of a matrix whose rows are contiguous (any stride between rows)."""
-    if shape is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.size(1) > 1 and t.stride(1) != 1:
+    rows, cols = have = t.shape
+    if shape is not None and have != shape:
+        raise ValueError(f"{name} has shape {tuple(have)}, expected {tuple(shape)}")
+    ld, inner = t.stride()
+    if cols > 1 and inner != 1:
         raise ValueError(f"{name} must have contiguous rows")
-    if t.size(0) <= 1:
-        return max(t.size(1), 1)
-    if t.stride(0) < t.size(1):
+    if rows <= 1:
+        return max(cols, 1)
+    if ld < cols:
         raise ValueError(f"rows of {name} overlap")
-    return t.stride(0)
+    return ld
 
 
 def _gpu(t: torch.Tensor, name: str) -> torch.device:
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a tensor")
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError(f"{name} must be a GPU tensor")
     return t.device
 
 
-def _call(device: torch.device, fn, *args) -> None:
-    """fn(*args, stream) with `device` current, on its current stream."""
-    with torch.cuda.device(device):
-        _lib.check(fn(*args, torch.cuda.current_stream(device).cuda_stream))
+def _call(device: torch.device, name: str, *args) -> None:
+    """The library's function on the current stream of `device`, made current."""
+    fn = getattr(_lib.load(), name)
+    index = device.index
+    if index == torch.cuda.current_device():
+        status = fn(*args, _raw_stream(index))
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, _raw_stream(index))
+    if status:
+        _lib.check(status)
 
 
 def _scratch(device: torch.device, nbytes: int, given: Optional[torch.Tensor]) -> torch.Tensor:
@@ -86,18 +101,39 @@ def _scratch(device: torch.device, nbytes: int, given: Optional[torch.Tensor]) -
         if torch.cuda.is_current_stream_capturing():
             return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
     from . import _workspace
-    return _workspace(device, torch.cuda.current_stream(device).cuda_stream, nbytes)
+    return _workspace(device, _raw_stream(device.index), nbytes)
 
 
 def _grouped_args(act: torch.Tensor, name: str, weight: torch.Tensor, wname: str,
-                  offsets: torch.Tensor):
+                  offsets: torch.Tensor, dtypes):
+    """Device, and the shape (experts, n, k) of the stacked matrices."""
     device = _gpu(act, name)
-    _check(act, name, device, tuple(_DTYPES), 2)
+    _check(act, name, device, _FLOATS, 2)
     _check(offsets, "offsets", device, (torch.int32,), 1)
-    _check(weight, wname, device, tuple(_DTYPES), 3)
+    _check(weight, wname, device, dtypes, 3)
     _contiguous(weight, wname)
-    _contiguous(offsets, "offsets", (weight.size(0) + 1,))
-    return device
+    shape = weight.shape
+    _contiguous(offsets, "offsets", (shape[0] + 1,))
+    return device, shape
+
+
+def _grouped_rows(name: str, act: torch.Tensor, weight: torch.Tensor, offsets: torch.Tensor,
+                  out: Optional[torch.Tensor], forward: bool) -> torch.Tensor:
+    arg = "x" if forward else "dy"
+    dtype = act.dtype if isinstance(act, torch.Tensor) else None
+    device, (experts, n, k) = _grouped_args(act, arg, weight, "weight", offsets, (dtype,))
+    rows = act.shape[0]
+    width, to = (k, n) if forward else (n, k)
+    ld = _rows(act, arg, (rows, width))
+    if out is None:
+        out = torch.empty(rows, to, dtype=dtype, device=device)
+        ldo = to
+    else:
+        _check(out, "out", device, (dtype,), 2)
+        ldo = _rows(out, "out", (rows, to))
+    _call(device, name, act.data_ptr(), ld, weight.data_ptr(), offsets.data_ptr(), experts, rows,
+          n, k, _DTYPES[dtype], out.data_ptr(), ldo)
+    return out
 
 
 def grouped_linear(x: torch.Tensor, weight: torch.Tensor, offsets: torch.Tensor,
@@ -109,18 +145,7 @@ def grouped_linear(x: torch.Tensor, weight: torch.Tensor, offsets: torch.Tensor,
     weight: (experts, n, k) contiguous, x's dtype; offsets: (experts + 1,) int32
     on the GPU, non-decreasing, read there.  Rows of no expert are left as they
     are in ``out`` (and undefined in an ``out`` made here)."""
-    device = _grouped_args(x, "x", weight, "weight", offsets)
-    experts, n, k = weight.shape
-    if weight.dtype != x.dtype:
-        raise TypeError(f"weight has dtype {weight.dtype}, expected {x.dtype}")
-    ldx = _rows(x, "x", (x.size(0), k))
-    if out is None:
-        out = torch.empty(x.size(0), n, dtype=x.dtype, device=device)
-    _check(out, "out", device, (x.dtype,), 2)
-    _call(device, _lib.load().mfsdp_grouped_linear, x.data_ptr(), ldx, weight.data_ptr(),
-          offsets.data_ptr(), experts, x.size(0), n, k, _DTYPES[x.dtype], out.data_ptr(),
-          _rows(out, "out", (x.size(0), n)))
-    return out
+    return _grouped_rows("mfsdp_grouped_linear", x, weight, offsets, out, True)
 
 
 def grouped_linear_dgrad(dy: torch.Tensor, weight: torch.Tensor, offsets: torch.Tensor,
@@ -128,29 +153,16 @@ def grouped_linear_dgrad(dy: torch.Tensor, weight: torch.Tensor, offsets: torch.
     """Gradient of ``grouped_linear``'s input: ``out[r] = dy[r] @ weight[e]``
     (mfsdp_grouped_linear_dgrad).  dy: (rows, n); out: (rows, k); the rest as
     there."""
-    device = _grouped_args(dy, "dy", weight, "weight", offsets)
-    experts, n, k = weight.shape
-    if weight.dtype != dy.dtype:
-        raise TypeError(f"weight has dtype {weight.dtype}, expected {dy.dtype}")
-    lddy = _rows(dy, "dy", (dy.size(0), n))
-    if out is None:
-        out = torch.empty(dy.size(0), k, dtype=dy.dtype, device=device)
-    _check(out, "out", device, (dy.dtype,), 2)
-    _call(device, _lib.load().mfsdp_grouped_linear_dgrad, dy.data_ptr(), lddy, weight.data_ptr(),
-          offsets.data_ptr(), experts, dy.size(0), n, k, _DTYPES[dy.dtype], out.data_ptr(),
-          _rows(out, "out", (dy.size(0), k)))
-    return out
+    return _grouped_rows("mfsdp_grouped_linear_dgrad", dy, weight, offsets, out, False)
 
 
-def _wgrad_scratch(dy: torch.Tensor, grad: torch.Tensor, given: Optional[torch.Tensor]):
+def _wgrad_scratch(device: torch.device, sizes, given: Optional[torch.Tensor]):
     """(address, bytes) of the workspace of a weight gradient, (None, 0) if it needs none."""
-    lib = _lib.load()
     need = ctypes.c_size_t(0)
-    _lib.check(lib.mfsdp_grouped_linear_wgrad_workspace_size(
-        grad.size(0), dy.size(0), grad.size(1), grad.size(2), _DTYPES[dy.dtype], ctypes.byref(need)))
+    _lib.check(_lib.load().mfsdp_grouped_linear_wgrad_workspace_size(*sizes, ctypes.byref(need)))
     if need.value == 0 and given is None:
         return None, 0
-    ws = _scratch(dy.device, need.value, given)
+    ws = _scratch(device, need.value, given)
     return ws.data_ptr(), ws.numel() * ws.element_size()
 
 
@@ -165,22 +177,25 @@ def grouped_linear_wgrad(dy: torch.Tensor, x: torch.Tensor, offsets: torch.Tenso
     that dtype or fp32, each ``grad[e]`` as ``muon_step`` takes it.  beta = 1
     adds a micro-batch to what is there; beta = 0 does not read it.  An expert
     without rows gets ``beta * grad[e]``.  Returns grad."""
-    device = _grouped_args(dy, "dy", grad, "grad", offsets)
-    experts, n, k = grad.shape
-    if grad.dtype not in (dy.dtype, torch.float32):
-        raise TypeError(f"grad has dtype {grad.dtype}, expected {dy.dtype} or torch.float32")
-    _check(x, "x", device, (dy.dtype,), 2)
-    _call(device, _lib.load().mfsdp_grouped_linear_wgrad, dy.data_ptr(),
-          _rows(dy, "dy", (dy.size(0), n)), x.data_ptr(), _rows(x, "x", (dy.size(0), k)),
-          offsets.data_ptr(), experts, dy.size(0), n, k, _DTYPES[dy.dtype], grad.data_ptr(),
-          _DTYPES[grad.dtype], beta, *_wgrad_scratch(dy, grad, workspace))
+    dtype = dy.dtype if isinstance(dy, torch.Tensor) else None
+    device, (experts, n, k) = _grouped_args(dy, "dy", grad, "grad", offsets,
+                                            (dtype, torch.float32))
+    rows = dy.shape[0]
+    _check(x, "x", device, (dtype,), 2)
+    _call(device, "mfsdp_grouped_linear_wgrad", dy.data_ptr(), _rows(dy, "dy", (rows, n)),
+          x.data_ptr(), _rows(x, "x", (rows, k)), offsets.data_ptr(), experts, rows, n, k,
+          _DTYPES[dtype], grad.data_ptr(), _DTYPES[grad.dtype], beta,
+          *_wgrad_scratch(device, (experts, rows, n, k, _DTYPES[dtype]), workspace))
     return grad
 
 
-def _check_ckpt(codes: torch.Tensor, scales: torch.Tensor, device, rows: int, k: int) -> None:
+def _check_codes(codes: torch.Tensor, device, rows: int, k: int) -> None:
     _check(codes, "codes", device, (torch.int8,), 2)
-    _check(scales, "scales", device, (torch.uint8,), 2)
     _contiguous(codes, "codes", (rows, k))
+
+
+def _check_scales(scales: torch.Tensor, device, rows: int, k: int) -> None:
+    _check(scales, "scales", device, (torch.uint8,), 2)
     _contiguous(scales, "scales", (rows, -(-k // CKPT_BLOCK)))
 
 
@@ -190,15 +205,16 @@ def grouped_linear_wgrad_ckpt(dy: torch.Tensor, codes: torch.Tensor, scales: tor
     """``grouped_linear_wgrad`` with x as its 8-bit checkpoint, (codes, scales)
     of ``ckpt_quantize`` (mfsdp_grouped_linear_wgrad_ckpt): the gradient for the
     restored x, which is never written out."""
-    device = _grouped_args(dy, "dy", grad, "grad", offsets)
-    experts, n, k = grad.shape
-    if grad.dtype not in (dy.dtype, torch.float32):
-        raise TypeError(f"grad has dtype {grad.dtype}, expected {dy.dtype} or torch.float32")
-    _check_ckpt(codes, scales, device, dy.size(0), k)
-    _call(device, _lib.load().mfsdp_grouped_linear_wgrad_ckpt, dy.data_ptr(),
-          _rows(dy, "dy", (dy.size(0), n)), codes.data_ptr(), scales.data_ptr(),
-          offsets.data_ptr(), experts, dy.size(0), n, k, _DTYPES[dy.dtype], grad.data_ptr(),
-          _DTYPES[grad.dtype], beta, *_wgrad_scratch(dy, grad, workspace))
+    dtype = dy.dtype if isinstance(dy, torch.Tensor) else None
+    device, (experts, n, k) = _grouped_args(dy, "dy", grad, "grad", offsets,
+                                            (dtype, torch.float32))
+    rows = dy.shape[0]
+    _check_codes(codes, device, rows, k)
+    _check_scales(scales, device, rows, k)
+    _call(device, "mfsdp_grouped_linear_wgrad_ckpt", dy.data_ptr(), _rows(dy, "dy", (rows, n)),
+          codes.data_ptr(), scales.data_ptr(), offsets.data_ptr(), experts, rows, n, k,
+          _DTYPES[dtype], grad.data_ptr(), _DTYPES[grad.dtype], beta,
+          *_wgrad_scratch(device, (experts, rows, n, k, _DTYPES[dtype]), workspace))
     return grad
 
 
@@ -212,14 +228,17 @@ def ckpt_quantize(x: torch.Tensor, codes: Optional[torch.Tensor] = None,
     x is held as q * 2^e, off by at most half of 2^e.  x: (rows, k) bf16 or
     fp32, rows contiguous at any stride."""
     device = _gpu(x, "x")
-    _check(x, "x", device, tuple(_DTYPES), 2)
+    _check(x, "x", device, _FLOATS, 2)
     rows, k = x.shape
     if codes is None:
         codes = torch.empty(rows, k, dtype=torch.int8, device=device)
+    else:
+        _check_codes(codes, device, rows, k)
     if scales is None:
         scales = torch.empty(rows, -(-k // CKPT_BLOCK), dtype=torch.uint8, device=device)
-    _check_ckpt(codes, scales, device, rows, k)
-    _call(device, _lib.load().mfsdp_ckpt_quantize, x.data_ptr(), _rows(x, "x"), rows, k,
+    else:
+        _check_scales(scales, device, rows, k)
+    _call(device, "mfsdp_ckpt_quantize", x.data_ptr(), _rows(x, "x"), rows, k,
           _DTYPES[x.dtype], codes.data_ptr(), scales.data_ptr())
     return codes, scales
 
@@ -230,14 +249,16 @@ def ckpt_restore(codes: torch.Tensor, scales: torch.Tensor, dtype: torch.dtype =
     mfsdp_ckpt_restore).  With ``out`` its dtype is taken."""
     device = _gpu(codes, "codes")
     _check(codes, "codes", device, (torch.int8,), 2)
+    _contiguous(codes, "codes")
     rows, k = codes.shape
-    _check_ckpt(codes, scales, device, rows, k)
+    _check_scales(scales, device, rows, k)
     if out is None:
         if dtype not in _DTYPES:
             raise TypeError(f"unsupported dtype {dtype}")
         out = torch.empty(rows, k, dtype=dtype, device=device)
-    _check(out, "out", device, tuple(_DTYPES), 2)
-    _call(device, _lib.load().mfsdp_ckpt_restore, codes.data_ptr(), scales.data_ptr(), rows, k,
+    else:
+        _check(out, "out", device, _FLOATS, 2)
+    _call(device, "mfsdp_ckpt_restore", codes.data_ptr(), scales.data_ptr(), rows, k,
           _DTYPES[out.dtype], out.data_ptr(), _rows(out, "out", (rows, k)))
     return out
 
@@ -260,7 +281,7 @@ def embedding(table: torch.Tensor, tokens: torch.Tensor, *, scale: float = 1.0,
     table's), or writes ``out``, (number of tokens, d) with rows at any
     stride."""
     device = _gpu(table, "table")
-    _check(table, "table", device, tuple(_DTYPES), 2)
+    _check(table, "table", device, _FLOATS, 2)
     _contiguous(table, "table")
     size = _check_tokens(tokens, device)
     vocab, d = table.shape
@@ -274,8 +295,8 @@ def embedding(table: torch.Tensor, tokens: torch.Tensor, *, scale: float = 1.0,
         shape = tuple(tokens.shape) + (d,)
     elif dtype is not None and dtype != out.dtype:
         raise TypeError(f"out has dtype {out.dtype}, expected {dtype}")
-    _check(out, "out", device, tuple(_DTYPES), 2)
-    _call(device, _lib.load().mfsdp_embedding, table.data_ptr(), _DTYPES[table.dtype], vocab, d,
+    _check(out, "out", device, _FLOATS, 2)
+    _call(device, "mfsdp_embedding", table.data_ptr(), _DTYPES[table.dtype], vocab, d,
           tokens.data_ptr(), size, n, scale, out.data_ptr(), _rows(out, "out", (n, d)),
           _DTYPES[out.dtype])
     return out if shape is None else out.view(shape)
@@ -294,7 +315,7 @@ def embedding_grad(dy: torch.Tensor, tokens: torch.Tensor, grad: torch.Tensor, *
     sorted order and depend on the inputs alone.  beta = 1 adds a micro-batch
     and leaves the rows without a token untouched.  Returns grad."""
     device = _gpu(dy, "dy")
-    _check(dy, "dy", device, tuple(_DTYPES), 2)
+    _check(dy, "dy", device, _FLOATS, 2)
     _check(grad, "grad", device, (torch.float32,), 2)
     _contiguous(grad, "grad")
     size = _check_tokens(tokens, device)
@@ -305,7 +326,7 @@ def embedding_grad(dy: torch.Tensor, tokens: torch.Tensor, grad: torch.Tensor, *
     need = ctypes.c_size_t(0)
     _lib.check(lib.mfsdp_embedding_grad_workspace_size(n, vocab, d, ctypes.byref(need)))
     ws = _scratch(device, need.value, workspace)
-    _call(device, lib.mfsdp_embedding_grad, dy.data_ptr(), ld, _DTYPES[dy.dtype],
+    _call(device, "mfsdp_embedding_grad", dy.data_ptr(), ld, _DTYPES[dy.dtype],
           tokens.data_ptr(), size, n, vocab, d, scale, beta, grad.data_ptr(), ws.data_ptr(),
           ws.numel() * ws.element_size())
     return grad
