@@ -79,7 +79,7 @@ __global__ __launch_bounds__(256) void embedding_kernel(EmbArgs a) {
 // ---------------------------------------------------------------------------
 // Stable radix sort of (token, position)
 // ---------------------------------------------------------------------------
-constexpr int kSortThreads = 256;
+constexpr int kSortThreads = 1024;
 constexpr int kSortWaves = kSortThreads / 64;
 constexpr int kSortBitsMax = 9;                       // digit bits of one pass
 constexpr int kSortBinsMax = 1 << kSortBitsMax;
@@ -119,7 +119,7 @@ __global__ __launch_bounds__(kSortThreads) void sort_hist_kernel(SortArgs s) {
 }
 
 // One pass over one workgroup's keys [i0, i1): each wave takes a contiguous
-// quarter, so that order is kept.  base[] holds where each bin of this
+// part, so that order is kept.  base[] holds where each bin of this
 // workgroup starts in the output; the per-wave counts then give each wave its
 // start, and within 64 keys a lane's place is the number of lower lanes with
 // the same digit (bits ballots).
@@ -170,13 +170,13 @@ __device__ __forceinline__ void sort_scatter(const SortArgs& s, int i0, int i1,
   }
 }
 
-// Exclusive scan of tot[0..bins) into base[], plus add[]; kSortThreads threads.
+// Exclusive scan of tot[0..bins) into base[], plus add[]; one bin per thread.
 __device__ __forceinline__ void sort_scan(const uint32_t* tot, const uint32_t* add, uint32_t* base,
                                           int bins, uint32_t* wave_sum) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int b0 = 2 * threadIdx.x;   // kSortBinsMax = 2 * kSortThreads
-  const uint32_t t0 = b0 < bins ? tot[b0] : 0, t1 = b0 + 1 < bins ? tot[b0 + 1] : 0;
-  uint32_t incl = t0 + t1;
+  const int b = threadIdx.x;
+  const uint32_t t = b < bins ? tot[b] : 0;
+  uint32_t incl = t;
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) {
     const uint32_t v = __shfl_up(incl, d, 64);
@@ -184,13 +184,12 @@ __device__ __forceinline__ void sort_scan(const uint32_t* tot, const uint32_t* a
   }
   if (lane == 63) wave_sum[wave] = incl;
   __syncthreads();
-  uint32_t before = incl - t0 - t1;
+  uint32_t before = incl - t;
   for (int w = 0; w < wave; ++w) before += wave_sum[w];
-  if (b0 < bins) base[b0] = before + add[b0];
-  if (b0 + 1 < bins) base[b0 + 1] = before + t0 + add[b0 + 1];
+  if (b < bins) base[b] = before + add[b];
   __syncthreads();
 }
-static_assert(kSortBinsMax == 2 * kSortThreads, "sort_scan takes two bins per thread");
+static_assert(kSortBinsMax <= kSortThreads, "sort_scan takes one bin per thread");
 
 __global__ __launch_bounds__(kSortThreads) void sort_scatter_kernel(SortArgs s) {
   __shared__ uint32_t base[kSortBinsMax], tot[kSortBinsMax], add[kSortBinsMax];
@@ -252,22 +251,23 @@ __global__ __launch_bounds__(kSortThreads) void sort_small_kernel(SortSmallArgs 
 // Sums over the sorted list
 // ---------------------------------------------------------------------------
 constexpr int kEmbRun = 64;       // longest run that one workgroup adds alone
-constexpr int kEmbRows = 32;      // table rows per workgroup
+constexpr int kEmbRows = 4;       // table rows per workgroup
 
 struct EmbGradArgs {
   const void* dy;          // tokens x d, row stride ld
   const uint32_t* key;     // sorted tokens (padding: vocab, last)
   const uint32_t* pos;     // their positions
   float* part;             // [chunks of kEmbRun sorted positions][2][d]
+  int32_t* begin;          // first sorted index of each block of kEmbRows table rows, and n
   float* grad;             // vocab x d
   int64_t vocab, ld;
   int32_t n, d;
+  int32_t tpr;             // threads per row: 64, 128 or 256
   float scale, beta;
 };
 
-// First sorted index whose key is >= v.
-__device__ __forceinline__ int emb_lower(const uint32_t* key, int n, int64_t v) {
-  int lo = 0, hi = n;
+// First sorted index in [lo, hi) whose key is >= v.
+__device__ __forceinline__ int emb_lower(const uint32_t* key, int lo, int hi, int64_t v) {
   while (lo < hi) {
     const int mid = (lo + hi) >> 1;
     if (static_cast<int64_t>(key[mid]) < v) lo = mid + 1; else hi = mid;
@@ -275,101 +275,198 @@ __device__ __forceinline__ int emb_lower(const uint32_t* key, int n, int64_t v) 
   return lo;
 }
 
-// Sum of dY over sorted positions [b, e), W columns from c, in order.
+// Columns of one thread: kEmbGroups groups of W, a.tpr * W apart, so that a
+// wave's accesses are contiguous (W = 4: 8 bytes of bf16 read, 16 of fp32
+// written per lane).  a.tpr threads, whole waves, take one row, so that rows
+// narrower than a workgroup are taken several at once.
+constexpr int kEmbGroups = 2;
+constexpr int kEmbFlight = 8;   // rows' loads in flight
+
+// W consecutive elements as loaded, and as floats.  Loads and conversions are
+// kept apart, and loads take no branch (columns that do not exist read column
+// 0): else each would be waited for before the next is issued.
+typedef uint32_t u32x2v_t __attribute__((ext_vector_type(2)));
 template <class E, int W>
-__device__ __forceinline__ void emb_sum(const EmbGradArgs& a, int b, int e, int c, float (&acc)[W]) {
-  using S = typename E::storage_t;
-  const S* dy = static_cast<const S*>(a.dy) + c;
-  int i = b;
-  auto add = [&](int j) {
-    float v[W];
-    const S* p = dy + a.pos[j] * a.ld;
-    if constexpr (W == 8) load8<E>(p, v); else v[0] = E::to_f32(*p);
-#pragma unroll
-    for (int k = 0; k < W; ++k) acc[k] += v[k];
-  };
-  for (; i + 4 <= e; i += 4) {
-    add(i);
-    add(i + 1);
-    add(i + 2);
-    add(i + 3);
+struct EmbRaw {
+  typename std::conditional<W == 1, typename E::storage_t,
+                            typename std::conditional<E::kVec == 8, u32x2v_t, f32x4_t>::type>::type r;
+  __device__ __forceinline__ void load(const typename E::storage_t* p) { r = gld<decltype(r)>(p); }
+  __device__ __forceinline__ void get(float (&v)[W]) const {
+    if constexpr (W == 1) {
+      v[0] = E::to_f32(r);
+    } else if constexpr (E::kVec == 8) {
+      v[0] = __uint_as_float(r.x << 16);
+      v[1] = __uint_as_float(r.x & 0xffff0000u);
+      v[2] = __uint_as_float(r.y << 16);
+      v[3] = __uint_as_float(r.y & 0xffff0000u);
+    } else {
+      v[0] = r.x;
+      v[1] = r.y;
+      v[2] = r.z;
+      v[3] = r.w;
+    }
   }
-  for (; i < e; ++i) add(i);
+};
+
+// Columns of this thread's groups: first column, or 0 where there is none.
+struct EmbCols {
+  int c[kEmbGroups];
+  bool on[kEmbGroups];
+  __device__ __forceinline__ EmbCols(int d, int wg, int t, int tpr, int w) {
+#pragma unroll
+    for (int q = 0; q < kEmbGroups; ++q) {
+      const int col = ((wg * kEmbGroups + q) * tpr + t) * w;
+      on[q] = t < tpr && col < d;
+      c[q] = on[q] ? col : 0;
+    }
+  }
+};
+
+// Adds rows i = b .. e - 1 at row_of(i) to acc, in order, with F rows' loads in
+// flight.  Called by whole waves: row_of may exchange lanes.
+template <class E, int W, int F, class RowOf>
+__device__ __forceinline__ void emb_sum(int b, int e, const EmbCols& cols, RowOf row_of,
+                                        float (&acc)[kEmbGroups][W]) {
+  for (int i = b; i < e; i += F) {
+    EmbRaw<E, W> raw[F][kEmbGroups];
+#pragma unroll
+    for (int j = 0; j < F; ++j) {
+      const typename E::storage_t* p = row_of(min(i + j, e - 1));
+#pragma unroll
+      for (int q = 0; q < kEmbGroups; ++q) raw[j][q].load(p + cols.c[q]);
+    }
+#pragma unroll
+    for (int j = 0; j < F; ++j)
+      if (i + j < e) {
+#pragma unroll
+        for (int q = 0; q < kEmbGroups; ++q) {
+          float v[W];
+          raw[j][q].get(v);
+#pragma unroll
+          for (int k = 0; k < W; ++k) acc[q][k] += v[k];
+        }
+      }
+  }
 }
 
 // Partial sums of the runs longer than kEmbRun: workgroup (chunk, columns).
 // Such a run covers the first or the last position of every chunk it meets,
 // so a chunk has at most two partial rows: slot 0 for the run at its first
-// position, slot 1 for another one at its last.
+// position, slot 1 for another one at its last.  Each wave holds the chunk's 64
+// keys, one a lane, and finds both runs' ends by a ballot; one key 64 places
+// away then tells whether a run is that long.  The workgroups behind those find
+// where each block of table rows begins in the sorted list, so that the next
+// kernel's many workgroups do not each search the whole list.
 template <class E, int W>
-__global__ __launch_bounds__(256) void emb_partial_kernel(EmbGradArgs a, int col_wgs) {
+__global__ __launch_bounds__(256) void emb_partial_kernel(EmbGradArgs a, int chunks, int col_wgs) {
+  static_assert(kEmbRun == 64, "one key per lane");
   const int chunk = blockIdx.x / col_wgs;
-  const int c = (static_cast<int>(blockIdx.x % col_wgs) * 256 + static_cast<int>(threadIdx.x)) * W;
+  if (chunk >= chunks) {
+    const int64_t i = (static_cast<int64_t>(blockIdx.x) - static_cast<int64_t>(chunks) * col_wgs) * 256 + threadIdx.x;
+    const int64_t blocks = (a.vocab + kEmbRows - 1) / kEmbRows;
+    if (i <= blocks) a.begin[i] = emb_lower(a.key, 0, a.n, min(i * kEmbRows, a.vocab));
+    return;
+  }
+  const int lane = threadIdx.x & 63;
   const int b = chunk * kEmbRun, e = min(b + kEmbRun, a.n);
-  __shared__ int lim[4];
-  const uint32_t kf = a.key[b], kl = a.key[e - 1];
-  if (threadIdx.x < 4)
-    lim[threadIdx.x] = emb_lower(a.key, a.n, static_cast<int64_t>(threadIdx.x < 2 ? kf : kl) + (threadIdx.x & 1));
-  __syncthreads();
-  if (c >= a.d) return;
+  const bool in = b + lane < e;
+  const uint32_t key = in ? a.key[b + lane] : 0xffffffffu;   // no token's key
+  const uint32_t kf = __shfl(key, 0, 64), kl = __shfl(key, e - b - 1, 64);
+  const uint32_t pos = in ? a.pos[b + lane] : 0;
+  const int end0 = b + __popcll(__ballot(key == kf));        // of the first position's run, in the chunk
+  const int beg1 = e - __popcll(__ballot(key == kl));        // of the last one's
+  // longer than 64: 64 places before its last known (or after its first) it goes on
+  const bool hot0 = (end0 == e && e < a.n && a.key[e] == kf) ||
+                    (end0 > kEmbRun && a.key[end0 - 1 - kEmbRun] == kf);
+  const bool hot1 = kl != kf && beg1 + kEmbRun < a.n && a.key[beg1 + kEmbRun] == kl;
+  const EmbCols cols(a.d, blockIdx.x % col_wgs, threadIdx.x, a.tpr, W);
+  using S = typename E::storage_t;
 #pragma unroll
   for (int slot = 0; slot < 2; ++slot) {
-    const int r0 = lim[2 * slot], r1 = lim[2 * slot + 1];
-    const uint32_t k = slot ? kl : kf;
-    if (r1 - r0 <= kEmbRun || static_cast<int64_t>(k) >= a.vocab || (slot && kl == kf)) continue;
-    float acc[W] = {};
-    emb_sum<E, W>(a, max(r0, b), min(r1, e), c, acc);
-    float* o = a.part + (static_cast<size_t>(chunk) * 2 + slot) * a.d + c;
+    if (!(slot ? hot1 : hot0) || static_cast<int64_t>(slot ? kl : kf) >= a.vocab) continue;
+    float acc[kEmbGroups][W] = {};
+    emb_sum<E, W, kEmbFlight>(
+        slot ? beg1 : b, slot ? e : end0, cols,
+        [&](int i) { return static_cast<const S*>(a.dy) + static_cast<int64_t>(__shfl(pos, i - b, 64)) * a.ld; }, acc);
+    float* o = a.part + (static_cast<size_t>(chunk) * 2 + slot) * a.d;
 #pragma unroll
-    for (int k2 = 0; k2 < W; k2 += W == 8 ? 4 : 1) {
-      if constexpr (W == 8) gst<float4>(o + k2, make_float4(acc[k2], acc[k2 + 1], acc[k2 + 2], acc[k2 + 3]));
-      else o[k2] = acc[k2];
-    }
+    for (int q = 0; q < kEmbGroups; ++q)
+      if (cols.on[q]) {
+#pragma unroll
+        for (int x = 0; x < W; ++x) o[cols.c[q] + x] = acc[q][x];
+      }
   }
 }
 
-// Table rows: workgroup (kEmbRows rows, columns).  Bound by HBM: dY is read
-// once and every gradient row written once (beta = 0: rows without a token
-// are zeroed here, beta = 1: they are not touched).
+// Table rows: workgroup (kEmbRows rows, columns).  Bound by HBM: dY is read once
+// and every gradient row written once (beta = 0: rows without a token are
+// zeroed here, beta = 1: they are not touched).  Up to 64 keys of the block's
+// list sit one a lane, so that each row's part of it comes from two ballots.
 template <class E, int W>
 __global__ __launch_bounds__(256) void emb_rows_kernel(EmbGradArgs a, int col_wgs) {
-  const int64_t v0 = static_cast<int64_t>(blockIdx.x / col_wgs) * kEmbRows;
-  const int c = (static_cast<int>(blockIdx.x % col_wgs) * 256 + static_cast<int>(threadIdx.x)) * W;
+  using S = typename E::storage_t;
+  const int64_t block = blockIdx.x / col_wgs;
+  const int64_t v0 = block * kEmbRows;
+  const int lane = threadIdx.x & 63;
+  const int sub = threadIdx.x / a.tpr;
+  const EmbCols cols(a.d, blockIdx.x % col_wgs, threadIdx.x % a.tpr, a.tpr, W);
   const int rows = static_cast<int>(min(static_cast<int64_t>(kEmbRows), a.vocab - v0));
-  __shared__ int start[kEmbRows + 1];
-  if (threadIdx.x <= static_cast<unsigned>(rows))
-    start[threadIdx.x] = emb_lower(a.key, a.n, v0 + threadIdx.x);
-  __syncthreads();
-  if (c >= a.d) return;
-  for (int r = 0; r < rows; ++r) {
-    const int b = start[r], e = start[r + 1];
-    if (b == e && a.beta == 1.f) continue;
-    float acc[W] = {};
-    if (e - b <= kEmbRun) {
-      emb_sum<E, W>(a, b, e, c, acc);
-    } else {
-      for (int chunk = b / kEmbRun; chunk <= (e - 1) / kEmbRun; ++chunk) {
-        const int slot = chunk * kEmbRun >= b ? 0 : 1;
-        const float* p = a.part + (static_cast<size_t>(chunk) * 2 + slot) * a.d + c;
-#pragma unroll
-        for (int k = 0; k < W; ++k) acc[k] += p[k];
+  const int lb = a.n == 0 ? 0 : a.begin[block], le = a.n == 0 ? 0 : a.begin[block + 1];
+  if (W == 4 && lb == le && a.beta == 0.f) {   // no token here: one contiguous stretch of zeros
+    float* o = a.grad + v0 * a.d;
+    const int64_t n4 = static_cast<int64_t>(rows) * a.d / 4;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x % col_wgs) * 256 + threadIdx.x; i < n4; i += 256 * col_wgs)
+      gst_stream(o + 4 * i, make_uint4(0, 0, 0, 0));
+    return;
+  }
+  const bool held = le - lb <= 64;
+  const uint32_t key = held && lb + lane < le ? a.key[lb + lane] : 0xffffffffu;
+  const uint32_t pos = held && lb + lane < le ? a.pos[lb + lane] : 0;
+  for (int r = sub; r < rows; r += 256 / a.tpr) {   // one row per wave: every branch is uniform
+    const uint32_t v = static_cast<uint32_t>(v0 + r);
+    int b = lb, e = lb;
+    if (le > lb) {
+      if (held) {
+        b = lb + __popcll(__ballot(key < v));
+        e = lb + __popcll(__ballot(key <= v));
+      } else {
+        b = emb_lower(a.key, lb, le, v);
+        e = emb_lower(a.key, b, le, static_cast<int64_t>(v) + 1);
       }
     }
-    float* o = a.grad + (v0 + r) * a.d + c;
-    if constexpr (W == 8) {
-      float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
+    if (b == e && a.beta == 1.f) continue;
+    float acc[kEmbGroups][W] = {};
+    if (e - b > kEmbRun) {   // partial rows of the chunks it meets
+      emb_sum<ElemF32, W, kEmbFlight>(
+          b / kEmbRun, (e - 1) / kEmbRun + 1, cols,
+          [&](int i) { return a.part + (static_cast<size_t>(i) * 2 + (i * kEmbRun >= b ? 0 : 1)) * a.d; }, acc);
+    } else if (e > b) {
+      emb_sum<E, W, kEmbFlight>(
+          b, e, cols,
+          [&](int i) {
+            const uint32_t at = held ? static_cast<uint32_t>(__shfl(pos, i - lb, 64)) : a.pos[i];
+            return static_cast<const S*>(a.dy) + static_cast<int64_t>(at) * a.ld;
+          },
+          acc);
+    }
+    float* o = a.grad + (v0 + r) * a.d;
+#pragma unroll
+    for (int q = 0; q < kEmbGroups; ++q) {
+      if (!cols.on[q]) continue;
+      float* oq = o + cols.c[q];
+      float out[W] = {};
       if (a.beta != 0.f) {
-        x = gld<float4>(o);
-        y = gld<float4>(o + 4);
-        x = make_float4(a.beta * x.x, a.beta * x.y, a.beta * x.z, a.beta * x.w);
-        y = make_float4(a.beta * y.x, a.beta * y.y, a.beta * y.z, a.beta * y.w);
+        EmbRaw<ElemF32, W> old;
+        old.load(oq);
+        old.get(out);
       }
-      gst<float4>(o, make_float4(fmaf(a.scale, acc[0], x.x), fmaf(a.scale, acc[1], x.y),
-                                 fmaf(a.scale, acc[2], x.z), fmaf(a.scale, acc[3], x.w)));
-      gst<float4>(o + 4, make_float4(fmaf(a.scale, acc[4], y.x), fmaf(a.scale, acc[5], y.y),
-                                     fmaf(a.scale, acc[6], y.z), fmaf(a.scale, acc[7], y.w)));
-    } else {
-      *o = fmaf(a.scale, acc[0], a.beta == 0.f ? 0.f : a.beta * *o);
+#pragma unroll
+      for (int x = 0; x < W; ++x) out[x] = fmaf(a.scale, acc[q][x], a.beta != 0.f ? a.beta * out[x] : 0.f);
+      if constexpr (W == 4)
+        gst_stream(oq, make_uint4(__float_as_uint(out[0]), __float_as_uint(out[1]), __float_as_uint(out[2]),
+                                  __float_as_uint(out[3])));
+      else
+        gst<float>(oq, out[0]);
     }
   }
 }

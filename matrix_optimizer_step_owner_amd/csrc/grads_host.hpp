@@ -385,7 +385,7 @@ mfsdp_status_t embedding_impl(const void* table, mfsdp_dtype_t table_dtype, int6
 // Workspace of an embedding gradient: two (key, position) lists, the digit
 // counts of the sort and the partial rows of long runs.
 struct EmbPlan {
-  size_t key0, pos0, key1, pos1, hist, part, total;
+  size_t key0, pos0, key1, pos1, hist, begin, part, total;
   int32_t key_bits, bits, passes, per_block, blocks;
 };
 
@@ -414,6 +414,7 @@ EmbPlan emb_plan(int64_t n, int64_t vocab, int64_t d) {
   p.key1 = take(list);
   p.pos1 = take(list);
   p.hist = take(p.blocks > 1 ? (static_cast<size_t>(p.blocks) << p.bits) * 4 : 0);
+  p.begin = take((static_cast<size_t>(vocab + kEmbRows - 1) / kEmbRows + 1) * 4);
   p.part = take(n > kEmbRun ? static_cast<size_t>((n + kEmbRun - 1) / kEmbRun) * 2 * d * 4 : 0);
   p.total = off;
   return p;
@@ -430,20 +431,20 @@ mfsdp_status_t emb_grad_sizes(int64_t n_tokens, int64_t vocab, int64_t d) {
 
 template <class E, int W>
 hipError_t launch_emb_sums(const EmbGradArgs& a, hipStream_t stream) {
-  const int64_t col_wgs = (a.d / W + 255) / 256;
-  hipError_t e = hipSuccess;
-  if (a.n > kEmbRun) {
-    const int64_t blocks = (a.n + kEmbRun - 1) / kEmbRun * col_wgs;
-    e = launch(MFSDP_KERNEL_EMBED_GRAD, stream, [&] {
+  const int64_t col_wgs = ceil_div(a.d, static_cast<int64_t>(a.tpr) * W * kEmbGroups);
+  const int64_t row_blocks = ceil_div(a.vocab, kEmbRows);
+  if (a.n > 0) {   // partial sums of long runs (if there can be any), row block bounds
+    const int64_t chunks = a.n > kEmbRun ? ceil_div(a.n, kEmbRun) : 0;
+    const int64_t blocks = chunks * col_wgs + ceil_div(row_blocks + 1, 256);
+    const hipError_t e = launch(MFSDP_KERNEL_EMBED_GRAD, stream, [&] {
       emb_partial_kernel<E, W><<<dim3(static_cast<unsigned>(blocks)), dim3(256), 0, stream>>>(
-          a, static_cast<int>(col_wgs));
+          a, static_cast<int>(chunks), static_cast<int>(col_wgs));
     });
     if (e != hipSuccess) return e;
   }
-  const int64_t blocks = (a.vocab + kEmbRows - 1) / kEmbRows * col_wgs;
   return launch(MFSDP_KERNEL_EMBED_GRAD, stream, [&] {
-    emb_rows_kernel<E, W><<<dim3(static_cast<unsigned>(blocks)), dim3(256), 0, stream>>>(
-        a, static_cast<int>(col_wgs));
+    emb_rows_kernel<E, W><<<dim3(static_cast<unsigned>(row_blocks * col_wgs)), dim3(256), 0,
+                            stream>>>(a, static_cast<int>(col_wgs));
   });
 }
 
@@ -485,11 +486,13 @@ mfsdp_status_t embedding_grad_impl(const void* dy, int64_t ld, mfsdp_dtype_t dty
     st = check_outputs(outs, ins);
     if (st != MFSDP_OK) return st;
   }
-  const bool vec = d % 8 == 0 && aligned(grad, 16) && aligned(dy, 16) &&
-                   (ld * static_cast<int64_t>(es)) % 16 == 0;
-  const int64_t col_wgs = ((vec ? d / 8 : d) + 255) / 256;
-  if ((vocab + kEmbRows - 1) / kEmbRows * col_wgs >= (int64_t(1) << 31) ||
-      (n_tokens + kEmbRun - 1) / kEmbRun * col_wgs >= (int64_t(1) << 31))
+  const bool vec = d % 4 == 0 && aligned(grad, 16) && aligned(dy, 4 * es) && ld % 4 == 0;
+  const int64_t cols = vec ? 4 : 1;
+  int32_t tpr = 64;
+  while (tpr < 256 && tpr * cols * kEmbGroups < d) tpr *= 2;
+  const int64_t col_wgs = ceil_div(d, tpr * cols * kEmbGroups);
+  if (ceil_div(vocab, kEmbRows) * col_wgs > kGroupBlocksMax ||
+      ceil_div(n_tokens, kEmbRun) * col_wgs + ceil_div(vocab, kEmbRows) / 256 + 2 > kGroupBlocksMax)
     return fail(MFSDP_ERR_UNSUPPORTED, "too many rows");
 
   char* ws = static_cast<char*>(workspace);
@@ -500,6 +503,7 @@ mfsdp_status_t embedding_grad_impl(const void* dy, int64_t ld, mfsdp_dtype_t dty
   a.ld = ld;
   a.n = static_cast<int32_t>(n_tokens);
   a.d = static_cast<int32_t>(d);
+  a.tpr = tpr;
   a.scale = scale;
   a.beta = beta;
   hipError_t e = hipSuccess;
@@ -508,7 +512,6 @@ mfsdp_status_t embedding_grad_impl(const void* dy, int64_t ld, mfsdp_dtype_t dty
     uint32_t* pos[2] = {reinterpret_cast<uint32_t*>(ws + p.pos0), reinterpret_cast<uint32_t*>(ws + p.pos1)};
     SortArgs s{};
     s.tokens = tokens;
-    s.hist = reinterpret_cast<uint32_t*>(ws + p.hist);
     s.vocab = vocab;
     s.n = a.n;
     s.tok64 = token_bytes == 8;
@@ -528,6 +531,8 @@ mfsdp_status_t embedding_grad_impl(const void* dy, int64_t ld, mfsdp_dtype_t dty
         sort_small_kernel<<<dim3(1), dim3(kSortThreads), 0, stream>>>(sm);
       });
     } else {
+      const dim3 grid(static_cast<unsigned>(p.blocks)), wg(kSortThreads);
+      s.hist = reinterpret_cast<uint32_t*>(ws + p.hist);
       for (int q = 0; q < p.passes && e == hipSuccess; ++q) {
         s.first = q == 0;
         s.shift = q * p.bits;
@@ -536,7 +541,6 @@ mfsdp_status_t embedding_grad_impl(const void* dy, int64_t ld, mfsdp_dtype_t dty
         at ^= 1;
         s.key_out = key[at];
         s.pos_out = pos[at];
-        const dim3 grid(static_cast<unsigned>(p.blocks)), wg(kSortThreads);
         e = launch(MFSDP_KERNEL_EMBED_GRAD, stream,
                    [&] { sort_hist_kernel<<<grid, wg, 0, stream>>>(s); });
         if (e == hipSuccess)
@@ -548,11 +552,12 @@ mfsdp_status_t embedding_grad_impl(const void* dy, int64_t ld, mfsdp_dtype_t dty
     a.key = key[at];
     a.pos = pos[at];
     a.part = reinterpret_cast<float*>(ws + p.part);
+    a.begin = reinterpret_cast<int32_t*>(ws + p.begin);
   }
   if (dtype == MFSDP_DTYPE_BF16)
-    e = vec ? launch_emb_sums<ElemBF16, 8>(a, stream) : launch_emb_sums<ElemBF16, 1>(a, stream);
+    e = vec ? launch_emb_sums<ElemBF16, 4>(a, stream) : launch_emb_sums<ElemBF16, 1>(a, stream);
   else
-    e = vec ? launch_emb_sums<ElemF32, 8>(a, stream) : launch_emb_sums<ElemF32, 1>(a, stream);
+    e = vec ? launch_emb_sums<ElemF32, 4>(a, stream) : launch_emb_sums<ElemF32, 1>(a, stream);
   if (e != hipSuccess)
     return fail(MFSDP_ERR_HIP, "embedding gradient launch: %s", hipGetErrorString(e));
   return MFSDP_OK;

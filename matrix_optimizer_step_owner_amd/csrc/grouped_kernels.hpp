@@ -301,7 +301,7 @@ __global__ __launch_bounds__(C::THREADS, 2) void grouped_tile_kernel(GroupArgs g
   constexpr int kStage = CKPT ? C::BP * ROW + kQCodes : C::STAGE_BYTES;
   constexpr int kStagesEnd = C::STAGES * kStage;
   constexpr int kQPanel = C::BQ * ROW;
-  constexpr int kScaleCols = C::BQ / kCkptBlock;
+  constexpr int kScaleCols = C::BQ < kCkptBlock ? 1 : C::BQ / kCkptBlock;
   constexpr int kScaleGroup = kCkptSteps * 32 * kScaleCols;  // floats
   constexpr int kLds = CKPT ? kStagesEnd + 2 * kQPanel + 2 * kScaleGroup * 4 : kStagesEnd;
   constexpr int QPW = CKPT ? kQCodes / 1024 / C::WAVES : C::QP;   // DMA pieces per wave
