@@ -52,14 +52,15 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // Workgroups of one launch with tiles of bp x bq.
 int64_t group_blocks(const GroupArgs& g, int mode, int bp, int bq) {
+  if (mode == kGroupWgrad && g.part_rows > 0)
+    return group_tiles_max(g.rows, g.experts, g.part_rows) * ceil_div(g.n, bp) * ceil_div(g.k, bq);
   if (mode == kGroupWgrad) return WgradOrder(g.n, g.k, bp, bq).blocks(g.experts);
   return group_tiles_max(g.rows, g.experts, bp) * ceil_div(mode == kGroupFwd ? g.n : g.k, bq);
 }
 
 template <class E, int MODE, class C, int LOAD>
 hipError_t launch_tile(const GroupArgs& g, hipStream_t stream) {
-  const dim3 grid(static_cast<unsigned>(group_blocks(g, MODE, C::BP, C::BQ)),
-                  MODE == kGroupWgrad ? g.splits : 1);
+  const dim3 grid(static_cast<unsigned>(group_blocks(g, MODE, C::BP, C::BQ)));
   return launch(MFSDP_KERNEL_GROUPED, stream, [&] {
     grouped_tile_kernel<E, MODE, C, LOAD><<<grid, dim3(C::THREADS), 0, stream>>>(g);
   });
@@ -76,32 +77,50 @@ using TileRows = GroupTile<32, 64, 1, 2, 4, 3, 4>;        // two workgroups per 
 using TileRowsReg = GroupTile<32, 64, 1, 2, 4, 2, 4>;
 using TileF32 = GroupTile<128, 128, 2, 2, 1, 4>;
 
-// Weight gradients with too few 256 x 256 tiles for the 256 CUs take 128 x 128
-// ones, and where those are too few for two per CU each segment is cut into
-// parts of 256 rows or more that a second kernel sums.
-bool wgrad_large(int64_t experts, int64_t n, int64_t k) {
-  return experts * ceil_div(n, 256) * ceil_div(k, 256) >= 192;
-}
+// Weight gradients: 256 x 256 tiles where n and k fill them and there are
+// enough for the 256 CUs, or where long segments can be cut into enough parts;
+// 128 x 128 tiles otherwise, two workgroups per CU.  Parts have a fixed number
+// of rows, so that experts of different lengths give equal work; a second
+// kernel sums them.  The choice depends on the sizes alone.
+struct WgradPlan {
+  bool large;
+  int32_t part_rows;   // 0: whole segments
+  size_t bytes;        // of the parts
+};
 
-int wgrad_splits(int64_t experts, int64_t rows, int64_t n, int64_t k, bool bf) {
-  if (experts == 0 || (bf && wgrad_large(experts, n, k))) return 1;
-  const int64_t tiles = experts * ceil_div(n, 128) * ceil_div(k, 128);
-  return static_cast<int>(
-      std::max<int64_t>(1, std::min<int64_t>({512 / tiles, rows / experts / 256, 16})));
+WgradPlan wgrad_plan(int64_t experts, int64_t rows, int64_t n, int64_t k, bool bf) {
+  WgradPlan p{};
+  if (experts == 0) return p;
+  const int64_t large = ceil_div(n, 256) * ceil_div(k, 256);
+  const int64_t square = ceil_div(n, 128) * ceil_div(k, 128);
+  p.large = bf && experts * large >= 192;
+  if (p.large || rows == 0) return p;
+  // a part: as many rows as leave two 128 x 128 tiles (one 256 x 256) per CU,
+  // each expert's last part, which is not full, among them; and enough rows to
+  // be worth its sum
+  const bool wide = bf && n >= 256 && k >= 256;
+  const int64_t tiles = wide ? large : square;
+  const int64_t room = wide ? 256 : 512, want = std::max(room - experts * tiles, room / 4);
+  const int64_t len = std::max<int64_t>(bf ? 128 : 64, round_up(ceil_div(rows * tiles, want), 64));
+  if (rows < len * experts * 5 / 4) return p;
+  p.large = wide;
+  p.part_rows = static_cast<int32_t>(len);
+  p.bytes = static_cast<size_t>(group_tiles_max(rows, experts, len)) * n * k * 4;
+  return p;
 }
 
 template <class E, int LOAD>
-hipError_t launch_wgrad(const GroupArgs& g, hipStream_t stream) {
+hipError_t launch_wgrad(const GroupArgs& g, bool large, hipStream_t stream) {
   hipError_t e;
   if constexpr (LOAD == kLoadReg || LOAD == kLoadRegCkpt)
     e = launch_tile<E, kGroupWgrad, TileSquare, LOAD>(g, stream);
   else if constexpr (E::kVec == 4)
     e = launch_tile<E, kGroupWgrad, TileF32, LOAD>(g, stream);
   else
-    e = wgrad_large(g.experts, g.n, g.k)
+    e = large
             ? launch_tile<E, kGroupWgrad, TileWgrad, LOAD>(g, stream)
             : launch_tile<E, kGroupWgrad, TileWgradSquare, LOAD>(g, stream);
-  if (e != hipSuccess || g.splits <= 1) return e;
+  if (e != hipSuccess || g.part_rows == 0) return e;
   const int64_t per = ceil_div(static_cast<int64_t>(g.n) * g.k, 2048);
   const dim3 grid(static_cast<unsigned>(g.experts * per));
   return launch(MFSDP_KERNEL_GROUPED, stream, [&] {
@@ -145,13 +164,13 @@ hipError_t launch_rows(const GroupArgs& g, bool dma, hipStream_t stream) {
 }
 
 template <class E>
-hipError_t launch_grouped(int mode, const GroupArgs& g, bool dma, hipStream_t stream) {
+hipError_t launch_grouped(int mode, const GroupArgs& g, bool dma, bool large, hipStream_t stream) {
   if (mode == kGroupFwd) return launch_rows<E, kGroupFwd>(g, dma, stream);
   if (mode == kGroupDgrad) return launch_rows<E, kGroupDgrad>(g, dma, stream);
-  if (!g.qs) return dma ? launch_wgrad<E, kLoadDma>(g, stream) : launch_wgrad<E, kLoadReg>(g, stream);
+  if (!g.qs) return dma ? launch_wgrad<E, kLoadDma>(g, large, stream) : launch_wgrad<E, kLoadReg>(g, large, stream);
   if constexpr (E::kVec == 8)
-    if (dma) return launch_wgrad<E, kLoadDmaCkpt>(g, stream);
-  return launch_wgrad<E, kLoadRegCkpt>(g, stream);
+    if (dma) return launch_wgrad<E, kLoadDmaCkpt>(g, large, stream);
+  return launch_wgrad<E, kLoadRegCkpt>(g, large, stream);
 }
 
 mfsdp_status_t grouped_sizes(int64_t experts, int64_t rows, int64_t n, int64_t k,
@@ -192,8 +211,8 @@ mfsdp_status_t grouped_impl(int mode, const void* p, int64_t ldp, const void* q,
   if (!aligned(p, es) || (!qs && !aligned(q, es)) || !aligned(out, eo) || !aligned(offsets, 4))
     return fail(MFSDP_ERR_INVALID_ARGUMENT, "a buffer is not aligned to its elements");
   const bool bf = dtype == MFSDP_DTYPE_BF16;
-  const int splits = mode == kGroupWgrad ? wgrad_splits(experts, rows, n, k, bf) : 1;
-  const size_t need = splits > 1 ? static_cast<size_t>(splits) * experts * n * k * 4 : 0;
+  const WgradPlan plan = mode == kGroupWgrad ? wgrad_plan(experts, rows, n, k, bf) : WgradPlan{};
+  const size_t need = plan.bytes;
   if (need) {
     if (!workspace) return fail(MFSDP_ERR_WORKSPACE, "workspace is null");
     if (!aligned(workspace, kWsAlign))
@@ -236,7 +255,7 @@ mfsdp_status_t grouped_impl(int mode, const void* p, int64_t ldp, const void* q,
   g.k = static_cast<int32_t>(k);
   g.beta = beta;
   g.out_f32 = out_dtype == MFSDP_DTYPE_F32 ? 1 : 0;
-  g.splits = splits;
+  g.part_rows = plan.part_rows;
   g.part = static_cast<float*>(workspace);
 
   // the smallest tiles
@@ -249,8 +268,8 @@ mfsdp_status_t grouped_impl(int mode, const void* p, int64_t ldp, const void* q,
   const bool dma = (!qs || (bf && k % 16 == 0)) && aligned(p, 16) && aligned(q, 16) && k % v == 0 &&
                    (n % v == 0 || mode == kGroupFwd) && ldp % v == 0 && ldq % v == 0 &&
                    std::max({n, k, ldp, ldq}) * static_cast<int64_t>(es) < (int64_t(1) << 23);
-  const hipError_t e = bf ? launch_grouped<ElemBF16>(mode, g, dma, stream)
-                          : launch_grouped<ElemF32>(mode, g, dma, stream);
+  const hipError_t e = bf ? launch_grouped<ElemBF16>(mode, g, dma, plan.large, stream)
+                          : launch_grouped<ElemF32>(mode, g, dma, plan.large, stream);
   if (e != hipSuccess) return fail(MFSDP_ERR_HIP, "grouped launch: %s", hipGetErrorString(e));
   return MFSDP_OK;
 }
@@ -605,8 +624,7 @@ mfsdp_status_t mfsdp_grouped_linear_wgrad_workspace_size(int64_t n_experts, int6
     if (!out_bytes) return fail(MFSDP_ERR_INVALID_ARGUMENT, "out_bytes is null");
     const mfsdp_status_t st = grouped_sizes(n_experts, rows, n, k, dtype);
     if (st != MFSDP_OK) return st;
-    const int splits = wgrad_splits(n_experts, rows, n, k, dtype == MFSDP_DTYPE_BF16);
-    *out_bytes = splits > 1 ? static_cast<size_t>(splits) * n_experts * n * k * 4 : 0;
+    *out_bytes = wgrad_plan(n_experts, rows, n, k, dtype == MFSDP_DTYPE_BF16).bytes;
     return MFSDP_OK;
   });
 }

@@ -30,8 +30,8 @@ struct GroupArgs {
   int32_t n, k;
   float beta;            // wgrad
   int32_t out_f32;       // wgrad: dW is fp32 whatever the operands' type
-  int32_t splits;        // wgrad: parts of each segment (blockIdx.y), summed by a second kernel
-  float* part;           // wgrad with splits > 1: [splits][experts][n][k]
+  int32_t part_rows;     // wgrad: segments are cut into parts of so many rows, 0: they are not
+  float* part;           // wgrad in parts: [parts][n][k], summed by a second kernel
 };
 
 // Columns of an activation row that share one checkpoint scale.
@@ -62,8 +62,14 @@ __device__ __forceinline__ void group_segment(const GroupArgs& g, int e, int& lo
 // together share weight panels.
 constexpr int kGroupBand = 8;
 
-__device__ __forceinline__ bool group_find(const GroupArgs& g, int b, int bp, int nq, int& expert,
-                                           int& ti, int& tj) {
+struct GroupSpan {
+  int expert;   // whose tile it is
+  int local;    // tile number within the expert
+  int rows;     // row tiles of the expert
+  int first;    // row tiles of the experts before it
+};
+
+__device__ __forceinline__ bool group_span(const GroupArgs& g, int b, int bp, int nq, GroupSpan& out) {
   const int lane = threadIdx.x & 63;
   const int c = (g.experts + 63) >> 6;
   const int e0 = min(lane * c, g.experts), e1 = min(e0 + c, g.experts);
@@ -82,28 +88,38 @@ __device__ __forceinline__ bool group_find(const GroupArgs& g, int b, int bp, in
   const int total = __builtin_amdgcn_readlane(incl, 63) * nq;
   if (b >= total) return false;
   const int want = xcd_remap(b, total);
-  int at = (incl - sum) * nq;
-  int fe = -1, fl = 0, fr = 0;
-  if (want >= at && want < incl * nq) {
+  int at = incl - sum;
+  int fe = -1, fl = 0, fr = 0, ff = 0;
+  if (want >= at * nq && want < incl * nq) {
     for (int e = e0; e < e1; ++e) {
       int lo, hi;
       group_segment(g, e, lo, hi);
       const int np = (hi - lo + bp - 1) / bp;
-      if (want < at + np * nq) {
+      if (want < (at + np) * nq) {
         fe = e;
-        fl = want - at;
+        fl = want - at * nq;
         fr = np;
+        ff = at;
         break;
       }
-      at += np * nq;
+      at += np;
     }
   }
   const int src = __builtin_ctzll(__ballot(fe >= 0));
-  expert = __builtin_amdgcn_readlane(fe, src);
-  const int local = __builtin_amdgcn_readlane(fl, src);
-  const int np = __builtin_amdgcn_readlane(fr, src);
-  const int band = local / (kGroupBand * nq), r = local - band * (kGroupBand * nq);
-  const int in_band = min(kGroupBand, np - band * kGroupBand);
+  out.expert = __builtin_amdgcn_readlane(fe, src);
+  out.local = __builtin_amdgcn_readlane(fl, src);
+  out.rows = __builtin_amdgcn_readlane(fr, src);
+  out.first = __builtin_amdgcn_readlane(ff, src);
+  return true;
+}
+
+__device__ __forceinline__ bool group_find(const GroupArgs& g, int b, int bp, int nq, int& expert,
+                                           int& ti, int& tj) {
+  GroupSpan s;
+  if (!group_span(g, b, bp, nq, s)) return false;
+  expert = s.expert;
+  const int band = s.local / (kGroupBand * nq), r = s.local - band * (kGroupBand * nq);
+  const int in_band = min(kGroupBand, s.rows - band * kGroupBand);
   ti = band * kGroupBand + r % in_band;
   tj = r / in_band;
   return true;
@@ -118,9 +134,10 @@ __device__ __forceinline__ int acc_q(int r, int lhalf) { return (r >> 2) * 8 + l
 // step is 64 * U bytes of t per row (32 U bf16, 16 U fp32), 2 U sub-steps of
 // one MFMA depth, kept in STAGES LDS buffers.  KS > 1: KS such sets of waves
 // share a step's sub-steps, and their sums are added at the end.
-template <int BP_, int BQ_, int WP_, int WQ_, int U_, int STAGES_, int KS_ = 1>
+template <int BP_, int BQ_, int WP_, int WQ_, int U_, int STAGES_, int KS_ = 1, int OCC_ = 2>
 struct GroupTile {
   static constexpr int BP = BP_, BQ = BQ_, WP = WP_, WQ = WQ_, U = U_, STAGES = STAGES_, KS = KS_;
+  static constexpr int OCC = OCC_;   // waves per SIMD that registers must leave room for
   static constexpr int WAVES = WP * WQ * KS, THREADS = 64 * WAVES;
   static constexpr int TP = BP / WP / 32, TQ = BQ / WQ / 32;
   static constexpr int SLOTS = TP * TQ;              // MFMA blocks per wave and sub-step
@@ -232,11 +249,6 @@ __device__ __forceinline__ int tswz(int kk) {
   return B >= 128 ? 4 * (kk & 3) : 4 * ((kk >> 1) & 1);
 }
 
-// Rows of one part of a split segment of R rows: whole 64-row groups.
-__device__ __forceinline__ int split_rows(int R, int splits) {
-  return ((R + splits - 1) / splits + 63) & ~63;
-}
-
 // Which (expert, row tile, column tile) workgroup b of a weight gradient takes.
 // Tiles of one expert go in chunks of up to 32 (a band of eight by four, which
 // share panels) to the XCDs in turn: experts differ in length, and an XCD
@@ -272,6 +284,25 @@ __device__ __forceinline__ bool wgrad_find(const GroupArgs& g, int b, int bp, in
   return true;
 }
 
+// The same where segments are cut into parts of g.part_rows rows: workgroup b
+// takes tile b' % tiles of part b' / tiles, parts counted over all experts, and
+// b' dealt so that an XCD runs neighbours.  `part` is the part's number over
+// all experts, lo and hi its rows.
+__device__ __forceinline__ bool wgrad_find_part(const GroupArgs& g, int b, int bp, int bq, int& part,
+                                                int& lo, int& hi, int& ti, int& tj) {
+  const int tq = (g.k + bq - 1) / bq, tiles = (g.n + bp - 1) / bp * tq;
+  GroupSpan s;
+  if (!group_span(g, b, g.part_rows, tiles, s)) return false;
+  part = s.first + s.local / tiles;
+  const int tile = s.local % tiles;
+  ti = tile / tq;
+  tj = tile % tq;
+  group_segment(g, s.expert, lo, hi);
+  lo += s.local / tiles * g.part_rows;
+  hi = min(hi, lo + g.part_rows);
+  return true;
+}
+
 // CKPT: Q is the int8 checkpoint of X.  Its codes arrive by DMA one step ahead
 // of P, 32 rows of BQ bytes per step, and while step t is multiplied every
 // thread turns 16 codes of step t + 1 into bf16 (exact: seven bits of
@@ -282,7 +313,7 @@ __device__ __forceinline__ bool wgrad_find(const GroupArgs& g, int b, int bp, in
 constexpr int kCkptSteps = 16;
 
 template <class E, int MODE, class C, int LOAD>
-__global__ __launch_bounds__(C::THREADS, 2) void grouped_tile_kernel(GroupArgs g) {
+__global__ __launch_bounds__(C::THREADS, C::OCC) void grouped_tile_kernel(GroupArgs g) {
   constexpr bool CKPT = LOAD == kLoadDmaCkpt;
   constexpr bool kReg = LOAD == kLoadReg || LOAD == kLoadRegCkpt;
   constexpr bool kCodes = LOAD == kLoadDmaCkpt || LOAD == kLoadRegCkpt;
@@ -319,21 +350,18 @@ __global__ __launch_bounds__(C::THREADS, 2) void grouped_tile_kernel(GroupArgs g
 
   // ---- tile and operands ----------------------------------------------------
   int e, ti, tj, lo, hi;
-  if (MODE == kGroupWgrad) {
-    if (!wgrad_find(g, blockIdx.x, C::BP, C::BQ, e, ti, tj)) return;
-  } else {
-    const int nq = ((MODE == kGroupFwd ? g.n : g.k) + C::BQ - 1) / C::BQ;
-    if (!group_find(g, blockIdx.x, C::BP, nq, e, ti, tj)) return;
-  }
-  group_segment(g, e, lo, hi);
   const size_t wsize = static_cast<size_t>(g.n) * g.k;
-  const bool split = MODE == kGroupWgrad && g.splits > 1;
-  if (split) {   // this workgroup's part of the segment; the sum skips empty parts
-    const int len = split_rows(hi - lo, g.splits);
-    const int64_t at = static_cast<int64_t>(lo) + static_cast<int64_t>(len) * blockIdx.y;
-    if (at >= hi) return;
-    lo = static_cast<int>(at);
-    hi = min(lo + len, hi);
+  const bool split = MODE == kGroupWgrad && g.part_rows > 0;
+  if (split) {
+    if (!wgrad_find_part(g, blockIdx.x, C::BP, C::BQ, e, lo, hi, ti, tj)) return;   // e: the part
+  } else {
+    if (MODE == kGroupWgrad) {
+      if (!wgrad_find(g, blockIdx.x, C::BP, C::BQ, e, ti, tj)) return;
+    } else {
+      const int nq = ((MODE == kGroupFwd ? g.n : g.k) + C::BQ - 1) / C::BQ;
+      if (!group_find(g, blockIdx.x, C::BP, nq, e, ti, tj)) return;
+    }
+    group_segment(g, e, lo, hi);
   }
   const int p0 = ti * C::BP, q0 = tj * C::BQ;
   const S* P = static_cast<const S*>(g.p) + lo * g.ldp;
@@ -774,7 +802,7 @@ __global__ __launch_bounds__(C::THREADS, 2) void grouped_tile_kernel(GroupArgs g
   int64_t ldo;
   if (MODE == kGroupWgrad) {
     ldo = g.k;
-    out = split ? reinterpret_cast<char*>(g.part + blockIdx.y * (g.experts * wsize)) : static_cast<char*>(g.out);
+    out = split ? reinterpret_cast<char*>(g.part) : static_cast<char*>(g.out);
     out += (e * wsize + p0 * ldo + q0) * (out_f32 ? 4 : 2);
   } else {
     ldo = g.ldo;
@@ -867,28 +895,36 @@ __global__ __launch_bounds__(C::THREADS, 2) void grouped_tile_kernel(GroupArgs g
   }
 }
 
-// Sum of the parts of a split weight gradient, in their order:
+// Sum of the parts of each expert's weight gradient, in their order:
 // dW = beta dW + sum_s part[s].  One workgroup takes 2048 elements of one
-// expert; a part past the end of the segment was not written and is not read.
+// expert.
 template <class EO>
 __global__ __launch_bounds__(256) void grouped_sum_kernel(GroupArgs g, int per_expert) {
   using O = typename EO::storage_t;
   const int e = blockIdx.x / per_expert;
   const size_t wsize = static_cast<size_t>(g.n) * g.k;
+  // parts of the experts before this one: each wave adds them up for itself
+  int first = 0;
+  for (int i = threadIdx.x & 63; i < e; i += 64) {
+    int lo, hi;
+    group_segment(g, i, lo, hi);
+    first += (hi - lo + g.part_rows - 1) / g.part_rows;
+  }
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) first += __shfl_xor(first, d, 64);
   int lo, hi;
   group_segment(g, e, lo, hi);
-  const int len = split_rows(hi - lo, g.splits);
-  const int parts = len > 0 ? (hi - lo + len - 1) / len : 0;
+  const int parts = (hi - lo + g.part_rows - 1) / g.part_rows;
   const size_t i = static_cast<size_t>(blockIdx.x % per_expert) * 2048 + threadIdx.x * 8;
   if (i >= wsize) return;
-  const size_t at = e * wsize + i, stride = g.experts * wsize;
-  O* out = static_cast<O*>(g.out) + at;
-  const float* part = g.part + at;
+  O* out = static_cast<O*>(g.out) + e * wsize + i;
+  const float* part = g.part + first * wsize + i;
   float v[8] = {};
   if (i + 8 <= wsize) {
+#pragma unroll 4
     for (int s = 0; s < parts; ++s) {
       float p[8];
-      load8_any<ElemF32>(part + s * stride, p);
+      load8_any<ElemF32>(part + s * wsize, p);
 #pragma unroll
       for (int k = 0; k < 8; ++k) v[k] += p[k];
     }
@@ -902,7 +938,7 @@ __global__ __launch_bounds__(256) void grouped_sum_kernel(GroupArgs g, int per_e
   } else {
     for (int k = 0; k < 8 && i + k < wsize; ++k) {
       float x = 0.f;
-      for (int s = 0; s < parts; ++s) x += part[s * stride + k];
+      for (int s = 0; s < parts; ++s) x += part[s * wsize + k];
       out[k] = EO::from_f32(g.beta != 0.f ? fmaf(g.beta, EO::to_f32(out[k]), x) : x);
     }
   }
