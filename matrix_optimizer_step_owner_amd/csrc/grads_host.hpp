@@ -257,7 +257,7 @@ mfsdp_status_t grouped_impl(int mode, const void* p, int64_t ldp, const void* q,
   g.out_f32 = out_dtype == MFSDP_DTYPE_F32 ? 1 : 0;
   g.part_rows = plan.part_rows;
   g.part = static_cast<float*>(workspace);
-
+  g.stream = aligned(out, 128) && (mode == kGroupWgrad ? k : ldo) * static_cast<int64_t>(eo) % 128 == 0;
   // the smallest tiles
   const int64_t blocks = mode == kGroupWgrad ? group_blocks(g, mode, 128, 128)
                                              : group_blocks(g, mode, 32, 64);

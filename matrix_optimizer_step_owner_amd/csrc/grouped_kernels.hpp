@@ -29,6 +29,7 @@ struct GroupArgs {
   int32_t experts, rows; // rows: rows of the activations (offsets are clamped to it)
   int32_t n, k;
   float beta;            // wgrad
+  int32_t stream;        // output rows are whole 128-byte lines
   int32_t out_f32;       // wgrad: dW is fp32 whatever the operands' type
   int32_t part_rows;     // wgrad: segments are cut into parts of so many rows, 0: they are not
   float* part;           // wgrad in parts: [parts][n][k], summed by a second kernel
@@ -114,10 +115,11 @@ __device__ __forceinline__ bool group_span(const GroupArgs& g, int b, int bp, in
 }
 
 __device__ __forceinline__ bool group_find(const GroupArgs& g, int b, int bp, int nq, int& expert,
-                                           int& ti, int& tj) {
+                                           int& ti, int& tj, bool& alone) {
   GroupSpan s;
   if (!group_span(g, b, bp, nq, s)) return false;
   expert = s.expert;
+  alone = s.rows == 1;
   const int band = s.local / (kGroupBand * nq), r = s.local - band * (kGroupBand * nq);
   const int in_band = min(kGroupBand, s.rows - band * kGroupBand);
   ti = band * kGroupBand + r % in_band;
@@ -188,7 +190,16 @@ __device__ __forceinline__ void store16_any(void* p, const uint4& v) {
   *(MFSDP_GLOBAL u32x4_el_t*)(p) = u32x4_t{v.x, v.y, v.z, v.w};
 }
 
-// load8 / store8 at any element.
+// Streamed store.  Outputs whose rows are whole 128-byte lines are streamed:
+// the weight gradients of 256 experts (403 MB) took 134 us with plain stores
+// and 107 us so, and products whose outputs fit the L2s measured the same
+// either way.  Others are not: lines that two workgroups share then reach HBM
+// in pieces (11 gradients of 6144 x 5608: 212 us plain, 367 us streamed).
+__device__ __forceinline__ void stream16_any(void* p, const uint4& v) {
+  __builtin_nontemporal_store(u32x4_t{v.x, v.y, v.z, v.w}, (MFSDP_GLOBAL u32x4_el_t*)(p));
+}
+
+// load8 and store8 at any element.
 template <class E>
 __device__ __forceinline__ void load8_any(const typename E::storage_t* p, float (&v)[8]) {
   Raw8 r;
@@ -230,6 +241,13 @@ __device__ __forceinline__ u32x4s_t dma_buffer(const char* base) {
 __device__ __forceinline__ void lds_dma16_buf(uint32_t lds, uint32_t voff, u32x4s_t buf) {
   const uint32_t ulds = static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(lds));
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+               :: "s"(ulds), "v"(voff), "s"(buf) : "memory", "m0");
+}
+
+// The same for data that no other workgroup reads (streamed).
+__device__ __forceinline__ void lds_dma16_buf_nt(uint32_t lds, uint32_t voff, u32x4s_t buf) {
+  const uint32_t ulds = static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(lds));
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen nt lds"
                :: "s"(ulds), "v"(voff), "s"(buf) : "memory", "m0");
 }
 
@@ -352,6 +370,12 @@ __global__ __launch_bounds__(C::THREADS, C::OCC) void grouped_tile_kernel(GroupA
   int e, ti, tj, lo, hi;
   const size_t wsize = static_cast<size_t>(g.n) * g.k;
   const bool split = MODE == kGroupWgrad && g.part_rows > 0;
+  // An expert with one row tile of few rows: its weights are read by this column
+  // of tiles alone, and streamed (eight 14336 x 4096 experts, 16 rows: 145 ->
+  // 131 us; not where a panel row is less than two lines, as in the input
+  // gradient: one expert there 36 -> 59 us).
+  constexpr bool kAlone = MODE == kGroupFwd && C::KS > 1;
+  bool alone = false;
   if (split) {
     if (!wgrad_find_part(g, blockIdx.x, C::BP, C::BQ, e, lo, hi, ti, tj)) return;   // e: the part
   } else {
@@ -359,7 +383,7 @@ __global__ __launch_bounds__(C::THREADS, C::OCC) void grouped_tile_kernel(GroupA
       if (!wgrad_find(g, blockIdx.x, C::BP, C::BQ, e, ti, tj)) return;
     } else {
       const int nq = ((MODE == kGroupFwd ? g.n : g.k) + C::BQ - 1) / C::BQ;
-      if (!group_find(g, blockIdx.x, C::BP, nq, e, ti, tj)) return;
+      if (!group_find(g, blockIdx.x, C::BP, nq, e, ti, tj, alone)) return;
     }
     group_segment(g, e, lo, hi);
   }
@@ -438,8 +462,11 @@ __global__ __launch_bounds__(C::THREADS, C::OCC) void grouped_tile_kernel(GroupA
     uint32_t at = lds0 + stage;
     if (CKPT && !is_p) at = lds0 + (stage + kStage == kStagesEnd ? 0 : stage + kStage);
     at += is_p ? (wave * C::PP + q) * 1024 : C::BP * ROW + (wave * QPW + q - C::PP) * 1024;
-    lds_dma16_buf(at, klim[q] < (is_p ? left : qleft) ? voff[q] : kDmaNone,
-                  dma_buffer(is_p ? pbase : qbase));
+    const uint32_t off = klim[q] < (is_p ? left : qleft) ? voff[q] : kDmaNone;
+    if (kAlone && !is_p && alone)
+      lds_dma16_buf_nt(at, off, dma_buffer(qbase));
+    else
+      lds_dma16_buf(at, off, dma_buffer(is_p ? pbase : qbase));
   };
   auto dma_next = [&] {
     pbase += pstep;
@@ -808,91 +835,95 @@ __global__ __launch_bounds__(C::THREADS, C::OCC) void grouped_tile_kernel(GroupA
     ldo = g.ldo;
     out = static_cast<char*>(g.out) + ((lo + p0) * ldo + q0) * static_cast<int64_t>(sizeof(S));
   }
-  constexpr int GROUPS = COLS / 8;          // 8-column groups per row
-  constexpr int RPP = 64 / GROUPS;          // rows per pass of a wave
-  if (!f32) {
-    constexpr int PITCH = COLS * 2 + 16;
-    char* mine = lds + (C::KS > 1 ? kLds / 2 : 0) + tw * (32 * PITCH);
-    static_assert(kTileWaves * 32 * PITCH <= kLds, "staging fits");
+  // stream_c: whether stores are streamed.  Two copies of the loops, chosen once:
+  // the compiler would merge two stores that differ in that alone.
+  auto write = [&](auto stream_c) {
+    constexpr bool kStream = decltype(stream_c)::value;
+    if (!f32) {
+      constexpr int GROUPS = COLS / 8;          // 16-byte pieces per row
+      constexpr int RPP = 64 / GROUPS;          // rows per pass of a wave
+      constexpr int PITCH = COLS * 2 + 16;
+      char* mine = lds + (C::KS > 1 ? kLds / 2 : 0) + tw * (32 * PITCH);
+      static_assert(kTileWaves * 32 * PITCH <= kLds, "staging fits");
 #pragma unroll
-    for (int i = 0; i < TP; ++i) {
+      for (int i = 0; i < TP; ++i) {
 #pragma unroll
-      for (int j = 0; j < TQ; ++j)
+        for (int j = 0; j < TQ; ++j)
 #pragma unroll
-        for (int r = 0; r < 16; r += 4)
-          *reinterpret_cast<uint2*>(mine + lrow * PITCH + (j * 32 + acc_q(r, lhalf)) * 2) =
-              make_uint2(pack_bf16x2(acc[i][j][r], acc[i][j][r + 1]), pack_bf16x2(acc[i][j][r + 2], acc[i][j][r + 3]));
+          for (int r = 0; r < 16; r += 4)
+            *reinterpret_cast<uint2*>(mine + lrow * PITCH + (j * 32 + acc_q(r, lhalf)) * 2) =
+                make_uint2(pack_bf16x2(acc[i][j][r], acc[i][j][r + 1]), pack_bf16x2(acc[i][j][r + 2], acc[i][j][r + 3]));
 #pragma unroll
-      for (int r0 = 0; r0 < 32; r0 += RPP) {
-        const int row = r0 + lane / GROUPS, col = lane % GROUPS * 8;
-        const uint4 v = *reinterpret_cast<const uint4*>(mine + row * PITCH + col * 2);
-        const int p = prow0 + i * 32 + row, q = qcol0 + col;
-        if (p < prem && q < qrem) {
-          uint16_t* o = reinterpret_cast<uint16_t*>(out) + p * ldo + q;
-          if (q + 8 <= qrem) {
-            store16_any(o, v);
-          } else {
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        for (int r0 = 0; r0 < 32; r0 += RPP) {
+          const int row = r0 + lane / GROUPS, col = lane % GROUPS * 8;
+          const uint4 v = *reinterpret_cast<const uint4*>(mine + row * PITCH + col * 2);
+          const int p = prow0 + i * 32 + row, q = qcol0 + col;
+          if (p < prem && q < qrem) {
+            uint16_t* o = reinterpret_cast<uint16_t*>(out) + p * ldo + q;
+            if (q + 8 <= qrem) {
+              if constexpr (kStream) stream16_any(o, v);
+              else store16_any(o, v);
+            } else {
+              const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-              if (q + k < qrem) o[k] = static_cast<uint16_t>(w[k >> 1] >> (16 * (k & 1)));
+              for (int k = 0; k < 8; ++k)
+                if (q + k < qrem) o[k] = static_cast<uint16_t>(w[k >> 1] >> (16 * (k & 1)));
+            }
           }
         }
       }
-    }
-  } else {
-    constexpr int PITCH = COLS * 4 + 16;
-    char* mine = lds + (C::KS > 1 ? kLds / 2 : 0) + tw * (32 * PITCH);
-    static_assert(kTileWaves * 32 * PITCH <= kLds, "staging fits");
+    } else {
+      constexpr int GROUPS = COLS / 4;
+      constexpr int RPP = 64 / GROUPS;
+      constexpr int PITCH = COLS * 4 + 16;
+      char* mine = lds + (C::KS > 1 ? kLds / 2 : 0) + tw * (32 * PITCH);
+      static_assert(kTileWaves * 32 * PITCH <= kLds, "staging fits");
 #pragma unroll
-    for (int i = 0; i < TP; ++i) {
+      for (int i = 0; i < TP; ++i) {
 #pragma unroll
-      for (int j = 0; j < TQ; ++j)
+        for (int j = 0; j < TQ; ++j)
 #pragma unroll
-        for (int r = 0; r < 16; r += 4)
-          *reinterpret_cast<float4*>(mine + lrow * PITCH + (j * 32 + acc_q(r, lhalf)) * 4) =
-              make_float4(acc[i][j][r], acc[i][j][r + 1], acc[i][j][r + 2], acc[i][j][r + 3]);
+          for (int r = 0; r < 16; r += 4)
+            *reinterpret_cast<float4*>(mine + lrow * PITCH + (j * 32 + acc_q(r, lhalf)) * 4) =
+                make_float4(acc[i][j][r], acc[i][j][r + 1], acc[i][j][r + 2], acc[i][j][r + 3]);
 #pragma unroll
-      for (int r0 = 0; r0 < 32; r0 += RPP) {
-        const int row = r0 + lane / GROUPS, col = lane % GROUPS * 8;
-        const float4 a = *reinterpret_cast<const float4*>(mine + row * PITCH + col * 4);
-        const float4 b = *reinterpret_cast<const float4*>(mine + row * PITCH + col * 4 + 16);
-        float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-        const int p = prow0 + i * 32 + row, q = qcol0 + col;
-        if (p >= prem || q >= qrem) continue;
-        const bool whole = q + 8 <= qrem;
-        if (out_f32) {
-          float* o = reinterpret_cast<float*>(out) + p * ldo + q;
-          if (whole) {
-            if (MODE == kGroupWgrad && beta != 0.f) {
-              float old[8];
-              load8_any<ElemF32>(o, old);
+        for (int r0 = 0; r0 < 32; r0 += RPP) {
+          const int row = r0 + lane / GROUPS, col = lane % GROUPS * 4;
+          const float4 a = *reinterpret_cast<const float4*>(mine + row * PITCH + col * 4);
+          float v[4] = {a.x, a.y, a.z, a.w};
+          const int p = prow0 + i * 32 + row, q = qcol0 + col;
+          if (p >= prem || q >= qrem) continue;
+          if (out_f32) {
+            float* o = reinterpret_cast<float*>(out) + p * ldo + q;
+            if (q + 4 <= qrem) {
+              if (MODE == kGroupWgrad && beta != 0.f) {
+                const uint4 old = load16_any(o);
+                v[0] = fmaf(beta, __uint_as_float(old.x), v[0]);
+                v[1] = fmaf(beta, __uint_as_float(old.y), v[1]);
+                v[2] = fmaf(beta, __uint_as_float(old.z), v[2]);
+                v[3] = fmaf(beta, __uint_as_float(old.w), v[3]);
+              }
+              if constexpr (kStream) stream16_any(o, Vec16<ElemF32>::pack(v));
+              else store16_any(o, Vec16<ElemF32>::pack(v));
+            } else {
 #pragma unroll
-              for (int k = 0; k < 8; ++k) v[k] = fmaf(beta, old[k], v[k]);
+              for (int k = 0; k < 4; ++k)
+                if (q + k < qrem) o[k] = MODE == kGroupWgrad && beta != 0.f ? fmaf(beta, o[k], v[k]) : v[k];
             }
-            store8_any<ElemF32>(o, v);
           } else {
+            uint16_t* o = reinterpret_cast<uint16_t*>(out) + p * ldo + q;
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-              if (q + k < qrem) o[k] = MODE == kGroupWgrad && beta != 0.f ? fmaf(beta, o[k], v[k]) : v[k];
-          }
-        } else {
-          uint16_t* o = reinterpret_cast<uint16_t*>(out) + p * ldo + q;
-          if (whole) {
-            float old[8];
-            load8_any<ElemBF16>(o, old);
-#pragma unroll
-            for (int k = 0; k < 8; ++k) v[k] = fmaf(beta, old[k], v[k]);
-            store8_any<ElemBF16>(o, v);
-          } else {
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
+            for (int k = 0; k < 4; ++k)
               if (q + k < qrem) o[k] = f32_to_bf16_rne(fmaf(beta, bf16_to_f32(o[k]), v[k]));
           }
         }
       }
     }
-  }
+  };
+  if (g.stream && !split)
+    write(std::integral_constant<bool, true>{});
+  else
+    write(std::integral_constant<bool, false>{});
 }
 
 // Sum of the parts of each expert's weight gradient, in their order:
