@@ -639,23 +639,33 @@ __global__ __launch_bounds__(C::THREADS, C::OCC) void grouped_tile_kernel(GroupA
 #pragma unroll
     for (int i = 0; i < kScaleLd; ++i) scale_lds[(j & 1) * kScaleGroup + tid + i * C::THREADS] = sc[i];
   };
-  auto convert = [&](uint32_t stage, int t) {   // codes of step t, kept in `stage`
-    const uint4 c = *reinterpret_cast<const uint4*>(lds + stage + C::BP * ROW + tid * 16);
-    const float s = scale_lds[((t / kCkptSteps) & 1) * kScaleGroup +
-                              (t % kCkptSteps * 32 + crow) * kScaleCols + ccol / kCkptBlock];
-    const uint32_t w[4] = {c.x, c.y, c.z, c.w};
-    char* panel = lds + kStagesEnd + (t & 1) * kQPanel + crow * (C::BQ * 2);
+  // Step t's codes, kept in `stage`, in five pieces: the reads, then four codes
+  // each, spread over the MFMA slots of a sub-step.
+  uint4 codes;
+  float scale;
+  uint32_t half[4];
+  auto convert = [&](uint32_t stage, int t, int piece) {
+    if (piece == 0) {
+      codes = *reinterpret_cast<const uint4*>(lds + stage + C::BP * ROW + tid * 16);
+      scale = scale_lds[((t / kCkptSteps) & 1) * kScaleGroup +
+                        (t % kCkptSteps * 32 + crow) * kScaleCols + ccol / kCkptBlock];
+      return;
+    }
+    const uint32_t w = piece == 1 ? codes.x : piece == 2 ? codes.y : piece == 3 ? codes.z : codes.w;
+    float v[4];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      float v[8];
-#pragma unroll
-      for (int b = 0; b < 8; ++b)
-        v[b] = static_cast<float>(static_cast<int8_t>(w[2 * h + (b >> 2)] >> (8 * (b & 3)))) * s;
-      *reinterpret_cast<uint4*>(panel + (((ccol / 8 + h) ^ tswz<C::BQ>(crow)) << 4)) =
-          make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
-                     pack_bf16x2(v[6], v[7]));
+    for (int b = 0; b < 4; ++b) v[b] = static_cast<float>(static_cast<int8_t>(w >> (8 * b))) * scale;
+    const int at = (piece - 1) & 1 ? 2 : 0;
+    half[at] = pack_bf16x2(v[0], v[1]);
+    half[at + 1] = pack_bf16x2(v[2], v[3]);
+    if (at) {
+      char* panel = lds + kStagesEnd + (t & 1) * kQPanel + crow * (C::BQ * 2);
+      *reinterpret_cast<uint4*>(panel + (((ccol / 8 + (piece >> 2)) ^ tswz<C::BQ>(crow)) << 4)) =
+          make_uint4(half[0], half[1], half[2], half[3]);
     }
   };
+  // slot of a sub-step in which a piece goes
+  auto convert_slot = [](int piece) { return piece == 0 ? 0 : 1 + piece * (C::SLOTS - 1) / 5; };
 
   if constexpr (kReg || C::KS > 1) {
     // One barrier per step: behind it every wave has read the step before, whose
@@ -733,7 +743,8 @@ __global__ __launch_bounds__(C::THREADS, C::OCC) void grouped_tile_kernel(GroupA
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier"
                  :: "n"((C::STAGES - 2) * PIECES + kEarly) : "memory");
     if constexpr (CKPT) {
-      convert(0, 0);
+#pragma unroll
+      for (int i = 0; i < 5; ++i) convert(0, 0, i);
       asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
     }
     uint32_t qcur = 0;
@@ -764,7 +775,9 @@ __global__ __launch_bounds__(C::THREADS, C::OCC) void grouped_tile_kernel(GroupA
             if (C::template slot_of<PIECES>(q) == (sub == kLast ? x : (sub + 1) * C::SLOTS + x))
               dma_piece(sub == kLast ? cur : fill, q);
           if constexpr (CKPT) {
-            if (sub == 0 && x == C::SLOTS / 4) convert(nxt, t + 1);
+#pragma unroll
+            for (int i = 0; i < 5; ++i)
+              if (sub == 0 && x == convert_slot(i)) convert(nxt, t + 1, i);
           }
           __builtin_amdgcn_sched_barrier(0);
         }
