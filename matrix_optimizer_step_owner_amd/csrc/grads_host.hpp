@@ -258,6 +258,8 @@ mfsdp_status_t grouped_impl(int mode, const void* p, int64_t ldp, const void* q,
   g.part_rows = plan.part_rows;
   g.part = static_cast<float*>(workspace);
   g.stream = aligned(out, 128) && (mode == kGroupWgrad ? k : ldo) * static_cast<int64_t>(eo) % 128 == 0;
+  // eight L2s of 4 MB
+  g.stream_w = std::min(experts, rows) * n * k * static_cast<int64_t>(es) > (int64_t(32) << 20);
   // the smallest tiles
   const int64_t blocks = mode == kGroupWgrad ? group_blocks(g, mode, 128, 128)
                                              : group_blocks(g, mode, 32, 64);

@@ -30,6 +30,7 @@ struct GroupArgs {
   int32_t n, k;
   float beta;            // wgrad
   int32_t stream;        // output rows are whole 128-byte lines
+  int32_t stream_w;      // fwd: the weights in use are more than the L2s hold
   int32_t out_f32;       // wgrad: dW is fp32 whatever the operands' type
   int32_t part_rows;     // wgrad: segments are cut into parts of so many rows, 0: they are not
   float* part;           // wgrad in parts: [parts][n][k], summed by a second kernel
@@ -119,7 +120,7 @@ __device__ __forceinline__ bool group_find(const GroupArgs& g, int b, int bp, in
   GroupSpan s;
   if (!group_span(g, b, bp, nq, s)) return false;
   expert = s.expert;
-  alone = s.rows == 1;
+  alone = s.rows == 1 && g.stream_w;
   const int band = s.local / (kGroupBand * nq), r = s.local - band * (kGroupBand * nq);
   const int in_band = min(kGroupBand, s.rows - band * kGroupBand);
   ti = band * kGroupBand + r % in_band;
@@ -371,7 +372,7 @@ __global__ __launch_bounds__(C::THREADS, C::OCC) void grouped_tile_kernel(GroupA
   const size_t wsize = static_cast<size_t>(g.n) * g.k;
   const bool split = MODE == kGroupWgrad && g.part_rows > 0;
   // An expert with one row tile of few rows: its weights are read by this column
-  // of tiles alone, and streamed (eight 14336 x 4096 experts, 16 rows: 145 ->
+  // of tiles alone, and streamed if they would not stay in the L2s (eight 14336 x 4096 experts, 16 rows: 145 ->
   // 131 us; not where a panel row is less than two lines, as in the input
   // gradient: one expert there 36 -> 59 us).
   constexpr bool kAlone = MODE == kGroupFwd && C::KS > 1;

@@ -17,7 +17,7 @@ weights with their whole gradients; the other tensors are packed for AdamW).
 from __future__ import annotations
 
 import ctypes
-from typing import Optional, Tuple
+from typing import Callable, Dict, Optional, Tuple
 
 import torch
 
@@ -30,8 +30,10 @@ _DTYPES = {torch.float32: _lib.DTYPE_F32, torch.bfloat16: _lib.DTYPE_BF16}
 _FLOATS = tuple(_DTYPES)
 
 
-# The handle of a device's current stream, without the Stream object that
-# torch.cuda.current_stream makes around it (over a microsecond a call).
+# The current device and the handle of its current stream, without what
+# torch.cuda.current_device and current_stream (a Stream object) add around
+# them: together over a microsecond a call.
+_current_device = torch._C._cuda_getDevice
 _raw_stream = torch._C._cuda_getCurrentRawStream
 
 
@@ -76,11 +78,16 @@ def _gpu(t: torch.Tensor, name: str) -> torch.device:
     return t.device
 
 
+_functions: Dict[str, Callable] = {}
+
+
 def _call(device: torch.device, name: str, *args) -> None:
     """The library's function on the current stream of `device`, made current."""
-    fn = getattr(_lib.load(), name)
+    fn = _functions.get(name)
+    if fn is None:
+        fn = _functions[name] = getattr(_lib.load(), name)
     index = device.index
-    if index == torch.cuda.current_device():
+    if index == _current_device():
         status = fn(*args, _raw_stream(index))
     else:
         with torch.cuda.device(device):
@@ -126,7 +133,7 @@ def _grouped_rows(name: str, act: torch.Tensor, weight: torch.Tensor, offsets: t
     width, to = (k, n) if forward else (n, k)
     ld = _rows(act, arg, (rows, width))
     if out is None:
-        out = torch.empty(rows, to, dtype=dtype, device=device)
+        out = act.new_empty((rows, to))
         ldo = to
     else:
         _check(out, "out", device, (dtype,), 2)
@@ -231,11 +238,11 @@ def ckpt_quantize(x: torch.Tensor, codes: Optional[torch.Tensor] = None,
     _check(x, "x", device, _FLOATS, 2)
     rows, k = x.shape
     if codes is None:
-        codes = torch.empty(rows, k, dtype=torch.int8, device=device)
+        codes = x.new_empty((rows, k), dtype=torch.int8)
     else:
         _check_codes(codes, device, rows, k)
     if scales is None:
-        scales = torch.empty(rows, -(-k // CKPT_BLOCK), dtype=torch.uint8, device=device)
+        scales = x.new_empty((rows, -(-k // CKPT_BLOCK)), dtype=torch.uint8)
     else:
         _check_scales(scales, device, rows, k)
     _call(device, "mfsdp_ckpt_quantize", x.data_ptr(), _rows(x, "x"), rows, k,
@@ -255,7 +262,7 @@ def ckpt_restore(codes: torch.Tensor, scales: torch.Tensor, dtype: torch.dtype =
     if out is None:
         if dtype not in _DTYPES:
             raise TypeError(f"unsupported dtype {dtype}")
-        out = torch.empty(rows, k, dtype=dtype, device=device)
+        out = codes.new_empty((rows, k), dtype=dtype)
     else:
         _check(out, "out", device, _FLOATS, 2)
     _call(device, "mfsdp_ckpt_restore", codes.data_ptr(), scales.data_ptr(), rows, k,
@@ -264,9 +271,12 @@ def ckpt_restore(codes: torch.Tensor, scales: torch.Tensor, dtype: torch.dtype =
 
 
 def _check_tokens(tokens: torch.Tensor, device) -> int:
-    _check(tokens, "tokens", device, (torch.int32, torch.int64), tokens.dim())
+    """Bytes of a token."""
+    if not isinstance(tokens, torch.Tensor):
+        raise TypeError("tokens must be a tensor")
+    _check(tokens, "tokens", device, (torch.int64, torch.int32), tokens.ndim)
     _contiguous(tokens, "tokens")
-    return tokens.element_size()
+    return 8 if tokens.dtype is torch.int64 else 4
 
 
 def embedding(table: torch.Tensor, tokens: torch.Tensor, *, scale: float = 1.0,
@@ -286,20 +296,21 @@ def embedding(table: torch.Tensor, tokens: torch.Tensor, *, scale: float = 1.0,
     size = _check_tokens(tokens, device)
     vocab, d = table.shape
     n = tokens.numel()
-    shape = None
     if out is None:
         dtype = table.dtype if dtype is None else dtype
         if dtype not in _DTYPES:
             raise TypeError(f"unsupported dtype {dtype}")
-        out = torch.empty(n, d, dtype=dtype, device=device)
-        shape = tuple(tokens.shape) + (d,)
-    elif dtype is not None and dtype != out.dtype:
-        raise TypeError(f"out has dtype {out.dtype}, expected {dtype}")
-    _check(out, "out", device, _FLOATS, 2)
+        out = table.new_empty((*tokens.shape, d), dtype=dtype)
+        ldo = d
+    else:
+        if dtype is not None and dtype != out.dtype:
+            raise TypeError(f"out has dtype {out.dtype}, expected {dtype}")
+        _check(out, "out", device, _FLOATS, 2)
+        ldo = _rows(out, "out", (n, d))
+        dtype = out.dtype
     _call(device, "mfsdp_embedding", table.data_ptr(), _DTYPES[table.dtype], vocab, d,
-          tokens.data_ptr(), size, n, scale, out.data_ptr(), _rows(out, "out", (n, d)),
-          _DTYPES[out.dtype])
-    return out if shape is None else out.view(shape)
+          tokens.data_ptr(), size, n, scale, out.data_ptr(), ldo, _DTYPES[dtype])
+    return out
 
 
 def embedding_grad(dy: torch.Tensor, tokens: torch.Tensor, grad: torch.Tensor, *,
@@ -322,9 +333,8 @@ def embedding_grad(dy: torch.Tensor, tokens: torch.Tensor, grad: torch.Tensor, *
     vocab, d = grad.shape
     n = tokens.numel()
     ld = _rows(dy, "dy", (n, d))
-    lib = _lib.load()
     need = ctypes.c_size_t(0)
-    _lib.check(lib.mfsdp_embedding_grad_workspace_size(n, vocab, d, ctypes.byref(need)))
+    _lib.check(_lib.load().mfsdp_embedding_grad_workspace_size(n, vocab, d, ctypes.byref(need)))
     ws = _scratch(device, need.value, workspace)
     _call(device, "mfsdp_embedding_grad", dy.data_ptr(), ld, _DTYPES[dy.dtype],
           tokens.data_ptr(), size, n, vocab, d, scale, beta, grad.data_ptr(), ws.data_ptr(),
