@@ -825,20 +825,21 @@ __global__ __launch_bounds__(C::THREADS, C::OCC) void grouped_tile_kernel(GroupA
 #pragma unroll
         for (int r = 0; r < 16; ++r) acc[x / TQ][x % TQ][r] += sums[at(s, x, r)];
     // this wave's staging below may overlap sums that another wave still reads
-    static_assert(kTileWaves * 32 * (TQ * 32 * 4 + 16) <= kLds / 2 &&
-                      (C::KS - 1) * kTileWaves * C::SLOTS * kBlock * 4 <= kLds / 2,
+    static_assert((C::KS - 1) * kTileWaves * C::SLOTS * kBlock * 4 <= kLds / 2,
                   "staging behind the sums");
   }
 
   // ---- epilogue -------------------------------------------------------------------
-  // Each wave turns its blocks through its own part of LDS, 32 rows at a time
-  // (no barrier), so that a store writes whole row pieces: lane l holds row
-  // l % 32 and four consecutive columns per four registers.
+  // 32 rows of each row of waves at a time go through LDS (lane l holds row
+  // l % 32 and four consecutive columns per four registers), and every wave
+  // then stores some of those rows over the tile's whole width: a store covers
+  // 512 bytes of a row or more where the tile is 256 wide, so that lines are
+  // written whole wherever the rows start.
   constexpr int COLS = TQ * 32;
   const float beta = split ? 0.f : g.beta;
   const bool out_f32 = V == 4 || (MODE == kGroupWgrad && (split || g.out_f32));
   const bool f32 = out_f32 || (MODE == kGroupWgrad && beta != 0.f);
-  const int prow0 = wp * TP * 32, qcol0 = wq * COLS;
+  const int prow0 = wp * TP * 32;
   char* out;
   int64_t ldo;
   if (MODE == kGroupWgrad) {
@@ -851,71 +852,61 @@ __global__ __launch_bounds__(C::THREADS, C::OCC) void grouped_tile_kernel(GroupA
   }
   // stream_c: whether stores are streamed.  Two copies of the loops, chosen once:
   // the compiler would merge two stores that differ in that alone.
-  auto write = [&](auto stream_c) {
-    constexpr bool kStream = decltype(stream_c)::value;
-    if (!f32) {
-      constexpr int GROUPS = COLS / 8;          // 16-byte pieces per row
-      constexpr int RPP = 64 / GROUPS;          // rows per pass of a wave
-      constexpr int PITCH = COLS * 2 + 16;
-      char* mine = lds + (C::KS > 1 ? kLds / 2 : 0) + tw * (32 * PITCH);
-      static_assert(kTileWaves * 32 * PITCH <= kLds, "staging fits");
+  auto write = [&](auto stream_c, auto f32_c) {
+    constexpr bool kStream = decltype(stream_c)::value, kF32 = decltype(f32_c)::value;
+    constexpr int ES = kF32 ? 4 : 2;                 // bytes of a staged value
+    constexpr int GROUPS = C::BQ * ES / 16;          // 16-byte pieces per row
+    constexpr int RPP = 64 / GROUPS;                 // rows per pass of a wave
+    constexpr int PITCH = C::BQ * ES + 16;
+    constexpr int BLOCK = C::WP * 32 * PITCH;
+    constexpr int kSpace = C::KS > 1 ? kLds / 2 : kLds;
+    constexpr int BUFS = C::TP > 1 && 2 * BLOCK <= kSpace ? 2 : 1;
+    static_assert(BLOCK <= kSpace && RPP >= 1 && 32 / C::WQ % RPP == 0, "staging fits");
+    char* stage = lds + (kLds - kSpace) + wp * (32 * PITCH);
 #pragma unroll
-      for (int i = 0; i < TP; ++i) {
+    for (int i = 0; i < TP; ++i) {
+      char* mine = stage + (BUFS == 2 ? (i & 1) * BLOCK : 0);
+      if (BUFS == 1 && i > 0) __syncthreads();       // the rows before have been read
 #pragma unroll
-        for (int j = 0; j < TQ; ++j)
+      for (int j = 0; j < TQ; ++j)
 #pragma unroll
-          for (int r = 0; r < 16; r += 4)
-            *reinterpret_cast<uint2*>(mine + lrow * PITCH + (j * 32 + acc_q(r, lhalf)) * 2) =
+        for (int r = 0; r < 16; r += 4) {
+          char* at = mine + lrow * PITCH + (wq * COLS + j * 32 + acc_q(r, lhalf)) * ES;
+          if constexpr (kF32)
+            *reinterpret_cast<float4*>(at) = make_float4(acc[i][j][r], acc[i][j][r + 1], acc[i][j][r + 2], acc[i][j][r + 3]);
+          else
+            *reinterpret_cast<uint2*>(at) =
                 make_uint2(pack_bf16x2(acc[i][j][r], acc[i][j][r + 1]), pack_bf16x2(acc[i][j][r + 2], acc[i][j][r + 3]));
-#pragma unroll
-        for (int r0 = 0; r0 < 32; r0 += RPP) {
-          const int row = r0 + lane / GROUPS, col = lane % GROUPS * 8;
-          const uint4 v = *reinterpret_cast<const uint4*>(mine + row * PITCH + col * 2);
-          const int p = prow0 + i * 32 + row, q = qcol0 + col;
-          if (p < prem && q < qrem) {
-            uint16_t* o = reinterpret_cast<uint16_t*>(out) + p * ldo + q;
-            if (q + 8 <= qrem) {
-              if constexpr (kStream) stream16_any(o, v);
-              else store16_any(o, v);
-            } else {
-              const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-              for (int k = 0; k < 8; ++k)
-                if (q + k < qrem) o[k] = static_cast<uint16_t>(w[k >> 1] >> (16 * (k & 1)));
-            }
-          }
         }
-      }
-    } else {
-      constexpr int GROUPS = COLS / 4;
-      constexpr int RPP = 64 / GROUPS;
-      constexpr int PITCH = COLS * 4 + 16;
-      char* mine = lds + (C::KS > 1 ? kLds / 2 : 0) + tw * (32 * PITCH);
-      static_assert(kTileWaves * 32 * PITCH <= kLds, "staging fits");
+      __syncthreads();
 #pragma unroll
-      for (int i = 0; i < TP; ++i) {
+      for (int r0 = 0; r0 < 32 / C::WQ; r0 += RPP) {
+        const int row = wq * (32 / C::WQ) + r0 + lane / GROUPS, q = lane % GROUPS * (16 / ES);
+        const uint4 raw = *reinterpret_cast<const uint4*>(mine + row * PITCH + q * ES);
+        const int p = prow0 + i * 32 + row;
+        if (p >= prem || q >= qrem) continue;
+        if constexpr (!kF32) {
+          uint16_t* o = reinterpret_cast<uint16_t*>(out) + p * ldo + q;
+          if (q + 8 <= qrem) {
+            if constexpr (kStream) stream16_any(o, raw);
+            else store16_any(o, raw);
+          } else {
+            const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
 #pragma unroll
-        for (int j = 0; j < TQ; ++j)
-#pragma unroll
-          for (int r = 0; r < 16; r += 4)
-            *reinterpret_cast<float4*>(mine + lrow * PITCH + (j * 32 + acc_q(r, lhalf)) * 4) =
-                make_float4(acc[i][j][r], acc[i][j][r + 1], acc[i][j][r + 2], acc[i][j][r + 3]);
-#pragma unroll
-        for (int r0 = 0; r0 < 32; r0 += RPP) {
-          const int row = r0 + lane / GROUPS, col = lane % GROUPS * 4;
-          const float4 a = *reinterpret_cast<const float4*>(mine + row * PITCH + col * 4);
-          float v[4] = {a.x, a.y, a.z, a.w};
-          const int p = prow0 + i * 32 + row, q = qcol0 + col;
-          if (p >= prem || q >= qrem) continue;
+            for (int k = 0; k < 8; ++k)
+              if (q + k < qrem) o[k] = static_cast<uint16_t>(w[k >> 1] >> (16 * (k & 1)));
+          }
+        } else {
+          float v[4];
+          Vec16<ElemF32>::unpack(raw, v);
           if (out_f32) {
             float* o = reinterpret_cast<float*>(out) + p * ldo + q;
             if (q + 4 <= qrem) {
               if (MODE == kGroupWgrad && beta != 0.f) {
-                const uint4 old = load16_any(o);
-                v[0] = fmaf(beta, __uint_as_float(old.x), v[0]);
-                v[1] = fmaf(beta, __uint_as_float(old.y), v[1]);
-                v[2] = fmaf(beta, __uint_as_float(old.z), v[2]);
-                v[3] = fmaf(beta, __uint_as_float(old.w), v[3]);
+                float old[4];
+                Vec16<ElemF32>::unpack(load16_any(o), old);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) v[k] = fmaf(beta, old[k], v[k]);
               }
               if constexpr (kStream) stream16_any(o, Vec16<ElemF32>::pack(v));
               else store16_any(o, Vec16<ElemF32>::pack(v));
@@ -924,7 +915,7 @@ __global__ __launch_bounds__(C::THREADS, C::OCC) void grouped_tile_kernel(GroupA
               for (int k = 0; k < 4; ++k)
                 if (q + k < qrem) o[k] = MODE == kGroupWgrad && beta != 0.f ? fmaf(beta, o[k], v[k]) : v[k];
             }
-          } else {
+          } else {   // beta * dW + sum in bf16
             uint16_t* o = reinterpret_cast<uint16_t*>(out) + p * ldo + q;
 #pragma unroll
             for (int k = 0; k < 4; ++k)
@@ -934,10 +925,20 @@ __global__ __launch_bounds__(C::THREADS, C::OCC) void grouped_tile_kernel(GroupA
       }
     }
   };
-  if (g.stream && !split)
-    write(std::integral_constant<bool, true>{});
-  else
-    write(std::integral_constant<bool, false>{});
+  using yes = std::integral_constant<bool, true>;
+  using no = std::integral_constant<bool, false>;
+  const bool stream = g.stream && !split;
+  if constexpr (V == 8) {
+    if (!f32) {
+      if (stream) write(yes{}, no{});
+      else write(no{}, no{});
+      return;
+    }
+  }
+  if constexpr (V == 4 || MODE == kGroupWgrad) {
+    if (stream) write(yes{}, yes{});
+    else write(no{}, yes{});
+  }
 }
 
 // Sum of the parts of each expert's weight gradient, in their order:
