@@ -38,14 +38,56 @@ __device__ __forceinline__ int64_t emb_token(const void* tokens, int tok64, int6
   return tok64 ? static_cast<const int64_t*>(tokens)[i] : static_cast<const int32_t*>(tokens)[i];
 }
 
-// A unit is eight columns of one row on the vector path (rows of both sides
-// start on 16 bytes, d a multiple of eight), one column otherwise.
-// Bound by HBM: each row is read once and written once.
+// W consecutive elements as loaded, and as floats.  Loads and conversions are
+// kept apart, so that several loads can be in flight before the first is waited
+// for.
+typedef uint32_t u32x2v_t __attribute__((ext_vector_type(2)));
+template <class E, int W>
+struct EmbRaw {
+  static constexpr int kBytes = W * (16 / E::kVec);
+  typename std::conditional<
+      W == 1, typename E::storage_t,
+      typename std::conditional<kBytes == 8, u32x2v_t, u32x4_t>::type>::type r;
+  __device__ __forceinline__ void load(const typename E::storage_t* p) { r = gld<decltype(r)>(p); }
+  __device__ __forceinline__ void get(float (&v)[W]) const {
+    if constexpr (W == 1) {
+      v[0] = E::to_f32(r);
+    } else {
+#pragma unroll
+      for (int i = 0; i < W; ++i) {
+        if constexpr (E::kVec == 8)
+          v[i] = __uint_as_float(i & 1 ? r[i >> 1] & 0xffff0000u : r[i >> 1] << 16);
+        else
+          v[i] = __uint_as_float(r[i]);
+      }
+    }
+  }
+  // streamed store of W values, rounded to the type
+  __device__ __forceinline__ static void put(typename E::storage_t* p, const float (&v)[W]) {
+    if constexpr (W == 1) {
+      gst<typename E::storage_t>(p, E::from_f32(v[0]));
+    } else {
+      decltype(EmbRaw::r) o;
+#pragma unroll
+      for (int i = 0; i < kBytes / 4; ++i) {
+        if constexpr (E::kVec == 8) o[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+        else o[i] = __float_as_uint(v[i]);
+      }
+      __builtin_nontemporal_store(o, (MFSDP_GLOBAL decltype(o)*)(p));
+    }
+  }
+};
+
+// A unit is W columns of one row: 16 bytes of the output, where rows of both
+// sides start on whole units, one column otherwise.  Bound by HBM: each row is read and
+// written once (rows of frequent tokens come from the caches, which the
+// streamed output leaves to them).
 template <class ET, class EO, bool VEC>
 __global__ __launch_bounds__(256) void embedding_kernel(EmbArgs a) {
   using T = typename ET::storage_t;
   using O = typename EO::storage_t;
-  constexpr int W = VEC ? 8 : 1;
+  constexpr int W = VEC ? EO::kVec : 1;
+  constexpr int PART = W < ET::kVec ? W : ET::kVec;   // columns of one load
   const int units = a.d / W;
   int64_t i;
   int u;
@@ -60,20 +102,21 @@ __global__ __launch_bounds__(256) void embedding_kernel(EmbArgs a) {
   }
   if (i >= a.n_tokens || u >= units) return;
   const int64_t tok = emb_token(a.tokens, a.tok64, i);
-  const bool in = tok >= 0 && tok < a.vocab;
-  O* dst = static_cast<O*>(a.out) + i * a.ldo + u * W;
-  const T* src = static_cast<const T*>(a.table) + (in ? tok : 0) * a.d + u * W;
-  if constexpr (VEC) {
-    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (in) {
-      load8<ET>(src, v);
+  float v[W] = {};
+  if (tok >= 0 && tok < a.vocab) {
+    EmbRaw<ET, PART> raw[W / PART];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] *= a.scale;
+    for (int p = 0; p < W / PART; ++p)
+      raw[p].load(static_cast<const T*>(a.table) + tok * a.d + u * W + p * PART);
+#pragma unroll
+    for (int p = 0; p < W / PART; ++p) {
+      float x[PART];
+      raw[p].get(x);
+#pragma unroll
+      for (int e = 0; e < PART; ++e) v[p * PART + e] = x[e] * a.scale;
     }
-    store8<EO>(dst, v);
-  } else {
-    *dst = EO::from_f32(in ? ET::to_f32(*src) * a.scale : 0.f);
   }
+  EmbRaw<EO, W>::put(static_cast<O*>(a.out) + i * a.ldo + u * W, v);
 }
 
 // ---------------------------------------------------------------------------
@@ -282,33 +325,8 @@ __device__ __forceinline__ int emb_lower(const uint32_t* key, int lo, int hi, in
 constexpr int kEmbGroups = 2;
 constexpr int kEmbFlight = 8;   // rows' loads in flight
 
-// W consecutive elements as loaded, and as floats.  Loads and conversions are
-// kept apart, and loads take no branch (columns that do not exist read column
-// 0): else each would be waited for before the next is issued.
-typedef uint32_t u32x2v_t __attribute__((ext_vector_type(2)));
-template <class E, int W>
-struct EmbRaw {
-  typename std::conditional<W == 1, typename E::storage_t,
-                            typename std::conditional<E::kVec == 8, u32x2v_t, f32x4_t>::type>::type r;
-  __device__ __forceinline__ void load(const typename E::storage_t* p) { r = gld<decltype(r)>(p); }
-  __device__ __forceinline__ void get(float (&v)[W]) const {
-    if constexpr (W == 1) {
-      v[0] = E::to_f32(r);
-    } else if constexpr (E::kVec == 8) {
-      v[0] = __uint_as_float(r.x << 16);
-      v[1] = __uint_as_float(r.x & 0xffff0000u);
-      v[2] = __uint_as_float(r.y << 16);
-      v[3] = __uint_as_float(r.y & 0xffff0000u);
-    } else {
-      v[0] = r.x;
-      v[1] = r.y;
-      v[2] = r.z;
-      v[3] = r.w;
-    }
-  }
-};
-
-// Columns of this thread's groups: first column, or 0 where there is none.
+// Columns of this thread's groups: first column, or 0 where there is none (a
+// load takes no branch: it would be waited for before the next is issued).
 struct EmbCols {
   int c[kEmbGroups];
   bool on[kEmbGroups];
@@ -462,11 +480,7 @@ __global__ __launch_bounds__(256) void emb_rows_kernel(EmbGradArgs a, int col_wg
       }
 #pragma unroll
       for (int x = 0; x < W; ++x) out[x] = fmaf(a.scale, acc[q][x], a.beta != 0.f ? a.beta * out[x] : 0.f);
-      if constexpr (W == 4)
-        gst_stream(oq, make_uint4(__float_as_uint(out[0]), __float_as_uint(out[1]), __float_as_uint(out[2]),
-                                  __float_as_uint(out[3])));
-      else
-        gst<float>(oq, out[0]);
+      EmbRaw<ElemF32, W>::put(oq, out);
     }
   }
 }

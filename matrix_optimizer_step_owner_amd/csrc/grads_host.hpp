@@ -382,9 +382,10 @@ mfsdp_status_t embedding_impl(const void* table, mfsdp_dtype_t table_dtype, int6
   a.d = static_cast<int32_t>(d);
   a.tok64 = token_bytes == 8;
   a.scale = scale;
-  const bool vec = d % 8 == 0 && aligned(table, 16) && aligned(out, 16) &&
-                   (ldo * static_cast<int64_t>(eo)) % 16 == 0;
-  const int64_t units = vec ? d / 8 : d;
+  const int64_t w = 16 / static_cast<int64_t>(eo);
+  const bool vec = d % w == 0 && aligned(table, std::min<size_t>(w * et, 16)) && aligned(out, 16) &&
+                   ldo % w == 0;
+  const int64_t units = vec ? d / w : d;
   int64_t blocks;
   if (units > 128) {
     a.chunks = static_cast<int32_t>((units + 255) / 256);
