@@ -335,6 +335,8 @@ mfsdp_status_t mfsdp_shampoo_stats(const mfsdp_stats_matrix_t* mats, int64_t n_m
  *     and tokens on the device, and can be captured into a graph (a graph
  *     keeps the workspace it was captured with: two graphs that may run at the
  *     same time need one each).
+ *   - The calls that take a workspace share it in stream order: one host
+ *     thread at a time per stream and workspace.
  *   - Results do not depend on timing: no atomics on sums.
  *   - Sums are fp32 throughout and rounded once, to the output's type.
  *   - Outputs must not overlap inputs, the workspace or each other

@@ -8,25 +8,43 @@
 
 namespace {
 
-// Extent in bytes of `rows` rows of `cols` elements, `ld` elements apart.
-size_t strided_bytes(int64_t rows, int64_t cols, int64_t ld, size_t es) {
-  return rows < 1 || cols < 1 ? 0 : (static_cast<size_t>(rows - 1) * ld + cols) * es;
+// A buffer of rows: `width` bytes each, `pitch` bytes apart.
+struct Extent {
+  uintptr_t lo, hi;
+  size_t pitch, width;
+  const char* what;
+};
+
+void add_rows(std::vector<Extent>* list, const void* p, int64_t rows, int64_t cols, int64_t ld,
+              size_t es, const char* what) {
+  if (rows < 1 || cols < 1) return;
+  const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
+  const size_t pitch = static_cast<size_t>(ld) * es, width = static_cast<size_t>(cols) * es;
+  list->push_back({lo, lo + (rows - 1) * pitch + width, pitch, width, what});
 }
 
-void add_range(std::vector<Range>* rs, const void* p, size_t nb, const char* what) {
+void add_bytes(std::vector<Extent>* list, const void* p, size_t nb, const char* what) {
   const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
-  if (nb) rs->push_back({lo, lo + nb, what, 0});
+  if (nb) list->push_back({lo, lo + nb, nb, nb, what});
+}
+
+bool overlap(const Extent& a, const Extent& b) {
+  if (a.hi <= b.lo || b.hi <= a.lo) return false;
+  if (a.pitch != b.pitch) return true;
+  // columns of one wider buffer: apart if each row's part is
+  const size_t d = a.lo < b.lo ? (b.lo - a.lo) % a.pitch : (a.pitch - (a.lo - b.lo) % a.pitch) % a.pitch;
+  return !(d >= a.width && d + b.width <= a.pitch);
 }
 
 // The outputs must be disjoint from the inputs and from each other; inputs may
 // overlap one another.
-mfsdp_status_t check_outputs(const std::vector<Range>& outs, const std::vector<Range>& ins) {
+mfsdp_status_t check_outputs(const std::vector<Extent>& outs, const std::vector<Extent>& ins) {
   for (size_t i = 0; i < outs.size(); ++i) {
     for (size_t j = i + 1; j < outs.size(); ++j)
-      if (outs[i].lo < outs[j].hi && outs[j].lo < outs[i].hi)
+      if (overlap(outs[i], outs[j]))
         return fail(MFSDP_ERR_ALIAS, "%s overlaps %s", outs[i].what, outs[j].what);
-    for (const Range& in : ins)
-      if (outs[i].lo < in.hi && in.lo < outs[i].hi)
+    for (const Extent& in : ins)
+      if (overlap(outs[i], in))
         return fail(MFSDP_ERR_ALIAS, "%s overlaps %s", outs[i].what, in.what);
   }
   return MFSDP_OK;
@@ -85,6 +103,7 @@ using TileF32 = GroupTile<128, 128, 2, 2, 1, 4>;
 struct WgradPlan {
   bool large;
   int32_t part_rows;   // 0: whole segments
+  int32_t parts_max;
   size_t bytes;        // of the parts
 };
 
@@ -105,7 +124,8 @@ WgradPlan wgrad_plan(int64_t experts, int64_t rows, int64_t n, int64_t k, bool b
   if (rows < len * experts * 5 / 4) return p;
   p.large = wide;
   p.part_rows = static_cast<int32_t>(len);
-  p.bytes = static_cast<size_t>(group_tiles_max(rows, experts, len)) * n * k * 4;
+  p.parts_max = static_cast<int32_t>(group_tiles_max(rows, experts, len));
+  p.bytes = static_cast<size_t>(p.parts_max) * n * k * 4;
   return p;
 }
 
@@ -221,20 +241,20 @@ mfsdp_status_t grouped_impl(int mode, const void* p, int64_t ldp, const void* q,
       return fail(MFSDP_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", workspace_bytes, need);
   }
   {
-    std::vector<Range> ins, outs;
+    std::vector<Extent> ins, outs;
     const size_t wb = static_cast<size_t>(experts) * n * k;
-    if (need) add_range(&outs, workspace, need, "workspace");
-    add_range(&ins, offsets, static_cast<size_t>(experts + 1) * 4, "offsets");
-    add_range(&ins, p, strided_bytes(rows, np, ldp, es), mode == kGroupFwd ? "x" : "dy");
+    if (need) add_bytes(&outs, workspace, need, "workspace");
+    add_bytes(&ins, offsets, static_cast<size_t>(experts + 1) * 4, "offsets");
+    add_rows(&ins, p, rows, np, ldp, es, mode == kGroupFwd ? "x" : "dy");
     if (mode == kGroupWgrad) {
-      add_range(&ins, q, strided_bytes(rows, k, ldq, qs ? 1 : es), qs ? "codes" : "x");
+      add_rows(&ins, q, rows, k, ldq, qs ? 1 : es, qs ? "codes" : "x");
       if (qs)
-        add_range(&ins, qs, static_cast<size_t>(rows) * ((k + kCkptBlock - 1) / kCkptBlock),
+        add_bytes(&ins, qs, static_cast<size_t>(rows) * ((k + kCkptBlock - 1) / kCkptBlock),
                   "scales");
-      add_range(&outs, out, wb * eo, "dw");
+      add_bytes(&outs, out, wb * eo, "dw");
     } else {
-      add_range(&ins, q, wb * es, "weight");
-      add_range(&outs, out, strided_bytes(rows, no, ldo, es), mode == kGroupFwd ? "y" : "dx");
+      add_bytes(&ins, q, wb * es, "weight");
+      add_rows(&outs, out, rows, no, ldo, es, mode == kGroupFwd ? "y" : "dx");
     }
     st = check_outputs(outs, ins);
     if (st != MFSDP_OK) return st;
@@ -256,6 +276,7 @@ mfsdp_status_t grouped_impl(int mode, const void* p, int64_t ldp, const void* q,
   g.beta = beta;
   g.out_f32 = out_dtype == MFSDP_DTYPE_F32 ? 1 : 0;
   g.part_rows = plan.part_rows;
+  g.parts_max = plan.parts_max;
   g.part = static_cast<float*>(workspace);
   g.stream = aligned(out, 128) && (mode == kGroupWgrad ? k : ldo) * static_cast<int64_t>(eo) % 128 == 0;
   // eight L2s of 4 MB
@@ -305,10 +326,10 @@ mfsdp_status_t ckpt_impl(bool quantize, void* x, int64_t ld, int8_t* codes, uint
   a.vec = aligned(x, 16) && (ld * static_cast<int64_t>(es)) % 16 == 0 && k % 8 == 0 &&
           aligned(codes, 8);
   {
-    std::vector<Range> xs, cs;
-    add_range(&xs, x, strided_bytes(rows, k, ld, es), "x");
-    add_range(&cs, codes, static_cast<size_t>(rows) * k, "codes");
-    add_range(&cs, scales, static_cast<size_t>(a.units), "scales");
+    std::vector<Extent> xs, cs;
+    add_rows(&xs, x, rows, k, ld, es, "x");
+    add_bytes(&cs, codes, static_cast<size_t>(rows) * k, "codes");
+    add_bytes(&cs, scales, static_cast<size_t>(a.units), "scales");
     const mfsdp_status_t st = quantize ? check_outputs(cs, xs) : check_outputs(xs, cs);
     if (st != MFSDP_OK) return st;
   }
@@ -365,10 +386,10 @@ mfsdp_status_t embedding_impl(const void* table, mfsdp_dtype_t table_dtype, int6
   if (!aligned(table, et) || !aligned(out, eo) || !aligned(tokens, token_bytes))
     return fail(MFSDP_ERR_INVALID_ARGUMENT, "a buffer is not aligned to its elements");
   {
-    std::vector<Range> ins, outs;
-    add_range(&ins, table, static_cast<size_t>(vocab) * d * et, "table");
-    add_range(&ins, tokens, static_cast<size_t>(n_tokens) * token_bytes, "tokens");
-    add_range(&outs, out, strided_bytes(n_tokens, d, ldo, eo), "out");
+    std::vector<Extent> ins, outs;
+    add_bytes(&ins, table, static_cast<size_t>(vocab) * d * et, "table");
+    add_bytes(&ins, tokens, static_cast<size_t>(n_tokens) * token_bytes, "tokens");
+    add_rows(&outs, out, n_tokens, d, ldo, eo, "out");
     const mfsdp_status_t st = check_outputs(outs, ins);
     if (st != MFSDP_OK) return st;
   }
@@ -500,11 +521,11 @@ mfsdp_status_t embedding_grad_impl(const void* dy, int64_t ld, mfsdp_dtype_t dty
                   p.total);
   }
   {
-    std::vector<Range> ins, outs;
-    add_range(&ins, dy, strided_bytes(n_tokens, d, ld, es), "dy");
-    add_range(&ins, tokens, static_cast<size_t>(n_tokens) * token_bytes, "tokens");
-    add_range(&outs, grad, static_cast<size_t>(vocab) * d * 4, "grad");
-    if (n_tokens > 0) add_range(&outs, workspace, p.total, "workspace");
+    std::vector<Extent> ins, outs;
+    add_rows(&ins, dy, n_tokens, d, ld, es, "dy");
+    add_bytes(&ins, tokens, static_cast<size_t>(n_tokens) * token_bytes, "tokens");
+    add_bytes(&outs, grad, static_cast<size_t>(vocab) * d * 4, "grad");
+    if (n_tokens > 0) add_bytes(&outs, workspace, p.total, "workspace");
     st = check_outputs(outs, ins);
     if (st != MFSDP_OK) return st;
   }

@@ -33,6 +33,7 @@ struct GroupArgs {
   int32_t stream_w;      // fwd: the weights in use are more than the L2s hold
   int32_t out_f32;       // wgrad: dW is fp32 whatever the operands' type
   int32_t part_rows;     // wgrad: segments are cut into parts of so many rows, 0: they are not
+  int32_t parts_max;     // parts that there is room for
   float* part;           // wgrad in parts: [parts][n][k], summed by a second kernel
 };
 
@@ -75,22 +76,24 @@ __device__ __forceinline__ bool group_span(const GroupArgs& g, int b, int bp, in
   const int lane = threadIdx.x & 63;
   const int c = (g.experts + 63) >> 6;
   const int e0 = min(lane * c, g.experts), e1 = min(e0 + c, g.experts);
-  int sum = 0;
+  int64_t sum = 0;
   for (int e = e0; e < e1; ++e) {
     int lo, hi;
     group_segment(g, e, lo, hi);
     sum += (hi - lo + bp - 1) / bp;
   }
-  int incl = sum;
+  int64_t incl = sum;
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) {
-    const int v = __shfl_up(incl, d, 64);
+    const int64_t v = __shfl_up(incl, d, 64);
     if (lane >= d) incl += v;
   }
-  const int total = __builtin_amdgcn_readlane(incl, 63) * nq;
+  // No more tiles than the grid has (the host bounds it by what ordered offsets
+  // can give; others give wrong results, not accesses outside).
+  const int total = static_cast<int>(min(__shfl(incl, 63, 64) * nq, static_cast<int64_t>(gridDim.x)));
   if (b >= total) return false;
   const int want = xcd_remap(b, total);
-  int at = incl - sum;
+  int64_t at = incl - sum;
   int fe = -1, fl = 0, fr = 0, ff = 0;
   if (want >= at * nq && want < incl * nq) {
     for (int e = e0; e < e1; ++e) {
@@ -99,15 +102,17 @@ __device__ __forceinline__ bool group_span(const GroupArgs& g, int b, int bp, in
       const int np = (hi - lo + bp - 1) / bp;
       if (want < (at + np) * nq) {
         fe = e;
-        fl = want - at * nq;
+        fl = static_cast<int>(want - at * nq);
         fr = np;
-        ff = at;
+        ff = static_cast<int>(at);
         break;
       }
       at += np;
     }
   }
-  const int src = __builtin_ctzll(__ballot(fe >= 0));
+  const uint64_t found = __ballot(fe >= 0);
+  if (found == 0) return false;
+  const int src = __builtin_ctzll(found);
   out.expert = __builtin_amdgcn_readlane(fe, src);
   out.local = __builtin_amdgcn_readlane(fl, src);
   out.rows = __builtin_amdgcn_readlane(fr, src);
@@ -950,7 +955,7 @@ __global__ __launch_bounds__(256) void grouped_sum_kernel(GroupArgs g, int per_e
   const int e = blockIdx.x / per_expert;
   const size_t wsize = static_cast<size_t>(g.n) * g.k;
   // parts of the experts before this one: each wave adds them up for itself
-  int first = 0;
+  int64_t first = 0;
   for (int i = threadIdx.x & 63; i < e; i += 64) {
     int lo, hi;
     group_segment(g, i, lo, hi);
@@ -958,9 +963,10 @@ __global__ __launch_bounds__(256) void grouped_sum_kernel(GroupArgs g, int per_e
   }
 #pragma unroll
   for (int d = 32; d > 0; d >>= 1) first += __shfl_xor(first, d, 64);
+  first = min(first, static_cast<int64_t>(g.parts_max));
   int lo, hi;
   group_segment(g, e, lo, hi);
-  const int parts = (hi - lo + g.part_rows - 1) / g.part_rows;
+  const int parts = min((hi - lo + g.part_rows - 1) / g.part_rows, g.parts_max - static_cast<int>(first));
   const size_t i = static_cast<size_t>(blockIdx.x % per_expert) * 2048 + threadIdx.x * 8;
   if (i >= wsize) return;
   O* out = static_cast<O*>(g.out) + e * wsize + i;

@@ -50,6 +50,7 @@ ROUTES = {
     "one expert": ([300], 0, 0),
     "empty ones": ([0, 5, 0, 0, 64, 1, 0], 3, 2),
     "none": ([0, 0, 0], 2, 1),
+    "two short": ([60, 60], 0, 0),
     "tiny": ([1, 2, 0, 1, 1, 3, 1, 0, 1], 0, 0),
     "mixed": ([33, 127, 0, 128, 129, 255, 256, 257, 31, 32], 0, 5),
     "skewed": ([1500, 3, 0, 40], 1, 0),
@@ -74,7 +75,7 @@ GROUPED = [("one row", "whole"), ("one expert", "whole"), ("empty ones", "ragged
            ("tiny", "odd"), ("mixed", "whole"), ("mixed", "ragged"), ("mixed", "odd"), ("mixed", "odd stride"), ("skewed", "ragged"),
            ("skewed", "long"), ("many", "narrow"), ("many", "odd"), ("empty ones", "one"), ("mixed", "short"), ("one row", "long"),
            ("tiny", "long"), ("parts", "whole"), ("parts", "narrow"), ("parts", "odd"), ("long one", "narrow"), ("long one", "ragged"),
-           ("five", "big"), ("many", "ragged")]
+           ("five", "big"), ("many", "ragged"), ("two short", "big"), ("parts", "ragged")]
 
 
 def setup(route, width, dtype, seed=0):
@@ -179,6 +180,104 @@ def test_wrong_offsets_stay_inside():
         want = ref.f64(dy[lo:hi]).t() @ ref.f64(x[lo:hi])
         mag = ref.f64(dy[lo:hi]).abs().t() @ ref.f64(x[lo:hi]).abs()
         assert ref.worst(grad[e], want, ref.half_step(F32) * want.abs() + 51 * ref.U * mag + 1e-300) <= 1.0
+
+
+def test_disordered_offsets_end():
+    # up and down again for every expert: far more tiles, and parts of the
+    # weight gradient, than ordered offsets can give.  The calls return, what
+    # lies behind the outputs stays as it was, and the next call is right.
+    rows, n, k, experts = 3000, 64, 64, 40
+    x, dy = rand((rows, k), BF, 1).to(DEV), rand((rows, n), BF, 2).to(DEV)
+    w = rand((experts, n, k), BF, 3).to(DEV)
+    off = torch.tensor([0, rows] * (experts // 2) + [0], dtype=torch.int32, device=DEV)
+    outs = [torch.full((rows + 64, n), 7.0, dtype=BF, device=DEV), torch.full((rows + 64, k), 7.0, dtype=BF, device=DEV),
+            torch.full((experts + 1, n, k), 7.0, device=DEV)]
+    two = torch.tensor([0, rows, 0, rows], dtype=torch.int32, device=DEV)
+    few = torch.full((4, n, k), 7.0, device=DEV)
+    mf.grouped_linear(x, w, off, out=outs[0][:rows])
+    mf.grouped_linear_dgrad(dy, w, off, out=outs[1][:rows])
+    mf.grouped_linear_wgrad(dy, x, off, outs[2][:experts])
+    mf.grouped_linear_wgrad(dy, x, two, few[:3])       # in parts
+    torch.cuda.synchronize()
+    assert all((o[rows:] == 7.0).all() for o in outs[:2]) and (outs[2][experts] == 7.0).all() and (few[3] == 7.0).all()
+    good = offsets_of([rows // experts] * experts)
+    y, mag, _ = ref.linear(x, w, good)
+    assert ref.worst(mf.grouped_linear(x, w, good.to(DEV)), y, ref.half_step(BF) * y.abs() + k * ref.U * mag) <= 1.0
+
+
+def test_no_rows():
+    w, off = rand((3, 16, 24), BF, 1).to(DEV), torch.zeros(4, dtype=torch.int32, device=DEV)
+    x, dy = torch.empty(0, 24, dtype=BF, device=DEV), torch.empty(0, 16, dtype=BF, device=DEV)
+    assert mf.grouped_linear(x, w, off).shape == (0, 16) and mf.grouped_linear_dgrad(dy, w, off).shape == (0, 24)
+    grad = torch.full((3, 16, 24), NAN, device=DEV)
+    assert not mf.grouped_linear_wgrad(dy, x, off, grad).any()
+    assert torch.equal(mf.grouped_linear_wgrad(dy, x, off, grad + 2.0, beta=0.5), torch.ones_like(grad))
+    codes, scales = mf.ckpt_quantize(x)
+    assert codes.shape == (0, 24) and scales.shape == (0, 1) and mf.ckpt_restore(codes, scales).shape == (0, 24)
+    assert not mf.grouped_linear_wgrad_ckpt(dy, codes, scales, off, grad).any()
+
+
+@pytest.mark.parametrize("dtype,k", [(BF, 4096), (BF, 4104), (F32, 4096)])
+def test_large_weights_few_rows(dtype, k):
+    # weights of 69 MB and more: more than the L2s hold, read by one tile column each
+    n, counts = 2056, [1, 0, 2, 40, 1]
+    off = offsets_of(counts)
+    x, dy, w = rand((44, k), dtype, 1), rand((44, n), dtype, 2), rand((5, n, k), dtype, 3, 0.05)
+    y, mag, _ = ref.linear(x, w, off)
+    assert ref.worst(mf.grouped_linear(x.to(DEV), w.to(DEV), off.to(DEV)), y, ref.half_step(dtype) * y.abs() + k * ref.U * mag) <= 1.0
+    dx, mag, _ = ref.dgrad(dy, w, off)
+    assert ref.worst(mf.grouped_linear_dgrad(dy.to(DEV), w.to(DEV), off.to(DEV)), dx, ref.half_step(dtype) * dx.abs() + n * ref.U * mag) <= 1.0
+
+
+def test_far_rows():
+    # byte offsets of rows and weights past 32 bits: 80000 rows of 32768 bf16
+    # values, the last few of them in use (rows behind the first 65536 start
+    # past 4 GiB)
+    rows, ld, n, k = 80000, 32768, 64, 128
+    buf = torch.empty(rows, ld, dtype=BF, device=DEV)
+    x, dy = buf[:, :k], buf[:, k:k + n]
+    xs, dys = rand((500, k), BF, 1), rand((500, n), BF, 2)
+    x[-500:], dy[-500:] = xs.to(DEV), dys.to(DEV)
+    off = torch.tensor([rows - 500, rows - 300, rows], dtype=torch.int32)
+    small = off - (rows - 500)
+    w = rand((2, n, k), BF, 3)
+    out = buf[:, 1024:1024 + n]
+    mf.grouped_linear(x, w.to(DEV), off.to(DEV), out=out)
+    y, mag, _ = ref.linear(xs, w, small)
+    assert ref.worst(out[-500:], y, ref.half_step(BF) * y.abs() + k * ref.U * mag) <= 1.0
+    grad = torch.empty(2, n, k, device=DEV)
+    mf.grouped_linear_wgrad(dy, x, off.to(DEV), grad)
+    dw, mag, terms = ref.wgrad(dys, xs, small)
+    assert ref.worst(grad, dw, wgrad_bound(dw, mag, terms, torch.zeros_like(dw), 0.0, F32)) <= 1.0
+    codes, scales = mf.ckpt_quantize(x[-500:])
+    cr, sr = ref.ckpt_quantize(xs)
+    assert np.array_equal(codes.cpu().numpy(), cr) and np.array_equal(scales.cpu().numpy(), sr)
+    t = torch.full((rows,), -1, device=DEV)
+    t[-500:] = torch.arange(500, device=DEV) % 7
+    g = mf.embedding_grad(x, t, torch.empty(9, k, device=DEV))
+    gr, mag, terms = ref.embedding_grad(xs, torch.arange(500) % 7, 9, 1.0)
+    assert ref.worst(g, gr, (terms[:, None] + 2) * ref.U * mag) <= 1.0
+    mf.embedding(g, t, out=buf[:, 2048:2048 + k])
+    want = ref.embedding(g.cpu(), torch.arange(500) % 7, 1.0)
+    assert ref.worst(buf[-500:, 2048:2048 + k], want, ref.half_step(BF) * (1 + 2 ** -20) * want.abs()) <= 1.0
+    assert not buf[:rows - 500:997, 2048:2048 + k].any()
+
+
+def test_timing_kinds():
+    x, w, off = rand((10, 16), BF, 1).to(DEV), rand((2, 8, 16), BF, 2).to(DEV), offsets_of([4, 6]).to(DEV)
+    mf.timing.enable(True)
+    try:
+        mf.timing.reset()
+        mf.grouped_linear(x, w, off)
+        mf.ckpt_restore(*mf.ckpt_quantize(x))
+        t = torch.zeros(10, dtype=torch.int64, device=DEV)
+        mf.embedding(x, t)
+        mf.embedding_grad(x, t, torch.empty(3, 16, device=DEV))
+        counts = [mf.timing.read(kind)[1] for kind in ("grouped", "ckpt", "embed", "embed_grad")]
+        assert counts[:3] == [1, 2, 1] and counts[3] >= 2
+    finally:
+        mf.timing.enable(False)
+        mf.timing.reset()
 
 
 def test_gradients_against_differences():

@@ -44,6 +44,8 @@ def wgrad_ckpt(codes=W, scales=WS, rows=100, e=4, dt=BF, dwt=BF, beta=0.0, dw=Y)
     (dict(rows=(1 << 30) + 1), UNSUPPORTED), (dict(e=(1 << 20) + 1), UNSUPPORTED),
     (dict(y=X), ALIAS), (dict(y=W + 64), ALIAS), (dict(y=OFF), ALIAS),
     (dict(y=X + 99 * 128 + 126), ALIAS),      # the last element of x
+    # columns of one buffer of 100 values a row: x has 64, y the 32 from column 63 on, or from 69 with a row's end in the next
+    (dict(ldx=100, ldy=100, y=X + 2 * 63), ALIAS), (dict(ldx=100, ldy=100, y=X + 2 * 69), ALIAS), (dict(ldx=100, ldy=100, y=X - 2 * 31), ALIAS),
 ])
 def test_grouped_linear_refusals(over, want):
     assert fwd(**over) == want
