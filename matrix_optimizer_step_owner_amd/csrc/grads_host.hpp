@@ -84,22 +84,27 @@ hipError_t launch_tile(const GroupArgs& g, hipStream_t stream) {
   });
 }
 
-using TileWgrad = GroupTile<256, 256, 2, 4, 1, 4>;        // both panels read along t: whole lines
+// Tiles.  Measured in us, bf16 unless said, experts x rows x n x k:
+using TileWgrad = GroupTile<256, 256, 2, 4, 1, 4>;        // both panels read along t
 using TileWgradSquare = GroupTile<128, 128, 2, 2, 1, 4>;  // two workgroups per CU
-using TileLarge = GroupTile<256, 256, 2, 4, 2, 2>;
+using TileLarge = GroupTile<256, 256, 2, 4, 2, 2>;        // whole 128-byte lines of t per row
 using TileWide = GroupTile<128, 256, 2, 4, 2, 3>;
 using TilePair = GroupTile<128, 256, 2, 2, 1, 3>;         // two workgroups per CU
-using TileSquare = GroupTile<128, 128, 2, 2, 2, 2>;       // two workgroups per CU
+using TileSquare = GroupTile<128, 128, 2, 2, 2, 2>;       // two workgroups per CU, through registers
 using TileSmall = GroupTile<64, 256, 1, 4, 1, 4>;         // two workgroups per CU
 using TileRows = GroupTile<32, 64, 1, 2, 4, 3, 4>;        // two workgroups per CU
+using TileFew = GroupTile<32, 32, 1, 1, 8, 3, 8>;
 using TileRowsReg = GroupTile<32, 64, 1, 2, 4, 2, 4>;
 using TileF32 = GroupTile<128, 128, 2, 2, 1, 4>;
 
 // Weight gradients: 256 x 256 tiles where n and k fill them and there are
 // enough for the 256 CUs, or where long segments can be cut into enough parts;
-// 128 x 128 tiles otherwise, two workgroups per CU.  Parts have a fixed number
-// of rows, so that experts of different lengths give equal work; a second
-// kernel sums them.  The choice depends on the sizes alone.
+// 128 x 128 tiles otherwise, two workgroups per CU (256 x 32771 x 512 x 1536:
+// 136 us with the large, 184 with the small ones; 8 x 2048 x 1536 x 1024: 19
+// either way).  Parts have a fixed number of rows, so that experts of different
+// lengths give equal work; a second kernel sums them (4 x 32768 x 512 x 512:
+// 201 us whole, 62 in equal numbers of parts per expert, 42 so).  The choice
+// depends on the sizes alone.
 struct WgradPlan {
   bool large;
   int32_t part_rows;   // 0: whole segments
@@ -151,10 +156,11 @@ hipError_t launch_wgrad(const GroupArgs& g, bool large, hipStream_t stream) {
   });
 }
 
+// Forward and input gradient.  Rows per expert (known on the host only on
+// average) decide the tile's height, the number of tiles whether there are
+// enough of that size for the 256 CUs.
 template <class E, int MODE>
 hipError_t launch_rows(const GroupArgs& g, bool dma, hipStream_t stream) {
-  // rows per expert decide the tile's height, and the number of tiles whether
-  // there are enough of that size for the 256 CUs
   const int64_t experts = std::min<int64_t>(g.experts, g.rows);
   const int64_t per = g.rows / experts;
   const int64_t width = MODE == kGroupFwd ? g.n : g.k, depth = MODE == kGroupFwd ? g.k : g.n;
@@ -162,21 +168,41 @@ hipError_t launch_rows(const GroupArgs& g, bool dma, hipStream_t stream) {
     const int64_t high = per < bp / 2 ? experts : g.rows / bp + experts / 2 + 1;
     return high * ceil_div(width, bq);
   };
+  auto few_rows = [&] {
+    // Under two tiles of 64 columns per four CUs, 32 columns and eight sets of
+    // waves: 256 x 8 x 512 x 1536 8.8 -> 7.6 us (fp32 21.7 -> 14.3), but with
+    // 224 tiles, 1 x 1 x 14336 x 4096, 21.8 -> 24.9.
+    if constexpr (MODE == kGroupFwd)
+      if (tiles(32, 64) <= 128) return launch_tile<E, MODE, TileFew, kLoadDma>(g, stream);
+    return launch_tile<E, MODE, TileRows, kLoadDma>(g, stream);
+  };
+  // Through registers: 7 x 2049 x 513 x 257 8.4 (few rows' tile) and 11.7 us,
+  // its input gradient 9.1 and 20.6; 8 x 8192 x 2047 x 2049 255 and 134 us.
   if (!dma)
     return per <= 48 || tiles(128, 128) < 128
                ? launch_tile<E, MODE, TileRowsReg, kLoadReg>(g, stream)
                : launch_tile<E, MODE, TileSquare, kLoadReg>(g, stream);
   if constexpr (E::kVec == 4) {
-    return per <= 96 || tiles(128, 128) < 192
-               ? launch_tile<E, MODE, TileRows, kLoadDma>(g, stream)
-               : launch_tile<E, MODE, TileF32, kLoadDma>(g, stream);
+    // fp32: 16 x 1024 x 2048 x 2048 104 (few rows) and 250 us; 64 x 8192 x 2048
+    // x 1024 equal; 1 x 8192 x 4096 x 4096 2279 and 1961 us.
+    return per <= 96 || tiles(128, 128) < 192 ? few_rows()
+                                              : launch_tile<E, MODE, TileF32, kLoadDma>(g, stream);
   } else {
-    if ((MODE == kGroupFwd && per <= 40) || tiles(64, 256) < 128)
-      return launch_tile<E, MODE, TileRows, kLoadDma>(g, stream);
+    // Forward of 32 x 1024 x 2048 x 2048: 61 us (51 streamed), 67 and more with
+    // taller tiles; its input gradient, whose narrow tiles read the weights in
+    // 128-byte pieces, 63, and 50 with taller ones.
+    if ((MODE == kGroupFwd && per <= 40) || tiles(64, 256) < 128) return few_rows();
+    // 64 x 1024 x 1024 x 2048, input gradient: 48 (64 rows) and 51 us
+    // (128 rows).
     if (per <= 24 || tiles(128, 256) < 100)
       return launch_tile<E, MODE, TileSmall, kLoadDma>(g, stream);
+    // 16 x 24576 x 5632 x 2048: 546 (256 rows) and 597 us (128 rows); 64 x 8192
+    // x 2048 x 1024, 128 rows per expert: 103 and 72 us.
     if (per >= 320 && tiles(256, 256) >= 256)
       return launch_tile<E, MODE, TileLarge, kLoadDma>(g, stream);
+    // Short sums leave a tile's start and end uncovered unless two workgroups
+    // share a CU: 256 x 32771 x 512 x 1536, input gradient (depth 512): 123
+    // (pair) and 136 us; forward (depth 1536): 134 and 120 us.
     return depth < 1024 && tiles(128, 256) >= 512
                ? launch_tile<E, MODE, TilePair, kLoadDma>(g, stream)
                : launch_tile<E, MODE, TileWide, kLoadDma>(g, stream);
