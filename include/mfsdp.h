@@ -15,6 +15,10 @@
  *   mfsdp_muon_step   -- Muon on the owner's list of whole matrices,
  *   mfsdp_adamw_tail  -- AdamW on a packed fp32 tail buffer.
  *
+ * Further down: the owner planner, packed tails, Shampoo-type statistics, and
+ * the operators that make the gradients of experts' matrices and of an
+ * embedding table.
+ *
  * Conventions shared by every entry point
  *   - Every pointer named "device" is a device (HBM) address on the current
  *     HIP device.  The caller owns every buffer; the library never allocates

@@ -12,7 +12,14 @@
 // of kEmbRun sorted positions by workgroups of their own, so that a frequent
 // token does not hold up one workgroup.  Results depend on nothing but the
 // inputs.
+//
+// Both are bound by HBM.  Lookup of 32768 rows of 4096 bf16 values: 76 us.
+// Gradient of the same list on a table of 100000 rows (1.64 GB written, 0.27
+// read): 416 us, of it 32 for the two passes of the sort, 25 for the partial
+// sums and 350 for the rows; filling the gradient with zeros alone takes 238.
 #pragma once
+
+#include <type_traits>
 
 #include "common.hpp"
 #include "ns_gemm.hpp"
