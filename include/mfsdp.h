@@ -379,7 +379,8 @@ mfsdp_status_t mfsdp_shampoo_stats(const mfsdp_stats_matrix_t* mats, int64_t n_m
  * Errors: MFSDP_ERR_INVALID_ARGUMENT (negative counts, widths < 1, strides
  * smaller than rows, null or misaligned pointers, non-finite beta),
  * MFSDP_ERR_UNSUPPORTED (dtypes; n, k or strides above 2^22, rows above 2^30,
- * n_experts above 2^20, more than 2^31 tiles), MFSDP_ERR_WORKSPACE,
+ * n_experts above 2^20, more than 2^23 tiles of 32 x 64 outputs or, for the
+ * weight gradient, of 128 x 128), MFSDP_ERR_WORKSPACE,
  * MFSDP_ERR_ALIAS, MFSDP_ERR_HIP.
  */
 mfsdp_status_t mfsdp_grouped_linear(const void* x, int64_t ld_x, const void* weight,
@@ -456,7 +457,9 @@ mfsdp_status_t mfsdp_ckpt_restore(const int8_t* codes, const uint8_t* scales, in
  * workspace  device, >= mfsdp_embedding_grad_workspace_size bytes, 256-byte
  *            aligned, scratch; none is needed for n_tokens == 0.
  * Errors: as above, MFSDP_ERR_WORKSPACE, and MFSDP_ERR_UNSUPPORTED for vocab
- * above 2^31 - 1, n_tokens above 2^28, d or strides above 2^22.
+ * above 2^31 - 1, n_tokens above 2^28, d or strides above 2^22, and for more
+ * than 2^24 workgroups (one takes four rows of up to 2048 columns of the
+ * gradient, or 4 KB of looked-up rows).
  */
 mfsdp_status_t mfsdp_embedding(const void* table, mfsdp_dtype_t table_dtype, int64_t vocab,
                                int64_t d, const void* tokens, int token_bytes, int64_t n_tokens,

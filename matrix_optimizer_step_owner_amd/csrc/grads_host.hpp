@@ -64,7 +64,9 @@ int64_t group_tiles_max(int64_t rows, int64_t experts, int64_t bp) {
   return (rows + std::min(rows, experts) * (bp - 1)) / bp;
 }
 
-constexpr int64_t kGroupBlocksMax = (int64_t(1) << 31) - 1;
+// Workgroups of a launch: a grid has fewer than 2^32 threads along x.
+constexpr int64_t kGroupBlocksMax = (int64_t(1) << 23) - 1;   // of 512 threads
+constexpr int64_t kBlocksMax = (int64_t(1) << 24) - 1;        // of 256
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
@@ -310,7 +312,10 @@ mfsdp_status_t grouped_impl(int mode, const void* p, int64_t ldp, const void* q,
   // the smallest tiles
   const int64_t blocks = mode == kGroupWgrad ? group_blocks(g, mode, 128, 128)
                                              : group_blocks(g, mode, 32, 64);
-  if (blocks > kGroupBlocksMax) return fail(MFSDP_ERR_UNSUPPORTED, "too many tiles");
+  // (and the sum of a weight gradient's parts, 2048 elements each)
+  const int64_t sums = plan.part_rows ? experts * ceil_div(n * k, 2048) : 0;
+  if (blocks > kGroupBlocksMax || sums > kBlocksMax)
+    return fail(MFSDP_ERR_UNSUPPORTED, "too many tiles");
   // 16-byte loads: every operand row starts on 16 bytes and has a whole number
   // of 16-byte pieces, and 256 rows of it lie within 2^31 bytes
   const int64_t v = 16 / static_cast<int64_t>(es);
@@ -360,7 +365,7 @@ mfsdp_status_t ckpt_impl(bool quantize, void* x, int64_t ld, int8_t* codes, uint
     if (st != MFSDP_OK) return st;
   }
   const int64_t blocks = (a.units + 16 * kCkptUnits - 1) / (16 * kCkptUnits);
-  if (blocks >= (int64_t(1) << 31)) return fail(MFSDP_ERR_UNSUPPORTED, "too many blocks");
+  if (blocks > kBlocksMax) return fail(MFSDP_ERR_UNSUPPORTED, "too many blocks");
   const dim3 grid(static_cast<unsigned>(blocks)), wg(256);
   const hipError_t e = launch(MFSDP_KERNEL_CKPT, stream, [&] {
     if (quantize) {
@@ -441,7 +446,7 @@ mfsdp_status_t embedding_impl(const void* table, mfsdp_dtype_t table_dtype, int6
     a.per_wg = static_cast<int32_t>(256 / units);
     blocks = (n_tokens + a.per_wg - 1) / a.per_wg;
   }
-  if (blocks >= (int64_t(1) << 31)) return fail(MFSDP_ERR_UNSUPPORTED, "too many rows");
+  if (blocks > kBlocksMax) return fail(MFSDP_ERR_UNSUPPORTED, "too many rows");
   const bool tb = table_dtype == MFSDP_DTYPE_BF16, ob = out_dtype == MFSDP_DTYPE_BF16;
   const hipError_t e = tb ? (ob ? launch_embedding<ElemBF16, ElemBF16>(a, vec, blocks, stream)
                                 : launch_embedding<ElemBF16, ElemF32>(a, vec, blocks, stream))
@@ -560,8 +565,8 @@ mfsdp_status_t embedding_grad_impl(const void* dy, int64_t ld, mfsdp_dtype_t dty
   int32_t tpr = 64;
   while (tpr < 256 && tpr * cols * kEmbGroups < d) tpr *= 2;
   const int64_t col_wgs = ceil_div(d, tpr * cols * kEmbGroups);
-  if (ceil_div(vocab, kEmbRows) * col_wgs > kGroupBlocksMax ||
-      ceil_div(n_tokens, kEmbRun) * col_wgs + ceil_div(vocab, kEmbRows) / 256 + 2 > kGroupBlocksMax)
+  if (ceil_div(vocab, kEmbRows) * col_wgs > kBlocksMax ||
+      ceil_div(n_tokens, kEmbRun) * col_wgs + ceil_div(vocab, kEmbRows) / 256 + 2 > kBlocksMax)
     return fail(MFSDP_ERR_UNSUPPORTED, "too many rows");
 
   char* ws = static_cast<char*>(workspace);

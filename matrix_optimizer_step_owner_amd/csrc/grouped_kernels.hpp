@@ -506,7 +506,7 @@ __global__ __launch_bounds__(C::THREADS, C::OCC) void grouped_tile_kernel(GroupA
     for (int q = 0; q < PIECES; ++q) {
       const bool is_p = q < C::PP;
       const bool along = is_p ? kPT : kQT;
-      int n = along ? (klim[q] < left ? cnt[q] : 0) : min(max(left - klim[q], 0), V);
+      const int n = klim[q] >= left ? 0 : along ? cnt[q] : min(left - klim[q], V);
       const char* src = (is_p ? pbase : qbase) + voff[q];
       uint4 v = make_uint4(0, 0, 0, 0);
       if (LOAD == kLoadRegCkpt && !is_p) {

@@ -42,6 +42,7 @@ def wgrad_ckpt(codes=W, scales=WS, rows=100, e=4, dt=BF, dwt=BF, beta=0.0, dw=Y)
     (dict(x=X + 1), INVALID), (dict(off=OFF + 2), INVALID), (dict(y=Y + 2, dt=F32), INVALID),
     (dict(dt=7), UNSUPPORTED), (dict(k=(1 << 24) + 1, ldx=(1 << 24) + 1), UNSUPPORTED),
     (dict(rows=(1 << 30) + 1), UNSUPPORTED), (dict(e=(1 << 20) + 1), UNSUPPORTED),
+    (dict(rows=1 << 28, n=64, ldy=64, k=1, ldx=1, x=A, w=A + 8 * GB, off=A + 9 * GB, y=A + 16 * GB), UNSUPPORTED),   # 2^23 tiles
     (dict(y=X), ALIAS), (dict(y=W + 64), ALIAS), (dict(y=OFF), ALIAS),
     (dict(y=X + 99 * 128 + 126), ALIAS),      # the last element of x
     # columns of one buffer of 100 values a row: x has 64, y the 32 from column 63 on, or from 69 with a row's end in the next
