@@ -770,11 +770,31 @@ __global__ __launch_bounds__(C::THREADS, C::OCC) void grouped_tile_kernel(GroupA
       for (int i = 0; i < 5; ++i) convert(0, 0, i);
       asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
     }
+    // A wave whose rows or columns the tile does not have only moves data: its
+    // share of the SIMD is the other waves' (16 x 24576 x 5632 x 2048 forward:
+    // 547 -> 536 us).  Not in weight gradients, whose tiles are seldom cut: 110
+    // -> 114 us on 256 x 32771 x 512 x 1536.
+    const bool idle = MODE != kGroupWgrad && (wp * TP * 32 >= prem || wq * TQ * 32 >= qrem);
+    if (idle) {
+#pragma unroll 1
+      for (int t = 0; t < nk; ++t) {
+#pragma unroll
+        for (int q = kEarly; q < PIECES; ++q) dma_piece(fill, q);
+        dma_next();
+        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier"
+                     :: "n"((C::STAGES - 2) * PIECES) : "memory");
+#pragma unroll
+        for (int q = 0; q < kEarly; ++q) dma_piece(cur, q);
+        fill = cur;
+        cur = cur + kStage == kStagesEnd ? 0 : cur + kStage;
+      }
+    }
+    const int steps = idle ? 0 : nk;
     uint32_t qcur = 0;
 #pragma unroll
     for (int r = 0; r < kReads; ++r) read_piece(0, 0, 0, r, fp[0], fq[0]);
 #pragma unroll 1
-    for (int t = 0; t < nk; ++t) {
+    for (int t = 0; t < steps; ++t) {
       const uint32_t nxt = cur + kStage == kStagesEnd ? 0 : cur + kStage;
       if constexpr (CKPT) {
         // the next group's scales: loaded at the start of a group, stored half
