@@ -17,6 +17,7 @@ weights with their whole gradients; the other tensors are packed for AdamW).
 from __future__ import annotations
 
 import ctypes
+import threading
 from typing import Callable, Dict, Optional, Tuple
 
 import torch
@@ -96,10 +97,18 @@ def _call(device: torch.device, name: str, *args) -> None:
         _lib.check(status)
 
 
+# The workspaces kept for calls that bring none, one per (device, stream) and
+# host thread.  Calls on one stream run in order and can share one, but only if
+# their launches are enqueued in order too: another thread may run between the
+# launches of one call, so each has its own.
+_kept = threading.local()
+
+
 def _scratch(device: torch.device, nbytes: int, given: Optional[torch.Tensor]) -> torch.Tensor:
-    """The caller's workspace; else one kept per (device, stream), which calls
-    on that stream share in order; else, under capture, one that belongs to the
-    graph (a kept one could be replayed by two graphs at once)."""
+    """The caller's workspace; else this thread's kept one of the current
+    stream; else, under capture, one that belongs to the graph (a kept one could
+    be replayed by two graphs at once).  The caller holds it until the launches
+    are enqueued."""
     if given is not None:
         _check(given, "workspace", device, (given.dtype,), given.dim())
         _contiguous(given, "workspace")
@@ -107,8 +116,13 @@ def _scratch(device: torch.device, nbytes: int, given: Optional[torch.Tensor]) -
     with torch.cuda.device(device):
         if torch.cuda.is_current_stream_capturing():
             return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
-    from . import _workspace
-    return _workspace(device, _raw_stream(device.index), nbytes)
+        key = (device.index, _raw_stream(device.index))
+        kept = _kept.__dict__
+        ws = kept.get(key)
+        if ws is None or ws.numel() < nbytes:
+            kept.pop(key, None)
+            ws = kept[key] = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
+        return ws
 
 
 def _grouped_args(act: torch.Tensor, name: str, weight: torch.Tensor, wname: str,
@@ -163,14 +177,19 @@ def grouped_linear_dgrad(dy: torch.Tensor, weight: torch.Tensor, offsets: torch.
     return _grouped_rows("mfsdp_grouped_linear_dgrad", dy, weight, offsets, out, False)
 
 
-def _wgrad_scratch(device: torch.device, sizes, given: Optional[torch.Tensor]):
-    """(address, bytes) of the workspace of a weight gradient, (None, 0) if it needs none."""
+def _wgrad_scratch(device: torch.device, sizes,
+                   given: Optional[torch.Tensor]) -> Optional[torch.Tensor]:
+    """The workspace of a weight gradient, None if it needs none."""
     need = ctypes.c_size_t(0)
     _lib.check(_lib.load().mfsdp_grouped_linear_wgrad_workspace_size(*sizes, ctypes.byref(need)))
     if need.value == 0 and given is None:
-        return None, 0
-    ws = _scratch(device, need.value, given)
-    return ws.data_ptr(), ws.numel() * ws.element_size()
+        return None
+    return _scratch(device, need.value, given)
+
+
+def _span(ws: Optional[torch.Tensor]):
+    """(address, bytes) of a workspace."""
+    return (None, 0) if ws is None else (ws.data_ptr(), ws.numel() * ws.element_size())
 
 
 def grouped_linear_wgrad(dy: torch.Tensor, x: torch.Tensor, offsets: torch.Tensor,
@@ -183,16 +202,20 @@ def grouped_linear_wgrad(dy: torch.Tensor, x: torch.Tensor, offsets: torch.Tenso
     dy: (rows, n), x: (rows, k), one dtype; grad: (experts, n, k) contiguous in
     that dtype or fp32, each ``grad[e]`` as ``muon_step`` takes it.  beta = 1
     adds a micro-batch to what is there; beta = 0 does not read it.  An expert
-    without rows gets ``beta * grad[e]``.  Returns grad."""
+    without rows gets ``beta * grad[e]``.  Returns grad.
+
+    workspace: scratch of at least mfsdp_grouped_linear_wgrad_workspace_size
+    bytes, 256-byte aligned; without it one is kept per stream and host thread.
+    One that is given is for one stream and one host thread at a time."""
     dtype = dy.dtype if isinstance(dy, torch.Tensor) else None
     device, (experts, n, k) = _grouped_args(dy, "dy", grad, "grad", offsets,
                                             (dtype, torch.float32))
     rows = dy.shape[0]
     _check(x, "x", device, (dtype,), 2)
+    ws = _wgrad_scratch(device, (experts, rows, n, k, _DTYPES[dtype]), workspace)
     _call(device, "mfsdp_grouped_linear_wgrad", dy.data_ptr(), _rows(dy, "dy", (rows, n)),
           x.data_ptr(), _rows(x, "x", (rows, k)), offsets.data_ptr(), experts, rows, n, k,
-          _DTYPES[dtype], grad.data_ptr(), _DTYPES[grad.dtype], beta,
-          *_wgrad_scratch(device, (experts, rows, n, k, _DTYPES[dtype]), workspace))
+          _DTYPES[dtype], grad.data_ptr(), _DTYPES[grad.dtype], beta, *_span(ws))
     return grad
 
 
@@ -211,17 +234,17 @@ def grouped_linear_wgrad_ckpt(dy: torch.Tensor, codes: torch.Tensor, scales: tor
                               workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
     """``grouped_linear_wgrad`` with x as its 8-bit checkpoint, (codes, scales)
     of ``ckpt_quantize`` (mfsdp_grouped_linear_wgrad_ckpt): the gradient for the
-    restored x, which is never written out."""
+    restored x, which is never written out.  workspace: as there."""
     dtype = dy.dtype if isinstance(dy, torch.Tensor) else None
     device, (experts, n, k) = _grouped_args(dy, "dy", grad, "grad", offsets,
                                             (dtype, torch.float32))
     rows = dy.shape[0]
     _check_codes(codes, device, rows, k)
     _check_scales(scales, device, rows, k)
+    ws = _wgrad_scratch(device, (experts, rows, n, k, _DTYPES[dtype]), workspace)
     _call(device, "mfsdp_grouped_linear_wgrad_ckpt", dy.data_ptr(), _rows(dy, "dy", (rows, n)),
           codes.data_ptr(), scales.data_ptr(), offsets.data_ptr(), experts, rows, n, k,
-          _DTYPES[dtype], grad.data_ptr(), _DTYPES[grad.dtype], beta,
-          *_wgrad_scratch(device, (experts, rows, n, k, _DTYPES[dtype]), workspace))
+          _DTYPES[dtype], grad.data_ptr(), _DTYPES[grad.dtype], beta, *_span(ws))
     return grad
 
 
@@ -324,7 +347,11 @@ def embedding_grad(dy: torch.Tensor, tokens: torch.Tensor, grad: torch.Tensor, *
     grad: (vocab, d) fp32 contiguous, for example the table's segment of the
     packed gradient that ``adamw_tail`` takes.  The sums run over the tokens in
     sorted order and depend on the inputs alone.  beta = 1 adds a micro-batch
-    and leaves the rows without a token untouched.  Returns grad."""
+    and leaves the rows without a token untouched.  Returns grad.
+
+    workspace: scratch of at least mfsdp_embedding_grad_workspace_size bytes,
+    256-byte aligned; without it one is kept per stream and host thread.  One
+    that is given is for one stream and one host thread at a time."""
     device = _gpu(dy, "dy")
     _check(dy, "dy", device, _FLOATS, 2)
     _check(grad, "grad", device, (torch.float32,), 2)
@@ -337,6 +364,5 @@ def embedding_grad(dy: torch.Tensor, tokens: torch.Tensor, grad: torch.Tensor, *
     _lib.check(_lib.load().mfsdp_embedding_grad_workspace_size(n, vocab, d, ctypes.byref(need)))
     ws = _scratch(device, need.value, workspace)
     _call(device, "mfsdp_embedding_grad", dy.data_ptr(), ld, _DTYPES[dy.dtype],
-          tokens.data_ptr(), size, n, vocab, d, scale, beta, grad.data_ptr(), ws.data_ptr(),
-          ws.numel() * ws.element_size())
+          tokens.data_ptr(), size, n, vocab, d, scale, beta, grad.data_ptr(), *_span(ws))
     return grad

@@ -1,0 +1,73 @@
+"""Workspaces that the gradient operators keep for their callers: whose they
+are and how long they live.  Tensors are on the CPU and nothing is launched.
+"""
+
+import contextlib
+import threading
+import weakref
+
+import pytest
+import torch
+
+import matrix_optimizer_step_owner_amd as mf
+from matrix_optimizer_step_owner_amd import _lib, grads
+
+CPU = torch.device("cpu")
+
+
+@pytest.fixture
+def host(monkeypatch):
+    """One stream, no GPU; `capturing` may be set."""
+    state = {"capturing": False}
+    monkeypatch.setattr(torch.cuda, "device", lambda d: contextlib.nullcontext())
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: state["capturing"])
+    monkeypatch.setattr(grads, "_raw_stream", lambda index: 77, raising=False)
+    return state
+
+
+def test_kept_from_call_to_call(host):
+    a = grads._scratch(CPU, 5000, None)
+    assert grads._scratch(CPU, 400, None) is a and grads._scratch(CPU, 5000, None) is a
+    b = grads._scratch(CPU, 6000, None)
+    assert b.numel() >= 6000 and grads._scratch(CPU, 10, None) is b
+
+
+def test_host_threads_do_not_share_one(host):
+    # ctypes lets another thread run between the launches of one call: two
+    # threads on one stream would sort and sum in the same scratch
+    got = {}
+
+    def take(name):
+        got[name] = grads._scratch(CPU, 4096, None)
+
+    take("here")
+    t = threading.Thread(target=take, args=("there",))
+    t.start()
+    t.join()
+    assert got["here"].data_ptr() != got["there"].data_ptr()
+
+
+def test_held_until_the_call_has_been_made(host, monkeypatch):
+    # under capture the workspace belongs to this call alone: whoever has its
+    # address has to hold it
+    refs = []
+    empty = torch.empty
+
+    def watched(*args, **kwargs):
+        t = empty(*args, **kwargs)
+        refs.append(weakref.ref(t))
+        return t
+
+    host["capturing"] = True
+    monkeypatch.setattr(torch, "empty", watched)
+    held = grads._wgrad_scratch(CPU, (2, 10000, 32, 64, _lib.DTYPE_BF16), None)
+    assert len(refs) == 1 and refs[0]() is not None
+    del held
+
+
+def test_the_steps_workspace_is_not_replaced(host, monkeypatch):
+    # a captured Muon step keeps the address it was captured with
+    monkeypatch.setattr(mf, "_WS_CACHE", {})
+    ws = mf._workspace(CPU, 77, 1000)
+    grads._scratch(CPU, 100000, None)
+    assert mf._workspace(CPU, 77, 1000) is ws
