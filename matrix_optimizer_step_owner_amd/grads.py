@@ -33,9 +33,13 @@ _FLOATS = tuple(_DTYPES)
 
 # The current device and the handle of its current stream, without what
 # torch.cuda.current_device and current_stream (a Stream object) add around
-# them: together over a microsecond a call.
-_current_device = torch._C._cuda_getDevice
-_raw_stream = torch._C._cuda_getCurrentRawStream
+# them: together over a microsecond a call.  Looked up when called: a torch
+# without a GPU backend has neither.
+_C = torch._C
+
+
+def _raw_stream(index: int) -> int:
+    return _C._cuda_getCurrentRawStream(index)
 
 
 def _check(t: torch.Tensor, name: str, device, dtypes, dim: int) -> None:
@@ -88,8 +92,8 @@ def _call(device: torch.device, name: str, *args) -> None:
     if fn is None:
         fn = _functions[name] = getattr(_lib.load(), name)
     index = device.index
-    if index == _current_device():
-        status = fn(*args, _raw_stream(index))
+    if index == _C._cuda_getDevice():
+        status = fn(*args, _C._cuda_getCurrentRawStream(index))
     else:
         with torch.cuda.device(device):
             status = fn(*args, _raw_stream(index))

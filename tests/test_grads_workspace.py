@@ -3,6 +3,9 @@ are and how long they live.  Tensors are on the CPU and nothing is launched.
 """
 
 import contextlib
+import os
+import subprocess
+import sys
 import threading
 import weakref
 
@@ -13,6 +16,7 @@ import matrix_optimizer_step_owner_amd as mf
 from matrix_optimizer_step_owner_amd import _lib, grads
 
 CPU = torch.device("cpu")
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 @pytest.fixture
@@ -71,3 +75,15 @@ def test_the_steps_workspace_is_not_replaced(host, monkeypatch):
     ws = mf._workspace(CPU, 77, 1000)
     grads._scratch(CPU, 100000, None)
     assert mf._workspace(CPU, 77, 1000) is ws
+
+
+def test_import_without_a_gpu_backend():
+    # a torch built for the CPU has none of these; the planner, the workloads
+    # and the library's host functions need no GPU
+    code = ("import torch\n"
+            "for name in [n for n in dir(torch._C) if n.startswith('_cuda_')]:\n"
+            "    delattr(torch._C, name)\n"
+            "import matrix_optimizer_step_owner_amd as mf\n"
+            "from matrix_optimizer_step_owner_amd import workloads\n"
+            "assert mf.CKPT_BLOCK == 128 and mf.default_scale(8, 2) == 2.0\n")
+    subprocess.run([sys.executable, "-c", code], check=True, cwd=ROOT, timeout=300)
