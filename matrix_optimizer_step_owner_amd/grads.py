@@ -114,6 +114,8 @@ def _scratch(device: torch.device, nbytes: int, given: Optional[torch.Tensor]) -
     be replayed by two graphs at once).  The caller holds it until the launches
     are enqueued."""
     if given is not None:
+        if not isinstance(given, torch.Tensor):
+            raise TypeError("workspace must be a tensor")
         _check(given, "workspace", device, (given.dtype,), given.dim())
         _contiguous(given, "workspace")
         return given
@@ -306,6 +308,15 @@ def _check_tokens(tokens: torch.Tensor, device) -> int:
     return 8 if tokens.dtype is torch.int64 else 4
 
 
+def _embedding_out(out: torch.Tensor, dtype: Optional[torch.dtype], device, n: int,
+                   d: int) -> int:
+    """Row stride of the caller's output."""
+    _check(out, "out", device, _FLOATS if dtype is None else (dtype,), 2)
+    if out.dtype not in _DTYPES:
+        raise TypeError(f"unsupported dtype {out.dtype}")
+    return _rows(out, "out", (n, d))
+
+
 def embedding(table: torch.Tensor, tokens: torch.Tensor, *, scale: float = 1.0,
               dtype: Optional[torch.dtype] = None,
               out: Optional[torch.Tensor] = None) -> torch.Tensor:
@@ -330,10 +341,7 @@ def embedding(table: torch.Tensor, tokens: torch.Tensor, *, scale: float = 1.0,
         out = table.new_empty((*tokens.shape, d), dtype=dtype)
         ldo = d
     else:
-        if dtype is not None and dtype != out.dtype:
-            raise TypeError(f"out has dtype {out.dtype}, expected {dtype}")
-        _check(out, "out", device, _FLOATS, 2)
-        ldo = _rows(out, "out", (n, d))
+        ldo = _embedding_out(out, dtype, device, n, d)
         dtype = out.dtype
     _call(device, "mfsdp_embedding", table.data_ptr(), _DTYPES[table.dtype], vocab, d,
           tokens.data_ptr(), size, n, scale, out.data_ptr(), ldo, _DTYPES[dtype])

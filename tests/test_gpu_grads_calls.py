@@ -54,3 +54,17 @@ def test_host_threads_on_one_stream():
     for i in range(2):
         for g, w in got[i]:
             assert torch.equal(g, want[i][0]) and torch.equal(w, want[i][1])
+
+
+def test_arguments_that_are_not_tensors():
+    x, off = rand((4, 8), BF, 1).to(DEV), offsets_of([4]).to(DEV)
+    w, t = torch.zeros(1, 8, 8, device=DEV), torch.zeros(4, dtype=torch.int64, device=DEV)
+    for call in (lambda: mf.grouped_linear_wgrad(x, x, off, w, workspace=[1]),
+                 lambda: mf.grouped_linear_wgrad_ckpt(x, *mf.ckpt_quantize(x), off, w, workspace=[1]),
+                 lambda: mf.embedding_grad(x, t, w[0], workspace=256), lambda: mf.embedding(w[0], t, out=[1.0]),
+                 lambda: mf.embedding(w[0], t, dtype=BF, out=[1.0]), lambda: mf.embedding(w[0], [0, 1]),
+                 lambda: mf.grouped_linear(x, [1], off), lambda: mf.grouped_linear(x, w.to(BF), off, out=3),
+                 lambda: mf.grouped_linear_wgrad(x, None, off, w), lambda: mf.ckpt_restore(3, None),
+                 lambda: mf.ckpt_restore(mf.ckpt_quantize(x)[0], None), lambda: mf.ckpt_quantize(x, codes=1)):
+        with pytest.raises(TypeError, match="must be a tensor"):
+            call()

@@ -87,3 +87,27 @@ def test_import_without_a_gpu_backend():
             "from matrix_optimizer_step_owner_amd import workloads\n"
             "assert mf.CKPT_BLOCK == 128 and mf.default_scale(8, 2) == 2.0\n")
     subprocess.run([sys.executable, "-c", code], check=True, cwd=ROOT, timeout=300)
+
+
+@pytest.mark.parametrize("what", [[1.0], 4096, "scratch"])
+def test_arguments_that_are_not_tensors(host, what):
+    with pytest.raises(TypeError, match="workspace must be a tensor"):
+        grads._scratch(CPU, 256, what)
+    with pytest.raises(TypeError, match="workspace must be a tensor"):
+        grads._wgrad_scratch(CPU, (1, 1, 1, 1, _lib.DTYPE_BF16), what)
+    with pytest.raises(TypeError, match="out must be a tensor"):
+        grads._embedding_out(what, torch.bfloat16, CPU, 3, 8)
+    with pytest.raises(TypeError, match="out must be a tensor"):
+        grads._embedding_out(what, None, CPU, 3, 8)
+
+
+def test_embedding_out():
+    out = torch.zeros(3, 10)
+    assert grads._embedding_out(out[:, :8], None, CPU, 3, 8) == 10
+    assert grads._embedding_out(out[:, :8], torch.float32, CPU, 3, 8) == 10
+    with pytest.raises(TypeError, match="expected torch.bfloat16"):
+        grads._embedding_out(out[:, :8], torch.bfloat16, CPU, 3, 8)
+    with pytest.raises(TypeError, match="dtype"):
+        grads._embedding_out(out.double()[:, :8], None, CPU, 3, 8)
+    with pytest.raises(ValueError, match="shape"):
+        grads._embedding_out(out, None, CPU, 3, 8)
