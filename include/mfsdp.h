@@ -413,6 +413,33 @@ mfsdp_status_t mfsdp_grouped_linear_wgrad_ckpt(const void* dy, int64_t ld_dy, co
                                                hipStream_t stream);
 
 /*
+ * The kernel that a product of these sizes is computed with (host arithmetic,
+ * no GPU): what a profile, or a test that means to run a certain kernel, checks
+ * its sizes against.  rows_aligned: whether every operand row starts on 16
+ * bytes.  A call that launches nothing gives zeros.
+ * Errors: MFSDP_ERR_INVALID_ARGUMENT, MFSDP_ERR_UNSUPPORTED, as the product's.
+ */
+typedef enum mfsdp_grouped_product {
+  MFSDP_GROUPED_FORWARD = 0,
+  MFSDP_GROUPED_DGRAD = 1,
+  MFSDP_GROUPED_WGRAD = 2,
+  MFSDP_GROUPED_WGRAD_CKPT = 3
+} mfsdp_grouped_product_t;
+
+typedef struct mfsdp_grouped_tile {
+  int32_t rows, cols;     /* outputs of one workgroup                        */
+  int32_t threads;        /* of one workgroup                                */
+  int32_t wave_sets;      /* sets of waves that share each step of the sum   */
+  int32_t lds_dma;        /* 1: operands go to LDS directly, 0: by registers */
+  int32_t part_rows;      /* weight gradient in parts: rows of one, else 0   */
+  int64_t workgroups;     /* of the launch, some of them without work        */
+} mfsdp_grouped_tile_t;
+
+mfsdp_status_t mfsdp_grouped_linear_tile(mfsdp_grouped_product_t product, int64_t n_experts,
+                                         int64_t rows, int64_t n, int64_t k, mfsdp_dtype_t dtype,
+                                         int rows_aligned, mfsdp_grouped_tile_t* out);
+
+/*
  * Activation checkpoints in 8 bits: a copy of an activation, half (bf16) or a
  * quarter (fp32) of its size, kept from the forward to the backward pass.
  * Each row is cut into blocks of MFSDP_CKPT_BLOCK columns (the last may be

@@ -28,7 +28,7 @@ EXPORTED = ("mfsdp_muon_workspace_size", "mfsdp_muon_step", "mfsdp_muon_step_noa
             "mfsdp_plan_owners", "mfsdp_tail_layout", "mfsdp_tail_pack",
             "mfsdp_tail_unpack", "mfsdp_stats_workspace_size", "mfsdp_shampoo_stats",
             "mfsdp_grouped_linear", "mfsdp_grouped_linear_dgrad", "mfsdp_grouped_linear_wgrad",
-            "mfsdp_grouped_linear_wgrad_workspace_size",
+            "mfsdp_grouped_linear_wgrad_workspace_size", "mfsdp_grouped_linear_tile",
             "mfsdp_grouped_linear_wgrad_ckpt", "mfsdp_ckpt_quantize", "mfsdp_ckpt_restore",
             "mfsdp_embedding", "mfsdp_embedding_grad_workspace_size", "mfsdp_embedding_grad",
             "mfsdp_status_string", "mfsdp_last_error",
@@ -52,6 +52,16 @@ class MfsdpStatsMatrix(ctypes.Structure):
                 ("right", ctypes.c_void_p),
                 ("rows", ctypes.c_int64),
                 ("cols", ctypes.c_int64)]
+
+
+class MfsdpGroupedTile(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int32),
+                ("cols", ctypes.c_int32),
+                ("threads", ctypes.c_int32),
+                ("wave_sets", ctypes.c_int32),
+                ("lds_dma", ctypes.c_int32),
+                ("part_rows", ctypes.c_int32),
+                ("workgroups", ctypes.c_int64)]
 
 
 class MfsdpError(RuntimeError):
@@ -136,6 +146,9 @@ def load() -> ctypes.CDLL:
         lib.mfsdp_grouped_linear_wgrad_workspace_size.argtypes = [i64, i64, i64, i64, c.c_int,
                                                                   c.POINTER(c.c_size_t)]
         lib.mfsdp_grouped_linear_wgrad_workspace_size.restype = c.c_int
+        lib.mfsdp_grouped_linear_tile.argtypes = [c.c_int, i64, i64, i64, i64, c.c_int, c.c_int,
+                                                  c.POINTER(MfsdpGroupedTile)]
+        lib.mfsdp_grouped_linear_tile.restype = c.c_int
         lib.mfsdp_ckpt_quantize.argtypes = [ptr, i64, i64, i64, c.c_int, ptr, ptr, ptr]
         lib.mfsdp_ckpt_quantize.restype = c.c_int
         lib.mfsdp_ckpt_restore.argtypes = [ptr, ptr, i64, i64, c.c_int, ptr, i64, ptr]

@@ -136,15 +136,92 @@ WgradPlan wgrad_plan(int64_t experts, int64_t rows, int64_t n, int64_t k, bool b
   return p;
 }
 
+// The kernels by name.  The rules below choose one from sizes, types and
+// alignment; launches and mfsdp_grouped_linear_tile both go by them.
+enum GroupKernel {
+  kUseLarge, kUseWide, kUsePair, kUseSmall, kUseRows, kUseFew, kUseF32,   // forward, input gradient
+  kUseSquareReg, kUseRowsReg,                                             // ... through registers
+  kUseWgrad, kUseWgradSquare, kUseWgradF32, kUseWgradReg                  // weight gradient
+};
+
+struct GroupShape {
+  int32_t rows, cols, threads, wave_sets;
+  bool dma;
+};
+
+template <class C>
+constexpr GroupShape shape_of(bool dma) {
+  return {C::BP, C::BQ, C::THREADS, C::KS, dma};
+}
+
+GroupShape group_shape(GroupKernel u) {
+  switch (u) {
+    case kUseLarge: return shape_of<TileLarge>(true);
+    case kUseWide: return shape_of<TileWide>(true);
+    case kUsePair: return shape_of<TilePair>(true);
+    case kUseSmall: return shape_of<TileSmall>(true);
+    case kUseRows: return shape_of<TileRows>(true);
+    case kUseFew: return shape_of<TileFew>(true);
+    case kUseF32: case kUseWgradF32: return shape_of<TileF32>(true);
+    case kUseRowsReg: return shape_of<TileRowsReg>(false);
+    case kUseWgrad: return shape_of<TileWgrad>(true);
+    case kUseWgradSquare: return shape_of<TileWgradSquare>(true);
+    case kUseSquareReg: case kUseWgradReg: break;
+  }
+  return shape_of<TileSquare>(false);
+}
+
+// Weight gradient.
+GroupKernel wgrad_kernel(bool bf, bool dma, bool large) {
+  return !dma ? kUseWgradReg : !bf ? kUseWgradF32 : large ? kUseWgrad : kUseWgradSquare;
+}
+
+// Forward and input gradient.  Rows per expert (known on the host only on
+// average) decide the tile's height, the number of tiles whether there are
+// enough of that size for the 256 CUs.
+GroupKernel rows_kernel(int mode, const GroupArgs& g, bool bf, bool dma) {
+  const int64_t experts = std::min<int64_t>(g.experts, g.rows);
+  const int64_t per = g.rows / experts;
+  const int64_t width = mode == kGroupFwd ? g.n : g.k, depth = mode == kGroupFwd ? g.k : g.n;
+  auto tiles = [&](int64_t bp, int64_t bq) {   // an expert with few rows has one row tile
+    const int64_t high = per < bp / 2 ? experts : g.rows / bp + experts / 2 + 1;
+    return high * ceil_div(width, bq);
+  };
+  // Under two tiles of 64 columns per four CUs, 32 columns and eight sets of
+  // waves: 256 x 8 x 512 x 1536 8.8 -> 7.6 us (fp32 21.7 -> 14.3), but with
+  // 224 tiles, 1 x 1 x 14336 x 4096, 21.8 -> 24.9.
+  const GroupKernel few_rows = mode == kGroupFwd && tiles(32, 64) <= 128 ? kUseFew : kUseRows;
+  // Through registers: 7 x 2049 x 513 x 257 8.4 (few rows' tile) and 11.7 us,
+  // its input gradient 9.1 and 20.6; 8 x 8192 x 2047 x 2049 255 and 134 us.
+  if (!dma) return per <= 48 || tiles(128, 128) < 128 ? kUseRowsReg : kUseSquareReg;
+  // fp32: 16 x 1024 x 2048 x 2048 104 (few rows) and 250 us; 64 x 8192 x 2048
+  // x 1024 equal; 1 x 8192 x 4096 x 4096 2279 and 1961 us.
+  if (!bf) return per <= 96 || tiles(128, 128) < 192 ? few_rows : kUseF32;
+  // Forward of 32 x 1024 x 2048 x 2048: 61 us (51 streamed), 67 and more with
+  // taller tiles; its input gradient, whose narrow tiles read the weights in
+  // 128-byte pieces, 63, and 50 with taller ones.
+  if ((mode == kGroupFwd && per <= 40) || tiles(64, 256) < 128) return few_rows;
+  // 64 x 1024 x 1024 x 2048, input gradient: 48 (64 rows) and 51 us
+  // (128 rows).
+  if (per <= 24 || tiles(128, 256) < 100) return kUseSmall;
+  // 16 x 24576 x 5632 x 2048: 546 (256 rows) and 597 us (128 rows); 64 x 8192
+  // x 2048 x 1024, 128 rows per expert: 103 and 72 us.
+  if (per >= 320 && tiles(256, 256) >= 256) return kUseLarge;
+  // Short sums leave a tile's start and end uncovered unless two workgroups
+  // share a CU: 256 x 32771 x 512 x 1536, input gradient (depth 512): 123
+  // (pair) and 136 us; forward (depth 1536): 134 and 120 us.
+  return depth < 1024 && tiles(128, 256) >= 512 ? kUsePair : kUseWide;
+}
+
 template <class E, int LOAD>
-hipError_t launch_wgrad(const GroupArgs& g, bool large, hipStream_t stream) {
+hipError_t launch_wgrad(const GroupArgs& g, GroupKernel use, hipStream_t stream) {
   hipError_t e;
   if constexpr (LOAD == kLoadReg || LOAD == kLoadRegCkpt)
     e = launch_tile<E, kGroupWgrad, TileSquare, LOAD>(g, stream);
   else if constexpr (E::kVec == 4)
     e = launch_tile<E, kGroupWgrad, TileF32, LOAD>(g, stream);
   else
-    e = large
+    e = use == kUseWgrad
             ? launch_tile<E, kGroupWgrad, TileWgrad, LOAD>(g, stream)
             : launch_tile<E, kGroupWgrad, TileWgradSquare, LOAD>(g, stream);
   if (e != hipSuccess || g.part_rows == 0) return e;
@@ -158,67 +235,52 @@ hipError_t launch_wgrad(const GroupArgs& g, bool large, hipStream_t stream) {
   });
 }
 
-// Forward and input gradient.  Rows per expert (known on the host only on
-// average) decide the tile's height, the number of tiles whether there are
-// enough of that size for the 256 CUs.
 template <class E, int MODE>
-hipError_t launch_rows(const GroupArgs& g, bool dma, hipStream_t stream) {
-  const int64_t experts = std::min<int64_t>(g.experts, g.rows);
-  const int64_t per = g.rows / experts;
-  const int64_t width = MODE == kGroupFwd ? g.n : g.k, depth = MODE == kGroupFwd ? g.k : g.n;
-  auto tiles = [&](int64_t bp, int64_t bq) {   // an expert with few rows has one row tile
-    const int64_t high = per < bp / 2 ? experts : g.rows / bp + experts / 2 + 1;
-    return high * ceil_div(width, bq);
-  };
-  auto few_rows = [&] {
-    // Under two tiles of 64 columns per four CUs, 32 columns and eight sets of
-    // waves: 256 x 8 x 512 x 1536 8.8 -> 7.6 us (fp32 21.7 -> 14.3), but with
-    // 224 tiles, 1 x 1 x 14336 x 4096, 21.8 -> 24.9.
-    if constexpr (MODE == kGroupFwd)
-      if (tiles(32, 64) <= 128) return launch_tile<E, MODE, TileFew, kLoadDma>(g, stream);
-    return launch_tile<E, MODE, TileRows, kLoadDma>(g, stream);
-  };
-  // Through registers: 7 x 2049 x 513 x 257 8.4 (few rows' tile) and 11.7 us,
-  // its input gradient 9.1 and 20.6; 8 x 8192 x 2047 x 2049 255 and 134 us.
-  if (!dma)
-    return per <= 48 || tiles(128, 128) < 128
-               ? launch_tile<E, MODE, TileRowsReg, kLoadReg>(g, stream)
-               : launch_tile<E, MODE, TileSquare, kLoadReg>(g, stream);
-  if constexpr (E::kVec == 4) {
-    // fp32: 16 x 1024 x 2048 x 2048 104 (few rows) and 250 us; 64 x 8192 x 2048
-    // x 1024 equal; 1 x 8192 x 4096 x 4096 2279 and 1961 us.
-    return per <= 96 || tiles(128, 128) < 192 ? few_rows()
-                                              : launch_tile<E, MODE, TileF32, kLoadDma>(g, stream);
-  } else {
-    // Forward of 32 x 1024 x 2048 x 2048: 61 us (51 streamed), 67 and more with
-    // taller tiles; its input gradient, whose narrow tiles read the weights in
-    // 128-byte pieces, 63, and 50 with taller ones.
-    if ((MODE == kGroupFwd && per <= 40) || tiles(64, 256) < 128) return few_rows();
-    // 64 x 1024 x 1024 x 2048, input gradient: 48 (64 rows) and 51 us
-    // (128 rows).
-    if (per <= 24 || tiles(128, 256) < 100)
-      return launch_tile<E, MODE, TileSmall, kLoadDma>(g, stream);
-    // 16 x 24576 x 5632 x 2048: 546 (256 rows) and 597 us (128 rows); 64 x 8192
-    // x 2048 x 1024, 128 rows per expert: 103 and 72 us.
-    if (per >= 320 && tiles(256, 256) >= 256)
-      return launch_tile<E, MODE, TileLarge, kLoadDma>(g, stream);
-    // Short sums leave a tile's start and end uncovered unless two workgroups
-    // share a CU: 256 x 32771 x 512 x 1536, input gradient (depth 512): 123
-    // (pair) and 136 us; forward (depth 1536): 134 and 120 us.
-    return depth < 1024 && tiles(128, 256) >= 512
-               ? launch_tile<E, MODE, TilePair, kLoadDma>(g, stream)
-               : launch_tile<E, MODE, TileWide, kLoadDma>(g, stream);
+hipError_t launch_rows(const GroupArgs& g, GroupKernel use, hipStream_t stream) {
+  switch (use) {
+    case kUseRows: return launch_tile<E, MODE, TileRows, kLoadDma>(g, stream);
+    case kUseRowsReg: return launch_tile<E, MODE, TileRowsReg, kLoadReg>(g, stream);
+    case kUseSquareReg: return launch_tile<E, MODE, TileSquare, kLoadReg>(g, stream);
+    default: break;
   }
+  if constexpr (MODE == kGroupFwd)
+    if (use == kUseFew) return launch_tile<E, MODE, TileFew, kLoadDma>(g, stream);
+  if constexpr (E::kVec == 4) {
+    if (use == kUseF32) return launch_tile<E, MODE, TileF32, kLoadDma>(g, stream);
+  } else {
+    switch (use) {
+      case kUseLarge: return launch_tile<E, MODE, TileLarge, kLoadDma>(g, stream);
+      case kUseWide: return launch_tile<E, MODE, TileWide, kLoadDma>(g, stream);
+      case kUsePair: return launch_tile<E, MODE, TilePair, kLoadDma>(g, stream);
+      case kUseSmall: return launch_tile<E, MODE, TileSmall, kLoadDma>(g, stream);
+      default: break;
+    }
+  }
+  return hipErrorInvalidValue;   // no kernel of this type and direction
 }
 
 template <class E>
-hipError_t launch_grouped(int mode, const GroupArgs& g, bool dma, bool large, hipStream_t stream) {
-  if (mode == kGroupFwd) return launch_rows<E, kGroupFwd>(g, dma, stream);
-  if (mode == kGroupDgrad) return launch_rows<E, kGroupDgrad>(g, dma, stream);
-  if (!g.qs) return dma ? launch_wgrad<E, kLoadDma>(g, large, stream) : launch_wgrad<E, kLoadReg>(g, large, stream);
+hipError_t launch_grouped(int mode, const GroupArgs& g, GroupKernel use, hipStream_t stream) {
+  if (mode == kGroupFwd) return launch_rows<E, kGroupFwd>(g, use, stream);
+  if (mode == kGroupDgrad) return launch_rows<E, kGroupDgrad>(g, use, stream);
+  const bool dma = use != kUseWgradReg;
+  if (!g.qs) return dma ? launch_wgrad<E, kLoadDma>(g, use, stream) : launch_wgrad<E, kLoadReg>(g, use, stream);
   if constexpr (E::kVec == 8)
-    if (dma) return launch_wgrad<E, kLoadDmaCkpt>(g, large, stream);
-  return launch_wgrad<E, kLoadRegCkpt>(g, large, stream);
+    if (dma) return launch_wgrad<E, kLoadDmaCkpt>(g, use, stream);
+  return launch_wgrad<E, kLoadRegCkpt>(g, use, stream);
+}
+
+// Whether operands can go to LDS by 16-byte DMA, rows starting on 16 bytes: they
+// have a whole number of 16-byte pieces, and 256 of them lie within 2^31 bytes
+// (`widest`: the largest width or stride).
+bool group_dma(int mode, bool codes, bool bf, int64_t n, int64_t k, int64_t widest) {
+  const int64_t es = bf ? 2 : 4, v = 16 / es;
+  return (!codes || (bf && k % 16 == 0)) && k % v == 0 && (n % v == 0 || mode == kGroupFwd) &&
+         widest * es < (int64_t(1) << 23);
+}
+
+GroupKernel group_kernel(int mode, const GroupArgs& g, bool bf, bool dma, const WgradPlan& plan) {
+  return mode == kGroupWgrad ? wgrad_kernel(bf, dma, plan.large) : rows_kernel(mode, g, bf, dma);
 }
 
 mfsdp_status_t grouped_sizes(int64_t experts, int64_t rows, int64_t n, int64_t k,
@@ -316,14 +378,12 @@ mfsdp_status_t grouped_impl(int mode, const void* p, int64_t ldp, const void* q,
   const int64_t sums = plan.part_rows ? experts * ceil_div(n * k, 2048) : 0;
   if (blocks > kGroupBlocksMax || sums > kBlocksMax)
     return fail(MFSDP_ERR_UNSUPPORTED, "too many tiles");
-  // 16-byte loads: every operand row starts on 16 bytes and has a whole number
-  // of 16-byte pieces, and 256 rows of it lie within 2^31 bytes
   const int64_t v = 16 / static_cast<int64_t>(es);
-  const bool dma = (!qs || (bf && k % 16 == 0)) && aligned(p, 16) && aligned(q, 16) && k % v == 0 &&
-                   (n % v == 0 || mode == kGroupFwd) && ldp % v == 0 && ldq % v == 0 &&
-                   std::max({n, k, ldp, ldq}) * static_cast<int64_t>(es) < (int64_t(1) << 23);
-  const hipError_t e = bf ? launch_grouped<ElemBF16>(mode, g, dma, plan.large, stream)
-                          : launch_grouped<ElemF32>(mode, g, dma, plan.large, stream);
+  const bool dma = aligned(p, 16) && aligned(q, 16) && ldp % v == 0 && ldq % v == 0 &&
+                   group_dma(mode, qs != nullptr, bf, n, k, std::max({n, k, ldp, ldq}));
+  const GroupKernel use = group_kernel(mode, g, bf, dma, plan);
+  const hipError_t e = bf ? launch_grouped<ElemBF16>(mode, g, use, stream)
+                          : launch_grouped<ElemF32>(mode, g, use, stream);
   if (e != hipSuccess) return fail(MFSDP_ERR_HIP, "grouped launch: %s", hipGetErrorString(e));
   return MFSDP_OK;
 }
@@ -710,6 +770,39 @@ mfsdp_status_t mfsdp_grouped_linear_wgrad_ckpt(const void* dy, int64_t ld_dy, co
     }
     return grouped_impl(kGroupWgrad, dy, ld_dy, codes, k, scales, offsets, n_experts, rows, n, k,
                         dtype, dw, 0, dw_dtype, beta, workspace, workspace_bytes, stream);
+  });
+}
+
+mfsdp_status_t mfsdp_grouped_linear_tile(mfsdp_grouped_product_t product, int64_t n_experts,
+                                         int64_t rows, int64_t n, int64_t k, mfsdp_dtype_t dtype,
+                                         int rows_aligned, mfsdp_grouped_tile_t* out) {
+  return guarded([&]() -> mfsdp_status_t {
+    g_last_error.clear();
+    if (!out || product < MFSDP_GROUPED_FORWARD || product > MFSDP_GROUPED_WGRAD_CKPT)
+      return fail(MFSDP_ERR_INVALID_ARGUMENT, "product %d, out %p", (int)product, (void*)out);
+    mfsdp_status_t st = grouped_sizes(n_experts, rows, n, k, dtype);
+    if (st != MFSDP_OK) return st;
+    *out = mfsdp_grouped_tile_t{};
+    const bool codes = product == MFSDP_GROUPED_WGRAD_CKPT, bf = dtype == MFSDP_DTYPE_BF16;
+    const int mode = codes ? kGroupWgrad : static_cast<int>(product);
+    if (n_experts == 0 || (rows == 0 && mode != kGroupWgrad)) return MFSDP_OK;   // no launch
+    GroupArgs g{};
+    g.experts = static_cast<int32_t>(n_experts);
+    g.rows = static_cast<int32_t>(rows);
+    g.n = static_cast<int32_t>(n);
+    g.k = static_cast<int32_t>(k);
+    const WgradPlan plan = mode == kGroupWgrad ? wgrad_plan(n_experts, rows, n, k, bf) : WgradPlan{};
+    g.part_rows = plan.part_rows;
+    const bool dma = rows_aligned && group_dma(mode, codes, bf, n, k, std::max(n, k));
+    const GroupShape s = group_shape(group_kernel(mode, g, bf, dma, plan));
+    out->rows = s.rows;
+    out->cols = s.cols;
+    out->threads = s.threads;
+    out->wave_sets = s.wave_sets;
+    out->lds_dma = s.dma ? 1 : 0;
+    out->part_rows = plan.part_rows;
+    out->workgroups = group_blocks(g, mode, s.rows, s.cols);
+    return MFSDP_OK;
   });
 }
 
