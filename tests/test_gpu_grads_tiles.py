@@ -62,3 +62,27 @@ def test_weight_gradients(case):
         else:
             mf.grouped_linear_wgrad_ckpt(dy.to(DEV), codes, scales, off.to(DEV), grad, beta=beta)
         assert ref.worst(grad, dw + beta * old, wgrad_bound(dw, mag, terms, old, beta, dt)) <= 1.0
+
+
+# (product, depth, kernel): kernels whose sets of waves share each step
+LONG_SUMS = [(gt.FWD, 1 << 20, gt.FEW), (gt.FWD, (1 << 20) + 1, gt.ROWS_REG), (gt.DGRAD, 1 << 20, gt.ROWS),
+             (gt.DGRAD, (1 << 20) + 1, gt.ROWS_REG)]
+
+
+@pytest.mark.parametrize("product,depth,kernel", LONG_SUMS)
+def test_long_fp32_sums(product, depth, kernel):
+    # A sum in fp32 is a sum of sums of 512 values, so its error does not grow
+    # with its whole length: 512 additions within a run, one for each run of a
+    # set of waves, one for each set.  All products are 1 + 2^-10: a single long
+    # chain loses that fraction at every addition once it has passed 2^14.
+    width = 8
+    n, k = (width, depth) if product == gt.FWD else (depth, width)
+    t = gt.tile(product, 1, 3, n, k, "fp32", gt.aligned("fp32", depth, k))[1]
+    assert (t.rows, t.cols, t.threads, t.wave_sets, t.lds_dma) == kernel
+    a = torch.ones(3, depth, device=DEV)
+    w = torch.full((1, n, k), 1.0 + 2.0 ** -10, device=DEV)
+    off = torch.tensor([0, 3], dtype=torch.int32, device=DEV)
+    got = (mf.grouped_linear if product == gt.FWD else mf.grouped_linear_dgrad)(a, w, off)
+    want = torch.full((3, width), depth * (1.0 + 2.0 ** -10), dtype=torch.float64)
+    additions = 512 + -(-depth // (512 * t.wave_sets)) + t.wave_sets + 2
+    assert ref.worst(got, want, (ref.half_step(F32) + additions * ref.U) * want) <= 1.0
