@@ -486,9 +486,6 @@ mfsdp_status_t embedding_impl(const void* table, mfsdp_dtype_t table_dtype, int6
   }
   EmbArgs a{};
   a.table = table;
-  a.tokens = tokens;
-  a.out = out;
-  a.n_tokens = n_tokens;
   a.vocab = vocab;
   a.ldo = ldo;
   a.d = static_cast<int32_t>(d);
@@ -498,20 +495,26 @@ mfsdp_status_t embedding_impl(const void* table, mfsdp_dtype_t table_dtype, int6
   const bool vec = d % w == 0 && aligned(table, std::min<size_t>(w * et, 16)) && aligned(out, 16) &&
                    ldo % w == 0;
   const int64_t units = vec ? d / w : d;
-  int64_t blocks;
+  int64_t most;   // tokens of one launch
   if (units > 128) {
     a.chunks = static_cast<int32_t>((units + 255) / 256);
-    blocks = n_tokens * a.chunks;
+    most = kBlocksMax / a.chunks;
   } else {
     a.per_wg = static_cast<int32_t>(256 / units);
-    blocks = (n_tokens + a.per_wg - 1) / a.per_wg;
+    most = kBlocksMax * a.per_wg;
   }
-  if (blocks > kBlocksMax) return fail(MFSDP_ERR_UNSUPPORTED, "too many rows");
   const bool tb = table_dtype == MFSDP_DTYPE_BF16, ob = out_dtype == MFSDP_DTYPE_BF16;
-  const hipError_t e = tb ? (ob ? launch_embedding<ElemBF16, ElemBF16>(a, vec, blocks, stream)
-                                : launch_embedding<ElemBF16, ElemF32>(a, vec, blocks, stream))
-                          : (ob ? launch_embedding<ElemF32, ElemBF16>(a, vec, blocks, stream)
-                                : launch_embedding<ElemF32, ElemF32>(a, vec, blocks, stream));
+  hipError_t e = hipSuccess;
+  for (int64_t t0 = 0; t0 < n_tokens && e == hipSuccess; t0 += most) {
+    a.tokens = static_cast<const char*>(tokens) + t0 * token_bytes;
+    a.out = static_cast<char*>(out) + t0 * ldo * static_cast<int64_t>(eo);
+    a.n_tokens = std::min(most, n_tokens - t0);
+    const int64_t blocks = a.chunks ? a.n_tokens * a.chunks : ceil_div(a.n_tokens, a.per_wg);
+    e = tb ? (ob ? launch_embedding<ElemBF16, ElemBF16>(a, vec, blocks, stream)
+                 : launch_embedding<ElemBF16, ElemF32>(a, vec, blocks, stream))
+           : (ob ? launch_embedding<ElemF32, ElemBF16>(a, vec, blocks, stream)
+                 : launch_embedding<ElemF32, ElemF32>(a, vec, blocks, stream));
+  }
   if (e != hipSuccess) return fail(MFSDP_ERR_HIP, "embedding launch: %s", hipGetErrorString(e));
   return MFSDP_OK;
 }

@@ -68,3 +68,18 @@ def test_arguments_that_are_not_tensors():
                  lambda: mf.ckpt_restore(mf.ckpt_quantize(x)[0], None), lambda: mf.ckpt_quantize(x, codes=1)):
         with pytest.raises(TypeError, match="must be a tensor"):
             call()
+
+
+def test_lookups_beyond_one_launch():
+    # 257 bf16 columns take two workgroups a token: 2^23 tokens are as many as
+    # one launch has
+    n, vocab, d = (1 << 23) + 11, 1000, 257
+    table = rand((vocab, d), BF, 1).to(DEV)
+    t = torch.randint(0, vocab, (n,), generator=torch.Generator().manual_seed(2), dtype=torch.int32).to(DEV)
+    t[5], t[-2] = -1, vocab
+    out = mf.embedding(table, t, out=torch.full((n, d), 7.0, dtype=BF, device=DEV))
+    assert not out[5].any() and not out[-2].any()
+    for lo in range(0, n, 1 << 21):
+        part = t[lo:lo + (1 << 21)].long()
+        on = (part >= 0) & (part < vocab)
+        assert torch.equal(out[lo:lo + (1 << 21)], torch.where(on[:, None], table[part.clamp(0, vocab - 1)], 0))
