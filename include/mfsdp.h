@@ -485,8 +485,8 @@ mfsdp_status_t mfsdp_ckpt_restore(const int8_t* codes, const uint8_t* scales, in
  *            aligned, scratch; none is needed for n_tokens == 0.
  * Errors: as above, MFSDP_ERR_WORKSPACE, and MFSDP_ERR_UNSUPPORTED for vocab
  * above 2^31 - 1, n_tokens above 2^28, d or strides above 2^22, and for a
- * gradient of more than 2^24 workgroups (one takes four rows of up to 2048
- * columns, of up to 512 where rows are not whole 16-byte units).
+ * gradient of 2^24 or more chunks of 64 tokens and 2048 columns (512 where rows
+ * are not whole 16-byte units).
  */
 mfsdp_status_t mfsdp_embedding(const void* table, mfsdp_dtype_t table_dtype, int64_t vocab,
                                int64_t d, const void* tokens, int token_bytes, int64_t n_tokens,

@@ -311,6 +311,7 @@ struct EmbGradArgs {
   int32_t* begin;          // first sorted index of each block of kEmbRows table rows, and n
   float* grad;             // vocab x d
   int64_t vocab, ld;
+  int64_t block0;          // first block of table rows of this launch
   int32_t n, d;
   int32_t tpr;             // threads per row: 64, 128 or 256
   float scale, beta;
@@ -430,7 +431,7 @@ __global__ __launch_bounds__(256) void emb_partial_kernel(EmbGradArgs a, int chu
 template <class E, int W>
 __global__ __launch_bounds__(256) void emb_rows_kernel(EmbGradArgs a, int col_wgs) {
   using S = typename E::storage_t;
-  const int64_t block = blockIdx.x / col_wgs;
+  const int64_t block = a.block0 + blockIdx.x / col_wgs;
   const int64_t v0 = block * kEmbRows;
   const int lane = threadIdx.x & 63;
   const int sub = threadIdx.x / a.tpr;

@@ -579,10 +579,18 @@ hipError_t launch_emb_sums(const EmbGradArgs& a, hipStream_t stream) {
     });
     if (e != hipSuccess) return e;
   }
-  return launch(MFSDP_KERNEL_EMBED_GRAD, stream, [&] {
-    emb_rows_kernel<E, W><<<dim3(static_cast<unsigned>(row_blocks * col_wgs)), dim3(256), 0,
-                            stream>>>(a, static_cast<int>(col_wgs));
-  });
+  const int64_t most = kBlocksMax / col_wgs;   // row blocks of one launch
+  for (int64_t b = 0; b < row_blocks; b += most) {
+    EmbGradArgs part = a;
+    part.block0 = b;
+    const int64_t blocks = std::min(most, row_blocks - b) * col_wgs;
+    const hipError_t e = launch(MFSDP_KERNEL_EMBED_GRAD, stream, [&] {
+      emb_rows_kernel<E, W><<<dim3(static_cast<unsigned>(blocks)), dim3(256), 0, stream>>>(
+          part, static_cast<int>(col_wgs));
+    });
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 mfsdp_status_t embedding_grad_impl(const void* dy, int64_t ld, mfsdp_dtype_t dtype,
@@ -628,8 +636,7 @@ mfsdp_status_t embedding_grad_impl(const void* dy, int64_t ld, mfsdp_dtype_t dty
   int32_t tpr = 64;
   while (tpr < 256 && tpr * cols * kEmbGroups < d) tpr *= 2;
   const int64_t col_wgs = ceil_div(d, tpr * cols * kEmbGroups);
-  if (ceil_div(vocab, kEmbRows) * col_wgs > kBlocksMax ||
-      ceil_div(n_tokens, kEmbRun) * col_wgs + ceil_div(vocab, kEmbRows) / 256 + 2 > kBlocksMax)
+  if (ceil_div(n_tokens, kEmbRun) * col_wgs + ceil_div(vocab, kEmbRows) / 256 + 2 > kBlocksMax)
     return fail(MFSDP_ERR_UNSUPPORTED, "too many rows");
 
   char* ws = static_cast<char*>(workspace);

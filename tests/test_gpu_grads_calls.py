@@ -83,3 +83,26 @@ def test_lookups_beyond_one_launch():
         part = t[lo:lo + (1 << 21)].long()
         on = (part >= 0) & (part < vocab)
         assert torch.equal(out[lo:lo + (1 << 21)], torch.where(on[:, None], table[part.clamp(0, vocab - 1)], 0))
+
+
+@pytest.mark.parametrize("d", [2, 4])
+@pytest.mark.parametrize("beta", [0.0, 1.0])
+def test_table_gradients_beyond_one_launch(d, beta):
+    # a workgroup takes four table rows: 2^26 rows are as many as one launch has
+    vocab, n = (1 << 26) + 5, 3000
+    g = torch.Generator().manual_seed(3)
+    t = torch.randint(0, vocab, (n,), generator=g)
+    t[:400] = torch.arange(400) % 18 + vocab - 18                      # both sides of the launches' border,
+    t[400:600] = vocab - 1                                             # one of them often
+    t[600], t[601], t[602] = 0, -1, vocab
+    dy = rand((n, d), F32, 4)
+    old = 0.5 if beta else 0.0
+    grad = mf.embedding_grad(dy.to(DEV), t.to(DEV), torch.full((vocab, d), 0.5 if beta else float("nan"), device=DEV), beta=beta)
+    on = (t >= 0) & (t < vocab)
+    rows, place = torch.unique(t[on], return_inverse=True)
+    compact = torch.full((n,), -1)
+    compact[on] = place
+    want, mag, terms = ref.embedding_grad(dy, compact, rows.numel(), 1.0)
+    assert ref.worst(grad[rows.to(DEV)], want + old, (terms[:, None] + 2) * ref.U * mag + 2 * ref.U * old) <= 1.0
+    grad[rows.to(DEV)] = old
+    assert (grad == old).all()          # every other row
