@@ -34,7 +34,7 @@ struct CkptArgs {
   int8_t* codes;       // rows x k, contiguous
   uint8_t* scales;     // rows x nb
   int64_t ld;
-  int64_t units;       // rows * nb
+  uint32_t units;      // rows * nb, under 2^29 in one launch
   int32_t k, nb;
   int32_t vec;         // rows of x start on 16 bytes and k is a multiple of 8
 };
@@ -44,11 +44,9 @@ struct CkptArgs {
 struct CkptUnit {
   int64_t row;
   int c0, left;
-  __device__ __forceinline__ CkptUnit(const CkptArgs& a, int64_t u) {
-    // a 32-bit division wherever that is enough
-    row = a.units >> 32 ? u / a.nb
-                        : static_cast<int64_t>(static_cast<uint32_t>(u) / static_cast<uint32_t>(a.nb));
-    c0 = static_cast<int>(u - row * a.nb) * kCkptBlock;
+  __device__ __forceinline__ CkptUnit(const CkptArgs& a, uint32_t u) {
+    row = u / static_cast<uint32_t>(a.nb);
+    c0 = static_cast<int>(u - static_cast<uint32_t>(row) * a.nb) * kCkptBlock;
     left = min(kCkptBlock, a.k - c0);
   }
 };
@@ -61,15 +59,15 @@ __device__ __forceinline__ int ckpt_col(int l16, int h) {
   return E::kVec == 8 ? l16 * 8 + h * 4 : h * 64 + l16 * 4;
 }
 
-__device__ __forceinline__ int64_t ckpt_unit0() {
-  return static_cast<int64_t>(blockIdx.x) * (16 * kCkptUnits) + (threadIdx.x >> 4);
+__device__ __forceinline__ uint32_t ckpt_unit0() {
+  return blockIdx.x * (16 * kCkptUnits) + (threadIdx.x >> 4);
 }
 
 template <class E>
 __global__ __launch_bounds__(256) void ckpt_quantize_kernel(CkptArgs a) {
   using S = typename E::storage_t;
   const int l16 = threadIdx.x & 15;
-  const int64_t unit0 = ckpt_unit0();
+  const uint32_t unit0 = ckpt_unit0();
   const bool vec = a.vec != 0;
   float v[kCkptUnits][8];
 #pragma unroll
@@ -141,7 +139,7 @@ template <class E>
 __global__ __launch_bounds__(256) void ckpt_restore_kernel(CkptArgs a) {
   using S = typename E::storage_t;
   const int l16 = threadIdx.x & 15;
-  const int64_t unit0 = ckpt_unit0();
+  const uint32_t unit0 = ckpt_unit0();
   const bool vec = a.vec != 0;
   uint32_t w[kCkptUnits][2];
   uint32_t b[kCkptUnits];

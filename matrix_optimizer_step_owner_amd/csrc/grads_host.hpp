@@ -407,35 +407,37 @@ mfsdp_status_t ckpt_impl(bool quantize, void* x, int64_t ld, int8_t* codes, uint
   if (!aligned(x, es))
     return fail(MFSDP_ERR_INVALID_ARGUMENT, "a buffer is not aligned to its elements");
   CkptArgs a{};
-  a.x = x;
-  a.codes = codes;
-  a.scales = scales;
   a.ld = ld;
   a.k = static_cast<int32_t>(k);
   a.nb = static_cast<int32_t>((k + kCkptBlock - 1) / kCkptBlock);
-  a.units = rows * a.nb;
   a.vec = aligned(x, 16) && (ld * static_cast<int64_t>(es)) % 16 == 0 && k % 8 == 0 &&
           aligned(codes, 8);
   {
     std::vector<Extent> xs, cs;
     add_rows(&xs, x, rows, k, ld, es, "x");
     add_bytes(&cs, codes, static_cast<size_t>(rows) * k, "codes");
-    add_bytes(&cs, scales, static_cast<size_t>(a.units), "scales");
+    add_bytes(&cs, scales, static_cast<size_t>(rows) * a.nb, "scales");
     const mfsdp_status_t st = quantize ? check_outputs(cs, xs) : check_outputs(xs, cs);
     if (st != MFSDP_OK) return st;
   }
-  const int64_t blocks = (a.units + 16 * kCkptUnits - 1) / (16 * kCkptUnits);
-  if (blocks > kBlocksMax) return fail(MFSDP_ERR_UNSUPPORTED, "too many blocks");
-  const dim3 grid(static_cast<unsigned>(blocks)), wg(256);
-  const hipError_t e = launch(MFSDP_KERNEL_CKPT, stream, [&] {
-    if (quantize) {
-      if (dtype == MFSDP_DTYPE_BF16) ckpt_quantize_kernel<ElemBF16><<<grid, wg, 0, stream>>>(a);
-      else ckpt_quantize_kernel<ElemF32><<<grid, wg, 0, stream>>>(a);
-    } else {
-      if (dtype == MFSDP_DTYPE_BF16) ckpt_restore_kernel<ElemBF16><<<grid, wg, 0, stream>>>(a);
-      else ckpt_restore_kernel<ElemF32><<<grid, wg, 0, stream>>>(a);
-    }
-  });
+  const int64_t most = kBlocksMax * 16 * kCkptUnits / a.nb;   // rows of one launch
+  hipError_t e = hipSuccess;
+  for (int64_t r = 0; r < rows && e == hipSuccess; r += most) {
+    a.x = static_cast<char*>(x) + r * ld * static_cast<int64_t>(es);
+    a.codes = codes + r * k;
+    a.scales = scales + r * a.nb;
+    a.units = static_cast<uint32_t>(std::min(most, rows - r) * a.nb);
+    const dim3 grid(static_cast<unsigned>(ceil_div(a.units, 16 * kCkptUnits))), wg(256);
+    e = launch(MFSDP_KERNEL_CKPT, stream, [&] {
+      if (quantize) {
+        if (dtype == MFSDP_DTYPE_BF16) ckpt_quantize_kernel<ElemBF16><<<grid, wg, 0, stream>>>(a);
+        else ckpt_quantize_kernel<ElemF32><<<grid, wg, 0, stream>>>(a);
+      } else {
+        if (dtype == MFSDP_DTYPE_BF16) ckpt_restore_kernel<ElemBF16><<<grid, wg, 0, stream>>>(a);
+        else ckpt_restore_kernel<ElemF32><<<grid, wg, 0, stream>>>(a);
+      }
+    });
+  }
   if (e != hipSuccess) return fail(MFSDP_ERR_HIP, "checkpoint launch: %s", hipGetErrorString(e));
   return MFSDP_OK;
 }

@@ -106,3 +106,19 @@ def test_table_gradients_beyond_one_launch(d, beta):
     assert ref.worst(grad[rows.to(DEV)], want + old, (terms[:, None] + 2) * ref.U * mag + 2 * ref.U * old) <= 1.0
     grad[rows.to(DEV)] = old
     assert (grad == old).all()          # every other row
+
+
+def test_checkpoints_beyond_one_launch():
+    # 32 blocks a workgroup: 2^29 rows of one block are as many as one launch
+    # has.  The parts of a long activation have the checkpoints that they have
+    # alone.
+    rows = (1 << 29) + 33
+    x = torch.empty(rows, 1, dtype=BF, device=DEV).normal_(generator=torch.Generator(DEV).manual_seed(1))
+    codes, scales = mf.ckpt_quantize(x)
+    back = mf.ckpt_restore(codes, scales, out=torch.full((rows, 1), 7.0, dtype=BF, device=DEV))
+    for lo in range(0, rows, 1 << 28):
+        c, s = mf.ckpt_quantize(x[lo:lo + (1 << 28)])
+        assert torch.equal(codes[lo:lo + (1 << 28)], c) and torch.equal(scales[lo:lo + (1 << 28)], s)
+        assert torch.equal(back[lo:lo + (1 << 28)], mf.ckpt_restore(c, s))
+    cr, sr = ref.ckpt_quantize(x[-100:])
+    assert torch.equal(codes[-100:].cpu(), torch.from_numpy(cr)) and torch.equal(scales[-100:].cpu(), torch.from_numpy(sr))
