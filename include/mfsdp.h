@@ -379,8 +379,9 @@ mfsdp_status_t mfsdp_shampoo_stats(const mfsdp_stats_matrix_t* mats, int64_t n_m
  * Errors: MFSDP_ERR_INVALID_ARGUMENT (negative counts, widths < 1, strides
  * smaller than rows, null or misaligned pointers, non-finite beta),
  * MFSDP_ERR_UNSUPPORTED (dtypes; n, k or strides above 2^22, rows above 2^30,
- * n_experts above 2^20, more than 2^23 tiles of 32 x 64 outputs or, for the
- * weight gradient, of 128 x 128), MFSDP_ERR_WORKSPACE,
+ * n_experts above 2^20, more than 2^23 tiles of the kernel that the call runs
+ * -- see mfsdp_grouped_linear_tile; in the forward and input gradient through
+ * registers, of 32 x 64 outputs), MFSDP_ERR_WORKSPACE,
  * MFSDP_ERR_ALIAS, MFSDP_ERR_HIP.
  */
 mfsdp_status_t mfsdp_grouped_linear(const void* x, int64_t ld_x, const void* weight,

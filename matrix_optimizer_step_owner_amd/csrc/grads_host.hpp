@@ -283,6 +283,17 @@ GroupKernel group_kernel(int mode, const GroupArgs& g, bool bf, bool dma, const 
   return mode == kGroupWgrad ? wgrad_kernel(bf, dma, plan.large) : rows_kernel(mode, g, bf, dma);
 }
 
+// Whether the launches' grids hold the call: its tiles (of forward and input
+// gradient through registers as many as 32 x 64 ones would be, whichever of the
+// two kernels runs) and the 2048-element pieces of a sum of parts.
+bool group_fits(int mode, const GroupArgs& g, GroupKernel use) {
+  const GroupShape s = group_shape(use);
+  const bool reg = mode != kGroupWgrad && !s.dma;
+  const int64_t blocks = reg ? group_blocks(g, mode, 32, 64) : group_blocks(g, mode, s.rows, s.cols);
+  const int64_t sums = g.part_rows ? g.experts * ceil_div(static_cast<int64_t>(g.n) * g.k, 2048) : 0;
+  return blocks <= kGroupBlocksMax && sums <= kBlocksMax;
+}
+
 mfsdp_status_t grouped_sizes(int64_t experts, int64_t rows, int64_t n, int64_t k,
                              mfsdp_dtype_t dtype) {
   if (dtype != MFSDP_DTYPE_F32 && dtype != MFSDP_DTYPE_BF16)
@@ -371,17 +382,11 @@ mfsdp_status_t grouped_impl(int mode, const void* p, int64_t ldp, const void* q,
   g.stream = aligned(out, 128) && (mode == kGroupWgrad ? k : ldo) * static_cast<int64_t>(eo) % 128 == 0;
   // eight L2s of 4 MB
   g.stream_w = std::min(experts, rows) * n * k * static_cast<int64_t>(es) > (int64_t(32) << 20);
-  // the smallest tiles
-  const int64_t blocks = mode == kGroupWgrad ? group_blocks(g, mode, 128, 128)
-                                             : group_blocks(g, mode, 32, 64);
-  // (and the sum of a weight gradient's parts, 2048 elements each)
-  const int64_t sums = plan.part_rows ? experts * ceil_div(n * k, 2048) : 0;
-  if (blocks > kGroupBlocksMax || sums > kBlocksMax)
-    return fail(MFSDP_ERR_UNSUPPORTED, "too many tiles");
   const int64_t v = 16 / static_cast<int64_t>(es);
   const bool dma = aligned(p, 16) && aligned(q, 16) && ldp % v == 0 && ldq % v == 0 &&
                    group_dma(mode, qs != nullptr, bf, n, k, std::max({n, k, ldp, ldq}));
   const GroupKernel use = group_kernel(mode, g, bf, dma, plan);
+  if (!group_fits(mode, g, use)) return fail(MFSDP_ERR_UNSUPPORTED, "too many tiles");
   const hipError_t e = bf ? launch_grouped<ElemBF16>(mode, g, use, stream)
                           : launch_grouped<ElemF32>(mode, g, use, stream);
   if (e != hipSuccess) return fail(MFSDP_ERR_HIP, "grouped launch: %s", hipGetErrorString(e));
@@ -806,7 +811,9 @@ mfsdp_status_t mfsdp_grouped_linear_tile(mfsdp_grouped_product_t product, int64_
     const WgradPlan plan = mode == kGroupWgrad ? wgrad_plan(n_experts, rows, n, k, bf) : WgradPlan{};
     g.part_rows = plan.part_rows;
     const bool dma = rows_aligned && group_dma(mode, codes, bf, n, k, std::max(n, k));
-    const GroupShape s = group_shape(group_kernel(mode, g, bf, dma, plan));
+    const GroupKernel use = group_kernel(mode, g, bf, dma, plan);
+    if (!group_fits(mode, g, use)) return fail(MFSDP_ERR_UNSUPPORTED, "too many tiles");
+    const GroupShape s = group_shape(use);
     out->rows = s.rows;
     out->cols = s.cols;
     out->threads = s.threads;

@@ -122,3 +122,16 @@ def test_checkpoints_beyond_one_launch():
         assert torch.equal(back[lo:lo + (1 << 28)], mf.ckpt_restore(c, s))
     cr, sr = ref.ckpt_quantize(x[-100:])
     assert torch.equal(codes[-100:].cpu(), torch.from_numpy(cr)) and torch.equal(scales[-100:].cpu(), torch.from_numpy(sr))
+
+
+def test_large_output_projection():
+    # 34 GB of outputs: more than 2^23 tiles of 32 x 64, 2^18 of those that run
+    rows, n, k = 131072, 131200, 64
+    x, w = rand((rows, k), BF, 1).to(DEV), rand((1, n, k), BF, 2, 0.05).to(DEV)
+    off = torch.tensor([0, rows], dtype=torch.int32, device=DEV)
+    y = mf.grouped_linear(x, w, off)
+    wd = w[0].double().t().contiguous()
+    for lo in (0, 65536 - 128, rows - 256):
+        a = x[lo:lo + 256].double()
+        want, mag = a @ wd, a.abs() @ wd.abs()
+        assert float(((y[lo:lo + 256].double() - want).abs() / (ref.half_step(BF) * want.abs() + k * ref.U * mag)).max()) <= 1.0

@@ -46,3 +46,16 @@ def test_refusals():
         assert status == ok and (t.rows, t.cols, t.threads, t.workgroups) == (0, 0, 0, 0)
     status, t = gt.tile(gt.WGRAD, 3, 0, 64, 64, "bf16")     # beta * dW, without rows
     assert status == ok and t.workgroups >= 3
+
+
+def test_tile_limits():
+    # counted in the tiles that the call would run: 2^23 of 256 x 256 outputs
+    # here, 34 GB of bf16 in 32 x 64 ones
+    status, t = gt.tile(gt.FWD, 1, 131072, 131200, 64, "bf16")
+    assert status == 0 and (t.rows, t.cols, t.workgroups) == (256, 256, 512 * 513)
+    status, t = gt.tile(gt.DGRAD, 1, 131072, 64, 131200, "bf16")
+    assert status == 0 and (t.rows, t.cols, t.workgroups) == (256, 256, 512 * 513)
+    assert gt.tile(gt.FWD, 1, 1 << 30, 1 << 22, 64, "bf16")[0] == 2       # 2^36 of them
+    # operands through registers: in 32 x 64 outputs
+    assert gt.tile(gt.FWD, 1, 1 << 28, 64, 1, "bf16")[0] == 2 and gt.tile(gt.FWD, 1, 1 << 27, 64, 1, "bf16")[0] == 0
+    assert gt.tile(gt.WGRAD, 1 << 20, 1 << 20, 400, 400, "bf16")[0] == 0 and gt.tile(gt.WGRAD, 1 << 20, 1 << 20, 400, 400, "fp32")[0] == 2
