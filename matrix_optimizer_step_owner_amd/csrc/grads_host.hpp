@@ -99,14 +99,16 @@ using TileFew = GroupTile<32, 32, 1, 1, 8, 3, 8>;
 using TileRowsReg = GroupTile<32, 64, 1, 2, 4, 2, 4>;
 using TileF32 = GroupTile<128, 128, 2, 2, 1, 4>;
 
-// Weight gradients: 256 x 256 tiles where n and k fill them and there are
-// enough for the 256 CUs, or where long segments can be cut into enough parts;
-// 128 x 128 tiles otherwise, two workgroups per CU (256 x 32771 x 512 x 1536:
-// 136 us with the large, 184 with the small ones; 8 x 2048 x 1536 x 1024: 19
-// either way).  Parts have a fixed number of rows, so that experts of different
-// lengths give equal work; a second kernel sums them (4 x 32768 x 512 x 512:
-// 201 us whole, 62 in equal numbers of parts per expert, 42 so).  The choice
-// depends on the sizes alone.
+// Weight gradients: 256 x 256 tiles where n and k fill more than half of one and
+// there are enough for the 256 CUs, or where long segments can be cut into
+// enough parts; 128 x 128 tiles otherwise, two workgroups per CU.  Both sides:
+// 256 x 32771 x 512 x 1536 136 us with the large, 184 with the small ones; 8 x
+// 2048 x 1536 x 1024 19 either way; 256 x 131072 x 1536 x 160 135 and 173; 256 x
+// 32768 x 192 x 192 15 and 14; 64 x 16384 x 128 x 2048 29 and 22; 256 x 32768 x
+// 64 x 64 13 and 9.  Parts have a fixed number of rows, so that experts of
+// different lengths give equal work; a second kernel sums them (4 x 32768 x 512
+// x 512: 201 us whole, 62 in equal numbers of parts per expert, 42 so).  The
+// choice depends on the sizes alone.
 struct WgradPlan {
   bool large;
   int32_t part_rows;   // 0: whole segments
@@ -119,7 +121,7 @@ WgradPlan wgrad_plan(int64_t experts, int64_t rows, int64_t n, int64_t k, bool b
   if (experts == 0) return p;
   const int64_t large = ceil_div(n, 256) * ceil_div(k, 256);
   const int64_t square = ceil_div(n, 128) * ceil_div(k, 128);
-  p.large = bf && experts * large >= 192;
+  p.large = bf && n > 128 && k > 128 && experts * large >= 192;
   if (p.large || rows == 0) return p;
   // a part: as many rows as leave two 128 x 128 tiles (one 256 x 256) per CU,
   // each expert's last part, which is not full, among them; and enough rows to

@@ -59,3 +59,13 @@ def test_tile_limits():
     # operands through registers: in 32 x 64 outputs
     assert gt.tile(gt.FWD, 1, 1 << 28, 64, 1, "bf16")[0] == 2 and gt.tile(gt.FWD, 1, 1 << 27, 64, 1, "bf16")[0] == 0
     assert gt.tile(gt.WGRAD, 1 << 20, 1 << 20, 400, 400, "bf16")[0] == 0 and gt.tile(gt.WGRAD, 1 << 20, 1 << 20, 400, 400, "fp32")[0] == 2
+
+
+@pytest.mark.parametrize("product", [gt.WGRAD, gt.CKPT])
+@pytest.mark.parametrize("n,k,side", [(64, 64, 128), (128, 128, 128), (64, 512, 128), (2048, 128, 128), (96, 1536, 128), (136, 144, 256),
+                                      (512, 192, 256), (160, 1536, 256), (512, 1536, 256)])
+def test_large_weight_gradient_tiles_have_outputs(product, n, k, side):
+    # 256 x 256 tiles, however many there are, only where n and k fill more than
+    # half of one
+    status, t = gt.tile(product, 256, 32768, n, k, "bf16")
+    assert status == 0 and (t.rows, t.cols, t.lds_dma) == (side, side, 1)
