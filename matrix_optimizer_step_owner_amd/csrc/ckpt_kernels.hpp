@@ -4,7 +4,8 @@
 // is held as whole numbers q in [-127, 127] and one power of two 2^e, the
 // smallest e >= -126 with max |x| <= 127 * 2^e:
 //   q = x / 2^e rounded to the nearest, ties to even;  x is held as q * 2^e.
-// The error is at most 2^(e-1), half a step, under max|x| / 126.  e stops at
+// The error is at most 2^(e-1), half a step: under max|x| / 127 where e > -126,
+// as max|x| > 127 * 2^(e-1) there.  e stops at
 // 121, above which q * 2^e could pass the largest float, and q at 127: only
 // values beyond 127.5 * 2^121 are then off by more (by under one step).  A power of
 // two makes the division exact and q * 2^e a bf16 number (seven bits of

@@ -102,12 +102,12 @@ using TileF32 = GroupTile<128, 128, 2, 2, 1, 4>;
 // Weight gradients: 256 x 256 tiles where n and k fill more than half of one and
 // there are enough for the 256 CUs, or where long segments can be cut into
 // enough parts; 128 x 128 tiles otherwise, two workgroups per CU.  Both sides:
-// 256 x 32771 x 512 x 1536 136 us with the large, 184 with the small ones; 8 x
-// 2048 x 1536 x 1024 19 either way; 256 x 131072 x 1536 x 160 135 and 173; 256 x
-// 32768 x 192 x 192 15 and 14; 64 x 16384 x 128 x 2048 29 and 22; 256 x 32768 x
-// 64 x 64 13 and 9.  Parts have a fixed number of rows, so that experts of
+// 256 x 32771 x 512 x 1536 113 us with the large, 134 with the small ones; 8 x
+// 2048 x 1536 x 1024 16 either way; 256 x 131072 x 1536 x 160 133 and 167; 256 x
+// 32768 x 192 x 192 14 either way; 64 x 16384 x 128 x 2048 28 and 24; 256 x 32768
+// x 64 x 64 12 and 8.  Parts have a fixed number of rows, so that experts of
 // different lengths give equal work; a second kernel sums them (4 x 32768 x 512
-// x 512: 201 us whole, 62 in equal numbers of parts per expert, 42 so).  The
+// x 512: 207 us whole, 62 in equal numbers of parts per expert, 42 so).  The
 // choice depends on the sizes alone.
 struct WgradPlan {
   bool large;
@@ -190,28 +190,29 @@ GroupKernel rows_kernel(int mode, const GroupArgs& g, bool bf, bool dma) {
     return high * ceil_div(width, bq);
   };
   // Under two tiles of 64 columns per four CUs, 32 columns and eight sets of
-  // waves: 256 x 8 x 512 x 1536 8.8 -> 7.6 us (fp32 21.7 -> 14.3), but with
-  // 224 tiles, 1 x 1 x 14336 x 4096, 21.8 -> 24.9.
+  // waves: 256 x 8 x 512 x 1536 8.5 -> 7.2 us (fp32 21.0 -> 13.2), but with
+  // 224 tiles, 1 x 1 x 14336 x 4096, 22.0 -> 24.5.
   const GroupKernel few_rows = mode == kGroupFwd && tiles(32, 64) <= 128 ? kUseFew : kUseRows;
-  // Through registers: 7 x 2049 x 513 x 257 8.4 (few rows' tile) and 11.7 us,
-  // its input gradient 9.1 and 20.6; 8 x 8192 x 2047 x 2049 255 and 134 us.
+  // Through registers: 7 x 2049 x 513 x 257 8.9 (few rows' tile) and 11.8 us,
+  // its input gradient 10.0 and 21.2 (fp32 19 and 54); 8 x 8192 x 2047 x 2049
+  // 244 and 138 us.
   if (!dma) return per <= 48 || tiles(128, 128) < 128 ? kUseRowsReg : kUseSquareReg;
-  // fp32: 16 x 1024 x 2048 x 2048 104 (few rows) and 250 us; 64 x 8192 x 2048
-  // x 1024 equal; 1 x 8192 x 4096 x 4096 2279 and 1961 us.
+  // fp32: 16 x 1024 x 2048 x 2048 114 (few rows) and 252 us; 64 x 8192 x 2048
+  // x 1024 398 and 387; 1 x 8192 x 4096 x 4096 2427 and 1994 us.
   if (!bf) return per <= 96 || tiles(128, 128) < 192 ? few_rows : kUseF32;
-  // Forward of 32 x 1024 x 2048 x 2048: 61 us (51 streamed), 67 and more with
-  // taller tiles; its input gradient, whose narrow tiles read the weights in
-  // 128-byte pieces, 63, and 50 with taller ones.
+  // Forward of 32 x 1024 x 2048 x 2048: 51 us, 67 and more with taller tiles;
+  // its input gradient, whose narrow tiles read the weights in 128-byte pieces,
+  // 61, and 50 with taller ones.
   if ((mode == kGroupFwd && per <= 40) || tiles(64, 256) < 128) return few_rows;
-  // 64 x 1024 x 1024 x 2048, input gradient: 48 (64 rows) and 51 us
+  // 64 x 1024 x 1024 x 2048, input gradient: 48 (64 rows) and 50 us
   // (128 rows).
   if (per <= 24 || tiles(128, 256) < 100) return kUseSmall;
-  // 16 x 24576 x 5632 x 2048: 546 (256 rows) and 597 us (128 rows); 64 x 8192
-  // x 2048 x 1024, 128 rows per expert: 103 and 72 us.
+  // 16 x 24576 x 5632 x 2048: 532 (256 rows) and 576 us (128 rows); 64 x 8192
+  // x 2048 x 1024, 128 rows per expert: 89 and 69 us.
   if (per >= 320 && tiles(256, 256) >= 256) return kUseLarge;
   // Short sums leave a tile's start and end uncovered unless two workgroups
-  // share a CU: 256 x 32771 x 512 x 1536, input gradient (depth 512): 123
-  // (pair) and 136 us; forward (depth 1536): 134 and 120 us.
+  // share a CU: 256 x 32771 x 512 x 1536, input gradient (depth 512): 118
+  // (pair) and 136 us; forward (depth 1536): 130 and 109 us.
   return depth < 1024 && tiles(128, 256) >= 512 ? kUsePair : kUseWide;
 }
 

@@ -16,9 +16,9 @@
 //
 // What bounds them, in bf16:
 //   - long segments: MFMA issue and the power of it.  8 experts of 14336 x 4096,
-//     16384 rows: forward 1.13, input gradient 1.06 and weight gradient 1.18
-//     PFLOP/s (1.00 from 8-bit codes), 58-62% of the MFMA cycles at 1.7-1.8 GHz;
-//     one expert of 4096 x 4096 with 8192 rows 1.35.  The difference is
+//     16384 rows: forward 1.06-1.10, input gradient 1.05 and weight gradient
+//     1.16 PFLOP/s (0.95-0.97 from 8-bit codes), 57-64% of the MFMA cycles at 1.7-1.8 GHz;
+//     one expert of 4096 x 4096 with 8192 rows 1.22-1.32.  The difference is
 //     workgroups that wait for the last round of tiles, tiles that a segment
 //     fills in part, and each tile's start and end, which nothing covers at
 //     one workgroup per CU.
@@ -26,7 +26,9 @@
 //     us: 4.4 to 4.9 TB/s, where a plain copy moves 5.1.
 //   - few rows: the weights' stream, 5.5-7.1 TB/s; the smallest calls, the
 //     latency of a dozen steps (7.6 us).
-// fp32 runs the same tiles on 32x32x2 MFMAs, 138-140 TFLOP/s.
+//   - weight gradients that add to a bf16 dW (beta != 0): its elements, read and
+//     written one by one; 256 experts 515 us, where the bytes take 185.
+// fp32 runs the same tiles on 32x32x2 MFMAs, 133-139 TFLOP/s.
 #pragma once
 
 #include "common.hpp"
