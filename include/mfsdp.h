@@ -511,7 +511,9 @@ const char* mfsdp_last_error(void);
 /*
  * Kernel timing for measurement tools.  Kernels of the library fall into the
  * kinds below.  While timing is enabled on a thread, every launch that thread
- * makes is bracketed by a pair of hipEvents recorded on the launch stream;
+ * makes is bracketed by a pair of hipEvents recorded on the launch stream
+ * (not while that stream is being captured into a graph: its launches are
+ * neither timed nor counted, then or when the graph is replayed);
  * mfsdp_timing_read synchronizes those events and returns, per kind, the
  * summed milliseconds and the number of launches since the last reset.
  * Events are created lazily by the library (no device-memory allocation) and

@@ -135,3 +135,25 @@ def test_large_output_projection():
         a = x[lo:lo + 256].double()
         want, mag = a @ wd, a.abs() @ wd.abs()
         assert float(((y[lo:lo + 256].double() - want).abs() / (ref.half_step(BF) * want.abs() + k * ref.U * mag)).max()) <= 1.0
+
+
+def test_timing_leaves_captured_launches_alone():
+    x, w, off = rand((10, 16), BF, 1).to(DEV), rand((2, 8, 16), BF, 2).to(DEV), offsets_of([4, 6]).to(DEV)
+    want = mf.grouped_linear(x, w, off)
+    y = torch.zeros_like(want)
+    mf.timing.enable(True)
+    try:
+        mf.timing.reset()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            mf.grouped_linear(x, w, off, out=y)
+        for _ in range(3):
+            y.zero_()
+            graph.replay()
+            assert torch.equal(y, want)
+        assert mf.timing.read("grouped")[1] == 0
+        mf.grouped_linear(x, w, off)
+        assert mf.timing.read("grouped")[1] == 1
+    finally:
+        mf.timing.enable(False)
+        mf.timing.reset()

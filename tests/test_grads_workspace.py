@@ -70,7 +70,8 @@ def test_held_until_the_call_has_been_made(host, monkeypatch):
 
 
 def test_the_steps_workspace_is_not_replaced(host, monkeypatch):
-    # a captured Muon step keeps the address it was captured with
+    # another thread may be in a Muon step on this stream, which goes on using
+    # the address it took
     monkeypatch.setattr(mf, "_WS_CACHE", {})
     ws = mf._workspace(CPU, 77, 1000)
     grads._scratch(CPU, 100000, None)
