@@ -1,0 +1,523 @@
+"""Cases for the operators around the experts' products of a training or decoding step.
+
+* ``route``: scores of E experts from logits, the k largest of each token, their
+  weights, and the plan that sorts the tokens' rows by expert.  With s the softmax
+  or the sigmoid of a row of logits and b the balance bias, an expert's key is
+  s + b; of ``groups`` equal groups those with the ``top`` largest sums of their
+  two largest keys stay; the k largest keys among them are chosen in order, ties
+  to the lowest index; weight = scale * s / (sum of the chosen s + 1e-20), or
+  scale * s.  A masked token has experts -1 and weights 0.  The plan: ``offsets``
+  of each expert's rows, ``slots`` (token * k + j of each row, tokens in order
+  within an expert, -1 behind the last) and ``place`` (row of each slot or -1).
+* ``route_grad``: the logits' gradient from the weights'.
+* ``exchange``: rows to their experts' order, xs[r] = x[slots[r] / k], and back,
+  y[t] = sum_j w[t, j] h[place[t, j]].
+* ``exchange_grads``: dh[place[t, j]] = w[t, j] dy[t], dw[t, j] = <dy[t], h[place[t, j]]>
+  and dx[t] = sum_j dxs[place[t, j]].
+* ``norm``: layer norm (or, not centred, division by the root mean square).
+* ``norm_grads``: its gradients, the weight's and the bias's in fp32 as the AdamW tail takes them.
+* ``scaled``: activations to 8-bit floats and their product with expert matrices kept so.
+* ``scaled_step``: matrices and activations to 8-bit floats, the product and the input's gradient.
+
+An 8-bit copy holds blocks (128 columns of a row of activations; 128 x 128 of a
+matrix) as e4m3 codes and one power of two 2^e, the smallest (e >= -126) with
+max |v| <= 448 * 2^e, kept as the byte e + 127: code = v / 2^e to the nearest, ties
+to even.  Code rows are filled up with zeros to a multiple of 128.
+"""
+
+import math
+
+import numpy as np
+import torch
+
+own = False
+
+BLOCK = 128
+TINY = 1e-20
+DTYPES = {"bf16": torch.bfloat16, "fp32": torch.float32}
+SIZE = {"bf16": 2, "fp32": 4}
+
+
+def listed():
+    return [
+        # one decoding step of sixteen sequences, 256 experts in eight groups
+        {"name": "route decode", "kind": "route", "dtype": "fp32", "tokens": 16, "experts": 256, "k": 8, "scores": "sigmoid", "bias": True, "groups": 8, "top": 4, "pad": 0.0},
+        # a training batch over the same experts
+        {"name": "route batch", "kind": "route", "dtype": "fp32", "tokens": 32771, "experts": 256, "k": 8, "scores": "sigmoid", "bias": True, "groups": 8, "top": 4, "pad": 0.0},
+        # a padded batch over 60 experts, bf16 logits
+        {"name": "route padded", "kind": "route", "dtype": "bf16", "tokens": 4099, "experts": 60, "k": 4, "scores": "softmax", "bias": False, "groups": 1, "top": 1, "pad": 0.125},
+        # the router's gradient of a training batch
+        {"name": "route grad batch", "kind": "route_grad", "dtype": "fp32", "tokens": 32771, "experts": 256, "k": 8, "scores": "softmax", "pad": 0.0},
+        # one decoding step of 32 sequences, eight experts each
+        {"name": "exchange decode", "kind": "exchange", "dtype": "bf16", "tokens": 32, "d": 2048, "experts": 256, "k": 8, "pad": 0.0},
+        # the backward pass of a training batch of a d=4096 model, an eighth of it padding
+        {"name": "exchange grads batch", "kind": "exchange_grads", "dtype": "bf16", "tokens": 8192, "d": 4096, "experts": 256, "k": 8, "pad": 0.125},
+        # one decoding step of 32 sequences
+        {"name": "norm decode", "kind": "norm", "dtype": "bf16", "rows": 32, "d": 4096, "centered": True, "bias": True},
+        # the backward pass of a norm of a d=5120 model's training batch
+        {"name": "norm grads batch", "kind": "norm_grads", "dtype": "bf16", "rows": 16384, "d": 5120, "centered": True, "bias": True},
+        # a short fp32 batch of an odd width, root mean square alone
+        {"name": "norm grads odd fp32", "kind": "norm_grads", "dtype": "fp32", "rows": 1001, "d": 1537, "centered": False, "bias": False},
+        # four tokens, two experts each, one decoding step of a small-expert layer (512 x 1536 experts)
+        {"name": "scaled decode", "kind": "scaled", "dtype": "bf16", "experts": 256, "rows": 8, "n": 512, "k": 1536, "skew": 0.5},
+        # a training batch over eight large experts (14336 x 4096), whose 8-bit copies are made once a step
+        {"name": "scaled large", "kind": "scaled", "dtype": "bf16", "experts": 8, "rows": 16384, "n": 14336, "k": 4096, "skew": 0.3},
+        # the first batch of a step over 256 small experts: their copies too, and both directions
+        {"name": "scaled step many small", "kind": "scaled_step", "dtype": "bf16", "experts": 256, "rows": 32771, "n": 512, "k": 1536, "skew": 0.5},
+    ]
+
+
+def _log(rng, lo, hi):
+    return int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))
+
+
+def _width(rng, lo, hi):
+    """Mostly whole 16-byte rows, as models have them, and any number now and then."""
+    v = _log(rng, lo, hi)
+    return v if rng.random() < 0.25 else max(64, v // 64 * 64) if rng.random() < 0.7 else max(8, v // 8 * 8)
+
+
+def draw(rng):
+    kind = rng.choice(["route", "route", "route_grad", "exchange", "exchange_grads", "norm", "norm_grads", "scaled", "scaled_step"])
+    c = {"kind": kind, "dtype": rng.choice(["bf16", "bf16", "fp32"])}
+    if kind.startswith("route"):
+        size, groups = _log(rng, 2, 64), rng.choice([1, 1, 2, 4, 8])
+        top = rng.randint(1, groups)
+        c.update(tokens=_log(rng, 1, 32768), experts=size * groups, k=rng.randint(1, min(16, size * top)), scores=rng.choice(["softmax", "sigmoid"]),
+                 pad=rng.choice([0.0, 0.1]))
+        return dict(c, bias=rng.random() < 0.5, groups=groups, top=top) if kind == "route" else c
+    if kind.startswith("exchange"):
+        while True:
+            c.update(tokens=_log(rng, 1, 8192), d=_width(rng, 64, 8192), experts=_log(rng, 2, 256), pad=rng.choice([0.0, 0.1]))
+            c["k"] = rng.randint(1, min(8, c["experts"]))
+            if c["tokens"] * c["d"] * c["k"] * SIZE[c["dtype"]] <= 8192 * 4096 * 8 * 2:
+                return c
+    if kind.startswith("norm"):
+        while True:
+            c.update(rows=_log(rng, 1, 32768), d=_width(rng, 64, 16384), centered=rng.random() < 0.6, bias=rng.random() < 0.5)
+            if c["rows"] * c["d"] * SIZE[c["dtype"]] <= 16384 * 5120 * 2:
+                return c
+    while True:
+        c.update(experts=_log(rng, 1, 256), rows=_log(rng, 1, 32768), n=_width(rng, 64, 14336), k=_width(rng, 64, 5632), skew=round(rng.uniform(0.0, 1.0), 2))
+        if c["experts"] * c["n"] * c["k"] <= 2 * 10 ** 8 and c["rows"] * c["n"] * c["k"] <= 4 * 10 ** 11:
+            return c
+
+
+def _power(biased):
+    """2^(biased - 127) exactly, from its bits."""
+    return (biased.to(torch.int32) << 23).view(torch.float32)
+
+
+def _exponent(top):
+    """Biased exponent byte of blocks with these maxima."""
+    m, p = torch.frexp(top)                                # top = m * 2^p, m in [1/2, 1) or 0
+    e = (p - 9 + (m > 0.875).to(p.dtype)).clamp(min=-126)
+    return torch.where(m == 0, torch.full_like(e, -126), e) + 127
+
+
+def _filled(x, dim):
+    """x in fp32, filled up with zeros to a multiple of 128 along a dimension."""
+    shape = list(x.shape)
+    shape[dim] = -(-shape[dim] // BLOCK) * BLOCK
+    out = torch.zeros(shape, dtype=torch.float32, device=x.device)
+    out.narrow(dim, 0, x.shape[dim]).copy_(x)
+    return out
+
+
+def _quantize(x):
+    """Activations (rows, k): codes (rows, filled k) and exponent bytes, one per 128 columns."""
+    v = _filled(x, 1).view(x.shape[0], -1, BLOCK)
+    e = _exponent(v.abs().amax(2))
+    return (v * _power(254 - e)[:, :, None]).to(torch.float8_e4m3fn).view(x.shape[0], -1), e.to(torch.uint8)
+
+
+def _quantize_matrices(w):
+    """Matrices (experts, n, k): codes (experts, n, filled k), bytes (experts, blocks of n, blocks of k)."""
+    experts, n, _ = w.shape
+    v = _filled(_filled(w, 2), 1)
+    v = v.view(experts, v.shape[1] // BLOCK, BLOCK, v.shape[2] // BLOCK, BLOCK)
+    e = _exponent(v.abs().amax((2, 4)))
+    codes = (v * _power(254 - e)[:, :, None, :, None]).to(torch.float8_e4m3fn)
+    return codes.view(experts, v.shape[1] * BLOCK, -1)[:, :n].contiguous(), e.to(torch.uint8)
+
+
+def _restore(codes, scales):
+    return codes.float() * _power(scales).repeat_interleave(BLOCK, 1)
+
+
+def _restore_matrices(codes, scales):
+    return codes.float() * _power(scales).repeat_interleave(BLOCK, 1)[:, : codes.shape[1]].repeat_interleave(BLOCK, 2)
+
+
+def _logits(normal, tokens, experts, dt):
+    """A router's outputs: some experts are liked more than others by every token."""
+    return (1.5 * normal(tokens, experts) + 0.7 * normal(experts)).to(dt)
+
+
+def _mask(g, case):
+    return torch.rand(case["tokens"], generator=g, device="cuda") >= case["pad"] if case["pad"] else None
+
+
+def prepare(case, seed):
+    g = torch.Generator(device="cuda").manual_seed(int(seed))
+    host = np.random.RandomState(int(seed) % (1 << 31))
+    kind, dt = case["kind"], DTYPES[case["dtype"]]
+
+    def normal(*shape):
+        return torch.randn(*shape, generator=g, device="cuda")
+
+    s = {"kind": kind, "dtype": dt}
+    if kind.startswith("route"):
+        s["logits"] = _logits(normal, case["tokens"], case["experts"], dt)
+        s["k"], s["scores"], s["mask"] = case["k"], case["scores"], _mask(g, case)
+        s["scale"] = 2.5 if s["scores"] == "sigmoid" else 1.0
+        if kind == "route":
+            s["bias"] = 0.05 * normal(case["experts"]) if case["bias"] else None
+            s["groups"], s["top"] = case["groups"], case["top"]
+        else:
+            s["dweights"] = 1e-3 * normal(case["tokens"], case["k"])
+            s["experts"] = _choose(s["logits"].double(), s["k"], s["mask"])
+    elif kind.startswith("exchange"):
+        tokens, d, k = case["tokens"], case["d"], case["k"]
+        x = _logits(normal, tokens, case["experts"], torch.float32)
+        chosen = _choose(x.double(), k, _mask(g, case))
+        s["k"], (_, s["slots"], s["place"]) = k, _plan(chosen, case["experts"])
+        s["weights"] = torch.where(chosen >= 0, torch.softmax(normal(tokens, k), 1), 0.0)
+        rows = tokens * k
+        if kind == "exchange":
+            s["x"], s["h"] = normal(tokens, d).to(dt), normal(rows, d).to(dt)
+            s["xs"] = torch.zeros(rows, d, dtype=dt, device="cuda")
+        else:
+            s["dy"], s["h"], s["dxs"] = (1e-3 * normal(tokens, d)).to(dt), normal(rows, d).to(dt), (1e-3 * normal(rows, d)).to(dt)
+            s["dh"] = torch.zeros(rows, d, dtype=dt, device="cuda")
+    elif kind.startswith("norm"):
+        rows, d = case["rows"], case["d"]
+        # activations: rows of different size and mean, some columns far larger than the rest
+        x = (normal(rows, d) + 0.3 * normal(rows, 1)) * torch.exp(normal(rows, 1))
+        s["x"] = (x * torch.where(torch.rand(d, generator=g, device="cuda") < 0.01, 10.0, 1.0)).to(dt)
+        s["weight"], s["bias"] = 1.0 + 0.1 * normal(d), 0.1 * normal(d) if case["bias"] else None
+        s["centered"], s["eps"] = case["centered"], 1e-5
+        if kind == "norm_grads":
+            s["dy"] = (1e-3 * normal(rows, d)).to(dt)
+            s["dweight"] = torch.empty(d, device="cuda")
+            s["dbias"] = torch.empty(d, device="cuda") if case["bias"] else None
+    else:
+        experts, rows, n, k = case["experts"], case["rows"], case["n"], case["k"]
+        # routing: log-normal popularity of the experts, rows sorted by expert
+        p = np.exp(case["skew"] * host.standard_normal(experts))
+        counts = host.multinomial(rows, p / p.sum())
+        s["counts"], s["longest"] = counts.tolist(), int(counts.max())
+        s["offsets"] = torch.from_numpy(np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)).cuda()
+        w = torch.empty(experts, n, k, dtype=dt, device="cuda").normal_(0.0, 0.02, generator=g)
+        s["x"] = normal(rows, k).to(dt)
+        if kind == "scaled":
+            s["codes"], s["scales"] = _quantize_matrices(w)
+        else:
+            s["w"], s["dy"] = w, (1e-3 * normal(rows, n)).to(dt)
+    return s
+
+
+def _choose(keys, k, mask):
+    """Indices of the k largest keys of each row, in order, ties to the lowest index; -1 for masked rows."""
+    chosen = torch.sort(keys, dim=1, descending=True, stable=True)[1][:, :k]
+    return (chosen if mask is None else torch.where(mask[:, None], chosen, -1)).to(torch.int32)
+
+
+def _plan(chosen, experts):
+    """(offsets, slots, place) of the chosen experts (tokens, k)."""
+    flat = chosen.reshape(-1).long()
+    held = flat >= 0
+    flat = torch.where(held, flat, experts)                # behind all of them
+    order = torch.sort(flat, stable=True)[1]
+    offsets = torch.searchsorted(flat[order], torch.arange(experts + 1, device=flat.device))
+    place = torch.empty_like(order)
+    place[order] = torch.arange(order.numel(), device=order.device)
+    slots = torch.where(held[order], order, -1)
+    return offsets.to(torch.int32), slots.to(torch.int32), torch.where(held, place, -1).to(torch.int32).view(chosen.shape)
+
+
+def _scores(x, scores):
+    if scores == "sigmoid":
+        return 1.0 / (1.0 + torch.exp(-x))
+    e = torch.exp(x - x.amax(1, keepdim=True))
+    return e / e.sum(1, keepdim=True)
+
+
+def _plain_route(s):
+    # keys next to one another decide in 64 bits
+    keys = score = _scores(s["logits"].double(), s["scores"])
+    tokens, experts = keys.shape
+    if s["bias"] is not None:
+        keys = keys + s["bias"].double()
+    if s["groups"] > 1:
+        of = keys.view(tokens, s["groups"], -1)
+        sums = torch.sort(of, dim=2, descending=True)[0][:, :, :2].sum(2)
+        stay = torch.zeros_like(sums, dtype=torch.bool).scatter_(1, torch.sort(sums, dim=1, descending=True, stable=True)[1][:, : s["top"]], True)
+        keys = torch.where(stay[:, :, None], of, -math.inf).view(tokens, experts)
+    chosen = _choose(keys, s["k"], s["mask"])
+    w = torch.where(chosen >= 0, score.gather(1, chosen.clamp(min=0).long()), 0.0)
+    w = (s["scale"] * w / (w.sum(1, keepdim=True) + TINY)).float()
+    offsets, slots, place = _plan(chosen, experts)
+    return {"experts": chosen, "weights": w, "offsets": offsets, "slots": slots, "place": place}
+
+
+def _plain_route_grad(s):
+    score = _scores(s["logits"].float(), s["scores"])
+    held, at = s["experts"] >= 0, s["experts"].clamp(min=0).long()
+    sel = score.gather(1, at)
+    d = sel.sum(1, keepdim=True) + TINY
+    ds = s["scale"] / d * (s["dweights"] - (s["dweights"] * sel).sum(1, keepdim=True) / d)
+    ds = torch.zeros_like(score).scatter_add_(1, at, torch.where(held, ds, 0.0))
+    if s["scores"] == "sigmoid":
+        return (ds * score * (1.0 - score)).to(s["dtype"])
+    return (score * (ds - (ds * score).sum(1, keepdim=True))).to(s["dtype"])
+
+
+def _plain_exchange(s):
+    slots, place = s["slots"], s["place"]
+    xs = torch.where(slots[:, None] >= 0, s["x"][slots.clamp(min=0) // s["k"]], s["xs"])
+    h = torch.where(place[:, :, None] >= 0, s["h"][place.clamp(min=0)].float(), 0.0)
+    return {"xs": xs, "y": (s["weights"][:, :, None] * h).sum(1).to(s["dtype"])}
+
+
+def _plain_exchange_grads(s):
+    slots, place = s["slots"], s["place"]
+    on, at = slots[:, None] >= 0, slots.clamp(min=0)
+    dh = torch.where(on, (s["weights"].view(-1)[at][:, None] * s["dy"][at // s["k"]].float()).to(s["dtype"]), s["dh"])
+    held, row = place[:, :, None] >= 0, place.clamp(min=0)
+    dw = torch.where(held[:, :, 0], (s["h"][row].float() * s["dy"].float()[:, None]).sum(2), 0.0)
+    dx = torch.where(held, s["dxs"][row].float(), 0.0).sum(1)
+    return {"dh": dh, "dw": dw, "dx": dx.to(s["dtype"])}
+
+
+def _plain_norm(s):
+    x = s["x"].float()
+    if s["centered"]:
+        x = x - x.mean(1, keepdim=True)
+    y = x * torch.rsqrt((x * x).mean(1, keepdim=True) + s["eps"]) * s["weight"]
+    return (y if s["bias"] is None else y + s["bias"]).to(s["dtype"])
+
+
+def _plain_norm_grads(s):
+    x, dy = s["x"].float(), s["dy"].float()
+    if s["centered"]:
+        x = x - x.mean(1, keepdim=True)
+    r = torch.rsqrt((x * x).mean(1, keepdim=True) + s["eps"])
+    xh, g = x * r, dy * s["weight"]
+    dx = g - xh * (g * xh).mean(1, keepdim=True)
+    if s["centered"]:
+        dx = dx - g.mean(1, keepdim=True)
+    out = {"dx": (r * dx).to(s["dtype"]), "dweight": (dy * xh).sum(0)}
+    return out if s["dbias"] is None else dict(out, dbias=dy.sum(0))
+
+
+def _places(s):
+    """Padded layout of the ragged rows: row of (expert, place), which places hold one, and each row's expert and place."""
+    off = s["offsets"].to(torch.int64)
+    row = off[:-1, None] + torch.arange(s["longest"], device=off.device)
+    held = row < off[1:, None]
+    r = torch.arange(s["x"].shape[0], device=off.device)
+    expert = torch.searchsorted(off[1:].contiguous(), r, right=True)
+    return torch.where(held, row, 0), held, expert, r - off[expert]
+
+
+def _product(x, w, places, dtype):
+    """Rows of x with their experts' matrices (experts, depth, width)."""
+    row, held, expert, place = places
+    return torch.bmm(torch.where(held[:, :, None], x[row], 0.0), w)[expert, place].to(dtype)
+
+
+def _plain_scaled(s):
+    k = s["x"].shape[1]
+    if "codes" in s:
+        w = _restore_matrices(s["codes"], s["scales"])[:, :, :k]
+    else:
+        w = _restore_matrices(*_quantize_matrices(s["w"]))[:, :, :k]
+    places = _places(s)
+    y = _product(_restore(*_quantize(s["x"]))[:, :k], w.transpose(1, 2), places, s["dtype"])
+    if "codes" in s:
+        return y
+    return {"y": y, "dx": _product(_restore(*_quantize(s["dy"]))[:, : s["dy"].shape[1]], w, places, s["dtype"])}
+
+
+def run(state):
+    s = state
+    kind = s["kind"]
+    if own:
+        import matrix_optimizer_step_owner_amd as mf
+        if kind == "route":
+            chosen, w = mf.route(s["logits"], s["k"], scores=s["scores"], bias=s["bias"], groups=s["groups"], top_groups=s["top"], scale=s["scale"], mask=s["mask"])
+            p = mf.route_plan(chosen, s["logits"].shape[1])
+            return {"experts": chosen, "weights": w, "offsets": p.offsets, "slots": p.slots, "place": p.place}
+        if kind == "route_grad":
+            return mf.route_grad(s["dweights"], s["logits"], s["experts"], scores=s["scores"], scale=s["scale"])
+        if kind == "exchange":
+            xs = mf.route_dispatch(s["x"], s["slots"], s["k"], out=s["xs"])
+            return {"xs": xs, "y": mf.route_combine(s["h"], s["place"], s["weights"])}
+        if kind == "exchange_grads":
+            dh, dw = mf.route_combine_grad(s["dy"], s["h"], s["place"], s["weights"], dh=s["dh"])
+            return {"dh": dh, "dw": dw, "dx": mf.route_combine(s["dxs"], s["place"])}
+        if kind == "norm":
+            return mf.layer_norm(s["x"], s["weight"], s["bias"], eps=s["eps"], centered=s["centered"])
+        if kind == "norm_grads":
+            dx = mf.layer_norm_grad(s["dy"], s["x"], s["weight"], s["dweight"], s["dbias"], eps=s["eps"], centered=s["centered"])
+            out = {"dx": dx, "dweight": s["dweight"]}
+            return out if s["dbias"] is None else dict(out, dbias=s["dbias"])
+        if kind == "scaled":
+            return mf.scaled_linear(*mf.scaled_quantize(s["x"]), s["codes"], s["scales"], s["offsets"], dtype=s["dtype"])
+        y = mf.scaled_linear(*mf.scaled_quantize(s["x"]), *mf.scaled_quantize_weight(s["w"]), s["offsets"], dtype=s["dtype"])
+        dx = mf.scaled_linear(*mf.scaled_quantize(s["dy"]), *mf.scaled_quantize_weight(s["w"], transpose=True), s["offsets"], dtype=s["dtype"])
+        return {"y": y, "dx": dx}
+    if kind == "route":
+        return _plain_route(s)
+    if kind == "route_grad":
+        return _plain_route_grad(s)
+    if kind == "exchange":
+        return _plain_exchange(s)
+    if kind == "exchange_grads":
+        return _plain_exchange_grads(s)
+    if kind == "norm":
+        return _plain_norm(s)
+    return _plain_norm_grads(s) if kind == "norm_grads" else _plain_scaled(s)
+
+
+def work(case):
+    kind, z = case["kind"], SIZE[case["dtype"]]
+    if kind.startswith("route"):
+        t, e, k = case["tokens"], case["experts"], case["k"]
+        if kind == "route":     # logits; experts and weights; slots and place
+            return {"bytes": t * (e * z + 16 * k) + 4 * e, "flops": 4 * t * e}
+        return {"bytes": t * (2 * e * z + 8 * k), "flops": 6 * t * e}
+    if kind.startswith("exchange"):
+        t, d, k = case["tokens"], case["d"], case["k"]
+        if kind == "exchange":
+            return {"bytes": z * t * d * (2 + 2 * k) + 12 * t * k, "flops": 2 * t * d * k}
+        return {"bytes": z * t * d * (2 + 3 * k) + 12 * t * k, "flops": 4 * t * d * k}
+    if kind.startswith("norm"):
+        m, d = case["rows"], case["d"]
+        n = 1 + int(case["bias"])
+        if kind == "norm":
+            return {"bytes": 2 * m * d * z + 4 * d * n, "flops": 6 * m * d}
+        return {"bytes": 3 * m * d * z + 4 * d * (1 + n), "flops": 12 * m * d}
+    m, n, k, e = case["rows"], case["n"], case["k"], case["experts"]
+    held = min(e, m) * n * k
+    if kind == "scaled":        # experts without rows need not be read
+        return {"bytes": z * m * (k + n) + held, "flops": 2 * m * n * k}
+    return {"bytes": z * (2 * m * (k + n) + held), "flops": 4 * m * n * k}
+
+
+def _power64(e):
+    return ((e.to(torch.int64) + 1023) << 52).view(torch.float64)
+
+
+def _held64(v, dims):
+    """The values that the 8-bit copies of blocks v stand for, a block over `dims`."""
+    v = v.double()
+    top = v.abs().amax(dims, keepdim=True).clamp(min=448.0 * 2.0 ** -126)
+    e = torch.floor(torch.log2(top)) - 10       # at or below the smallest: at most three steps up
+    e = torch.where(top > 448.0 * _power64(e), e + 1, e)
+    e = torch.where(top > 448.0 * _power64(e), e + 1, e)
+    e = _power64(torch.where(top > 448.0 * _power64(e), e + 1, e))
+    v = v / e
+    # three bits of fraction from 2^-6 on, whole 2^-9 below
+    step = _power64(torch.floor(torch.log2(v.abs().clamp(min=2.0 ** -6))) - 3)
+    return torch.round(v / step) * step * e
+
+
+def _rows64(x):
+    return _held64(_filled(x, 1).view(x.shape[0], -1, BLOCK), (2,)).view(x.shape[0], -1)[:, : x.shape[1]]
+
+
+def _matrix64(w):
+    v = _filled(_filled(w, 1), 0)
+    v = v.view(v.shape[0] // BLOCK, BLOCK, v.shape[1] // BLOCK, BLOCK)
+    return _held64(v, (1, 3)).reshape(v.shape[0] * BLOCK, -1)[: w.shape[0], : w.shape[1]]
+
+
+def _route64(case, s):
+    x = s["logits"].double().cpu().numpy()
+    tokens, experts = x.shape
+    if s["scores"] == "sigmoid":
+        p = 0.5 + 0.5 * np.tanh(x / 2)
+    else:
+        p = np.exp(x - np.log(np.exp(x).sum(1))[:, None])
+    on = np.ones(tokens, bool) if s["mask"] is None else s["mask"].cpu().numpy()
+    if case["kind"] == "route":
+        keys = p if s["bias"] is None else p + s["bias"].double().cpu().numpy()
+        size = experts // s["groups"]
+        if s["groups"] > 1:
+            part = np.partition(keys.reshape(tokens, -1, size), size - min(2, size), axis=2)[:, :, -min(2, size):].sum(2)
+            rank = np.argsort(np.argsort(-part, axis=1, kind="stable"), axis=1)
+            keys = np.where(np.repeat(rank < s["top"], size, axis=1), keys, -np.inf)
+        chosen = np.argsort(-keys, axis=1, kind="stable")[:, : s["k"]]
+        sel = np.take_along_axis(p, chosen, 1)
+        w = np.where(on[:, None], s["scale"] * sel / sel.sum(1)[:, None], 0.0)
+        chosen = np.where(on[:, None], chosen, -1).astype(np.int32)
+        flat = chosen.reshape(-1)
+        rows = np.flatnonzero(flat >= 0)
+        rows = rows[np.argsort(flat[rows], kind="stable")]
+        slots, place = np.full(flat.size, -1, np.int32), np.full(flat.size, -1, np.int32)
+        slots[: rows.size], place[rows] = rows, np.arange(rows.size)
+        offsets = np.concatenate([[0], np.cumsum(np.bincount(flat[flat >= 0], minlength=experts))]).astype(np.int32)
+        out = {"experts": chosen, "weights": w, "offsets": offsets, "slots": slots, "place": place.reshape(chosen.shape)}
+        return {key: torch.from_numpy(v) for key, v in out.items()}
+    at = s["experts"].cpu().numpy().clip(0)
+    sel, dw = np.take_along_axis(p, at, 1), s["dweights"].double().cpu().numpy()
+    total = sel.sum(1, keepdims=True)
+    jac = s["scale"] * (dw * total - (dw * sel).sum(1, keepdims=True)) / total ** 2
+    ds = np.zeros_like(p)
+    np.put_along_axis(ds, at, jac * on[:, None], 1)
+    return torch.from_numpy(ds * p * (1 - p) if s["scores"] == "sigmoid" else ds * p - p * (ds * p).sum(1, keepdims=True))
+
+
+def exact(case, seed):
+    s = prepare(case, seed)
+    kind = s["kind"]
+    if kind.startswith("route"):
+        return _route64(case, s)
+    if kind.startswith("exchange"):
+        tokens, k = s["place"].shape
+        held = s["slots"] >= 0
+        slot = s["slots"][held].long()
+        w = s["weights"].double()
+        if kind == "exchange":
+            xs = s["xs"].double()
+            xs[held] = s["x"].double()[slot // k]
+            y = torch.zeros(tokens, xs.shape[1], dtype=torch.float64, device=xs.device)
+            for j in range(k):
+                on = s["place"][:, j] >= 0
+                y[on] += w[on, j, None] * s["h"][s["place"][on, j].long()].double()
+            return {"xs": xs, "y": y}
+        dh = torch.zeros(s["dh"].shape, dtype=torch.float64, device=w.device)
+        dw, dx = torch.zeros_like(w), torch.zeros(s["dy"].shape, dtype=torch.float64, device=w.device)
+        for j in range(k):
+            on = s["place"][:, j] >= 0
+            row, dy = s["place"][on, j].long(), s["dy"][on].double()
+            dh[row] = w[on, j, None] * dy
+            dw[on, j] = (dy * s["h"][row].double()).sum(1)
+            dx[on] += s["dxs"][row].double()
+        return {"dh": dh, "dw": dw, "dx": dx}
+    if kind.startswith("norm"):
+        x, w = s["x"].double(), s["weight"].double()
+        mean = x.mean(1, keepdim=True) if s["centered"] else 0.0
+        sd = torch.sqrt(((x - mean) ** 2).mean(1, keepdim=True) + s["eps"])
+        xh = (x - mean) / sd
+        if kind == "norm":
+            return xh * w if s["bias"] is None else xh * w + s["bias"].double()
+        dy = s["dy"].double()
+        dx = (dy * w - xh * (dy * w * xh).mean(1, keepdim=True) - ((dy * w).mean(1, keepdim=True) if s["centered"] else 0.0)) / sd
+        out = {"dx": dx, "dweight": (dy * xh).sum(0)}
+        return out if s["dbias"] is None else dict(out, dbias=dy.sum(0))
+    x, at, y, dx = _rows64(s["x"]), 0, [], []
+    dy = _rows64(s["dy"]) if "dy" in s else None
+    for e, m in enumerate(s["counts"]):
+        if "codes" in s:    # kept copies: codes times the powers that their bytes name
+            c = s["codes"][e].double()
+            b = _power64(s["scales"][e].to(torch.int64) - 127)
+            w = (c * b.repeat_interleave(BLOCK, 0)[: c.shape[0]].repeat_interleave(BLOCK, 1))[:, : x.shape[1]]
+        else:
+            w = _matrix64(s["w"][e])
+            dx.append(dy[at:at + m] @ w)
+        y.append(x[at:at + m] @ w.t())
+        at += m
+    return torch.cat(y) if "codes" in s else {"y": torch.cat(y), "dx": torch.cat(dx)}
