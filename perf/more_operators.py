@@ -7,10 +7,10 @@
   two largest keys stay; the k largest keys among them are chosen in order, ties
   to the lowest index; weight = scale * s / (sum of the chosen s + 1e-20), or
   scale * s.  A masked token has experts -1 and weights 0.  The plan: ``offsets``
-  of each expert's rows, ``slots`` (token * k + j of each row, tokens in order
-  within an expert, -1 behind the last) and ``place`` (row of each slot or -1).
+  of each expert's rows and ``place``, the row of each (token, j) or -1, tokens
+  in order within an expert.
 * ``route_grad``: the logits' gradient from the weights'.
-* ``exchange``: rows to their experts' order, xs[r] = x[slots[r] / k], and back,
+* ``exchange``: rows to their experts' order, xs[place[t, j]] = x[t], and back,
   y[t] = sum_j w[t, j] h[place[t, j]].
 * ``exchange_grads``: dh[place[t, j]] = w[t, j] dy[t], dw[t, j] = <dy[t], h[place[t, j]]>
   and dx[t] = sum_j dxs[place[t, j]].
@@ -181,7 +181,7 @@ def prepare(case, seed):
         tokens, d, k = case["tokens"], case["d"], case["k"]
         x = _logits(normal, tokens, case["experts"], torch.float32)
         chosen = _choose(x.double(), k, _mask(g, case))
-        s["k"], (_, s["slots"], s["place"]) = k, _plan(chosen, case["experts"])
+        s["place"] = _plan(chosen, case["experts"])[1]
         s["weights"] = torch.where(chosen >= 0, torch.softmax(normal(tokens, k), 1), 0.0)
         rows = tokens * k
         if kind == "exchange":
@@ -224,7 +224,7 @@ def _choose(keys, k, mask):
 
 
 def _plan(chosen, experts):
-    """(offsets, slots, place) of the chosen experts (tokens, k)."""
+    """(offsets, place) of the chosen experts (tokens, k)."""
     flat = chosen.reshape(-1).long()
     held = flat >= 0
     flat = torch.where(held, flat, experts)                # behind all of them
@@ -232,8 +232,7 @@ def _plan(chosen, experts):
     offsets = torch.searchsorted(flat[order], torch.arange(experts + 1, device=flat.device))
     place = torch.empty_like(order)
     place[order] = torch.arange(order.numel(), device=order.device)
-    slots = torch.where(held[order], order, -1)
-    return offsets.to(torch.int32), slots.to(torch.int32), torch.where(held, place, -1).to(torch.int32).view(chosen.shape)
+    return offsets.to(torch.int32), torch.where(held, place, -1).to(torch.int32).view(chosen.shape)
 
 
 def _scores(x, scores):
@@ -257,8 +256,8 @@ def _plain_route(s):
     chosen = _choose(keys, s["k"], s["mask"])
     w = torch.where(chosen >= 0, score.gather(1, chosen.clamp(min=0).long()), 0.0)
     w = (s["scale"] * w / (w.sum(1, keepdim=True) + TINY)).float()
-    offsets, slots, place = _plan(chosen, experts)
-    return {"experts": chosen, "weights": w, "offsets": offsets, "slots": slots, "place": place}
+    offsets, place = _plan(chosen, experts)
+    return {"experts": chosen, "weights": w, "offsets": offsets, "place": place}
 
 
 def _plain_route_grad(s):
@@ -273,19 +272,25 @@ def _plain_route_grad(s):
     return (score * (ds - (ds * score).sum(1, keepdim=True))).to(s["dtype"])
 
 
+def _rows_to(place, values, out):
+    """out with the value of each (token, j) at its row; those without one go to a row behind the last."""
+    rows = out.shape[0]
+    at = torch.where(place >= 0, place, rows).view(-1).long()
+    return torch.cat([out, out[:1]]).index_copy_(0, at, values.reshape(rows, -1))[:rows]
+
+
 def _plain_exchange(s):
-    slots, place = s["slots"], s["place"]
-    xs = torch.where(slots[:, None] >= 0, s["x"][slots.clamp(min=0) // s["k"]], s["xs"])
-    h = torch.where(place[:, :, None] >= 0, s["h"][place.clamp(min=0)].float(), 0.0)
+    place, h = s["place"], s["h"]
+    xs = _rows_to(place, s["x"][:, None].expand(-1, place.shape[1], -1), s["xs"])
+    h = torch.where(place[:, :, None] >= 0, h[place.clamp(min=0)].float(), 0.0)
     return {"xs": xs, "y": (s["weights"][:, :, None] * h).sum(1).to(s["dtype"])}
 
 
 def _plain_exchange_grads(s):
-    slots, place = s["slots"], s["place"]
-    on, at = slots[:, None] >= 0, slots.clamp(min=0)
-    dh = torch.where(on, (s["weights"].view(-1)[at][:, None] * s["dy"][at // s["k"]].float()).to(s["dtype"]), s["dh"])
+    place, dy = s["place"], s["dy"].float()[:, None]
     held, row = place[:, :, None] >= 0, place.clamp(min=0)
-    dw = torch.where(held[:, :, 0], (s["h"][row].float() * s["dy"].float()[:, None]).sum(2), 0.0)
+    dh = _rows_to(place, (s["weights"][:, :, None] * dy).to(s["dtype"]), s["dh"])
+    dw = torch.where(held[:, :, 0], (s["h"][row].float() * dy).sum(2), 0.0)
     dx = torch.where(held, s["dxs"][row].float(), 0.0).sum(1)
     return {"dh": dh, "dw": dw, "dx": dx.to(s["dtype"])}
 
@@ -348,11 +353,11 @@ def run(state):
         if kind == "route":
             chosen, w = mf.route(s["logits"], s["k"], scores=s["scores"], bias=s["bias"], groups=s["groups"], top_groups=s["top"], scale=s["scale"], mask=s["mask"])
             p = mf.route_plan(chosen, s["logits"].shape[1])
-            return {"experts": chosen, "weights": w, "offsets": p.offsets, "slots": p.slots, "place": p.place}
+            return {"experts": chosen, "weights": w, "offsets": p.offsets, "place": p.place}
         if kind == "route_grad":
             return mf.route_grad(s["dweights"], s["logits"], s["experts"], scores=s["scores"], scale=s["scale"])
         if kind == "exchange":
-            xs = mf.route_dispatch(s["x"], s["slots"], s["k"], out=s["xs"])
+            xs = mf.route_dispatch(s["x"], s["place"], out=s["xs"])
             return {"xs": xs, "y": mf.route_combine(s["h"], s["place"], s["weights"])}
         if kind == "exchange_grads":
             dh, dw = mf.route_combine_grad(s["dy"], s["h"], s["place"], s["weights"], dh=s["dh"])
@@ -385,8 +390,8 @@ def work(case):
     kind, z = case["kind"], SIZE[case["dtype"]]
     if kind.startswith("route"):
         t, e, k = case["tokens"], case["experts"], case["k"]
-        if kind == "route":     # logits; experts and weights; slots and place
-            return {"bytes": t * (e * z + 16 * k) + 4 * e, "flops": 4 * t * e}
+        if kind == "route":     # logits; experts, weights and place
+            return {"bytes": t * (e * z + 12 * k) + 4 * e, "flops": 4 * t * e}
         return {"bytes": t * (2 * e * z + 8 * k), "flops": 6 * t * e}
     if kind.startswith("exchange"):
         t, d, k = case["tokens"], case["d"], case["k"]
@@ -456,10 +461,10 @@ def _route64(case, s):
         flat = chosen.reshape(-1)
         rows = np.flatnonzero(flat >= 0)
         rows = rows[np.argsort(flat[rows], kind="stable")]
-        slots, place = np.full(flat.size, -1, np.int32), np.full(flat.size, -1, np.int32)
-        slots[: rows.size], place[rows] = rows, np.arange(rows.size)
+        place = np.full(flat.size, -1, np.int32)
+        place[rows] = np.arange(rows.size)
         offsets = np.concatenate([[0], np.cumsum(np.bincount(flat[flat >= 0], minlength=experts))]).astype(np.int32)
-        out = {"experts": chosen, "weights": w, "offsets": offsets, "slots": slots, "place": place.reshape(chosen.shape)}
+        out = {"experts": chosen, "weights": w, "offsets": offsets, "place": place.reshape(chosen.shape)}
         return {key: torch.from_numpy(v) for key, v in out.items()}
     at = s["experts"].cpu().numpy().clip(0)
     sel, dw = np.take_along_axis(p, at, 1), s["dweights"].double().cpu().numpy()
@@ -476,17 +481,15 @@ def exact(case, seed):
     if kind.startswith("route"):
         return _route64(case, s)
     if kind.startswith("exchange"):
-        tokens, k = s["place"].shape
-        held = s["slots"] >= 0
-        slot = s["slots"][held].long()
-        w = s["weights"].double()
+        k, w = s["place"].shape[1], s["weights"].double()
         if kind == "exchange":
             xs = s["xs"].double()
-            xs[held] = s["x"].double()[slot // k]
-            y = torch.zeros(tokens, xs.shape[1], dtype=torch.float64, device=xs.device)
+            y = torch.zeros(s["x"].shape, dtype=torch.float64, device=w.device)
             for j in range(k):
                 on = s["place"][:, j] >= 0
-                y[on] += w[on, j, None] * s["h"][s["place"][on, j].long()].double()
+                row = s["place"][on, j].long()
+                xs[row] = s["x"][on].double()
+                y[on] += w[on, j, None] * s["h"][row].double()
             return {"xs": xs, "y": y}
         dh = torch.zeros(s["dh"].shape, dtype=torch.float64, device=w.device)
         dw, dx = torch.zeros_like(w), torch.zeros(s["dy"].shape, dtype=torch.float64, device=w.device)
