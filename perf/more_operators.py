@@ -370,8 +370,9 @@ def run(state):
             return out if s["dbias"] is None else dict(out, dbias=s["dbias"])
         if kind == "scaled":
             return mf.scaled_linear(*mf.scaled_quantize(s["x"]), s["codes"], s["scales"], s["offsets"], dtype=s["dtype"])
-        y = mf.scaled_linear(*mf.scaled_quantize(s["x"]), *mf.scaled_quantize_weight(s["w"]), s["offsets"], dtype=s["dtype"])
-        dx = mf.scaled_linear(*mf.scaled_quantize(s["dy"]), *mf.scaled_quantize_weight(s["w"], transpose=True), s["offsets"], dtype=s["dtype"])
+        codes, scales, tcodes, tscales = mf.scaled_quantize_weight(s["w"], both=True)
+        y = mf.scaled_linear(*mf.scaled_quantize(s["x"]), codes, scales, s["offsets"], dtype=s["dtype"])
+        dx = mf.scaled_linear(*mf.scaled_quantize(s["dy"]), tcodes, tscales, s["offsets"], dtype=s["dtype"])
         return {"y": y, "dx": dx}
     if kind == "route":
         return _plain_route(s)
