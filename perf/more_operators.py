@@ -22,7 +22,8 @@
 An 8-bit copy holds blocks (128 columns of a row of activations; 128 x 128 of a
 matrix) as e4m3 codes and one power of two 2^e, the smallest (e >= -126) with
 max |v| <= 448 * 2^e, kept as the byte e + 127: code = v / 2^e to the nearest, ties
-to even.  Code rows are filled up with zeros to a multiple of 128.
+to even.  Code rows are filled up with zeros to a multiple of 128.  Products of
+8-bit copies are bf16, whatever the copies were made from.
 """
 
 import math
@@ -326,10 +327,10 @@ def _places(s):
     return torch.where(held, row, 0), held, expert, r - off[expert]
 
 
-def _product(x, w, places, dtype):
+def _product(x, w, places):
     """Rows of x with their experts' matrices (experts, depth, width)."""
     row, held, expert, place = places
-    return torch.bmm(torch.where(held[:, :, None], x[row], 0.0), w)[expert, place].to(dtype)
+    return torch.bmm(torch.where(held[:, :, None], x[row], 0.0), w)[expert, place].to(torch.bfloat16)
 
 
 def _plain_scaled(s):
@@ -339,10 +340,10 @@ def _plain_scaled(s):
     else:
         w = _restore_matrices(*_quantize_matrices(s["w"]))[:, :, :k]
     places = _places(s)
-    y = _product(_restore(*_quantize(s["x"]))[:, :k], w.transpose(1, 2), places, s["dtype"])
+    y = _product(_restore(*_quantize(s["x"]))[:, :k], w.transpose(1, 2), places)
     if "codes" in s:
         return y
-    return {"y": y, "dx": _product(_restore(*_quantize(s["dy"]))[:, : s["dy"].shape[1]], w, places, s["dtype"])}
+    return {"y": y, "dx": _product(_restore(*_quantize(s["dy"]))[:, : s["dy"].shape[1]], w, places)}
 
 
 def run(state):
@@ -369,10 +370,10 @@ def run(state):
             out = {"dx": dx, "dweight": s["dweight"]}
             return out if s["dbias"] is None else dict(out, dbias=s["dbias"])
         if kind == "scaled":
-            return mf.scaled_linear(*mf.scaled_quantize(s["x"]), s["codes"], s["scales"], s["offsets"], dtype=s["dtype"])
+            return mf.scaled_linear(*mf.scaled_quantize(s["x"]), s["codes"], s["scales"], s["offsets"])
         codes, scales, tcodes, tscales = mf.scaled_quantize_weight(s["w"], both=True)
-        y = mf.scaled_linear(*mf.scaled_quantize(s["x"]), codes, scales, s["offsets"], dtype=s["dtype"])
-        dx = mf.scaled_linear(*mf.scaled_quantize(s["dy"]), tcodes, tscales, s["offsets"], dtype=s["dtype"])
+        y = mf.scaled_linear(*mf.scaled_quantize(s["x"]), codes, scales, s["offsets"])
+        dx = mf.scaled_linear(*mf.scaled_quantize(s["dy"]), tcodes, tscales, s["offsets"])
         return {"y": y, "dx": dx}
     if kind == "route":
         return _plain_route(s)
@@ -408,8 +409,8 @@ def work(case):
     m, n, k, e = case["rows"], case["n"], case["k"], case["experts"]
     held = min(e, m) * n * k
     if kind == "scaled":        # experts without rows need not be read
-        return {"bytes": z * m * (k + n) + held, "flops": 2 * m * n * k}
-    return {"bytes": z * (2 * m * (k + n) + held), "flops": 4 * m * n * k}
+        return {"bytes": m * (z * k + 2 * n) + held, "flops": 2 * m * n * k}
+    return {"bytes": m * (z + 2) * (k + n) + z * held, "flops": 4 * m * n * k}
 
 
 def _power64(e):
