@@ -15,9 +15,10 @@
  *   mfsdp_muon_step   -- Muon on the owner's list of whole matrices,
  *   mfsdp_adamw_tail  -- AdamW on a packed fp32 tail buffer.
  *
- * Further down: the owner planner, packed tails, Shampoo-type statistics, and
- * the operators that make the gradients of experts' matrices and of an
- * embedding table.
+ * Further down: the owner planner, packed tails, Shampoo-type statistics, the
+ * operators that make the gradients of experts' matrices and of an embedding
+ * table, and those around them: routing, the exchange of rows, layer norm and
+ * products in 8-bit floats.
  *
  * Conventions shared by every entry point
  *   - Every pointer named "device" is a device (HBM) address on the current
@@ -502,6 +503,200 @@ mfsdp_status_t mfsdp_embedding_grad(const void* dy, int64_t ld_dy, mfsdp_dtype_t
                                     int64_t vocab, int64_t d, float scale, float beta, float* grad,
                                     void* workspace, size_t workspace_bytes, hipStream_t stream);
 
+/*
+ * Around the experts' products: which rows go where, the norms before them, and
+ * the products in 8-bit floats.  The pages name experts and norm gains (tail
+ * tensors of AdamW) but give no formulas: these are the usual ones.  The rules
+ * of the gradient operators above hold here too (asynchronous, no allocation,
+ * capturable, no atomics on sums, fp32 sums rounded once, outputs disjoint from
+ * inputs, buffers aligned to their elements).  Rows may have any stride and
+ * start at any element.
+ *
+ * Routing: the k experts of each token and their weights, from a row of logits x.
+ *   s       softmax(x) or sigmoid(x)
+ *   key     s + bias (no bias: s)
+ *   groups  n_experts / groups neighbouring experts each; those with the
+ *           top_groups largest sums of their two largest keys stay (groups == 1:
+ *           all do)
+ *   experts the k largest keys among those that stay, in descending order
+ *   weights scale * s_j / (sum of the k chosen s + 1e-20), or scale * s_j without
+ *           renormalize: the bias chooses and does not weigh
+ * The choice is that of exact arithmetic on the logits and biases as stored, as
+ * far as 64 bits tell it; ties go to the lowest index.  A NaN key is behind
+ * -infinity; a row with a NaN or +infinity has NaN weights where its scores are
+ * NaN, its experts are still k different ones.
+ *   logits   device, tokens x n_experts, row stride ld_logits, bf16 or fp32
+ *   bias     device fp32, n_experts, or NULL
+ *   mask     device, tokens bytes, or NULL: a token with 0 is padding, has experts
+ *            -1 and weights 0, and its logits are not read
+ *   experts  device int32, tokens x k;  weights device fp32, tokens x k
+ * Gradient: of the logits, from that of the weights.  experts as chosen (an index
+ * outside [0, n_experts) is none; one that is named twice counts twice); a token
+ * without any has a row of zeros.  The choice itself has no gradient, and the
+ * bias none.
+ *   dweights device fp32, tokens x k;  dlogits device, as logits
+ * tokens == 0 returns MFSDP_OK, no work.
+ * Errors: MFSDP_ERR_INVALID_ARGUMENT (k outside [1, n_experts], groups that do
+ * not divide n_experts, top_groups outside [1, groups] or with fewer than k
+ * experts, strides smaller than rows, null or misaligned pointers, non-finite
+ * scale), MFSDP_ERR_UNSUPPORTED (n_experts above 1024, k above 32, groups above
+ * 64, 2^25 tokens or more, more than 2^30 choices), MFSDP_ERR_ALIAS,
+ * MFSDP_ERR_HIP.
+ */
+typedef enum mfsdp_route_score {
+  MFSDP_ROUTE_SOFTMAX = 0,
+  MFSDP_ROUTE_SIGMOID = 1
+} mfsdp_route_score_t;
+
+mfsdp_status_t mfsdp_route(const void* logits, int64_t ld_logits, const float* bias,
+                           const uint8_t* mask, int64_t tokens, int64_t n_experts, int64_t k,
+                           mfsdp_dtype_t dtype, mfsdp_route_score_t scores, int64_t groups,
+                           int64_t top_groups, int renormalize, float scale, int32_t* experts,
+                           float* weights, hipStream_t stream);
+
+mfsdp_status_t mfsdp_route_grad(const float* dweights, const void* logits, int64_t ld_logits,
+                                const int32_t* experts, int64_t tokens, int64_t n_experts,
+                                int64_t k, mfsdp_dtype_t dtype, mfsdp_route_score_t scores,
+                                int renormalize, float scale, void* dlogits, int64_t ld_dlogits,
+                                hipStream_t stream);
+
+/*
+ * Plan of a routing: the rows of the choices, sorted by expert, tokens in order
+ * within one.
+ *   experts  device int32, tokens x k; outside [0, n_experts): no row
+ *   offsets  device int32, n_experts + 1: as the products grouped by expert take
+ *            them; offsets[n_experts] is the number of rows in use
+ *   place    device int32, tokens x k: the row of each choice, or -1
+ * workspace  device, >= mfsdp_route_plan_workspace_size bytes (that may be 0, and
+ *            workspace NULL), 256-byte aligned, scratch.
+ * tokens == 0 gives offsets of zeros.  Errors as above, MFSDP_ERR_WORKSPACE; up to
+ * 2^30 choices.
+ */
+mfsdp_status_t mfsdp_route_plan_workspace_size(int64_t tokens, int64_t k, int64_t n_experts,
+                                               size_t* out_bytes);
+
+mfsdp_status_t mfsdp_route_plan(const int32_t* experts, int64_t tokens, int64_t k,
+                                int64_t n_experts, int32_t* offsets, int32_t* place,
+                                void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * Balance: bias[e] += rate where expert e has fewer choices than the mean, -= rate
+ * where it has more (decided in whole numbers).
+ *   bias    device fp32, n_experts, updated in place
+ *   counts  device int32 or int64 (count_bytes 4 or 8), n_experts: choices of each
+ *           expert, summed over the ranks where there are several
+ */
+mfsdp_status_t mfsdp_route_balance(float* bias, const void* counts, int count_bytes,
+                                   int64_t n_experts, float rate, hipStream_t stream);
+
+/*
+ * Exchange of rows, by a plan's place (a row outside [0, rows) is none, and is
+ * neither read nor written; rows of no choice are left as they were):
+ *   dispatch          out[place[t][j]] = x[t]
+ *   combine           y[t] = beta*y[t] + sum_j weights[t][j] * h[place[t][j]], j in order
+ *                     (weights NULL: 1, which is dispatch's gradient); beta == 0
+ *                     does not read y
+ *   combine gradient  dh[place[t][j]] = weights[t][j] * dy[t]
+ *                     dweights[t][j] = <dy[t], h[place[t][j]]>, 0 for none
+ * x, y, dy: tokens x d; out, h, dh: rows x d, bf16 or fp32, any row stride.  Two
+ * choices that name the same row are written in no order.
+ * tokens == 0 returns MFSDP_OK, no work.  Errors as above; k up to 32, up to 2^30
+ * choices and rows, d and strides up to 2^22.
+ */
+mfsdp_status_t mfsdp_route_dispatch(const void* x, int64_t ld_x, const int32_t* place,
+                                    int64_t tokens, int64_t k, int64_t rows, int64_t d,
+                                    mfsdp_dtype_t dtype, void* out, int64_t ld_out,
+                                    hipStream_t stream);
+
+mfsdp_status_t mfsdp_route_combine(const void* h, int64_t ld_h, const int32_t* place,
+                                   const float* weights, int64_t tokens, int64_t k, int64_t rows,
+                                   int64_t d, mfsdp_dtype_t dtype, float beta, void* y,
+                                   int64_t ld_y, hipStream_t stream);
+
+mfsdp_status_t mfsdp_route_combine_grad(const void* dy, int64_t ld_dy, const void* h, int64_t ld_h,
+                                        const int32_t* place, const float* weights, int64_t tokens,
+                                        int64_t k, int64_t rows, int64_t d, mfsdp_dtype_t dtype,
+                                        void* dh, int64_t ld_dh, float* dweights,
+                                        hipStream_t stream);
+
+/*
+ * Layer norm of rows of d values, in fp32 and rounded once:
+ *   m = mean(x) (0 if not centered), v = mean((x - m)^2), xh = (x - m) / sqrt(v + eps)
+ *   y = xh * weight + bias
+ * (centered == 0 is the division by the root mean square, as in RMSNorm).
+ *   x, y          device, rows x d, any row stride, bf16 or fp32
+ *   weight, bias  device, d, bf16 or fp32 (weight_dtype; for example segments of a
+ *                 packed tail); bias may be NULL
+ * Gradients, with g = dy * weight; nothing of the forward is needed but x:
+ *   dx      = (g - xh * mean(g * xh) - mean(g)) / sqrt(v + eps)   (the last mean if centered)
+ *   dweight = beta*dweight + sum over rows of dy * xh     device fp32, d
+ *   dbias   = beta*dbias + sum over rows of dy            device fp32, d, or NULL
+ * for example segments of the packed gradient of mfsdp_adamw_tail; beta == 0 does
+ * not read them.  Sums over rows are in a fixed order: equal inputs, sizes and
+ * alignment give equal bits.
+ * workspace  device, >= mfsdp_layer_norm_grad_workspace_size bytes, 256-byte
+ *            aligned, scratch; none is needed for rows == 0.
+ * rows == 0 returns MFSDP_OK; the gradients are then scaled by beta.
+ * Errors as above; eps finite and >= 0; d and strides up to 2^22, rows up to 2^30.
+ */
+mfsdp_status_t mfsdp_layer_norm(const void* x, int64_t ld_x, const void* weight, const void* bias,
+                                mfsdp_dtype_t weight_dtype, int64_t rows, int64_t d,
+                                mfsdp_dtype_t dtype, int centered, float eps, void* y,
+                                int64_t ld_y, hipStream_t stream);
+
+mfsdp_status_t mfsdp_layer_norm_grad_workspace_size(int64_t rows, int64_t d, mfsdp_dtype_t dtype,
+                                                    int with_bias, size_t* out_bytes);
+
+mfsdp_status_t mfsdp_layer_norm_grad(const void* dy, int64_t ld_dy, const void* x, int64_t ld_x,
+                                     const void* weight, mfsdp_dtype_t weight_dtype, int64_t rows,
+                                     int64_t d, mfsdp_dtype_t dtype, int centered, float eps,
+                                     float beta, void* dx, int64_t ld_dx, float* dweight,
+                                     float* dbias, void* workspace, size_t workspace_bytes,
+                                     hipStream_t stream);
+
+/*
+ * Products in 8-bit floats: e4m3 codes (OCP: 448 is the largest) with one power of
+ * two 2^e per block of MFSDP_SCALED_BLOCK, the smallest e >= -126 with
+ * max|v| <= 448 * 2^e, kept as the byte e + 127 (255: the block held an infinity or
+ * a NaN, and its codes are NaN).  code = v / 2^e to the nearest, ties to even.  A
+ * block is 128 columns of one row of activations, or 128 x 128 of a matrix.  Rows
+ * of codes are filled up with zero codes to whole blocks: "filled" below is the
+ * width rounded up to a multiple of 128.
+ *   activations   x rows x k (any stride)     codes rows x filled k
+ *                                             scales rows x ceil(k / 128)
+ *   matrices      n_experts x n x k,          codes n_experts x n x filled k
+ *                 contiguous                  scales n_experts x ceil(n/128) x ceil(k/128)
+ *     transposed                              tcodes n_experts x k x filled n
+ *                                             tscales n_experts x ceil(k/128) x ceil(n/128)
+ *                 one call makes either copy or both (the same codes: either may
+ *                 be NULL with its scales)
+ *   product       y[r] = x[r] W_e^T for the rows offsets[e] <= r < offsets[e+1], the
+ *                 values being code * 2^e; y rows x n, bf16.  The input gradient
+ *                 is the same product, of dy's codes (depth n) with the transposed
+ *                 ones (width k).  Sums: of eight neighbouring products 13 bits
+ *                 below the largest are kept (the 8-bit MFMAs' own), those are
+ *                 added in fp32, and the result is rounded once.
+ * offsets, rows of nobody and limits are those of the products grouped by expert.
+ * Codes are 16-byte aligned.  rows == 0 or n_experts == 0 returns MFSDP_OK, no
+ * work.  Errors as above; widths up to 2^22 - 128.
+ */
+#define MFSDP_SCALED_BLOCK 128
+
+mfsdp_status_t mfsdp_scaled_quantize(const void* x, int64_t ld_x, int64_t rows, int64_t k,
+                                     mfsdp_dtype_t dtype, uint8_t* codes, uint8_t* scales,
+                                     hipStream_t stream);
+
+mfsdp_status_t mfsdp_scaled_quantize_weight(const void* weight, int64_t n_experts, int64_t n,
+                                            int64_t k, mfsdp_dtype_t dtype, uint8_t* codes,
+                                            uint8_t* scales, uint8_t* tcodes, uint8_t* tscales,
+                                            hipStream_t stream);
+
+mfsdp_status_t mfsdp_scaled_linear(const uint8_t* codes, const uint8_t* scales,
+                                   const uint8_t* weight_codes, const uint8_t* weight_scales,
+                                   const int32_t* offsets, int64_t n_experts, int64_t rows,
+                                   int64_t n, int64_t k, void* y, int64_t ld_y,
+                                   hipStream_t stream);
+
 /* Static, human-readable name of a status code. */
 const char* mfsdp_status_string(mfsdp_status_t status);
 
@@ -535,7 +730,11 @@ typedef enum mfsdp_kernel_kind {
   MFSDP_KERNEL_CKPT = 12,     /* 8-bit checkpoints                   */
   MFSDP_KERNEL_EMBED = 13,    /* embedding lookup                    */
   MFSDP_KERNEL_EMBED_GRAD = 14, /* embedding gradient (all launches) */
-  MFSDP_KERNEL_KINDS = 15
+  MFSDP_KERNEL_ROUTE = 15,      /* routing, its gradient, plan, balance */
+  MFSDP_KERNEL_EXCHANGE = 16,   /* dispatch, combine and its gradient   */
+  MFSDP_KERNEL_LAYER_NORM = 17, /* layer norm and its gradients         */
+  MFSDP_KERNEL_SCALED = 18,     /* 8-bit floats and their products      */
+  MFSDP_KERNEL_KINDS = 19
 } mfsdp_kernel_kind_t;
 
 mfsdp_status_t mfsdp_timing_enable(int enable);

@@ -25,12 +25,19 @@ from ._lib import MfsdpError, NOALLOC_SCRATCH_BYTES, NS_EPS
 from .grads import (CKPT_BLOCK, ckpt_quantize, ckpt_restore, embedding, embedding_grad,
                     grouped_linear, grouped_linear_dgrad, grouped_linear_wgrad,
                     grouped_linear_wgrad_ckpt)
+from .norms import layer_norm, layer_norm_grad
+from .routing import (RoutePlan, route, route_balance, route_combine, route_combine_grad,
+                      route_dispatch, route_grad, route_plan)
+from .scaled import SCALED_BLOCK, scaled_linear, scaled_quantize, scaled_quantize_weight
 
 __all__ = ["muon_step", "muon_step_noalloc", "MuonStep", "adamw_tail", "muon_workspace_size",
            "default_scale", "plan_owners", "tail_layout", "tail_pack", "tail_unpack",
            "shampoo_stats", "grouped_linear", "grouped_linear_dgrad", "grouped_linear_wgrad",
            "grouped_linear_wgrad_ckpt", "ckpt_quantize", "ckpt_restore", "embedding",
-           "embedding_grad", "CKPT_BLOCK", "mfma_probe", "timing", "MfsdpError", "NS_EPS", "NOALLOC_SCRATCH_BYTES",
+           "embedding_grad", "CKPT_BLOCK", "route", "route_grad", "route_plan", "RoutePlan",
+           "route_balance", "route_dispatch", "route_combine", "route_combine_grad",
+           "layer_norm", "layer_norm_grad", "scaled_quantize", "scaled_quantize_weight",
+           "scaled_linear", "SCALED_BLOCK", "mfma_probe", "timing", "MfsdpError", "NS_EPS", "NOALLOC_SCRATCH_BYTES",
            "library_path"]
 
 library_path = _lib.LIB_PATH

@@ -20,7 +20,9 @@ NS_EPS = 1e-7
 NOALLOC_SCRATCH_BYTES = 256 << 20
 KERNEL_KINDS = {"momentum": 0, "norm": 1, "gram": 2, "poly": 3, "update": 4,
                 "apply": 5, "adamw": 6, "final": 7, "stats_prep": 8, "syrk": 9,
-                "small": 10, "grouped": 11, "ckpt": 12, "embed": 13, "embed_grad": 14}
+                "small": 10, "grouped": 11, "ckpt": 12, "embed": 13, "embed_grad": 14,
+                "route": 15, "exchange": 16, "layer_norm": 17, "scaled": 18}
+ROUTE_SCORES = {"softmax": 0, "sigmoid": 1}
 
 #: Every symbol include/mfsdp.h declares.
 EXPORTED = ("mfsdp_muon_workspace_size", "mfsdp_muon_step", "mfsdp_muon_step_noalloc",
@@ -31,6 +33,11 @@ EXPORTED = ("mfsdp_muon_workspace_size", "mfsdp_muon_step", "mfsdp_muon_step_noa
             "mfsdp_grouped_linear_wgrad_workspace_size", "mfsdp_grouped_linear_tile",
             "mfsdp_grouped_linear_wgrad_ckpt", "mfsdp_ckpt_quantize", "mfsdp_ckpt_restore",
             "mfsdp_embedding", "mfsdp_embedding_grad_workspace_size", "mfsdp_embedding_grad",
+            "mfsdp_route", "mfsdp_route_grad", "mfsdp_route_plan_workspace_size",
+            "mfsdp_route_plan", "mfsdp_route_balance", "mfsdp_route_dispatch",
+            "mfsdp_route_combine", "mfsdp_route_combine_grad",
+            "mfsdp_layer_norm", "mfsdp_layer_norm_grad_workspace_size", "mfsdp_layer_norm_grad",
+            "mfsdp_scaled_quantize", "mfsdp_scaled_quantize_weight", "mfsdp_scaled_linear",
             "mfsdp_status_string", "mfsdp_last_error",
             "mfsdp_timing_enable", "mfsdp_timing_reset", "mfsdp_timing_read",
             "mfsdp_mfma_probe")
@@ -161,6 +168,32 @@ def load() -> ctypes.CDLL:
         lib.mfsdp_embedding_grad.argtypes = [ptr, i64, c.c_int, ptr, c.c_int, i64, i64, i64, f32,
                                              f32, ptr, ptr, c.c_size_t, ptr]
         lib.mfsdp_embedding_grad.restype = c.c_int
+        size, i32 = c.c_size_t, c.c_int
+        for name, args in {
+                "mfsdp_route": [ptr, i64, ptr, ptr, i64, i64, i64, i32, i32, i64, i64, i32, f32,
+                                ptr, ptr, ptr],
+                "mfsdp_route_grad": [ptr, ptr, i64, ptr, i64, i64, i64, i32, i32, i32, f32, ptr,
+                                     i64, ptr],
+                "mfsdp_route_plan_workspace_size": [i64, i64, i64, c.POINTER(size)],
+                "mfsdp_route_plan": [ptr, i64, i64, i64, ptr, ptr, ptr, size, ptr],
+                "mfsdp_route_balance": [ptr, ptr, i32, i64, f32, ptr],
+                "mfsdp_route_dispatch": [ptr, i64, ptr, i64, i64, i64, i64, i32, ptr, i64, ptr],
+                "mfsdp_route_combine": [ptr, i64, ptr, ptr, i64, i64, i64, i64, i32, f32, ptr,
+                                        i64, ptr],
+                "mfsdp_route_combine_grad": [ptr, i64, ptr, i64, ptr, ptr, i64, i64, i64, i64,
+                                             i32, ptr, i64, ptr, ptr],
+                "mfsdp_layer_norm": [ptr, i64, ptr, ptr, i32, i64, i64, i32, i32, f32, ptr, i64,
+                                     ptr],
+                "mfsdp_layer_norm_grad_workspace_size": [i64, i64, i32, i32, c.POINTER(size)],
+                "mfsdp_layer_norm_grad": [ptr, i64, ptr, i64, ptr, i32, i64, i64, i32, i32, f32,
+                                          f32, ptr, i64, ptr, ptr, ptr, size, ptr],
+                "mfsdp_scaled_quantize": [ptr, i64, i64, i64, i32, ptr, ptr, ptr],
+                "mfsdp_scaled_quantize_weight": [ptr, i64, i64, i64, i32, ptr, ptr, ptr, ptr,
+                                                 ptr],
+                "mfsdp_scaled_linear": [ptr, ptr, ptr, ptr, ptr, i64, i64, i64, i64, ptr, i64,
+                                        ptr]}.items():
+            getattr(lib, name).argtypes = args
+            getattr(lib, name).restype = i32
         lib.mfsdp_status_string.argtypes = [c.c_int]
         lib.mfsdp_status_string.restype = c.c_char_p
         lib.mfsdp_last_error.argtypes = []

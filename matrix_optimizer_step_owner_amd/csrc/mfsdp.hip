@@ -28,11 +28,15 @@
 #include "common.hpp"
 #include "embedding_kernels.hpp"
 #include "ew_kernels.hpp"
+#include "exchange_kernels.hpp"
 #include "grouped_kernels.hpp"
+#include "layer_norm_kernels.hpp"
 #include "ns_gemm.hpp"
 #include "ns_small.hpp"
 #include "planner.hpp"
 #include "probe_kernels.hpp"
+#include "route_kernels.hpp"
+#include "scaled_kernels.hpp"
 #include "stats_kernels.hpp"
 #include "tail_kernels.hpp"
 
@@ -1384,3 +1388,4 @@ mfsdp_status_t mfsdp_timing_read(mfsdp_kernel_kind_t kind, double* total_ms, int
 }  // extern "C"
 
 #include "grads_host.hpp"
+#include "layers_host.hpp"
