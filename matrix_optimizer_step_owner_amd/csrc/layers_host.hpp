@@ -134,6 +134,8 @@ mfsdp_status_t route_impl(const void* logits, int64_t ld, const float* bias, con
   const dim3 grid(static_cast<unsigned>(ceil_div(tokens, 4))), wg(256);
   const hipError_t e = launch_per_expert(n, [&](auto per) {
     constexpr int PER = decltype(per)::value;
+    const int lanes = a.group_size % PER == 0 ? a.group_size / PER : 0;
+    a.lanes = lanes > 0 && (lanes & (lanes - 1)) == 0 ? lanes : 0;
     return launch(MFSDP_KERNEL_ROUTE, stream, [&] {
       if (dtype == MFSDP_DTYPE_BF16) route_kernel<ElemBF16, PER><<<grid, wg, 0, stream>>>(a);
       else route_kernel<ElemF32, PER><<<grid, wg, 0, stream>>>(a);
@@ -571,6 +573,45 @@ mfsdp_status_t scaled_weight_impl(const void* w, int64_t experts, int64_t n, int
   return launched(e, "8-bit float matrices");
 }
 
+// Tiles.  The rule below chooses among them; times in us, experts x rows x n x k:
+using ScaledLarge = ScaledTile<256, 256, 2, 4, 2, 2>;
+using ScaledPair = ScaledTile<128, 128, 2, 2, 2, 2>;         // two workgroups per CU
+using ScaledRows = ScaledTile<32, 64, 1, 2, 4, 3, 4, 4>;     // two workgroups per CU
+using ScaledFew = ScaledTile<32, 32, 1, 1, 4, 3, 4, 4>;
+
+template <class C>
+hipError_t launch_scaled(const ScaledArgs& a, hipStream_t stream) {
+  const dim3 grid(static_cast<unsigned>(group_tiles_max(a.g.rows, a.g.experts, C::BP) * ceil_div(a.g.n, C::BQ)));
+  return launch(MFSDP_KERNEL_SCALED, stream, [&] { scaled_tile_kernel<C><<<grid, dim3(C::THREADS), 0, stream>>>(a); });
+}
+
+enum ScaledKernel { kScaledLarge, kScaledPair, kScaledRows, kScaledFew };
+
+// Row tiles are estimated from the mean of the experts that have rows.
+ScaledKernel scaled_kernel(int64_t experts, int64_t rows, int64_t n, int64_t k) {
+  const int64_t used = std::min(experts, rows), per = rows / used;
+  auto tiles = [&](int64_t bp, int64_t bq) {
+    return static_cast<double>(std::max(used, rows / bp + used / 2) * ceil_div(n, bq));
+  };
+  // One row tile of 32 x 64 per expert reads each weight once.  Up to three tiles
+  // per CU: 1 x 64 x 14336 x 4096 21 against 34 us with 128 x 128, 8 x 128 x 4096 x
+  // 4096 30 and 39.  More of them where few rows wait for long rows of weights: 8
+  // x 128 x 14336 x 4096 90 and 113, 256 x 256 x 512 x 1536 30 and 36; but 32 x 256
+  // x 2048 x 2048 32 and 28.  32 x 32 where there are few: 1 x 16 x 4096 x 4096 10.3
+  // against 11.5.
+  const double narrow = per < 32 ? static_cast<double>(used * ceil_div(n, 64)) : tiles(32, 64);
+  if (narrow <= 768 || (per < 32 && (per <= 4 || k >= 4096))) return narrow <= 128 ? kScaledFew : kScaledRows;
+  // Rounds of the 256 CUs, in the time of one of 256 x 256: one of two 128 x 128
+  // per CU takes 0.72, and half of a further one overlaps (1 x 2048 x 4096 x 4096 47
+  // and 36, 1 x 1024 x 14336 x 4096 53 and 65, 32 x 6144 x 2048 x 2048 53 and 39).
+  // Few rows fill large tiles unevenly: 256 x 32771 x 512 x 1536 61 and 51 with
+  // segments that differ by half, 48 and 51 with nearly equal ones.
+  const double large = std::ceil(tiles(256, 256) / 256) * (per < 256 ? 1.3 : 1.0);
+  const double pairs = tiles(128, 128) / 512, small = 0.72 * (pairs <= 1 ? 1 : pairs + 0.45);
+  if (large > small) return kScaledPair;
+  return kScaledLarge;
+}
+
 mfsdp_status_t scaled_linear_impl(const uint8_t* codes, const uint8_t* scales, const uint8_t* wcodes,
                                   const uint8_t* wscales, const int32_t* offsets, int64_t experts, int64_t rows,
                                   int64_t n, int64_t k, void* y, int64_t ldy, hipStream_t stream) {
@@ -609,10 +650,16 @@ mfsdp_status_t scaled_linear_impl(const uint8_t* codes, const uint8_t* scales, c
   a.qs = wscales;
   a.kb = static_cast<int32_t>(kb);
   a.nb = static_cast<int32_t>(nb);
-  const int64_t blocks = group_tiles_max(rows, experts, 32) * nb;
-  if (blocks > kBlocksMax) return fail(MFSDP_ERR_UNSUPPORTED, "too many tiles");
-  const dim3 grid(static_cast<unsigned>(blocks)), wg(256);
-  const hipError_t e = launch(MFSDP_KERNEL_SCALED, stream, [&] { scaled_rows_kernel<<<grid, wg, 0, stream>>>(a); });
+  a.g.stream = aligned(y, 128) && ldy * 2 % 128 == 0;
+  hipError_t e = hipErrorInvalidValue;
+  int use = scaled_kernel(experts, rows, n, depth);
+  if (const char* v = getenv("MFSDP_T")) use = atoi(v);
+  switch (use) {
+    case kScaledLarge: e = launch_scaled<ScaledLarge>(a, stream); break;
+    case kScaledPair: e = launch_scaled<ScaledPair>(a, stream); break;
+    case kScaledRows: e = launch_scaled<ScaledRows>(a, stream); break;
+    case kScaledFew: e = launch_scaled<ScaledFew>(a, stream); break;
+  }
   return launched(e, "8-bit float product");
 }
 

@@ -4,8 +4,8 @@
 // One wave takes one token.  Lane l holds the PER consecutive experts from
 // l * PER on, so that the order of lanes is the order of experts and the first
 // lane of a ballot is the lowest index among equals.  A round of the choice is
-// the largest key in a wave (six DPP steps on order-preserving integers), one
-// ballot, and the winner's key set to 0.
+// the largest of the lanes' first keys (six DPP steps on order-preserving
+// integers), one ballot, and the winner's sorted list moved up.
 //
 // Which experts are chosen is decided as in exact arithmetic.  Without a bias
 // and groups the order of scores is that of the logits, and no score is needed.
@@ -34,6 +34,7 @@ struct RouteArgs {
   int64_t ld;
   int32_t tokens, n, k;
   int32_t groups, top, group_size;
+  int32_t lanes;          // lanes of a group, if that is a power of two, else 0
   int32_t sigmoid, renorm;
   float scale;
 };
@@ -106,9 +107,14 @@ __device__ __forceinline__ float route_score(float x, int sigmoid, float top, fl
   return sigmoid ? 1.f / (1.f + expf(-x)) : expf(x - top) / sum;
 }
 
-// Largest logit and sum of exp(x - largest) of a row (softmax).
+// exp(x) by the hardware's 2^x: relatively off by (|x| + 2) 2^-23, a fifth of the
+// instructions.  For keys and sums; the chosen scores are taken from expf.
+__device__ __forceinline__ float route_exp(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504f); }
+
+// Largest logit and sum of exp(x - largest) of a row (softmax); x becomes the
+// exponentials.
 template <int PER>
-__device__ __forceinline__ void route_softmax(const float (&x)[PER], int first, int n, float& top, float& sum) {
+__device__ __forceinline__ void route_softmax(float (&x)[PER], int first, int n, float& top, float& sum) {
   uint32_t m = 0;
 #pragma unroll
   for (int i = 0; i < PER; ++i)
@@ -116,94 +122,227 @@ __device__ __forceinline__ void route_softmax(const float (&x)[PER], int first, 
   top = route_value(wave_max(m));
   float s = 0.f;
 #pragma unroll
-  for (int i = 0; i < PER; ++i)
-    if (first + i < n) s += expf(x[i] - top);
+  for (int i = 0; i < PER; ++i) {
+    x[i] = first + i < n ? route_exp(x[i] - top) : 0.f;
+    s += x[i];
+  }
   sum = warp_sum(s);
 }
 
-// Groups: returns the bits of those that stay.  vk: keys of score + bias, 0
-// where there is no expert.  `close`: the border between the last group that
-// stays and the first that does not is nearer than the sums' rounding.
-template <int PER, class V, class K>
-__device__ __forceinline__ uint64_t route_groups(const RouteArgs& a, const K (&vk)[PER], const int (&gid)[PER],
-                                                 int lane, bool& close) {
-  V mine = V(0);
-  for (int g = 0; g < a.groups; ++g) {
-    K best = 0;
-#pragma unroll
-    for (int i = 0; i < PER; ++i)
-      if (gid[i] == g) best = max(best, vk[i]);
-    const K one = wave_max(best);
-    const int owner = __builtin_ctzll(__ballot(best == one));
-    // second: the owner leaves out its first one that is equal
-    K next = 0;
-    bool skip = lane == owner;
-#pragma unroll
-    for (int i = 0; i < PER; ++i)
-      if (gid[i] == g) {
-        if (skip && vk[i] == one) skip = false;
-        else next = max(next, vk[i]);
-      }
-    const K two = wave_max(next);
-    V sum = route_value(one);
-    if (a.group_size > 1) sum += route_value(two);
-    if (lane == g) mine = sum;
-  }
-  const K key = lane < a.groups ? route_key(mine) : K(0);
-  int rank = 0;
-  for (int g = 0; g < a.groups; ++g) {
-    K other;
-    if constexpr (sizeof(K) == 8)
-      other = static_cast<uint64_t>(static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(key >> 32), g))) << 32 |
-              static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(key), g));
-    else
-      other = static_cast<K>(__builtin_amdgcn_readlane(static_cast<int>(key), g));
-    rank += other > key || (other == key && g < lane) ? 1 : 0;
-  }
-  const bool stays = lane < a.groups && rank < a.top;
-  if constexpr (sizeof(K) == 4) {
-    if (a.top < a.groups) {
-      // each of a sum's two keys is off by at most 33 * 2^-23 (s (|x - top| + 32)
-      // is under 33) and half a step of itself
-      const float out = route_value(wave_max(stays || lane >= a.groups ? 0u : key));
-      const float in = route_value(~wave_max(stays ? ~key : 0u));
-      const float tol = 0x1p-23f * (132.f + 8.f * (fabsf(in) + fabsf(out)));
-      close = !(in - out > tol);
-    }
-  }
-  return __ballot(stays);
+// Distance within which fp32 keys do not decide, for keys of size `key`.  A
+// softmax's score is off by (|x - top| + 32) 2^-23 of itself (the sum's 22 additions
+// and its terms' own rounding among them) and s |x - top| is under 1/e; a sigmoid's by
+// less than 8 2^-23.  `most` bounds the scores.  Twice that for two of them, and
+// their additions' rounding.
+__device__ __forceinline__ float route_doubt(float most, float key) {
+  return 0x1p-22f * (34.f * most + 1.f + 2.f * fabsf(key));
 }
 
-// The k largest keys in order, lane j receiving expert j (others -1); their keys
-// are set to 0.
+// Two largest keys of a lane's own.
 template <int PER, class K>
-__device__ __forceinline__ int route_pick(K (&key)[PER], int first, int k, int lane) {
+__device__ __forceinline__ void route_two(const K (&k)[PER], K& one, K& two) {
+  one = k[0];
+  two = 0;
+#pragma unroll
+  for (int i = 1; i < PER; ++i) {
+    two = max(two, min(one, k[i]));
+    one = max(one, k[i]);
+  }
+}
+
+// The same lane's value, LANES / 2 further in its row of LANES, for LANES <= 16 as a
+// mirror: callers hold the same in both halves' lanes.
+template <int LANES>
+__device__ __forceinline__ uint32_t route_swap(uint32_t v) {
+  if constexpr (LANES == 2) return static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(v), 0xb1, 0xf, 0xf, true));
+  if constexpr (LANES == 4) return static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(v), 0x4e, 0xf, 0xf, true));
+  if constexpr (LANES == 8) return static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(v), 0x141, 0xf, 0xf, true));
+  if constexpr (LANES == 16) return static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(v), 0x140, 0xf, 0xf, true));
+  return static_cast<uint32_t>(__shfl_xor(static_cast<int>(v), LANES / 2, 64));
+}
+template <int LANES>
+__device__ __forceinline__ uint64_t route_swap(uint64_t v) {
+  return static_cast<uint64_t>(route_swap<LANES>(static_cast<uint32_t>(v >> 32))) << 32 | route_swap<LANES>(static_cast<uint32_t>(v));
+}
+
+// Groups: which of this lane's experts stay, as bits.  vk: keys of score + bias, 0
+// where there is no expert.  `close`: the border between the last group that
+// stays and the first that does not is nearer than `doubt` says of the sums.
+template <int PER, class V, class K>
+__device__ __forceinline__ uint32_t route_groups(const RouteArgs& a, const K (&vk)[PER], int lane, float most,
+                                                 bool& close) {
+  const int first = lane * PER;
+  int step;       // lanes between the first lanes of groups; group g's sum is with lane g * step
+  V mine = V(0);
+  if (a.lanes > 0) {
+    // a group is a.lanes lanes, a power of two: their two largest by exchanges
+    K one, two;
+    route_two<PER, K>(vk, one, two);
+    auto merge = [&](auto lanes_c) {
+      constexpr int L = decltype(lanes_c)::value;
+      if (a.lanes < L) return;
+      const K o1 = route_swap<L>(one), o2 = route_swap<L>(two);
+      two = max(max(two, o2), min(one, o1));
+      one = max(one, o1);
+    };
+    merge(std::integral_constant<int, 2>{});
+    merge(std::integral_constant<int, 4>{});
+    merge(std::integral_constant<int, 8>{});
+    merge(std::integral_constant<int, 16>{});
+    merge(std::integral_constant<int, 32>{});
+    merge(std::integral_constant<int, 64>{});
+    mine = route_value(one);
+    if (a.group_size > 1) mine += route_value(two);
+    step = a.lanes;
+  } else {
+    for (int g = 0; g < a.groups; ++g) {
+      const int lo = g * a.group_size, hi = lo + a.group_size;
+      K in[PER], one, two;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) in[i] = first + i >= lo && first + i < hi ? vk[i] : K(0);
+      route_two<PER, K>(in, one, two);
+      const K best = wave_max(one);
+      const int owner = __builtin_ctzll(__ballot(one == best));
+      const K next = wave_max(lane == owner ? two : one);
+      V sum = route_value(best);
+      if (a.group_size > 1) sum += route_value(next);
+      if (lane == g) mine = sum;
+    }
+    step = 1;
+  }
+  const K key = route_key(mine);
+  // how many groups are before a lane's own (and where it has none, before none)
+  const int own = lane / step;
+  int rank = 0;
+  for (int g = 0; g < a.groups; ++g) {
+    const int at = g * step;
+    K other;
+    if constexpr (sizeof(K) == 8)
+      other = static_cast<uint64_t>(static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(key >> 32), at))) << 32 |
+              static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(key), at));
+    else
+      other = static_cast<K>(__builtin_amdgcn_readlane(static_cast<int>(key), at));
+    rank += other > key || (other == key && g < own) ? 1 : 0;
+  }
+  const bool group = lane < a.groups * step, stays = group && rank < a.top;
+  if constexpr (sizeof(K) == 4) {
+    if (a.top < a.groups) {
+      const float out = route_value(wave_max(group && !stays ? key : 0u));
+      const float in = route_value(~wave_max(stays ? ~key : 0u));
+      close = !(in - out > 2.f * route_doubt(most, fabsf(in) + fabsf(out)));
+    }
+  }
+  const uint64_t bits = __ballot(stays);
+  uint32_t mask = 0;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int at = a.lanes > 0 ? lane : (first + i) / a.group_size;
+    mask |= static_cast<uint32_t>(bits >> (at & 63) & 1) << i;
+  }
+  return mask;
+}
+
+// The k largest keys in order, lane j receiving expert j (others -1).  Lists of up
+// to eight are sorted first (exchanges of neighbours, which keep equal keys in
+// order, with their places as the digits of one word): a round then needs
+// neither the largest of a lane's own nor a search for it, and the winner's list
+// moves up by one.  On return key[0] is the largest that a lane has left
+// (PER <= 8).
+template <int PER, class K>
+__device__ __forceinline__ int route_pick(K (&key)[PER], int k, int lane) {
   int mine = -1;
-  for (int j = 0; j < k; ++j) {
-    K best = key[0];
+  if constexpr (PER <= 8) {
+    uint32_t place[PER];
 #pragma unroll
-    for (int i = 1; i < PER; ++i) best = max(best, key[i]);
-    const K m = wave_max(best);
-    if (m == 0) break;
-    const int owner = __builtin_ctzll(__ballot(best == m));
-    int at = 0;
+    for (int i = 0; i < PER; ++i) place[i] = i;
 #pragma unroll
-    for (int i = PER - 1; i >= 0; --i)
-      if (key[i] == m) at = i;
+    for (int end = PER - 1; end > 0; --end)
 #pragma unroll
-    for (int i = 0; i < PER; ++i)
-      if (lane == owner && i == at) key[i] = 0;
-    const int e = __builtin_amdgcn_readlane(first + at, owner);
-    if (lane == j) mine = e;
+      for (int i = 0; i < end; ++i) {
+        const bool swap = key[i] < key[i + 1];
+        const K hi = swap ? key[i + 1] : key[i], lo = swap ? key[i] : key[i + 1];
+        const uint32_t ph = swap ? place[i + 1] : place[i], pl = swap ? place[i] : place[i + 1];
+        key[i] = hi;
+        key[i + 1] = lo;
+        place[i] = ph;
+        place[i + 1] = pl;
+      }
+    uint32_t digits = 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) digits |= place[i] << (4 * i);
+    for (int j = 0; j < k; ++j) {
+      const K m = wave_max(key[0]);
+      const int owner = __builtin_ctzll(__ballot(key[0] == m));
+      const int e = owner * PER + (__builtin_amdgcn_readlane(static_cast<int>(digits), owner) & 15);
+      const bool won = lane == owner;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) key[i] = won ? (i + 1 < PER ? key[(i + 1) % PER] : K(0)) : key[i];
+      digits = won ? digits >> 4 : digits;
+      if (lane == j) mine = e;
+    }
+  } else {
+    for (int j = 0; j < k; ++j) {
+      K best = key[0];
+#pragma unroll
+      for (int i = 1; i < PER; ++i) best = max(best, key[i]);
+      const K m = wave_max(best);
+      const int owner = __builtin_ctzll(__ballot(best == m));
+      int at = 0;
+#pragma unroll
+      for (int i = PER - 1; i >= 0; --i)
+        if (key[i] == m) at = i;
+#pragma unroll
+      for (int i = 0; i < PER; ++i)
+        if (lane == owner && i == at) key[i] = 0;
+      const int e = __builtin_amdgcn_readlane(lane * PER + at, owner);
+      if (lane == j) mine = e;
+    }
+#pragma unroll
+    for (int i = 1; i < PER; ++i) key[0] = max(key[0], key[i]);
   }
   return mine;
+}
+
+// The choice in fp64, where fp32 leaves it open.
+template <class E, int PER>
+__device__ __forceinline__ int route_exact(const RouteArgs& a, const typename E::storage_t* row, float top, int lane) {
+  const int first = lane * PER;
+  float x[PER], b[PER];
+  route_load<E, PER>(row, first, a.n, 0.f, x);
+#pragma unroll
+  for (int i = 0; i < PER; ++i) b[i] = 0.f;
+  if (a.bias) route_load<ElemF32, PER>(a.bias, first, a.n, 0.f, b);
+  const double dtop = top;
+  double sum = 1.0;
+  if (!a.sigmoid) {
+    double s = 0.0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+      if (first + i < a.n) s += exp(static_cast<double>(x[i]) - dtop);
+    sum = warp_sum(s);
+  }
+  uint64_t key[PER];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const double s = a.sigmoid ? 1.0 / (1.0 + exp(-static_cast<double>(x[i]))) : exp(static_cast<double>(x[i]) - dtop) / sum;
+    key[i] = first + i < a.n ? route_key(s + static_cast<double>(b[i])) : 0ull;
+  }
+  uint32_t stay = 0xffffffffu;
+  bool none = false;
+  if (a.groups > 1) stay = route_groups<PER, double, uint64_t>(a, key, lane, 0.f, none);
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    if (!(stay >> i & 1)) key[i] = 0;
+    else if (!a.bias && key[i]) key[i] = route_key(x[i]);
+  }
+  return route_pick<PER, uint64_t>(key, a.k, lane);
 }
 
 template <class E, int PER>
 __global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
   using S = typename E::storage_t;
   const int lane = threadIdx.x & 63;
-  const int64_t t = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   if (t >= a.tokens) return;
   int32_t* chosen = a.chosen + t * a.k;
   float* weights = a.weights + t * a.k;
@@ -218,97 +357,61 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
   const int first = lane * PER;
   float x[PER];
   route_load<E, PER>(row, first, a.n, 0.f, x);
-  float top = 0.f, sum = 1.f;
-  if (!a.sigmoid) route_softmax<PER>(x, first, a.n, top, sum);
-
   uint32_t key[PER];
-  int mine;
-  if (!a.bias && a.groups == 1) {
 #pragma unroll
-    for (int i = 0; i < PER; ++i) key[i] = first + i < a.n ? route_key(x[i]) : 0u;
-    mine = route_pick<PER>(key, first, a.k, lane);
+  for (int i = 0; i < PER; ++i) key[i] = first + i < a.n ? route_key(x[i]) : 0u;
+  float top = 0.f, sum = 1.f;
+  if (!a.sigmoid) route_softmax<PER>(x, first, a.n, top, sum);     // x: exponentials
+
+  bool close = false;
+  int mine;
+  float mx, mb = 0.f;
+  const bool on = lane < a.k;
+  if (!a.bias && a.groups == 1) {
+    mine = route_pick<PER, uint32_t>(key, a.k, lane);
+    mx = on ? E::to_f32(gld<S>(row + mine)) : 0.f;
   } else {
-    float b[PER];
-    int gid[PER];
+    const float most = a.sigmoid ? 1.f : 1.f / sum;
+    float v[PER];
+#pragma unroll
+    for (int i = 0; i < PER; ++i) v[i] = 0.f;
+    if (a.bias) route_load<ElemF32, PER>(a.bias, first, a.n, 0.f, v);
+    uint32_t vk[PER];
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-      b[i] = 0.f;
-      gid[i] = (first + i) / a.group_size;
+      v[i] += a.sigmoid ? __builtin_amdgcn_rcpf(1.f + route_exp(-x[i])) : x[i] * most;
+      vk[i] = first + i < a.n ? route_key(v[i]) : 0u;
     }
-    if (a.bias) route_load<ElemF32, PER>(a.bias, first, a.n, 0.f, b);
-#pragma unroll
-    for (int i = 0; i < PER; ++i)
-      key[i] = first + i < a.n ? route_key(route_score(x[i], a.sigmoid, top, sum) + b[i]) : 0u;
-    bool close = false;
-    uint64_t stay = 1;
     if (a.groups > 1) {
-      stay = route_groups<PER, float>(a, key, gid, lane, close);
+      const uint32_t stay = route_groups<PER, float, uint32_t>(a, vk, lane, most, close);
 #pragma unroll
       for (int i = 0; i < PER; ++i)
-        if (!(stay >> gid[i] & 1) || first + i >= a.n) key[i] = 0;
+        if (!(stay >> i & 1)) key[i] = vk[i] = 0;
     }
     if (!a.bias) {   // within the groups the logits decide
-#pragma unroll
-      for (int i = 0; i < PER; ++i)
-        if (key[i]) key[i] = route_key(x[i]);
-      mine = route_pick<PER>(key, first, a.k, lane);
+      mine = route_pick<PER, uint32_t>(key, a.k, lane);
+      mx = on ? E::to_f32(gld<S>(row + mine)) : 0.f;
     } else {
-      mine = route_pick<PER>(key, first, a.k, lane);
-      // neighbours in the order: their keys' rounding against their distance
-      const float mx = mine >= 0 ? E::to_f32(gld<S>(row + mine)) : 0.f;
-      const float mb = mine >= 0 ? gld<float>(a.bias + mine) : 0.f;
-      const float ms = route_score(mx, a.sigmoid, top, sum), mk = ms + mb;
-      auto rounding = [&](float score, float xi, float k) {
-        return 0x1p-23f * (score * (32.f + (a.sigmoid ? 0.f : fabsf(xi - top))) + 2.f * fabsf(k));
-      };
-      const float off = rounding(ms, mx, mk);
+      mine = route_pick<PER, uint32_t>(vk, a.k, lane);
+      // neighbours in the order, unless they are equal, and the last against
+      // what is left
+      mx = on ? E::to_f32(gld<S>(row + mine)) : 0.f;
+      mb = on ? gld<float>(a.bias + mine) : 0.f;
+      const float mk = (a.sigmoid ? __builtin_amdgcn_rcpf(1.f + route_exp(-mx)) : route_exp(mx - top) * most) + mb;
+      const float doubt = route_doubt(most, mk);
       const float ox = __shfl_down(mx, 1, 64), ob = __shfl_down(mb, 1, 64), ok = __shfl_down(mk, 1, 64);
-      const float tol = off + __shfl_down(off, 1, 64);
-      bool open = lane + 1 < a.k && !(mk - ok > tol) && !(ox == mx && ob == mb);
-      // the last against all that were not chosen: the next of them alone would
-      // not do, as one that is equal to the last hides others behind it
-      auto last = [&](float v) { return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), a.k - 1)); };
-      const float lx = last(mx), lb = last(mb), lk = last(mk), lo = last(off);
-#pragma unroll
-      for (int i = 0; i < PER; ++i) {
-        if (key[i] == 0) continue;
-        const float ki = route_value(key[i]);
-        open = open || (!(lk - ki > lo + rounding(fabsf(ki - b[i]), x[i], ki)) && !(x[i] == lx && b[i] == lb));
-      }
+      bool open = lane + 1 < a.k && !(mk - ok > doubt) && !(ox == mx && ob == mb);
+      auto last = [&](float q) { return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(q), a.k - 1)); };
+      open = open || (vk[0] != 0 && !(last(mk) - route_value(vk[0]) > last(doubt)));
       close = close || __ballot(open) != 0;
     }
-    if (__builtin_expect(__ballot(close) != 0, 0)) {
-      double d[PER], dtop = 0.0, dsum = 1.0;
-      if (!a.sigmoid) {
-        dtop = top;
-        double s = 0.0;
-#pragma unroll
-        for (int i = 0; i < PER; ++i)
-          if (first + i < a.n) s += exp(static_cast<double>(x[i]) - dtop);
-        dsum = warp_sum(s);
-      }
-      uint64_t dk[PER];
-#pragma unroll
-      for (int i = 0; i < PER; ++i) {
-        const double v = a.sigmoid ? 1.0 / (1.0 + exp(-static_cast<double>(x[i]))) : exp(static_cast<double>(x[i]) - dtop) / dsum;
-        d[i] = v + static_cast<double>(b[i]);
-        dk[i] = first + i < a.n ? route_key(d[i]) : 0ull;
-      }
-      if (a.groups > 1) {
-        bool none = false;
-        stay = route_groups<PER, double>(a, dk, gid, lane, none);
-      }
-#pragma unroll
-      for (int i = 0; i < PER; ++i) {
-        if (!(stay >> gid[i] & 1) || first + i >= a.n) dk[i] = 0;
-        else if (!a.bias) dk[i] = route_key(x[i]);
-      }
-      mine = route_pick<PER>(dk, first, a.k, lane);
-    }
+  }
+  if (__builtin_expect(close, 0)) {
+    mine = route_exact<E, PER>(a, row, top, lane);
+    mx = on ? E::to_f32(gld<S>(row + mine)) : 0.f;
   }
 
-  const bool on = lane < a.k;
-  const float s = on ? route_score(E::to_f32(gld<S>(row + max(mine, 0))), a.sigmoid, top, sum) : 0.f;
+  const float s = on ? route_score(mx, a.sigmoid, top, sum) : 0.f;
   const float total = a.renorm ? warp_sum(s) + kRouteTiny : 1.f;
   if (on) {
     chosen[lane] = mine;
@@ -379,8 +482,9 @@ __global__ __launch_bounds__(256) void route_grad_kernel(RouteGradArgs a) {
         if (ej == first + i) dx[i] += dj;
     }
     if (!a.sigmoid) {
+      const float inv = 1.f / sum;
 #pragma unroll
-      for (int i = 0; i < PER; ++i) dx[i] = expf(x[i] - top) / sum * (dx[i] - c);
+      for (int i = 0; i < PER; ++i) dx[i] = x[i] * inv * (dx[i] - c);     // x: exponentials
     }
   }
   if (first + PER <= a.n && PER % E::kVec == 0) {
@@ -526,15 +630,27 @@ __global__ __launch_bounds__(kPlanThreads) void plan_place_kernel(PlanArgs a) {
       if (e != 0xffffffffu) atomicAdd(&tot[e], 1u);
     }
   } else {
-    for (int b = threadIdx.x; b < a.experts; b += kPlanThreads) {
+    // every workgroup adds up all counts: as many threads per expert as there
+    // are, eight loads of each in flight
+    for (int b = threadIdx.x; b < a.experts; b += kPlanThreads) tot[b] = add[b] = 0;
+    __syncthreads();
+    const int wide = (a.experts + 63) & ~63, slices = kPlanThreads / wide;
+    const int b = threadIdx.x % wide, blocks = static_cast<int>(gridDim.x), here = static_cast<int>(blockIdx.x);
+    if (b < a.experts && static_cast<int>(threadIdx.x) < slices * wide) {
       uint32_t t = 0, before = 0;
-      for (unsigned w = 0; w < gridDim.x; ++w) {
-        const uint32_t c = a.hist[static_cast<size_t>(w) * a.experts + b];
-        if (w < blockIdx.x) before += c;
-        t += c;
+      for (int w = threadIdx.x / wide; w < blocks; w += 8 * slices) {
+        uint32_t c[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) c[i] = a.hist[static_cast<size_t>(min(w + i * slices, blocks - 1)) * a.experts + b];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int at = w + i * slices;
+          t += at < blocks ? c[i] : 0;
+          before += at < here ? c[i] : 0;
+        }
       }
-      tot[b] = t;
-      add[b] = before;
+      atomicAdd(&tot[b], t);
+      atomicAdd(&add[b], before);
     }
   }
   __syncthreads();

@@ -229,40 +229,314 @@ __device__ __forceinline__ i32x8_t scaled_frag(const uint4& a, const uint4& b) {
                  static_cast<int>(b.x), static_cast<int>(b.y), static_cast<int>(b.z), static_cast<int>(b.w)};
 }
 
-// 32 rows x 128 columns per workgroup, 32 x 32 per wave, operands straight from
-// memory.
-__global__ __launch_bounds__(256) void scaled_rows_kernel(ScaledArgs a) {
+// Tile BP x BQ of the output by WP x WQ waves, each TP x TQ MFMA blocks of 32 x 32.
+// A step is 64 * U codes of the depth (U even: whole scale blocks), U sub-steps
+// of one MFMA, kept in STAGES LDS buffers with the rows' exponent bytes behind
+// them as words.  KS > 1: KS sets of waves share a step's sub-steps, and their
+// sums are added at the end.
+template <int BP_, int BQ_, int WP_, int WQ_, int U_, int STAGES_, int KS_ = 1, int OCC_ = 2>
+struct ScaledTile {
+  static constexpr int BP = BP_, BQ = BQ_, WP = WP_, WQ = WQ_, U = U_, STAGES = STAGES_, KS = KS_, OCC = OCC_;
+  static constexpr int WAVES = WP * WQ * KS, THREADS = 64 * WAVES;
+  static constexpr int TP = BP / WP / 32, TQ = BQ / WQ / 32;
+  static constexpr int SLOTS = TP * TQ, SUBS = U;
+  static constexpr int ROW = 64 * U;                  // bytes of a panel row
+  static constexpr int PP = BP * U / 16 / WAVES;      // 1 KB pieces per wave and step, P panel
+  static constexpr int QP = BQ * U / 16 / WAVES;      // ... Q panel
+  // rows of both panels' exponent bytes, whole pieces of 64 of each
+  static constexpr int PLINES = BP < 64 ? 64 : BP, LINES = PLINES + (BQ < 64 ? 64 : BQ);
+  static constexpr int NS = LINES / 64 * (U / 2);     // pieces of 64 exponent bytes per step
+  static constexpr int SP = (NS + WAVES - 1) / WAVES; // ... per wave (some of them twice)
+  static constexpr int PIECES = PP + QP + SP;
+  static constexpr int PANELS = (BP + BQ) * ROW;
+  static constexpr int STAGE_BYTES = PANELS + LINES * (U / 2) * 4;
+  static_assert(U % 2 == 0 && LINES % 64 == 0 && PLINES % 64 == 0, "whole scale blocks");
+  static_assert(PP * 16 * WAVES == BP * U && QP * 16 * WAVES == BQ * U, "whole pieces");
+  static_assert(TP * 32 * WP == BP && TQ * 32 * WQ == BQ && SUBS % KS == 0, "whole blocks");
+  static_assert(TQ <= 4, "a wave's columns lie in one scale block");
+};
+
+// One wave-wide global -> LDS copy of 64 bytes, each as one word: lane l's byte at
+// base + voff lands, zero-extended, at lds + 4 * l.
+__device__ __forceinline__ void lds_dma1_buf(uint32_t lds, uint32_t voff, u32x4s_t buf) {
+  const uint32_t ulds = static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(lds));
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_ubyte %1, %2, 0 offen lds"
+               :: "s"(ulds), "v"(voff), "s"(buf) : "memory", "m0");
+}
+
+template <class C>
+__global__ __launch_bounds__(C::THREADS, C::OCC) void scaled_tile_kernel(ScaledArgs a) {
+  constexpr int TP = C::TP, TQ = C::TQ, ROW = C::ROW, U = C::U;
+  constexpr int kStage = C::STAGE_BYTES, kStagesEnd = C::STAGES * kStage;
+  constexpr int kLds = kStagesEnd;
+  __shared__ __align__(16) char lds[kLds];
   const GroupArgs& g = a.g;
-  int e, ti, tj;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  constexpr int kTileWaves = C::WP * C::WQ;
+  const int tw = wave % kTileWaves, ks = wave / kTileWaves;
+  const int wp = tw / C::WQ, wq = tw % C::WQ;
+  const int lrow = lane & 31, lhalf = lane >> 5;
+
+  int e, ti, tj, lo, hi;
   bool alone;
-  if (!group_find(g, blockIdx.x, 32, (g.n + 127) / 128, e, ti, tj, alone)) return;
-  int lo, hi;
+  if (!group_find(g, blockIdx.x, C::BP, (g.n + C::BQ - 1) / C::BQ, e, ti, tj, alone)) return;
   group_segment(g, e, lo, hi);
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, lrow = lane & 31, lhalf = lane >> 5;
-  const int p0 = ti * 32, q0 = tj * 128 + wave * 32;
-  if (q0 >= g.n) return;
-  const int prow = lo + min(p0 + lrow, hi - lo - 1), qrow = min(q0 + lrow, g.n - 1);   // rows that exist
-  const uint8_t* P = static_cast<const uint8_t*>(g.p) + static_cast<int64_t>(prow) * g.k + lhalf * 32;
-  const uint8_t* Q = static_cast<const uint8_t*>(g.q) + (static_cast<int64_t>(e) * g.n + qrow) * g.k + lhalf * 32;
-  const uint8_t* ps = a.ps + static_cast<int64_t>(prow) * a.kb;
-  const uint8_t* qs = a.qs + (static_cast<int64_t>(e) * a.nb + tj) * a.kb;
-  f32x16_t acc = {};
-  for (int b = 0; b < a.kb; ++b) {
-    const int sp = gld<uint8_t>(ps + b), sq = gld<uint8_t>(qs + b);
+  const int p0 = ti * C::BP, q0 = tj * C::BQ;
+  const int prem = hi - lo - p0, qrem = g.n - q0;
+  const char* pbase = static_cast<const char*>(g.p) + (static_cast<int64_t>(lo) + p0) * g.k;
+  const char* qbase = static_cast<const char*>(g.q) + (static_cast<int64_t>(e) * g.n + q0) * g.k;
+  const char* psbase = reinterpret_cast<const char*>(a.ps) + (static_cast<int64_t>(lo) + p0) * a.kb;
+  const char* qsbase = reinterpret_cast<const char*>(a.qs) + (static_cast<int64_t>(e) * a.nb + q0 / kScaledBlock) * a.kb;
+
+  // ---- DMA: this wave's pieces of a step --------------------------------------
+  // Panels: 16 / U rows x 64 U bytes per piece, chunk c of row r at r * 64 U +
+  // (c ^ rswz(r)) * 16.  voff: the lane's byte offset from the step's base, kDmaNone
+  // for rows outside the tile; klim: the first depth that the chunk holds, past
+  // the end of it zeros are loaded.  Exponent bytes: klim is their block.
+  uint32_t voff[C::PIECES];
+  int klim[C::PIECES];
+  uint32_t sdst[C::SP];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const i32x8_t fp = scaled_frag(gld<uint4>(P + b * 128 + h * 64), gld<uint4>(P + b * 128 + h * 64 + 16));
-      const i32x8_t fq = scaled_frag(gld<uint4>(Q + b * 128 + h * 64), gld<uint4>(Q + b * 128 + h * 64 + 16));
-      acc = scaled_mfma(fq, fp, acc, sq, sp);
+  for (int q = 0; q < C::PP + C::QP; ++q) {
+    const bool is_p = q < C::PP;
+    const int piece = is_p ? wave * C::PP + q : wave * C::QP + q - C::PP;
+    const int row = piece * (16 / U) + lane / (4 * U), c = (lane & (4 * U - 1)) ^ rswz<U>(row);
+    voff[q] = row < (is_p ? prem : qrem) ? static_cast<uint32_t>(row * g.k + c * 16) : kDmaNone;
+    klim[q] = c * 16;
+  }
+  bool sp_piece[C::SP];
+#pragma unroll
+  for (int i = 0; i < C::SP; ++i) {
+    const int piece = (wave * C::SP + i) % C::NS;
+    const int b = piece / (C::LINES / 64), line = piece % (C::LINES / 64) * 64 + lane;   // block of the step, row
+    const bool is_p = line < C::PLINES;
+    const int row = is_p ? line : line - C::PLINES;
+    sp_piece[i] = is_p;
+    voff[C::PP + C::QP + i] = row < (is_p ? min(prem, C::BP) : min(qrem, C::BQ)) ? static_cast<uint32_t>((is_p ? row : row / kScaledBlock) * a.kb + b) : kDmaNone;
+    klim[C::PP + C::QP + i] = b * kScaledBlock;
+    sdst[i] = static_cast<uint32_t>(C::PANELS + (piece * 64) * 4);
+  }
+  const uint32_t lds0 = lds_addr(lds);
+  int left = g.k;      // depth from the next step to fetch on
+  auto dma_piece = [&](uint32_t stage, int q) {
+    const uint32_t off = (U == 2 ? 0 : klim[q]) < left ? voff[q] : kDmaNone;    // U = 2: a step is one block
+    if (q < C::PP + C::QP) {
+      const bool is_p = q < C::PP;
+      const uint32_t at = lds0 + stage + (is_p ? (wave * C::PP + q) * 1024 : C::BP * ROW + (wave * C::QP + q - C::PP) * 1024);
+      lds_dma16_buf(at, off, dma_buffer(is_p ? pbase : qbase));
+    } else {
+      const int i = q - C::PP - C::QP;
+      lds_dma1_buf(lds0 + stage + sdst[i], off, dma_buffer(__builtin_amdgcn_readfirstlane(sp_piece[i]) ? psbase : qsbase));
+    }
+  };
+  auto dma_next = [&] {
+    pbase += ROW;
+    qbase += ROW;
+    psbase += U / 2;
+    qsbase += U / 2;
+    left -= ROW;
+  };
+
+  // ---- fragments ----------------------------------------------------------------
+  // Lane l holds, for sub-step s, the 32 codes from 64 s + 32 (l / 32) on of row l % 32
+  // of each 32-row block (which codes of the depth an MFMA's lane holds does not
+  // matter, as long as both operands agree).
+  // P's fragments are in one set of registers, each read again as soon as its last
+  // product of a sub-step is issued; Q's, which all of them need, in two.
+  i32x8_t fp[TP], fq[2][TQ];
+  int sp[TP], sq[2];
+  // byte of half h of sub-step s in a 32-row block; blocks are whole swizzle periods
+  // apart, so their distance is an immediate
+  uint32_t foff[U][2];
+#pragma unroll
+  for (int s = 0; s < U; ++s)
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      foff[s][h] = static_cast<uint32_t>(lrow * ROW + (((4 * s + 2 * lhalf + h) ^ rswz<U>(lrow)) << 4));
+  auto read_half = [&](uint32_t panel, int block, int s, int half, i32x8_t& f) {
+    const uint4 v = *reinterpret_cast<const uint4*>(lds + (panel + foff[s][half]) + block * 32 * ROW);
+    f[4 * half] = static_cast<int>(v.x);
+    f[4 * half + 1] = static_cast<int>(v.y);
+    f[4 * half + 2] = static_cast<int>(v.z);
+    f[4 * half + 3] = static_cast<int>(v.w);
+  };
+  auto read_scale = [&](uint32_t stage, int s, int line) {
+    return *reinterpret_cast<const int*>(lds + stage + C::PANELS + ((s / 2) * C::LINES + line) * 4);
+  };
+  auto read_p = [&](uint32_t stage, int s, int i) {
+    read_half(stage + wp * (TP * 32 * ROW), i, s, 0, fp[i]);
+    read_half(stage + wp * (TP * 32 * ROW), i, s, 1, fp[i]);
+    sp[i] = read_scale(stage, s, (wp * TP + i) * 32 + lrow);
+  };
+  auto read_q = [&](uint32_t stage, int s, int r, int buf) {     // 2 TQ halves
+    read_half(stage + C::BP * ROW + wq * (TQ * 32 * ROW), r / 2, s, r & 1, fq[buf][r / 2]);
+    if (r == 0) sq[buf] = read_scale(stage, s, C::PLINES + wq * TQ * 32);
+  };
+  f32x16_t acc[TP][TQ];
+#pragma unroll
+  for (int i = 0; i < TP; ++i)
+#pragma unroll
+    for (int j = 0; j < TQ; ++j) acc[i][j] = f32x16_t{};
+  auto multiply = [&](int x, int buf) {
+    const int i = x / TQ, j = x % TQ;
+    acc[i][j] = scaled_mfma(fq[buf][j], fp[i], acc[i][j], sq[buf], sp[i]);
+  };
+
+  const int nk = (g.k + ROW - 1) / ROW;
+#pragma unroll
+  for (int s = 0; s < C::STAGES - 1; ++s) {
+#pragma unroll
+    for (int q = 0; q < C::PIECES; ++q) dma_piece(s * kStage, q);
+    dma_next();
+  }
+  uint32_t cur = 0, fill = kStagesEnd - kStage;
+  if constexpr (C::KS > 1) {
+    constexpr int kSubs = C::SUBS / C::KS;
+#pragma unroll 1
+    for (int t = 0; t < nk; ++t) {
+      asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" :: "n"((C::STAGES - 2) * C::PIECES) : "memory");
+#pragma unroll
+      for (int q = 0; q < C::PIECES; ++q) dma_piece(fill, q);
+      dma_next();
+#pragma unroll
+      for (int i = 0; i < kSubs; ++i) {
+#pragma unroll
+        for (int r = 0; r < TP; ++r) read_p(cur, ks * kSubs + i, r);
+#pragma unroll
+        for (int r = 0; r < 2 * TQ; ++r) read_q(cur, ks * kSubs + i, r, i & 1);
+#pragma unroll
+        for (int x = 0; x < C::SLOTS; ++x) multiply(x, i & 1);
+      }
+      fill = cur;
+      cur = cur + kStage == kStagesEnd ? 0 : cur + kStage;
+    }
+  } else {
+    // Step t computes on stage t % STAGES.  Behind the first row of blocks of its
+    // last sub-step, all of whose fragments have then been read, the waves wait
+    // until step t + 1 has landed (only later steps' pieces may be in flight) and
+    // their own reads are done, and meet a barrier: behind it they read step t +
+    // 1's first fragments, and the stage of step t is refilled.  Steps past the
+    // end load zeros and are never multiplied.
+    constexpr int kLast = C::SUBS - 1, kMeet = TQ - 1;
+    constexpr int kAfter = C::SLOTS - kMeet;      // slots from the barrier on
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" :: "n"((C::STAGES - 2) * C::PIECES) : "memory");
+#pragma unroll
+    for (int q = 0; q < C::PIECES; ++q) dma_piece(fill, q);
+    dma_next();
+    // A wave whose rows or columns the tile does not have only moves data.
+    const bool idle = wp * TP * 32 >= prem || wq * TQ * 32 >= qrem;
+    if (idle) {
+#pragma unroll 1
+      for (int t = 0; t < nk; ++t) {
+        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" :: "n"((C::STAGES - 2) * C::PIECES) : "memory");
+#pragma unroll
+        for (int q = 0; q < C::PIECES; ++q) dma_piece(cur, q);
+        dma_next();
+        cur = cur + kStage == kStagesEnd ? 0 : cur + kStage;
+      }
+    }
+    const int steps = idle ? 0 : nk;
+#pragma unroll
+    for (int r = 0; r < TP; ++r) read_p(0, 0, r);
+#pragma unroll
+    for (int r = 0; r < 2 * TQ; ++r) read_q(0, 0, r, 0);
+#pragma unroll 1
+    for (int t = 0; t < steps; ++t) {
+      const uint32_t nxt = cur + kStage == kStagesEnd ? 0 : cur + kStage;
+#pragma unroll
+      for (int sub = 0; sub < C::SUBS; ++sub) {
+#pragma unroll
+        for (int x = 0; x < C::SLOTS; ++x) {
+          multiply(x, sub & 1);
+          if (sub == kLast && x == kMeet)
+            asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" :: "n"((C::STAGES - 2) * C::PIECES) : "memory");
+          const uint32_t from = sub < kLast ? cur : nxt;
+          const int s = sub < kLast ? sub + 1 : 0;
+          if (x % TQ == TQ - 1) read_p(from, s, x / TQ);
+          // Q's next fragments, two halves a slot from the barrier's on
+          if (x >= kMeet) {
+#pragma unroll
+            for (int r = 0; r < 2 * TQ; ++r)
+              if (r / 2 % kAfter == x - kMeet) read_q(from, s, r, (sub + 1) & 1);
+          }
+          if (sub == kLast && x >= kMeet) {
+#pragma unroll
+            for (int q = x - kMeet; q < C::PIECES; q += kAfter) dma_piece(cur, q);
+          }
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      }
+      dma_next();
+      cur = nxt;
     }
   }
-  if (p0 + lrow >= hi - lo) return;
-  uint16_t* out = static_cast<uint16_t*>(g.out) + static_cast<int64_t>(lo + p0 + lrow) * g.ldo + q0;
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+
+  if constexpr (C::KS > 1) {   // the other sets' sums, in their order
+    constexpr int kBlock = 64 * 16;
+    float* sums = reinterpret_cast<float*>(lds);
+    static_assert((C::KS - 1) * kTileWaves * C::SLOTS * kBlock * 4 <= kLds / 2, "sums fit, staging behind them");
+    auto at = [&](int set, int x, int r) { return ((set * kTileWaves + tw) * C::SLOTS + x) * kBlock + r * 64 + lane; };
+    if (ks > 0) {
 #pragma unroll
-  for (int r = 0; r < 16; ++r) {
-    const int q = acc_q(r, lhalf);
-    if (q0 + q < g.n) gst<uint16_t>(out + q, f32_to_bf16_rne(acc[r]));
+      for (int x = 0; x < C::SLOTS; ++x)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) sums[at(ks - 1, x, r)] = acc[x / TQ][x % TQ][r];
+    }
+    __syncthreads();
+    if (ks > 0) return;
+#pragma unroll
+    for (int s = 0; s < C::KS - 1; ++s)
+#pragma unroll
+      for (int x = 0; x < C::SLOTS; ++x)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) acc[x / TQ][x % TQ][r] += sums[at(s, x, r)];
   }
+
+  // ---- epilogue: 32 rows of each row of waves at a time through LDS, so that a
+  // store covers a row over the tile's whole width ---------------------------------
+  constexpr int COLS = TQ * 32;
+  uint16_t* out = static_cast<uint16_t*>(g.out) + (static_cast<int64_t>(lo) + p0) * g.ldo + q0;
+  constexpr int GROUPS = C::BQ / 8, RPP = 64 / GROUPS, PITCH = C::BQ * 2 + 16;
+  constexpr int BLOCK = C::WP * 32 * PITCH, kSpace = C::KS > 1 ? kLds / 2 : kLds;
+  constexpr int BUFS = TP > 1 && 2 * BLOCK <= kSpace ? 2 : 1;
+  static_assert(BLOCK <= kSpace && RPP >= 1 && 32 / C::WQ % RPP == 0, "staging fits");
+  char* stage = lds + (kLds - kSpace) + wp * (32 * PITCH);
+  auto write = [&](auto stream_c) {
+    constexpr bool kStream = decltype(stream_c)::value;
+#pragma unroll
+    for (int i = 0; i < TP; ++i) {
+      char* mine = stage + (BUFS == 2 ? (i & 1) * BLOCK : 0);
+      if (BUFS == 1 && i > 0) __syncthreads();
+#pragma unroll
+      for (int j = 0; j < TQ; ++j)
+#pragma unroll
+        for (int r = 0; r < 16; r += 4)
+          *reinterpret_cast<uint2*>(mine + lrow * PITCH + (wq * COLS + j * 32 + acc_q(r, lhalf)) * 2) =
+              make_uint2(pack_bf16x2(acc[i][j][r], acc[i][j][r + 1]), pack_bf16x2(acc[i][j][r + 2], acc[i][j][r + 3]));
+      __syncthreads();
+#pragma unroll
+      for (int r0 = 0; r0 < 32 / C::WQ; r0 += RPP) {
+        const int row = wq * (32 / C::WQ) + r0 + lane / GROUPS, q = lane % GROUPS * 8;
+        const uint4 raw = *reinterpret_cast<const uint4*>(mine + row * PITCH + q * 2);
+        const int p = (wp * TP + i) * 32 + row;
+        if (p >= prem || q >= qrem) continue;
+        uint16_t* o = out + p * g.ldo + q;
+        if (q + 8 <= qrem) {
+          if constexpr (kStream) stream16_any(o, raw);
+          else store16_any(o, raw);
+        } else {
+          const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            if (q + k < qrem) o[k] = static_cast<uint16_t>(w[k >> 1] >> (16 * (k & 1)));
+        }
+      }
+    }
+  };
+  if (g.stream) write(std::integral_constant<bool, true>{});
+  else write(std::integral_constant<bool, false>{});
 }
 
 }  // namespace mfsdp
