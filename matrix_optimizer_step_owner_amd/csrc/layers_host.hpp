@@ -652,9 +652,7 @@ mfsdp_status_t scaled_linear_impl(const uint8_t* codes, const uint8_t* scales, c
   a.nb = static_cast<int32_t>(nb);
   a.g.stream = aligned(y, 128) && ldy * 2 % 128 == 0;
   hipError_t e = hipErrorInvalidValue;
-  int use = scaled_kernel(experts, rows, n, depth);
-  if (const char* v = getenv("MFSDP_T")) use = atoi(v);
-  switch (use) {
+  switch (scaled_kernel(experts, rows, n, depth)) {
     case kScaledLarge: e = launch_scaled<ScaledLarge>(a, stream); break;
     case kScaledPair: e = launch_scaled<ScaledPair>(a, stream); break;
     case kScaledRows: e = launch_scaled<ScaledRows>(a, stream); break;

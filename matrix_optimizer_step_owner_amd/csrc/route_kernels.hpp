@@ -77,6 +77,21 @@ __device__ __forceinline__ uint64_t wave_max(uint64_t v) {
   return static_cast<uint64_t>(hi) << 32 | lo;
 }
 
+// Sum over the wave, on every lane, by the same steps.
+__device__ __forceinline__ float wave_sum(float v) {
+  auto step = [&](uint32_t w) { v += __uint_as_float(w); };
+  step(dpp_or0<0x111, 0xf>(__float_as_uint(v)));
+  step(dpp_or0<0x112, 0xf>(__float_as_uint(v)));
+  step(dpp_or0<0x114, 0xf>(__float_as_uint(v)));
+  step(dpp_or0<0x118, 0xf>(__float_as_uint(v)));
+  step(dpp_or0<0x142, 0xa>(__float_as_uint(v)));
+  step(dpp_or0<0x143, 0xc>(__float_as_uint(v)));
+  return __uint_as_float(static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(__float_as_uint(v)), 63)));
+}
+
+// The next lane's value (lane 63: 0).
+__device__ __forceinline__ float wave_next(float v) { return __uint_as_float(dpp_or0<0x130, 0xf>(__float_as_uint(v))); }
+
 // PER elements from p + lane * PER on, those before n; others as `fill`.
 template <class E, int PER>
 __device__ __forceinline__ void route_load(const typename E::storage_t* p, int first, int n, float fill,
@@ -102,19 +117,21 @@ __device__ __forceinline__ void route_load(const typename E::storage_t* p, int f
   }
 }
 
-// Score of one expert; top and sum are the row's (softmax).
-__device__ __forceinline__ float route_score(float x, int sigmoid, float top, float sum) {
-  return sigmoid ? 1.f / (1.f + expf(-x)) : expf(x - top) / sum;
+// Score of one expert; top and inv are the row's largest logit and 1 / sum (softmax).
+__device__ __forceinline__ float route_score(float x, int sigmoid, float top, float inv) {
+  const float e = expf(sigmoid ? -x : x - top);
+  return sigmoid ? __builtin_amdgcn_rcpf(1.f + e) : e * inv;
 }
 
 // exp(x) by the hardware's 2^x: relatively off by (|x| + 2) 2^-23, a fifth of the
-// instructions.  For keys and sums; the chosen scores are taken from expf.
+// instructions.  For keys, sums and gradients; the weights' scores are taken from
+// expf.  Quotients are products with the hardware's reciprocal, one step off.
 __device__ __forceinline__ float route_exp(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504f); }
 
-// Largest logit and sum of exp(x - largest) of a row (softmax); x becomes the
+// Largest logit and 1 / sum of exp(x - largest) of a row (softmax); x becomes the
 // exponentials.
 template <int PER>
-__device__ __forceinline__ void route_softmax(float (&x)[PER], int first, int n, float& top, float& sum) {
+__device__ __forceinline__ void route_softmax(float (&x)[PER], int first, int n, float& top, float& inv) {
   uint32_t m = 0;
 #pragma unroll
   for (int i = 0; i < PER; ++i)
@@ -126,7 +143,7 @@ __device__ __forceinline__ void route_softmax(float (&x)[PER], int first, int n,
     x[i] = first + i < n ? route_exp(x[i] - top) : 0.f;
     s += x[i];
   }
-  sum = warp_sum(s);
+  inv = __builtin_amdgcn_rcpf(wave_sum(s));
 }
 
 // Distance within which fp32 keys do not decide, for keys of size `key`.  A
@@ -243,15 +260,14 @@ __device__ __forceinline__ uint32_t route_groups(const RouteArgs& a, const K (&v
 }
 
 // The k largest keys in order, lane j receiving expert j (others -1).  Lists of up
-// to eight are sorted first (exchanges of neighbours, which keep equal keys in
+// to four are sorted first (exchanges of neighbours, which keep equal keys in
 // order, with their places as the digits of one word): a round then needs
 // neither the largest of a lane's own nor a search for it, and the winner's list
-// moves up by one.  On return key[0] is the largest that a lane has left
-// (PER <= 8).
+// moves up by one.  (Lists of eight lose by it: 32768 x 512, k = 10, 64 and 42 us.)  On return key[0] is the largest that a lane has left.
 template <int PER, class K>
 __device__ __forceinline__ int route_pick(K (&key)[PER], int k, int lane) {
   int mine = -1;
-  if constexpr (PER <= 8) {
+  if constexpr (PER <= 4) {
     uint32_t place[PER];
 #pragma unroll
     for (int i = 0; i < PER; ++i) place[i] = i;
@@ -278,7 +294,7 @@ __device__ __forceinline__ int route_pick(K (&key)[PER], int k, int lane) {
 #pragma unroll
       for (int i = 0; i < PER; ++i) key[i] = won ? (i + 1 < PER ? key[(i + 1) % PER] : K(0)) : key[i];
       digits = won ? digits >> 4 : digits;
-      if (lane == j) mine = e;
+      mine = lane == j ? e : mine;
     }
   } else {
     for (int j = 0; j < k; ++j) {
@@ -357,21 +373,22 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
   const int first = lane * PER;
   float x[PER];
   route_load<E, PER>(row, first, a.n, 0.f, x);
-  uint32_t key[PER];
-#pragma unroll
-  for (int i = 0; i < PER; ++i) key[i] = first + i < a.n ? route_key(x[i]) : 0u;
-  float top = 0.f, sum = 1.f;
-  if (!a.sigmoid) route_softmax<PER>(x, first, a.n, top, sum);     // x: exponentials
-
-  bool close = false;
-  int mine;
-  float mx, mb = 0.f;
   const bool on = lane < a.k;
+  float top = 0.f, inv = 1.f;
+  uint32_t key[PER];
+  int mine;
+  float mx;
+  if (!a.bias) {      // the logits decide (within the groups)
+#pragma unroll
+    for (int i = 0; i < PER; ++i) key[i] = first + i < a.n ? route_key(x[i]) : 0u;
+  }
+  if (!a.sigmoid) route_softmax<PER>(x, first, a.n, top, inv);     // x: exponentials
+  bool close = false;
   if (!a.bias && a.groups == 1) {
     mine = route_pick<PER, uint32_t>(key, a.k, lane);
     mx = on ? E::to_f32(gld<S>(row + mine)) : 0.f;
   } else {
-    const float most = a.sigmoid ? 1.f : 1.f / sum;
+    const float most = a.sigmoid ? 1.f : inv;
     float v[PER];
 #pragma unroll
     for (int i = 0; i < PER; ++i) v[i] = 0.f;
@@ -385,10 +402,12 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
     if (a.groups > 1) {
       const uint32_t stay = route_groups<PER, float, uint32_t>(a, vk, lane, most, close);
 #pragma unroll
-      for (int i = 0; i < PER; ++i)
-        if (!(stay >> i & 1)) key[i] = vk[i] = 0;
+      for (int i = 0; i < PER; ++i) {
+        if (a.bias) vk[i] = stay >> i & 1 ? vk[i] : 0u;
+        else key[i] = stay >> i & 1 ? key[i] : 0u;
+      }
     }
-    if (!a.bias) {   // within the groups the logits decide
+    if (!a.bias) {
       mine = route_pick<PER, uint32_t>(key, a.k, lane);
       mx = on ? E::to_f32(gld<S>(row + mine)) : 0.f;
     } else {
@@ -396,11 +415,10 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
       // neighbours in the order, unless they are equal, and the last against
       // what is left
       mx = on ? E::to_f32(gld<S>(row + mine)) : 0.f;
-      mb = on ? gld<float>(a.bias + mine) : 0.f;
+      const float mb = on ? gld<float>(a.bias + mine) : 0.f;
       const float mk = (a.sigmoid ? __builtin_amdgcn_rcpf(1.f + route_exp(-mx)) : route_exp(mx - top) * most) + mb;
       const float doubt = route_doubt(most, mk);
-      const float ox = __shfl_down(mx, 1, 64), ob = __shfl_down(mb, 1, 64), ok = __shfl_down(mk, 1, 64);
-      bool open = lane + 1 < a.k && !(mk - ok > doubt) && !(ox == mx && ob == mb);
+      bool open = lane + 1 < a.k && !(mk - wave_next(mk) > doubt) && !(wave_next(mx) == mx && wave_next(mb) == mb);
       auto last = [&](float q) { return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(q), a.k - 1)); };
       open = open || (vk[0] != 0 && !(last(mk) - route_value(vk[0]) > last(doubt)));
       close = close || __ballot(open) != 0;
@@ -411,11 +429,11 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
     mx = on ? E::to_f32(gld<S>(row + mine)) : 0.f;
   }
 
-  const float s = on ? route_score(mx, a.sigmoid, top, sum) : 0.f;
-  const float total = a.renorm ? warp_sum(s) + kRouteTiny : 1.f;
+  const float s = on ? route_score(mx, a.sigmoid, top, inv) : 0.f;
+  const float factor = a.renorm ? a.scale * __builtin_amdgcn_rcpf(wave_sum(s) + kRouteTiny) : a.scale;
   if (on) {
     chosen[lane] = mine;
-    weights[lane] = a.scale * s / total;
+    weights[lane] = s * factor;
   }
 }
 
@@ -437,11 +455,16 @@ struct RouteGradArgs {
 //   ds_j = scale / D (g_j - sum_i g_i s_i / D)     (scale g_j if not renormalised)
 //   softmax  dx_e = p_e (ds_e - sum_j ds_j s_j)    ds_e = 0 where not chosen
 //   sigmoid  dx_e = ds_e s_e (1 - s_e)
+// Bound by HBM; the chosen experts' terms reach the lanes that hold them
+// through LDS (a loop over them, which experts that are named twice still take,
+// was 40% of the instructions).
 template <class E, int PER>
 __global__ __launch_bounds__(256) void route_grad_kernel(RouteGradArgs a) {
   using S = typename E::storage_t;
-  const int lane = threadIdx.x & 63;
-  const int64_t t = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
+  __shared__ __align__(16) float term[4][64 * PER];
+  __shared__ int tag[4][64 * PER];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * 4 + wave;
   if (t >= a.tokens) return;
   const S* row = static_cast<const S*>(a.logits) + t * a.ld;
   S* out = static_cast<S*>(a.out) + t * a.ldo;
@@ -455,36 +478,45 @@ __global__ __launch_bounds__(256) void route_grad_kernel(RouteGradArgs a) {
   if (__ballot(on) != 0) {    // a padded token's logits are not read
     const float xe = on ? E::to_f32(gld<S>(row + e)) : 0.f;
     const float g = on ? a.dw[t * a.k + lane] : 0.f;
-    float x[PER], top = 0.f, sum = 1.f;
+    float x[PER], top = 0.f, inv = 1.f;
     if (!a.sigmoid) {
       route_load<E, PER>(row, first, a.n, 0.f, x);
-      route_softmax<PER>(x, first, a.n, top, sum);
+      route_softmax<PER>(x, first, a.n, top, inv);      // x: exponentials
     }
-    const float s = on ? route_score(xe, a.sigmoid, top, sum) : 0.f;
+    const float q = route_exp(a.sigmoid ? -fabsf(xe) : xe - top), r = __builtin_amdgcn_rcpf(1.f + q);
+    const float s = !on ? 0.f : !a.sigmoid ? q * inv : xe >= 0.f ? r : q * r;
     float ds = a.scale * g;
     if (a.renorm) {
-      const float d = warp_sum(s) + kRouteTiny;
-      ds = a.scale / d * (g - warp_sum(g * s) / d);
+      const float d = __builtin_amdgcn_rcpf(wave_sum(s) + kRouteTiny);
+      ds = a.scale * d * (g - wave_sum(g * s) * d);
     }
     if (!on) ds = 0.f;
     float c = 0.f;
-    if (a.sigmoid) {
-      const float q = expf(-fabsf(xe));         // s (1 - s), no difference
-      ds *= q / ((1.f + q) * (1.f + q));
-    } else {
-      c = warp_sum(ds * s);
-    }
-    for (int j = 0; j < a.k; ++j) {             // an expert that is named twice adds up
-      const int ej = __builtin_amdgcn_readlane(e, j);
-      const float dj = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(ds), j));
+    if (a.sigmoid) ds *= q * r * r;             // s (1 - s), no difference
+    else c = wave_sum(ds * s);
+    // one wave's own part of LDS: its operations are in order
 #pragma unroll
-      for (int i = 0; i < PER; ++i)
-        if (ej == first + i) dx[i] += dj;
+    for (int i = 0; i < PER; ++i) term[wave][first + i] = 0.f;
+    if (on) tag[wave][e] = lane;
+    __builtin_amdgcn_wave_barrier();
+    if (on) term[wave][e] = ds;
+    const bool twice = on && tag[wave][e] != lane;
+    __builtin_amdgcn_wave_barrier();
+    if (__builtin_expect(__ballot(twice) == 0, 1)) {
+#pragma unroll
+      for (int i = 0; i < PER; ++i) dx[i] = term[wave][first + i];
+    } else {
+      for (int j = 0; j < a.k; ++j) {           // an expert that is named twice adds up
+        const int ej = __builtin_amdgcn_readlane(e, j);
+        const float dj = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(ds), j));
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+          if (ej == first + i) dx[i] += dj;
+      }
     }
     if (!a.sigmoid) {
-      const float inv = 1.f / sum;
 #pragma unroll
-      for (int i = 0; i < PER; ++i) dx[i] = x[i] * inv * (dx[i] - c);     // x: exponentials
+      for (int i = 0; i < PER; ++i) dx[i] = x[i] * inv * (dx[i] - c);
     }
   }
   if (first + PER <= a.n && PER % E::kVec == 0) {
