@@ -241,4 +241,39 @@ __device__ __forceinline__ double warp_sum(double v) {
   return v;
 }
 
+// Largest value in the wave, on every lane (as a scalar).
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint32_t dpp_or0(uint32_t v) {
+  return static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), CTRL, ROWS, 0xf, false));
+}
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+  v = max(v, dpp_or0<0x111, 0xf>(v));   // row_shr:1, :2, :4, :8
+  v = max(v, dpp_or0<0x112, 0xf>(v));
+  v = max(v, dpp_or0<0x114, 0xf>(v));
+  v = max(v, dpp_or0<0x118, 0xf>(v));
+  v = max(v, dpp_or0<0x142, 0xa>(v));   // row_bcast:15, :31
+  v = max(v, dpp_or0<0x143, 0xc>(v));
+  return static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(v), 63));
+}
+__device__ __forceinline__ uint64_t wave_max(uint64_t v) {
+  const uint32_t hi = wave_max(static_cast<uint32_t>(v >> 32));
+  const uint32_t lo = wave_max(static_cast<uint32_t>(v >> 32) == hi ? static_cast<uint32_t>(v) : 0u);
+  return static_cast<uint64_t>(hi) << 32 | lo;
+}
+
+// Sum over the wave, on every lane, by the same steps.
+__device__ __forceinline__ float wave_sum(float v) {
+  auto step = [&](uint32_t w) { v += __uint_as_float(w); };
+  step(dpp_or0<0x111, 0xf>(__float_as_uint(v)));
+  step(dpp_or0<0x112, 0xf>(__float_as_uint(v)));
+  step(dpp_or0<0x114, 0xf>(__float_as_uint(v)));
+  step(dpp_or0<0x118, 0xf>(__float_as_uint(v)));
+  step(dpp_or0<0x142, 0xa>(__float_as_uint(v)));
+  step(dpp_or0<0x143, 0xc>(__float_as_uint(v)));
+  return __uint_as_float(static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(__float_as_uint(v)), 63)));
+}
+
+// The next lane's value (lane 63: 0).
+__device__ __forceinline__ float wave_next(float v) { return __uint_as_float(dpp_or0<0x130, 0xf>(__float_as_uint(v))); }
+
 }  // namespace mfsdp

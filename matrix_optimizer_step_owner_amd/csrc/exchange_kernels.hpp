@@ -33,11 +33,17 @@ struct ExchangeArgs {
   float beta;
 };
 
+// Streamed load of 16 bytes at any element.
+__device__ __forceinline__ uint4 load16_stream(const void* p) {
+  const u32x4_t v = __builtin_nontemporal_load((const MFSDP_GLOBAL u32x4_el_t*)(p));
+  return make_uint4(v.x, v.y, v.z, v.w);
+}
+
 // 16 bytes of E from p on, of which `left` elements exist (others 0).
-template <class E>
+template <class E, bool STREAM = false>
 __device__ __forceinline__ uint4 unit_load(const typename E::storage_t* p, int left) {
   using S = typename E::storage_t;
-  if (left >= E::kVec) return load16_any(p);
+  if (left >= E::kVec) return STREAM ? load16_stream(p) : load16_any(p);
   S v[E::kVec];
 #pragma unroll
   for (int i = 0; i < E::kVec; ++i) v[i] = i < left ? gld<S>(p + i) : S(0);

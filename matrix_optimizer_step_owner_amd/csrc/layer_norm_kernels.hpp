@@ -10,9 +10,14 @@
 // of each workgroup's rows, in their order, and then of the workgroups' in
 // theirs, in two launches: no atomics, equal inputs give equal bits.
 //
-// One workgroup takes one row at a time, UPT units of 16 bytes per thread in
-// registers (UPT = 0: rows that do not fit, read again from the caches).  Bound
-// by HBM.
+// Rows of up to 2048 units of 16 bytes stay in registers, UPT units per thread of L
+// lanes of a wave (64 / L rows to a wave) or, L = 0, of a workgroup.  Each takes
+// many rows and loads the next one while it adds up this one.  Wider rows are read again
+// from the caches, and the sums over rows by a kernel over columns.
+//
+// Bound by HBM, and close to it by the vector units: a value costs some 14
+// instructions of four cycles in the gradient, which 16 values per lane, their
+// deviations kept, and two sums of two values per row (instead of three) leave it.
 #pragma once
 
 #include "common.hpp"
@@ -27,263 +32,424 @@ struct NormArgs {
   const void* b;         // d, the type of w, or null
   void* out;             // y or dx, row stride ldo
   float* part;           // [groups][dbias ? 2 : 1][d] partial sums
+  float* stats;          // [rows][2] mean and 1 / sqrt(variance + eps), of wide rows
   float* dw;             // d
   float* db;             // d, or null
   int64_t ldx, ldy, ldo;
   int32_t rows, d;
   int32_t centered, w_bf16;
-  int32_t groups;        // workgroups of the gradient
+  int32_t groups;        // waves or workgroups that rows are dealt to
   float eps, beta;
 };
 
 constexpr int kNormThreadsMax = 512;
 
-// Sum over the workgroup, on every thread; `part` is used twice in turn.
-template <int N>
-__device__ __forceinline__ void norm_sum(float (&v)[N], float (*part)[N]) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
-#pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = warp_sum(v[i]);
-  if (waves == 1) return;
-  __syncthreads();
-  if (lane == 0) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) part[wave][i] = v[i];
+// First column of this thread's u-th unit.
+template <int L, int V>
+__device__ __forceinline__ int norm_col(int u) {
+  const int threads = L ? L : static_cast<int>(blockDim.x), own = L ? static_cast<int>(threadIdx.x) % L : static_cast<int>(threadIdx.x);
+  return (u * threads + own) * V;
+}
+
+// Rows: the first of this group of threads (a wave, or a workgroup), and this
+// thread's among those that the group takes at once.
+template <int L>
+struct NormRows {
+  static constexpr int AT_ONCE = L ? 64 / L : 1;
+  int group, sub;
+  int64_t step;
+  __device__ __forceinline__ explicit NormRows(const NormArgs& a) {
+    group = L ? static_cast<int>(blockIdx.x) * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) : static_cast<int>(blockIdx.x);
+    sub = L ? static_cast<int>(threadIdx.x & 63) / L : 0;
+    step = static_cast<int64_t>(a.groups) * AT_ONCE;
   }
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    float s = 0.f;
-    for (int w = 0; w < waves; ++w) s += part[w][i];
-    v[i] = s;
+};
+
+// Sum over each L neighbouring lanes, on all of them.
+template <int L>
+__device__ __forceinline__ float lanes_sum(float v) {
+  if constexpr (L == 64) return wave_sum(v);
+  auto add = [&](uint32_t w) { v += __uint_as_float(w); };
+  auto bits = [&] { return static_cast<int>(__float_as_uint(v)); };
+  add(static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(bits(), 0xb1, 0xf, 0xf, true)));    // neighbours
+  add(static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(bits(), 0x4e, 0xf, 0xf, true)));    // pairs
+  add(static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(bits(), 0x141, 0xf, 0xf, true)));   // mirrors of 8
+  if constexpr (L >= 16) add(static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(bits(), 0x140, 0xf, 0xf, true)));   // of 16
+  if constexpr (L >= 32) v += __shfl_xor(v, 16, 64);
+  return v;
+}
+
+// LDS of a row's sums; rows have two sets in turn.
+struct NormParts {
+  float2 p[2][2][kNormThreadsMax / 64];
+};
+
+// Two sums over a row's threads, on all of them.  One barrier: each pair of a row has
+// LDS of its own, and rows have two sets in turn, so that a slow wave's reads are
+// behind it before they are written again.  The barrier waits for LDS alone:
+// __syncthreads would also wait for the next row's loads and this one's stores.
+template <int L>
+__device__ __forceinline__ void norm_sum(float& v0, float& v1, float2* part) {
+  if constexpr (L != 0) {
+    v0 = lanes_sum<L>(v0);
+    v1 = lanes_sum<L>(v1);
+    return;
+  }
+  v0 = wave_sum(v0);
+  v1 = wave_sum(v1);
+  const int waves = blockDim.x >> 6;
+  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = make_float2(v0, v1);
+  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  v0 = v1 = 0.f;
+  for (int w = 0; w < waves; ++w) {
+    const float2 t = part[w];
+    v0 += t.x;
+    v1 += t.y;
   }
 }
 
-// V values of a weight (or bias) from column c on, `left` of them.
+// V values of a weight (or bias) from column c on; 0 past the row, and without one.
 template <int V>
-__device__ __forceinline__ void norm_weight(const void* w, int bf, int c, int left, float (&v)[V]) {
+__device__ __forceinline__ void norm_weight(const void* w, int bf, int c, int d, float (&v)[V]) {
 #pragma unroll
   for (int i = 0; i < V; ++i) v[i] = 0.f;
-  if (!w) return;
-  if (left >= V) {
-    if (bf) {
-      const uint16_t* p = static_cast<const uint16_t*>(w) + c;
+  if (!w || c >= d) return;
+  if (c + V <= d && !bf) {
 #pragma unroll
-      for (int i = 0; i < V; ++i) v[i] = bf16_to_f32(p[i]);
-    } else {
-      const float* p = static_cast<const float*>(w) + c;
+    for (int i = 0; i < V; i += 4) {
+      float f[4];
+      Vec16<ElemF32>::unpack(load16_any(static_cast<const float*>(w) + c + i), f);
 #pragma unroll
-      for (int i = 0; i < V; i += 4) {
-        const uint4 t = load16_any(p + i);
-        float f[4];
-        Vec16<ElemF32>::unpack(t, f);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) v[i + q] = f[q];
-      }
+      for (int q = 0; q < 4; ++q) v[i + q] = f[q];
     }
     return;
   }
 #pragma unroll
   for (int i = 0; i < V; ++i)
-    if (i < left) v[i] = bf ? bf16_to_f32(static_cast<const uint16_t*>(w)[c + i]) : static_cast<const float*>(w)[c + i];
+    if (c + i < d) v[i] = bf ? bf16_to_f32(static_cast<const uint16_t*>(w)[c + i]) : static_cast<const float*>(w)[c + i];
 }
 
-// First column of this thread's u-th unit.
-template <int V>
-__device__ __forceinline__ int norm_col(int u) {
-  return (u * static_cast<int>(blockDim.x) + static_cast<int>(threadIdx.x)) * V;
-}
-
-// One row: in registers, or (UPT = 0) where it lies.
-template <class E, int UPT>
+// One row in registers.  FULL: the threads' units are exactly the row; else some
+// threads' last unit is not, or not wholly, the row's (the host chooses the number
+// of threads so).
+template <class E, int UPT, int L, bool FULL>
 struct NormRow {
   using S = typename E::storage_t;
   static constexpr int V = E::kVec;
-  uint4 raw[UPT > 0 ? UPT : 1];
-  const S* p;
-  int d;
-  __device__ __forceinline__ void load(const S* row, int d_) {
-    p = row;
-    d = d_;
-    if constexpr (UPT > 0) {
+  uint4 raw[UPT];
+  __device__ __forceinline__ void load(const S* row, int d) {
 #pragma unroll
-      for (int u = 0; u < UPT; ++u) raw[u] = fetch(u);
+    for (int u = 0; u < UPT; ++u) {
+      const int c = norm_col<L, V>(u);
+      if (FULL || u + 1 < UPT) raw[u] = load16_any(row + c);
+      else raw[u] = c < d ? unit_load<E>(row + c, d - c) : make_uint4(0, 0, 0, 0);
     }
   }
-  __device__ __forceinline__ uint4 fetch(int u) const {
-    const int c = norm_col<V>(u);
-    return c < d ? unit_load<E>(p + c, d - c) : make_uint4(0, 0, 0, 0);
-  }
-  __device__ __forceinline__ void get(int u, float (&v)[V]) const {
-    if constexpr (UPT > 0) Vec16<E>::unpack(raw[u], v);
-    else Vec16<E>::unpack(fetch(u), v);
-  }
+  __device__ __forceinline__ void get(int u, float (&v)[V]) const { Vec16<E>::unpack(raw[u], v); }
 };
 
-// f(u) for this thread's units.
-template <int UPT, int V, class F>
-__device__ __forceinline__ void norm_units(int d, F&& f) {
-  if constexpr (UPT > 0) {
-#pragma unroll
-    for (int u = 0; u < UPT; ++u) f(u);
-  } else {
-    for (int u = 0; norm_col<V>(u) < d; ++u) f(u);
-  }
-}
+// A deviation, 0 past the row (not FULL, of the last unit).
+template <int UPT, int V, int L, bool FULL>
+struct NormKeep {
+  int left;
+  __device__ __forceinline__ explicit NormKeep(int d) { left = d - norm_col<L, V>(UPT - 1); }
+  __device__ __forceinline__ float operator()(int u, int i, float v) const { return FULL || u + 1 < UPT || i < left ? v : 0.f; }
+};
 
-// Mean and 1 / sqrt(variance + eps).  Two sums: the squares' deviations are
-// taken from the mean itself, so a large mean costs no digits.
-template <class E, int UPT>
-__device__ __forceinline__ void norm_stats(const NormArgs& a, const NormRow<E, UPT>& x, float (*part)[1],
-                                           float& mean, float& r) {
+template <class E, int UPT, int L, bool FULL>
+__global__ __launch_bounds__(L ? 256 : kNormThreadsMax) void layer_norm_kernel(NormArgs a) {
+  using S = typename E::storage_t;
   constexpr int V = E::kVec;
-  mean = 0.f;
-  float s[1] = {0.f};
-  if (a.centered) {
-    norm_units<UPT, V>(a.d, [&](int u) {
-      float v[V];
-      x.get(u, v);
+  __shared__ NormParts parts;
+  const NormRows<L> at(a);
+  if (L && at.group >= a.groups) return;
+  NormRow<E, UPT, L, FULL> x;
+  // rows of one wave's lanes end together: past the last, it is read again
+  auto fetch = [&](int64_t row) { x.load(static_cast<const S*>(a.x) + min(row, static_cast<int64_t>(a.rows) - 1) * a.ldx, a.d); };
+  int64_t row0 = static_cast<int64_t>(at.group) * at.AT_ONCE;
+  fetch(row0 + at.sub);
+  float w[UPT][V], b[UPT][V];
 #pragma unroll
-      for (int i = 0; i < V; ++i) s[0] += v[i];
-    });
-    norm_sum<1>(s, part);
-    mean = s[0] / static_cast<float>(a.d);
+  for (int u = 0; u < UPT; ++u) {
+    norm_weight<V>(a.w, a.w_bf16, norm_col<L, V>(u), a.d, w[u]);
+    norm_weight<V>(a.b, a.w_bf16, norm_col<L, V>(u), a.d, b[u]);
   }
-  s[0] = 0.f;
-  norm_units<UPT, V>(a.d, [&](int u) {
-    float v[V];
-    x.get(u, v);
-    const int left = a.d - norm_col<V>(u);
+  const NormKeep<UPT, V, L, FULL> keep(a.d);
+  const float inv = 1.f / static_cast<float>(a.d);
+  int set = 0;
+  for (; row0 < a.rows; row0 += at.step, set ^= 1) {
+    const int64_t row = row0 + at.sub;
+    float xc[UPT][V], s = 0.f, none = 0.f;
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const float c = i < left ? v[i] - mean : 0.f;
-      s[0] = fmaf(c, c, s[0]);
+    for (int u = 0; u < UPT; ++u) {
+      x.get(u, xc[u]);
+#pragma unroll
+      for (int i = 0; i < V; ++i) s += xc[u][i];
     }
-  });
-  norm_sum<1>(s, part);
-  r = 1.f / sqrtf(s[0] / static_cast<float>(a.d) + a.eps);
-}
-
-template <class E, int UPT>
-__global__ __launch_bounds__(kNormThreadsMax) void layer_norm_kernel(NormArgs a) {
-  using S = typename E::storage_t;
-  constexpr int V = E::kVec;
-  __shared__ float part[kNormThreadsMax / 64][1];
-  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
-    NormRow<E, UPT> x;
-    x.load(static_cast<const S*>(a.x) + row * a.ldx, a.d);
-    float mean, r;
-    norm_stats<E, UPT>(a, x, part, mean, r);
-    S* y = static_cast<S*>(a.out) + row * a.ldo;
-    norm_units<UPT, V>(a.d, [&](int u) {
-      const int c = norm_col<V>(u), left = a.d - c;
-      if (left <= 0) return;
-      float v[V], w[V], b[V];
-      x.get(u, v);
-      norm_weight<V>(a.w, a.w_bf16, c, left, w);
-      norm_weight<V>(a.b, a.w_bf16, c, left, b);
+    if (row0 + at.step < a.rows) fetch(row + at.step);
+    float mean = 0.f;
+    if (a.centered) {
+      norm_sum<L>(s, none, parts.p[set][0]);
+      mean = s * inv;
+    }
+    float q = 0.f;
 #pragma unroll
-      for (int i = 0; i < V; ++i) v[i] = fmaf((v[i] - mean) * r, w[i], b[i]);
-      unit_store<E>(y + c, left, Vec16<E>::pack(v));
-    });
+    for (int u = 0; u < UPT; ++u)
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        xc[u][i] = keep(u, i, xc[u][i] - mean);
+        q = fmaf(xc[u][i], xc[u][i], q);
+      }
+    norm_sum<L>(q, none, parts.p[set][1]);
+    const float r = rsqrtf(q * inv + a.eps);
+    if (L && row >= a.rows) continue;
+    S* y = static_cast<S*>(a.out) + row * a.ldo;
+#pragma unroll
+    for (int u = 0; u < UPT; ++u) {
+      const int c = norm_col<L, V>(u);
+#pragma unroll
+      for (int i = 0; i < V; ++i) xc[u][i] = fmaf(xc[u][i] * r, w[u][i], b[u][i]);
+      if (FULL || u + 1 < UPT) unit_store<E>(y + c, V, Vec16<E>::pack(xc[u]));
+      else if (c < a.d) unit_store<E>(y + c, a.d - c, Vec16<E>::pack(xc[u]));
+    }
   }
 }
 
-template <class E, int UPT>
-__global__ __launch_bounds__(kNormThreadsMax) void layer_norm_grad_kernel(NormArgs a) {
+// Each group of threads that takes rows (a workgroup, or a wave) has partial sums
+// of its own.
+template <class E, int UPT, int L, bool FULL>
+__global__ __launch_bounds__(L ? 256 : kNormThreadsMax) void layer_norm_grad_kernel(NormArgs a) {
   using S = typename E::storage_t;
   constexpr int V = E::kVec;
-  constexpr int N = UPT > 0 ? UPT : 1;
-  __shared__ float part1[kNormThreadsMax / 64][1];
-  __shared__ float part2[kNormThreadsMax / 64][2];
-  const int sums = a.db ? 2 : 1;
-  float* pw = a.part + static_cast<size_t>(blockIdx.x) * sums * a.d;
-  float* pb = pw + a.d;
-  float w[N][V], accw[N][V], accb[N][V];
+  __shared__ NormParts parts;
+  const NormRows<L> at(a);
+  if (L && at.group >= a.groups) return;
+  NormRow<E, UPT, L, FULL> x, dy;
+  auto fetch = [&](int64_t row) {
+    row = min(row, static_cast<int64_t>(a.rows) - 1);
+    x.load(static_cast<const S*>(a.x) + row * a.ldx, a.d);
+    dy.load(static_cast<const S*>(a.dy) + row * a.ldy, a.d);
+  };
+  int64_t row0 = static_cast<int64_t>(at.group) * at.AT_ONCE;
+  fetch(row0 + at.sub);
+  float w[UPT][V], accw[UPT][V], accb[UPT][V];
 #pragma unroll
-  for (int u = 0; u < N; ++u) {
-    if constexpr (UPT > 0) norm_weight<V>(norm_col<V>(u) < a.d ? a.w : nullptr, a.w_bf16, norm_col<V>(u), a.d - norm_col<V>(u), w[u]);
+  for (int u = 0; u < UPT; ++u) {
+    norm_weight<V>(a.w, a.w_bf16, norm_col<L, V>(u), a.d, w[u]);
 #pragma unroll
     for (int i = 0; i < V; ++i) accw[u][i] = accb[u][i] = 0.f;
   }
+  const NormKeep<UPT, V, L, FULL> keep(a.d);
   const float inv = 1.f / static_cast<float>(a.d);
-  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
-    NormRow<E, UPT> x, dy;
-    x.load(static_cast<const S*>(a.x) + row * a.ldx, a.d);
-    dy.load(static_cast<const S*>(a.dy) + row * a.ldy, a.d);
-    float mean, r;
-    norm_stats<E, UPT>(a, x, part1, mean, r);
-    float c[2] = {0.f, 0.f};    // sums of g and g xh
-    auto weight = [&](int u, float (&v)[V]) {
-      if constexpr (UPT > 0) {
+  int set = 0;
+  for (; row0 < a.rows; row0 += at.step, set ^= 1) {
+    const int64_t row = row0 + at.sub;
+    float xc[UPT][V], dv[UPT][V], s = 0.f, c0 = 0.f;
 #pragma unroll
-        for (int i = 0; i < V; ++i) v[i] = w[u][i];
-      } else {
-        norm_weight<V>(a.w, a.w_bf16, norm_col<V>(u), a.d - norm_col<V>(u), v);
-      }
-    };
-    norm_units<UPT, V>(a.d, [&](int u) {
-      float xv[V], gv[V], wv[V];
-      x.get(u, xv);
-      dy.get(u, gv);
-      weight(u, wv);
+    for (int u = 0; u < UPT; ++u) {
+      x.get(u, xc[u]);
+      dy.get(u, dv[u]);
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        const float g = gv[i] * wv[i], xh = (xv[i] - mean) * r;     // past the row dy is 0
-        c[0] += g;
-        c[1] = fmaf(g, xh, c[1]);
+        s += xc[u][i];
+        c0 = fmaf(dv[u][i], w[u][i], c0);
       }
-    });
-    norm_sum<2>(c, part2);
-    const float c0 = a.centered ? c[0] * inv : 0.f, c1 = c[1] * inv;
+    }
+    if (row0 + at.step < a.rows) fetch(row + at.step);
+    float mean = 0.f;
+    if (a.centered) {
+      norm_sum<L>(s, c0, parts.p[set][0]);
+      mean = s * inv;
+      c0 *= inv;
+    } else {
+      c0 = 0.f;
+    }
+    float q = 0.f, c1 = 0.f;      // sums of xc^2 and of g xc
+#pragma unroll
+    for (int u = 0; u < UPT; ++u)
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        xc[u][i] = keep(u, i, xc[u][i] - mean);
+        q = fmaf(xc[u][i], xc[u][i], q);
+        c1 = fmaf(dv[u][i] * w[u][i], xc[u][i], c1);
+      }
+    norm_sum<L>(q, c1, parts.p[set][1]);
+    const float r = rsqrtf(q * inv + a.eps);
+    if (L && row >= a.rows) continue;       // (the last round: nothing follows)
+    // dx = r g - r c0 - xc r^3 mean(g xc)
+    const float k0 = -r * c0, k1 = -(r * r) * r * (c1 * inv);
     S* dx = static_cast<S*>(a.out) + row * a.ldo;
-    const bool first = row == blockIdx.x;
-    norm_units<UPT, V>(a.d, [&](int u) {
-      const int col = norm_col<V>(u), left = a.d - col;
-      if (left <= 0) return;
-      float xv[V], gv[V], wv[V], o[V], dw[V];
-      x.get(u, xv);
-      dy.get(u, gv);
-      weight(u, wv);
+#pragma unroll
+    for (int u = 0; u < UPT; ++u) {
+      const int c = norm_col<L, V>(u);
+      float o[V];
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        const float xh = (xv[i] - mean) * r;
-        o[i] = r * (fmaf(-xh, c1, gv[i] * wv[i]) - c0);
-        dw[i] = gv[i] * xh;
+        const float rd = r * dv[u][i];
+        o[i] = fmaf(xc[u][i], k1, fmaf(rd, w[u][i], k0));
+        accw[u][i] = fmaf(rd, xc[u][i], accw[u][i]);
+        accb[u][i] += dv[u][i];
       }
-      unit_store<E>(dx + col, left, Vec16<E>::pack(o));
-      if constexpr (UPT > 0) {
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-          accw[u][i] += dw[i];
-          accb[u][i] += gv[i];
-        }
-      } else {    // this thread's own columns of the partial sums
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-          if (i < left) {
-            pw[col + i] = first ? dw[i] : pw[col + i] + dw[i];
-            if (a.db) pb[col + i] = first ? gv[i] : pb[col + i] + gv[i];
-          }
-      }
-    });
+      if (FULL || u + 1 < UPT) unit_store<E>(dx + c, V, Vec16<E>::pack(o));
+      else if (c < a.d) unit_store<E>(dx + c, a.d - c, Vec16<E>::pack(o));
+    }
   }
-  if constexpr (UPT > 0) {
+  if constexpr (L != 0 && L < 64) {   // the wave's rows, in a tree
 #pragma unroll
-    for (int u = 0; u < N; ++u) {
-      const int col = norm_col<V>(u);
+    for (int u = 0; u < UPT; ++u)
 #pragma unroll
       for (int i = 0; i < V; ++i)
-        if (col + i < a.d) {
-          pw[col + i] = accw[u][i];
-          if (a.db) pb[col + i] = accb[u][i];
+#pragma unroll
+        for (int d = L; d < 64; d *= 2) {
+          accw[u][i] += __shfl_xor(accw[u][i], d, 64);
+          accb[u][i] += __shfl_xor(accb[u][i], d, 64);
         }
+    if (at.sub > 0) return;
+  }
+  float* pw = a.part + static_cast<size_t>(at.group) * (a.db ? 2 : 1) * a.d;
+#pragma unroll
+  for (int u = 0; u < UPT; ++u) {
+    const int c = norm_col<L, V>(u);
+#pragma unroll
+    for (int h = 0; h < V; h += 4) {
+      const float fw[4] = {accw[u][h], accw[u][h + 1], accw[u][h + 2], accw[u][h + 3]};
+      const float fb[4] = {accb[u][h], accb[u][h + 1], accb[u][h + 2], accb[u][h + 3]};
+      if (!FULL && c + h >= a.d) continue;
+      if (FULL || c + h + 4 <= a.d) {
+        store16_any(pw + c + h, Vec16<ElemF32>::pack(fw));
+        if (a.db) store16_any(pw + a.d + c + h, Vec16<ElemF32>::pack(fb));
+      } else {
+        for (int i = 0; c + h + i < a.d; ++i) {
+          pw[c + h + i] = fw[i];
+          if (a.db) pw[a.d + c + h + i] = fb[i];
+        }
+      }
     }
   }
 }
 
-// dw = beta dw + sum over the workgroups' partial sums: 64 columns of one of the
-// two per workgroup, kNormSlices waves each with its own contiguous part.
+// ---------------------------------------------------------------------------
+// Rows that do not fit: one workgroup per row, each pass reads it again.
+// ---------------------------------------------------------------------------
+// f(c, x, dy) for this thread's units of a row.
+template <class E, class F>
+__device__ __forceinline__ void norm_wide(const typename E::storage_t* x, const typename E::storage_t* dy, int d, F&& f) {
+  constexpr int V = E::kVec;
+  for (int c = static_cast<int>(threadIdx.x) * V; c < d; c += static_cast<int>(blockDim.x) * V) {
+    float xv[V], gv[V];
+    Vec16<E>::unpack(unit_load<E>(x + c, d - c), xv);
+    if (dy) Vec16<E>::unpack(unit_load<E>(dy + c, d - c), gv);
+    f(c, xv, gv);
+  }
+}
+
+template <class E, bool GRAD>
+__global__ __launch_bounds__(kNormThreadsMax) void layer_norm_wide_kernel(NormArgs a) {
+  using S = typename E::storage_t;
+  constexpr int V = E::kVec;
+  __shared__ NormParts parts;
+  const float inv = 1.f / static_cast<float>(a.d);
+  int set = 0;
+  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, set ^= 1) {
+    const S* x = static_cast<const S*>(a.x) + row * a.ldx;
+    const S* dy = GRAD ? static_cast<const S*>(a.dy) + row * a.ldy : nullptr;
+    float s = 0.f, c0 = 0.f, mean = 0.f;
+    if (a.centered) {
+      norm_wide<E>(x, dy, a.d, [&](int c, const float (&xv)[V], const float (&gv)[V]) {
+        float w[V];
+        if (GRAD) norm_weight<V>(a.w, a.w_bf16, c, a.d, w);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          s += xv[i];
+          if (GRAD) c0 = fmaf(gv[i], w[i], c0);
+        }
+      });
+      norm_sum<0>(s, c0, parts.p[set][0]);
+      mean = s * inv;
+      c0 *= inv;
+    }
+    float q = 0.f, c1 = 0.f;
+    norm_wide<E>(x, dy, a.d, [&](int c, const float (&xv)[V], const float (&gv)[V]) {
+      float w[V];
+      if (GRAD) norm_weight<V>(a.w, a.w_bf16, c, a.d, w);
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const float xc = c + i < a.d ? xv[i] - mean : 0.f;
+        q = fmaf(xc, xc, q);
+        if (GRAD) c1 = fmaf(gv[i] * w[i], xc, c1);
+      }
+    });
+    norm_sum<0>(q, c1, parts.p[set][1]);
+    const float r = rsqrtf(q * inv + a.eps);
+    const float k0 = -r * c0, k1 = -(r * r) * r * (c1 * inv);
+    S* out = static_cast<S*>(a.out) + row * a.ldo;
+    norm_wide<E>(x, dy, a.d, [&](int c, const float (&xv)[V], const float (&gv)[V]) {
+      float w[V], o[V];
+      norm_weight<V>(a.w, a.w_bf16, c, a.d, w);
+      if constexpr (GRAD) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) o[i] = fmaf(xv[i] - mean, k1, fmaf(r * gv[i], w[i], k0));
+      } else {
+        float b[V];
+        norm_weight<V>(a.b, a.w_bf16, c, a.d, b);
+#pragma unroll
+        for (int i = 0; i < V; ++i) o[i] = fmaf((xv[i] - mean) * r, w[i], b[i]);
+      }
+      unit_store<E>(out + c, a.d - c, Vec16<E>::pack(o));
+    });
+    if (GRAD && threadIdx.x == 0) {
+      a.stats[2 * row] = mean;
+      a.stats[2 * row + 1] = r;
+    }
+  }
+}
+
+// Partial sums over rows by columns: a workgroup takes 256 units of a group's rows.
+template <class E>
+__global__ __launch_bounds__(256) void layer_norm_columns_kernel(NormArgs a, int blocks) {
+  using S = typename E::storage_t;
+  constexpr int V = E::kVec, F = 4;       // rows in flight
+  const int group = static_cast<int>(blockIdx.x) / blocks;
+  const int c = (static_cast<int>(blockIdx.x) % blocks * 256 + static_cast<int>(threadIdx.x)) * V;
+  if (c >= a.d) return;
+  const int64_t per = (a.rows + a.groups - 1) / a.groups;
+  const int64_t r0 = group * per, r1 = min(r0 + per, static_cast<int64_t>(a.rows));
+  float accw[V], accb[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) accw[i] = accb[i] = 0.f;
+  for (int64_t r = r0; r < r1; r += F) {
+    uint4 x[F], dy[F];
+#pragma unroll
+    for (int j = 0; j < F; ++j) {
+      const int64_t row = min(r + j, r1 - 1);
+      x[j] = unit_load<E>(static_cast<const S*>(a.x) + row * a.ldx + c, a.d - c);
+      dy[j] = unit_load<E>(static_cast<const S*>(a.dy) + row * a.ldy + c, a.d - c);
+    }
+#pragma unroll
+    for (int j = 0; j < F; ++j) {
+      if (r + j >= r1) break;
+      const float mean = a.stats[2 * (r + j)], rs = a.stats[2 * (r + j) + 1];
+      float xv[V], gv[V];
+      Vec16<E>::unpack(x[j], xv);
+      Vec16<E>::unpack(dy[j], gv);
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        accw[i] = fmaf(gv[i] * rs, xv[i] - mean, accw[i]);
+        accb[i] += gv[i];
+      }
+    }
+  }
+  float* pw = a.part + static_cast<size_t>(group) * (a.db ? 2 : 1) * a.d + c;
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+    if (c + i < a.d) {
+      pw[i] = accw[i];
+      if (a.db) pw[a.d + i] = accb[i];
+    }
+}
+
+// dw = beta dw + sum over the groups' partial sums: 64 columns of one of the two
+// per workgroup, kNormSlices waves each with its own contiguous part.
 constexpr int kNormSlices = 16;
 
 __global__ __launch_bounds__(64 * kNormSlices) void layer_norm_sum_kernel(NormArgs a) {

@@ -359,21 +359,37 @@ mfsdp_status_t exchange_impl(ExchangeMode mode, const void* x, int64_t ldx, cons
 // ---------------------------------------------------------------------------
 struct NormPlan {
   int upt, threads;     // units of 16 bytes per thread (0: read again), threads of a workgroup
-  int64_t groups;       // workgroups of the gradient
+  int lanes;            // of a wave per row, 0: a workgroup
+  bool full;            // the threads' units are exactly the row
+  int64_t groups;       // waves or workgroups that the rows are dealt to
 };
 
-NormPlan norm_plan(int64_t rows, int64_t d, bool bf) {
-  const int64_t units = ceil_div(d, bf ? 8 : 4);
-  NormPlan p{0, kNormThreadsMax, 0};
-  for (int upt : {1, 2, 4}) {
-    const int64_t threads = round_up(ceil_div(units, upt), 64);
-    if (threads <= (upt == 4 ? kNormThreadsMax : 256)) {
-      p.upt = upt;
-      p.threads = static_cast<int>(threads);
-      break;
-    }
+NormPlan norm_plan(int64_t rows, int64_t d, bool bf, bool grad) {
+  const int64_t v = bf ? 8 : 4, units = ceil_div(d, v);
+  NormPlan p{};
+  if (units <= 2 * 64) {
+    p.upt = units <= 64 ? 1 : 2;
+    p.lanes = units <= 8 ? 8 : units <= 16 ? 16 : units <= 32 ? 32 : 64;
+    p.threads = 256;
+  } else {
+    p.upt = units <= 2 * kNormThreadsMax ? 2 : units <= 4 * kNormThreadsMax ? 4 : 0;
+    p.threads = p.upt ? static_cast<int>(round_up(ceil_div(units, p.upt), 64)) : kNormThreadsMax;
   }
-  p.groups = std::min<int64_t>(rows, 512);
+  p.full = p.upt && d == (p.lanes ? p.lanes : p.threads) * p.upt * v;
+  // The gradient: as many workgroups per CU as make eight waves.  Fewer leave loads
+  // and additions uncovered, more add partial sums: 16384 x 5120 bf16 121, 98 and
+  // 115 us with one, two and three; 16384 x 4096 96, 72 and 73; 32768 x 2048 98, 72
+  // and 80 with two, four and eight; 4096 x 16384 82 and 97 with one and two.
+  // Wide rows: some thousand workgroups of 256 units of columns.
+  if (!p.upt) p.groups = std::max<int64_t>(16, 1024 / ceil_div(units, 256));
+  else if (p.lanes || !grad) p.groups = 2048;
+  else p.groups = 256 * ceil_div(8, p.threads / 64);
+  if (p.lanes) {    // waves, of eight rounds at least: 32768 x 128 bf16 15 us with 1024, 19 with 2048; 524288 x 128 113 and 84
+    const int64_t rounds = ceil_div(rows, 64 / p.lanes);
+    p.groups = std::min<int64_t>(grad ? ceil_div(rounds, 8) : rounds, p.groups);
+  } else {
+    p.groups = std::min(rows, p.groups);
+  }
   return p;
 }
 
@@ -384,18 +400,54 @@ mfsdp_status_t norm_sizes(int64_t rows, int64_t d, mfsdp_dtype_t dtype) {
   return MFSDP_OK;
 }
 
-size_t norm_part_bytes(int64_t rows, int64_t d, bool bf, bool bias) {
-  return static_cast<size_t>(norm_plan(rows, d, bf).groups) * (bias ? 2 : 1) * d * 4;
+size_t norm_part_bytes(const NormPlan& p, int64_t d, bool bias) {
+  return align_up(static_cast<size_t>(p.groups) * (bias ? 2 : 1) * d * 4, kWsAlign);
 }
 
-template <class F>
-hipError_t launch_norm(int upt, F&& f) {
-  switch (upt) {
-    case 1: return f(std::integral_constant<int, 1>{});
-    case 2: return f(std::integral_constant<int, 2>{});
-    case 4: return f(std::integral_constant<int, 4>{});
+size_t norm_workspace(const NormPlan& p, int64_t rows, int64_t d, bool bias) {
+  return norm_part_bytes(p, d, bias) + (p.upt ? 0 : static_cast<size_t>(rows) * 8);
+}
+
+template <class E, int UPT, int L, bool FULL>
+void launch_norm(const NormArgs& a, const NormPlan& p, bool grad, hipStream_t stream) {
+  const dim3 grid(static_cast<unsigned>(L ? ceil_div(p.groups, 4) : p.groups)), wg(static_cast<unsigned>(p.threads));
+  if (grad) layer_norm_grad_kernel<E, UPT, L, FULL><<<grid, wg, 0, stream>>>(a);
+  else layer_norm_kernel<E, UPT, L, FULL><<<grid, wg, 0, stream>>>(a);
+}
+
+template <class E>
+hipError_t launch_norm(const NormArgs& a, const NormPlan& p, bool grad, hipStream_t stream) {
+  if (p.upt == 0) {
+    // under 2^32 threads of a launch; a workgroup takes further rows in turn
+    const dim3 grid(static_cast<unsigned>(std::min<int64_t>(a.rows, int64_t(1) << 22))), wg(kNormThreadsMax);
+    hipError_t e = launch(MFSDP_KERNEL_LAYER_NORM, stream, [&] {
+      if (grad) layer_norm_wide_kernel<E, true><<<grid, wg, 0, stream>>>(a);
+      else layer_norm_wide_kernel<E, false><<<grid, wg, 0, stream>>>(a);
+    });
+    if (e != hipSuccess || !grad) return e;
+    const int blocks = static_cast<int>(ceil_div(a.d, 256 * E::kVec));
+    const dim3 columns(static_cast<unsigned>(p.groups * blocks));
+    return launch(MFSDP_KERNEL_LAYER_NORM, stream,
+                  [&] { layer_norm_columns_kernel<E><<<columns, dim3(256), 0, stream>>>(a, blocks); });
   }
-  return f(std::integral_constant<int, 0>{});
+  return launch(MFSDP_KERNEL_LAYER_NORM, stream, [&] {
+    auto go = [&](auto upt, auto lanes) {
+      constexpr int UPT = decltype(upt)::value, L = decltype(lanes)::value;
+      if (p.full) launch_norm<E, UPT, L, true>(a, p, grad, stream);
+      else launch_norm<E, UPT, L, false>(a, p, grad, stream);
+    };
+    using std::integral_constant;
+    const integral_constant<int, 0> all;
+    const integral_constant<int, 1> one;
+    const integral_constant<int, 2> two;
+    switch (p.lanes) {
+      case 0: p.upt == 2 ? go(two, all) : go(integral_constant<int, 4>{}, all); break;
+      case 8: go(one, integral_constant<int, 8>{}); break;
+      case 16: go(one, integral_constant<int, 16>{}); break;
+      case 32: go(one, integral_constant<int, 32>{}); break;
+      default: p.upt == 1 ? go(one, integral_constant<int, 64>{}) : go(two, integral_constant<int, 64>{});
+    }
+  });
 }
 
 // grad: dy is given, out is dx.
@@ -418,8 +470,8 @@ mfsdp_status_t norm_impl(bool grad, const void* dy, int64_t ldy, const void* x, 
       !aligned(dweight, 4) || !aligned(dbias, 4))
     return misaligned();
   const bool bf = dtype == MFSDP_DTYPE_BF16;
-  const NormPlan p = norm_plan(rows, d, bf);
-  const size_t need = grad ? norm_part_bytes(rows, d, bf, dbias != nullptr) : 0;
+  const NormPlan p = norm_plan(rows, d, bf, grad);
+  const size_t need = grad ? norm_workspace(p, rows, d, dbias != nullptr) : 0;
   st = check_workspace(workspace, workspace_bytes, need);
   if (st != MFSDP_OK) return st;
   Buffers b;
@@ -443,6 +495,7 @@ mfsdp_status_t norm_impl(bool grad, const void* dy, int64_t ldy, const void* x, 
   a.b = bias;
   a.out = out;
   a.part = static_cast<float*>(workspace);
+  a.stats = a.part ? a.part + norm_part_bytes(p, d, dbias != nullptr) / 4 : nullptr;
   a.dw = dweight;
   a.db = dbias;
   a.ldx = ldx;
@@ -455,25 +508,8 @@ mfsdp_status_t norm_impl(bool grad, const void* dy, int64_t ldy, const void* x, 
   a.groups = static_cast<int32_t>(p.groups);
   a.eps = eps;
   a.beta = beta;
-  const dim3 wg(static_cast<unsigned>(p.threads));
   hipError_t e = hipSuccess;
-  if (rows > 0) {
-    // under 2^32 threads of a launch; a workgroup takes further rows in turn
-    const int64_t blocks = grad ? p.groups : std::min<int64_t>(rows, int64_t(1) << 22);
-    const dim3 grid(static_cast<unsigned>(blocks));
-    e = launch_norm(p.upt, [&](auto upt) {
-      constexpr int UPT = decltype(upt)::value;
-      return launch(MFSDP_KERNEL_LAYER_NORM, stream, [&] {
-        if (grad) {
-          if (bf) layer_norm_grad_kernel<ElemBF16, UPT><<<grid, wg, 0, stream>>>(a);
-          else layer_norm_grad_kernel<ElemF32, UPT><<<grid, wg, 0, stream>>>(a);
-        } else {
-          if (bf) layer_norm_kernel<ElemBF16, UPT><<<grid, wg, 0, stream>>>(a);
-          else layer_norm_kernel<ElemF32, UPT><<<grid, wg, 0, stream>>>(a);
-        }
-      });
-    });
-  }
+  if (rows > 0) e = bf ? launch_norm<ElemBF16>(a, p, grad, stream) : launch_norm<ElemF32>(a, p, grad, stream);
   if (grad && e == hipSuccess) {
     const dim3 grid(static_cast<unsigned>(ceil_div(d, 64) * (dbias ? 2 : 1)));
     e = launch(MFSDP_KERNEL_LAYER_NORM, stream, [&] { layer_norm_sum_kernel<<<grid, dim3(64 * kNormSlices), 0, stream>>>(a); });
@@ -751,7 +787,7 @@ mfsdp_status_t mfsdp_layer_norm_grad_workspace_size(int64_t rows, int64_t d, mfs
     g_last_error.clear();
     if (!out_bytes) return fail(MFSDP_ERR_INVALID_ARGUMENT, "out_bytes is null");
     const mfsdp_status_t st = norm_sizes(rows, d, dtype);
-    if (st == MFSDP_OK) *out_bytes = norm_part_bytes(rows, d, dtype == MFSDP_DTYPE_BF16, with_bias != 0);
+    if (st == MFSDP_OK) *out_bytes = rows ? norm_workspace(norm_plan(rows, d, dtype == MFSDP_DTYPE_BF16, true), rows, d, with_bias != 0) : 0;
     return st;
   });
 }

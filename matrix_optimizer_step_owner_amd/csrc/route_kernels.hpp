@@ -57,41 +57,6 @@ __device__ __forceinline__ double route_value(uint64_t k) {
   return __longlong_as_double(static_cast<int64_t>(k >> 63 ? k ^ (1ull << 63) : ~k));
 }
 
-// Largest value in the wave, on every lane (as a scalar).
-template <int CTRL, int ROWS>
-__device__ __forceinline__ uint32_t dpp_or0(uint32_t v) {
-  return static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), CTRL, ROWS, 0xf, false));
-}
-__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
-  v = max(v, dpp_or0<0x111, 0xf>(v));   // row_shr:1, :2, :4, :8
-  v = max(v, dpp_or0<0x112, 0xf>(v));
-  v = max(v, dpp_or0<0x114, 0xf>(v));
-  v = max(v, dpp_or0<0x118, 0xf>(v));
-  v = max(v, dpp_or0<0x142, 0xa>(v));   // row_bcast:15, :31
-  v = max(v, dpp_or0<0x143, 0xc>(v));
-  return static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(v), 63));
-}
-__device__ __forceinline__ uint64_t wave_max(uint64_t v) {
-  const uint32_t hi = wave_max(static_cast<uint32_t>(v >> 32));
-  const uint32_t lo = wave_max(static_cast<uint32_t>(v >> 32) == hi ? static_cast<uint32_t>(v) : 0u);
-  return static_cast<uint64_t>(hi) << 32 | lo;
-}
-
-// Sum over the wave, on every lane, by the same steps.
-__device__ __forceinline__ float wave_sum(float v) {
-  auto step = [&](uint32_t w) { v += __uint_as_float(w); };
-  step(dpp_or0<0x111, 0xf>(__float_as_uint(v)));
-  step(dpp_or0<0x112, 0xf>(__float_as_uint(v)));
-  step(dpp_or0<0x114, 0xf>(__float_as_uint(v)));
-  step(dpp_or0<0x118, 0xf>(__float_as_uint(v)));
-  step(dpp_or0<0x142, 0xa>(__float_as_uint(v)));
-  step(dpp_or0<0x143, 0xc>(__float_as_uint(v)));
-  return __uint_as_float(static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(__float_as_uint(v)), 63)));
-}
-
-// The next lane's value (lane 63: 0).
-__device__ __forceinline__ float wave_next(float v) { return __uint_as_float(dpp_or0<0x130, 0xf>(__float_as_uint(v))); }
-
 // PER elements from p + lane * PER on, those before n; others as `fill`.
 template <class E, int PER>
 __device__ __forceinline__ void route_load(const typename E::storage_t* p, int first, int n, float fill,
@@ -249,43 +214,47 @@ __device__ __forceinline__ uint32_t route_groups(const RouteArgs& a, const K (&v
       close = !(in - out > 2.f * route_doubt(most, fabsf(in) + fabsf(out)));
     }
   }
+  if (a.lanes > 0) return stays ? 0xffffffffu : 0u;
   const uint64_t bits = __ballot(stays);
   uint32_t mask = 0;
 #pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    const int at = a.lanes > 0 ? lane : (first + i) / a.group_size;
-    mask |= static_cast<uint32_t>(bits >> (at & 63) & 1) << i;
-  }
+  for (int i = 0; i < PER; ++i)
+    mask |= first + i < a.n ? static_cast<uint32_t>(bits >> ((first + i) / a.group_size) & 1) << i : 0u;
   return mask;
 }
 
 // The k largest keys in order, lane j receiving expert j (others -1).  Lists of up
-// to four are sorted first (exchanges of neighbours, which keep equal keys in
-// order, with their places as the digits of one word): a round then needs
-// neither the largest of a lane's own nor a search for it, and the winner's list
-// moves up by one.  (Lists of eight lose by it: 32768 x 512, k = 10, 64 and 42 us.)  On return key[0] is the largest that a lane has left.
+// to four are sorted first, with their places, by rank, as the digits of one word
+// (of equal keys the lower place is first): a round then needs neither the
+// largest of a lane's own nor a search for it, and the winner's list moves up by
+// one.  (Lists of eight lose by it: 32768 x 512, k = 10, 64 and 42 us.)  On return
+// key[0] is the largest that a lane has left.
 template <int PER, class K>
 __device__ __forceinline__ int route_pick(K (&key)[PER], int k, int lane) {
   int mine = -1;
   if constexpr (PER <= 4) {
-    uint32_t place[PER];
+    int rank[PER];
 #pragma unroll
-    for (int i = 0; i < PER; ++i) place[i] = i;
+    for (int i = 0; i < PER; ++i) rank[i] = i;
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+#pragma unroll
+      for (int q = i + 1; q < PER; ++q) {
+        const int after = key[i] < key[q] ? 1 : 0;
+        rank[i] += after;
+        rank[q] -= after;
+      }
+    uint32_t digits = 0;
+#pragma unroll
+    for (int i = 1; i < PER; ++i) digits |= static_cast<uint32_t>(i) << (4 * rank[i]);
 #pragma unroll
     for (int end = PER - 1; end > 0; --end)
 #pragma unroll
       for (int i = 0; i < end; ++i) {
-        const bool swap = key[i] < key[i + 1];
-        const K hi = swap ? key[i + 1] : key[i], lo = swap ? key[i] : key[i + 1];
-        const uint32_t ph = swap ? place[i + 1] : place[i], pl = swap ? place[i] : place[i + 1];
+        const K hi = max(key[i], key[i + 1]);
+        key[i + 1] = min(key[i], key[i + 1]);
         key[i] = hi;
-        key[i + 1] = lo;
-        place[i] = ph;
-        place[i + 1] = pl;
       }
-    uint32_t digits = 0;
-#pragma unroll
-    for (int i = 0; i < PER; ++i) digits |= place[i] << (4 * i);
     for (int j = 0; j < k; ++j) {
       const K m = wave_max(key[0]);
       const int owner = __builtin_ctzll(__ballot(key[0] == m));
