@@ -324,6 +324,8 @@ mfsdp_status_t exchange_impl(ExchangeMode mode, const void* x, int64_t ldx, cons
   a.tpt = 64;
   while (a.tpt < 256 && a.tpt * (grad ? 2 : 1) < units) a.tpt *= 2;
   a.chunks = grad ? 1 : static_cast<int32_t>(ceil_div(units, a.tpt));
+  // more than the 256 MB of the last-level cache
+  const bool streamed_rows = std::min(rows, tokens * k) * d * static_cast<int64_t>(es) > (int64_t(1) << 28);
   const int64_t per = 256 / a.tpt, most = kBlocksMax / a.chunks * per;    // tokens of one launch
   hipError_t e = hipSuccess;
   for (int64_t t0 = 0; t0 < tokens && e == hipSuccess; t0 += most) {
@@ -337,18 +339,17 @@ mfsdp_status_t exchange_impl(ExchangeMode mode, const void* x, int64_t ldx, cons
     a.dw = dw ? dw + slot : nullptr;
     a.tokens = static_cast<int32_t>(std::min(most, tokens - t0));
     const dim3 grid(static_cast<unsigned>(ceil_div(a.tokens, per) * a.chunks)), wg(256);
-    const bool bf = dtype == MFSDP_DTYPE_BF16;
     e = launch(MFSDP_KERNEL_EXCHANGE, stream, [&] {
-      if (mode == kDispatch) {
-        if (bf) dispatch_kernel<ElemBF16><<<grid, wg, 0, stream>>>(a);
-        else dispatch_kernel<ElemF32><<<grid, wg, 0, stream>>>(a);
-      } else if (mode == kCombine) {
-        if (bf) combine_kernel<ElemBF16><<<grid, wg, 0, stream>>>(a);
-        else combine_kernel<ElemF32><<<grid, wg, 0, stream>>>(a);
-      } else {
-        if (bf) combine_grad_kernel<ElemBF16><<<grid, wg, 0, stream>>>(a);
-        else combine_grad_kernel<ElemF32><<<grid, wg, 0, stream>>>(a);
-      }
+      auto go = [&](auto elem, auto streamed) {
+        using E = decltype(elem);
+        constexpr bool STREAM = decltype(streamed)::value;
+        if (mode == kDispatch) dispatch_kernel<E><<<grid, wg, 0, stream>>>(a);
+        else if (mode == kCombine) combine_kernel<E, STREAM><<<grid, wg, 0, stream>>>(a);
+        else combine_grad_kernel<E, STREAM><<<grid, wg, 0, stream>>>(a);
+      };
+      auto type = [&](auto streamed) { dtype == MFSDP_DTYPE_BF16 ? go(ElemBF16{}, streamed) : go(ElemF32{}, streamed); };
+      if (mode != kDispatch && streamed_rows) type(std::integral_constant<bool, true>{});
+      else type(std::integral_constant<bool, false>{});
     });
   }
   return launched(e, "exchange");

@@ -264,6 +264,21 @@ __device__ __forceinline__ void lds_dma1_buf(uint32_t lds, uint32_t voff, u32x4s
                :: "s"(ulds), "v"(voff), "s"(buf) : "memory", "m0");
 }
 
+// group_find with an expert's row tiles in bands of equal height, five to eleven: a
+// last band of one or two rows would read all of a matrix for a few tiles, and at
+// this rate waits for it (eight 14336 x 4096 experts with about 2048 rows each).
+__device__ __forceinline__ bool scaled_find(const GroupArgs& g, int b, int bp, int nq, int& expert, int& ti, int& tj) {
+  GroupSpan s;
+  if (!group_span(g, b, bp, nq, s)) return false;
+  expert = s.expert;
+  const int bands = max(1, (s.rows + kGroupBand / 2) / kGroupBand), height = (s.rows + bands - 1) / bands;
+  const int band = s.local / (height * nq), r = s.local - band * (height * nq);
+  const int in_band = min(height, s.rows - band * height);
+  ti = band * height + r % in_band;
+  tj = r / in_band;
+  return true;
+}
+
 template <class C>
 __global__ __launch_bounds__(C::THREADS, C::OCC) void scaled_tile_kernel(ScaledArgs a) {
   constexpr int TP = C::TP, TQ = C::TQ, ROW = C::ROW, U = C::U;
@@ -279,8 +294,7 @@ __global__ __launch_bounds__(C::THREADS, C::OCC) void scaled_tile_kernel(ScaledA
   const int lrow = lane & 31, lhalf = lane >> 5;
 
   int e, ti, tj, lo, hi;
-  bool alone;
-  if (!group_find(g, blockIdx.x, C::BP, (g.n + C::BQ - 1) / C::BQ, e, ti, tj, alone)) return;
+  if (!scaled_find(g, blockIdx.x, C::BP, (g.n + C::BQ - 1) / C::BQ, e, ti, tj)) return;
   group_segment(g, e, lo, hi);
   const int p0 = ti * C::BP, q0 = tj * C::BQ;
   const int prem = hi - lo - p0, qrem = g.n - q0;
