@@ -38,6 +38,7 @@ EXPORTED = ("mfsdp_muon_workspace_size", "mfsdp_muon_step", "mfsdp_muon_step_noa
             "mfsdp_route_combine", "mfsdp_route_combine_grad",
             "mfsdp_layer_norm", "mfsdp_layer_norm_grad_workspace_size", "mfsdp_layer_norm_grad",
             "mfsdp_scaled_quantize", "mfsdp_scaled_quantize_weight", "mfsdp_scaled_linear",
+            "mfsdp_scaled_linear_tile",
             "mfsdp_status_string", "mfsdp_last_error",
             "mfsdp_timing_enable", "mfsdp_timing_reset", "mfsdp_timing_read",
             "mfsdp_mfma_probe")
@@ -190,6 +191,7 @@ def load() -> ctypes.CDLL:
                 "mfsdp_scaled_quantize": [ptr, i64, i64, i64, i32, ptr, ptr, ptr],
                 "mfsdp_scaled_quantize_weight": [ptr, i64, i64, i64, i32, ptr, ptr, ptr, ptr,
                                                  ptr],
+                "mfsdp_scaled_linear_tile": [i64, i64, i64, i64, c.POINTER(MfsdpGroupedTile)],
                 "mfsdp_scaled_linear": [ptr, ptr, ptr, ptr, ptr, i64, i64, i64, i64, ptr, i64,
                                         ptr]}.items():
             getattr(lib, name).argtypes = args

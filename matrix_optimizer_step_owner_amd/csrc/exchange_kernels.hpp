@@ -28,7 +28,7 @@ struct ExchangeArgs {
   float* dw;              // gradient: tokens x k
   int64_t ldx, ldy, ldo;
   int32_t tokens, rows, k, d;
-  int32_t tpt;            // threads per token: 64, 128 or 256
+  int32_t tpt;            // threads per token, up to 256; in the gradient 64, 128 or 256
   int32_t chunks;         // workgroups per token (dispatch, combine)
   float beta;
 };
@@ -79,7 +79,7 @@ struct ExchangeUnit {
   __device__ __forceinline__ explicit ExchangeUnit(const ExchangeArgs& a) {
     const int per = 256 / a.tpt;
     const int64_t b = blockIdx.x / a.chunks;
-    t = b * per + threadIdx.x / a.tpt;
+    t = static_cast<int>(threadIdx.x) < per * a.tpt ? b * per + threadIdx.x / a.tpt : a.tokens;   // none
     u = static_cast<int>(blockIdx.x % a.chunks) * a.tpt + static_cast<int>(threadIdx.x % a.tpt);
     step = a.chunks * a.tpt;
   }

@@ -321,11 +321,17 @@ mfsdp_status_t exchange_impl(ExchangeMode mode, const void* x, int64_t ldx, cons
   a.d = static_cast<int32_t>(d);
   a.beta = beta;
   const int64_t units = ceil_div(d, 16 / static_cast<int64_t>(es));
-  a.tpt = 64;
-  while (a.tpt < 256 && a.tpt * (grad ? 2 : 1) < units) a.tpt *= 2;
-  a.chunks = grad ? 1 : static_cast<int32_t>(ceil_div(units, a.tpt));
-  // more than the 256 MB of the last-level cache
-  const bool streamed_rows = std::min(rows, tokens * k) * d * static_cast<int64_t>(es) > (int64_t(1) << 28);
+  if (grad) {     // whole waves
+    a.chunks = 1;
+    a.tpt = 64;
+    while (a.tpt < 256 && a.tpt * 2 < units) a.tpt *= 2;
+  } else {
+    a.chunks = static_cast<int32_t>(ceil_div(units, 256));
+    a.tpt = static_cast<int32_t>(ceil_div(units, a.chunks));
+  }
+  // more than the 256 MB of the last-level cache, and lines that rows do not share
+  const bool streamed_rows = std::min(rows, tokens * k) * d * static_cast<int64_t>(es) > (int64_t(1) << 28) &&
+                             aligned(x, 64) && ldx * es % 64 == 0;
   const int64_t per = 256 / a.tpt, most = kBlocksMax / a.chunks * per;    // tokens of one launch
   hipError_t e = hipSuccess;
   for (int64_t t0 = 0; t0 < tokens && e == hipSuccess; t0 += most) {
@@ -649,6 +655,16 @@ ScaledKernel scaled_kernel(int64_t experts, int64_t rows, int64_t n, int64_t k) 
   return kScaledLarge;
 }
 
+GroupShape scaled_shape(ScaledKernel u) {
+  switch (u) {
+    case kScaledLarge: return shape_of<ScaledLarge>(true);
+    case kScaledPair: return shape_of<ScaledPair>(true);
+    case kScaledRows: return shape_of<ScaledRows>(true);
+    case kScaledFew: break;
+  }
+  return shape_of<ScaledFew>(true);
+}
+
 mfsdp_status_t scaled_linear_impl(const uint8_t* codes, const uint8_t* scales, const uint8_t* wcodes,
                                   const uint8_t* wscales, const int32_t* offsets, int64_t experts, int64_t rows,
                                   int64_t n, int64_t k, void* y, int64_t ldy, hipStream_t stream) {
@@ -662,6 +678,10 @@ mfsdp_status_t scaled_linear_impl(const uint8_t* codes, const uint8_t* scales, c
   if (!aligned(y, 2) || !aligned(offsets, 4)) return misaligned();
   if (!aligned(codes, 16) || !aligned(wcodes, 16)) return fail(MFSDP_ERR_INVALID_ARGUMENT, "codes must be 16-byte aligned");
   const int64_t nb = ceil_div(n, kScaledBlock), kb = ceil_div(k, kScaledBlock), depth = kb * kScaledBlock;
+  const ScaledKernel use = scaled_kernel(experts, rows, n, depth);
+  const GroupShape shape = scaled_shape(use);
+  if (group_tiles_max(rows, experts, shape.rows) * ceil_div(n, shape.cols) > kGroupBlocksMax)
+    return fail(MFSDP_ERR_UNSUPPORTED, "too many tiles");
   Buffers b;
   b.rows(y, rows, n, ldy, 2, "y");
   b.outputs_end();
@@ -689,7 +709,7 @@ mfsdp_status_t scaled_linear_impl(const uint8_t* codes, const uint8_t* scales, c
   a.nb = static_cast<int32_t>(nb);
   a.g.stream = aligned(y, 128) && ldy * 2 % 128 == 0;
   hipError_t e = hipErrorInvalidValue;
-  switch (scaled_kernel(experts, rows, n, depth)) {
+  switch (use) {
     case kScaledLarge: e = launch_scaled<ScaledLarge>(a, stream); break;
     case kScaledPair: e = launch_scaled<ScaledPair>(a, stream); break;
     case kScaledRows: e = launch_scaled<ScaledRows>(a, stream); break;
@@ -822,6 +842,26 @@ mfsdp_status_t mfsdp_scaled_linear(const uint8_t* codes, const uint8_t* scales, 
   return guarded([&] {
     return scaled_linear_impl(codes, scales, weight_codes, weight_scales, offsets, n_experts, rows, n, k, y,
                               ld_y, stream);
+  });
+}
+
+mfsdp_status_t mfsdp_scaled_linear_tile(int64_t n_experts, int64_t rows, int64_t n, int64_t k,
+                                        mfsdp_grouped_tile_t* out) {
+  return guarded([&]() -> mfsdp_status_t {
+    g_last_error.clear();
+    if (!out) return fail(MFSDP_ERR_INVALID_ARGUMENT, "out is null");
+    const mfsdp_status_t st = grouped_sizes(n_experts, rows, n, k, MFSDP_DTYPE_BF16);
+    if (st != MFSDP_OK) return st;
+    *out = mfsdp_grouped_tile_t{};
+    if (n_experts == 0 || rows == 0) return MFSDP_OK;   // no launch
+    const GroupShape s = scaled_shape(scaled_kernel(n_experts, rows, n, round_up(k, kScaledBlock)));
+    out->rows = s.rows;
+    out->cols = s.cols;
+    out->threads = s.threads;
+    out->wave_sets = s.wave_sets;
+    out->lds_dma = 1;
+    out->workgroups = group_tiles_max(rows, n_experts, s.rows) * ceil_div(n, s.cols);
+    return MFSDP_OK;
   });
 }
 
