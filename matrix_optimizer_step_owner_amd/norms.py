@@ -12,6 +12,7 @@ matrices, norm gains among them, are packed for AdamW).
 from __future__ import annotations
 
 import ctypes
+import functools
 from typing import Optional
 
 import torch
@@ -51,6 +52,14 @@ def layer_norm(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tenso
     return out
 
 
+@functools.lru_cache(maxsize=256)
+def _grad_bytes(rows: int, d: int, dtype: int, with_bias: bool) -> int:
+    need = ctypes.c_size_t(0)
+    _lib.check(_lib.load().mfsdp_layer_norm_grad_workspace_size(rows, d, dtype, with_bias,
+                                                                ctypes.byref(need)))
+    return need.value
+
+
 def layer_norm_grad(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor,
                     dweight: torch.Tensor, dbias: Optional[torch.Tensor] = None, *,
                     eps: float = 1e-5, centered: bool = True, beta: float = 0.0,
@@ -83,10 +92,8 @@ def layer_norm_grad(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor,
         _check(out, "out", device, (x.dtype,), 2)
         ldo = _rows(out, "out", (rows, d))
     dtype = _DTYPES[x.dtype]
-    need = ctypes.c_size_t(0)
-    _lib.check(_lib.load().mfsdp_layer_norm_grad_workspace_size(rows, d, dtype, db is not None,
-                                                                ctypes.byref(need)))
-    ws = None if need.value == 0 and workspace is None else _scratch(device, need.value, workspace)
+    need = _grad_bytes(rows, d, dtype, db is not None)
+    ws = None if need == 0 and workspace is None else _scratch(device, need, workspace)
     _call(device, "mfsdp_layer_norm_grad", dy.data_ptr(), ldy, x.data_ptr(), _rows(x, "x"), w,
           _DTYPES[weight.dtype], rows, d, dtype, centered, eps, beta, out.data_ptr(), ldo, dw, db,
           *_span(ws))

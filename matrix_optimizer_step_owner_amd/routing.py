@@ -22,6 +22,7 @@ calls of their own.
 from __future__ import annotations
 
 import ctypes
+import functools
 from typing import NamedTuple, Optional, Tuple
 
 import torch
@@ -117,6 +118,13 @@ def route_grad(dweights: torch.Tensor, logits: torch.Tensor, experts: torch.Tens
     return out
 
 
+@functools.lru_cache(maxsize=256)
+def _plan_bytes(tokens: int, k: int, n_experts: int) -> int:
+    need = ctypes.c_size_t(0)
+    _lib.check(_lib.load().mfsdp_route_plan_workspace_size(tokens, k, n_experts, ctypes.byref(need)))
+    return need.value
+
+
 def route_plan(experts: torch.Tensor, n_experts: int, *, offsets: Optional[torch.Tensor] = None,
                place: Optional[torch.Tensor] = None,
                workspace: Optional[torch.Tensor] = None) -> RoutePlan:
@@ -139,9 +147,8 @@ def route_plan(experts: torch.Tensor, n_experts: int, *, offsets: Optional[torch
         place = experts.new_empty((tokens, k))
     else:
         _whole(place, "place", device, _I32, (tokens, k))
-    need = ctypes.c_size_t(0)
-    _lib.check(_lib.load().mfsdp_route_plan_workspace_size(tokens, k, n_experts, ctypes.byref(need)))
-    ws = None if need.value == 0 and workspace is None else _scratch(device, need.value, workspace)
+    need = _plan_bytes(tokens, k, n_experts)
+    ws = None if need == 0 and workspace is None else _scratch(device, need, workspace)
     _call(device, "mfsdp_route_plan", experts.data_ptr(), tokens, k, n_experts, offsets.data_ptr(),
           place.data_ptr(), *_span(ws))
     return RoutePlan(offsets, place)
