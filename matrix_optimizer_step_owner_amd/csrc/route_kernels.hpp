@@ -192,26 +192,29 @@ __device__ __forceinline__ uint32_t route_groups(const RouteArgs& a, const K (&v
     }
     step = 1;
   }
-  const K key = route_key(mine);
   // how many groups are before a lane's own (and where it has none, before none)
+  const K key = route_key(mine);
   const int own = lane / step;
+  const bool group = lane < a.groups * step;
   int rank = 0;
-  for (int g = 0; g < a.groups; ++g) {
-    const int at = g * step;
-    K other;
-    if constexpr (sizeof(K) == 8)
-      other = static_cast<uint64_t>(static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(key >> 32), at))) << 32 |
-              static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(key), at));
-    else
-      other = static_cast<K>(__builtin_amdgcn_readlane(static_cast<int>(key), at));
-    rank += other > key || (other == key && g < own) ? 1 : 0;
-  }
-  const bool group = lane < a.groups * step, stays = group && rank < a.top;
-  if constexpr (sizeof(K) == 4) {
+  bool stays;
+  if constexpr (sizeof(K) == 8) {
+    for (int g = 0; g < a.groups; ++g) {
+      const int at = g * step;
+      const K other = static_cast<uint64_t>(static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(key >> 32), at))) << 32 |
+                      static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(key), at));
+      rank += other > key || (other == key && g < own) ? 1 : 0;
+    }
+    stays = group && rank < a.top;
+  } else {
+    // equal sums at the border show as too many that stay: fp64 then
+    for (int g = 0, at = 0; g < a.groups; ++g, at += step)
+      rank += static_cast<K>(__builtin_amdgcn_readlane(static_cast<int>(key), at)) > key ? 1 : 0;
+    stays = group && rank < a.top;
     if (a.top < a.groups) {
       const float out = route_value(wave_max(group && !stays ? key : 0u));
       const float in = route_value(~wave_max(stays ? ~key : 0u));
-      close = !(in - out > 2.f * route_doubt(most, fabsf(in) + fabsf(out)));
+      close = !(in - out > 2.f * route_doubt(most, fabsf(in) + fabsf(out))) || __popcll(__ballot(stays)) != a.top * step;
     }
   }
   if (a.lanes > 0) return stays ? 0xffffffffu : 0u;
@@ -640,17 +643,18 @@ __global__ __launch_bounds__(kPlanThreads) void plan_place_kernel(PlanArgs a) {
     __syncthreads();
     const int wide = (a.experts + 63) & ~63, slices = kPlanThreads / wide;
     const int b = threadIdx.x % wide, blocks = static_cast<int>(gridDim.x), here = static_cast<int>(blockIdx.x);
-    if (b < a.experts && static_cast<int>(threadIdx.x) < slices * wide) {
+    const int slice = __builtin_amdgcn_readfirstlane(threadIdx.x / wide);     // whole waves: addresses and ends are scalars
+    if (b < a.experts && slice < slices) {
       uint32_t t = 0, before = 0;
-      for (int w = threadIdx.x / wide; w < blocks; w += 16 * slices) {
+      for (int w = slice; w < blocks; w += 16 * slices) {
         uint32_t c[16];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) c[i] = a.hist[static_cast<size_t>(min(w + i * slices, blocks - 1)) * a.experts + b];
+        for (int i = 0; i < 16; ++i) c[i] = (a.hist + static_cast<size_t>(min(w + i * slices, blocks - 1)) * a.experts)[b];
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           const int at = w + i * slices;
-          t += at < blocks ? c[i] : 0;
-          before += at < here ? c[i] : 0;
+          if (at < blocks) t += c[i];
+          if (at < here) before += c[i];
         }
       }
       atomicAdd(&tot[b], t);
