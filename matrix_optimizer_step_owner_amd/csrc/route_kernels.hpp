@@ -518,8 +518,9 @@ struct PlanArgs {
   const int32_t* chosen;   // n slots; outside [0, experts): no row
   int32_t* offsets;        // experts + 1
   int32_t* place;          // n
-  uint32_t* hist;          // [blocks][experts]
+  uint32_t* hist;          // [blocks][pitch]: counts of each expert
   int32_t n, experts;
+  int32_t pitch;           // experts, a multiple of four
   int32_t bits;            // of an expert's number
   int32_t per_block;       // slots per workgroup, a multiple of kPlanThreads
 };
@@ -540,7 +541,7 @@ __global__ __launch_bounds__(kPlanThreads) void plan_hist_kernel(PlanArgs a) {
   }
   __syncthreads();
   for (int b = threadIdx.x; b < a.experts; b += kPlanThreads)
-    a.hist[static_cast<size_t>(blockIdx.x) * a.experts + b] = h[b];
+    a.hist[static_cast<size_t>(blockIdx.x) * a.pitch + b] = h[b];
 }
 
 // Rows of this workgroup's slots.  base: first row of each expert's slots here.
@@ -637,28 +638,36 @@ __global__ __launch_bounds__(kPlanThreads) void plan_place_kernel(PlanArgs a) {
       if (e != 0xffffffffu) atomicAdd(&tot[e], 1u);
     }
   } else {
-    // every workgroup adds up all counts: as many threads per expert as there
-    // are, sixteen loads of each in flight
+    // every workgroup adds up all counts: four experts a thread, as many threads per
+    // four as there are, eight loads of each in flight
     for (int b = threadIdx.x; b < a.experts; b += kPlanThreads) tot[b] = add[b] = 0;
     __syncthreads();
-    const int wide = (a.experts + 63) & ~63, slices = kPlanThreads / wide;
-    const int b = threadIdx.x % wide, blocks = static_cast<int>(gridDim.x), here = static_cast<int>(blockIdx.x);
+    const int wide = (a.pitch / 4 + 63) & ~63, slices = kPlanThreads / wide;
+    const int b = threadIdx.x % wide * 4, blocks = static_cast<int>(gridDim.x), here = static_cast<int>(blockIdx.x);
     const int slice = __builtin_amdgcn_readfirstlane(threadIdx.x / wide);     // whole waves: addresses and ends are scalars
     if (b < a.experts && slice < slices) {
-      uint32_t t = 0, before = 0;
-      for (int w = slice; w < blocks; w += 16 * slices) {
-        uint32_t c[16];
+      uint32_t t[4] = {}, before[4] = {};
+      for (int w = slice; w < blocks; w += 8 * slices) {
+        uint4 c[8];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) c[i] = (a.hist + static_cast<size_t>(min(w + i * slices, blocks - 1)) * a.experts)[b];
+        for (int i = 0; i < 8; ++i) c[i] = gld<uint4>(a.hist + static_cast<size_t>(min(w + i * slices, blocks - 1)) * a.pitch + b);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
+        for (int i = 0; i < 8; ++i) {
           const int at = w + i * slices;
-          if (at < blocks) t += c[i];
-          if (at < here) before += c[i];
+          const uint32_t v[4] = {c[i].x, c[i].y, c[i].z, c[i].w};
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            if (at < blocks) t[q] += v[q];
+            if (at < here) before[q] += v[q];
+          }
         }
       }
-      atomicAdd(&tot[b], t);
-      atomicAdd(&add[b], before);
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if (b + q < a.experts) {
+          atomicAdd(&tot[b + q], t[q]);
+          atomicAdd(&add[b + q], before[q]);
+        }
     }
   }
   __syncthreads();
