@@ -32,7 +32,7 @@ def layer_norm(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tenso
                out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """``(x - mean) / sqrt(variance + eps) * weight + bias`` of each row, in fp32
     and rounded once; not ``centered`` it divides by the root mean square
-    (mfsdp_layer_norm).
+    (mfsdp_layer_norm).  The sum of a row's squares has to be an fp32 number.
 
     x: (rows, d) bf16 or fp32, rows contiguous at any stride; weight, bias: (d,)
     of one dtype, fp32 (segments of a packed tail) or bf16."""

@@ -145,7 +145,7 @@ def test_route_gradient_against_differences(kind, renormalize):
     assert abs(slope - float((grad * h).sum())) <= size * (10 * 20 * 64 * t * t + 1e-15 / t + 400 * ref.U * 20)
 
 
-@pytest.mark.parametrize("tokens,k,n", [(0, 1, 4), (1, 1, 1), (3, 2, 5), (64, 1, 64), (65, 3, 7), (1000, 8, 256), (1024, 8, 256), (1025, 8, 256), (2000, 6, 60),
+@pytest.mark.parametrize("tokens,k,n", [(0, 1, 4), (1, 1, 1), (3, 2, 5), (64, 1, 64), (65, 3, 7), (768, 8, 256), (769, 8, 256), (1000, 8, 256), (1024, 8, 256), (1025, 8, 256), (2000, 6, 60),
                                         (5000, 8, 1024), (40000, 8, 33), (9000, 1, 1), (300000, 2, 128), (700, 32, 40)])
 @pytest.mark.parametrize("kind", ["even", "one", "none", "wild"])
 def test_plan(tokens, k, n, kind):
@@ -339,6 +339,20 @@ def test_norm_of_constant_and_large_rows():
     x[1, 5], x[2, 7] = NAN, INF
     y = mf.layer_norm(x.to(DEV), torch.ones(64, device=DEV))
     assert torch.isfinite(y[0]).all() and torch.isnan(y[1]).all() and torch.isnan(y[2, 7])
+
+
+@pytest.mark.parametrize("centered", [True, False])
+@pytest.mark.parametrize("d", [40, 3000, 9000])     # lanes, a workgroup, rows that are read again
+@pytest.mark.parametrize("power", [-45, 45])
+def test_norm_of_tiny_and_huge_rows(power, d, centered):
+    # without eps, a row's size leaves the result; its cube is outside fp32's range
+    x, dy, w = (rand((3, d), F32, 1).double() * 2.0 ** power).float(), rand((3, d), F32, 2), 1 + rand((d,), F32, 3, 0.1)
+    y, bound = ref.norm(x, w, None, 0.0, centered)
+    assert gref.worst(mf.layer_norm(x.to(DEV), w.to(DEV), eps=0.0, centered=centered), y, bound + ref.half_step(F32) * y.abs()) <= 1.0
+    (dx, bx), (dw, bw), _ = ref.norm_grad(dy, x, w, 0.0, centered)
+    g = torch.zeros(d, device=DEV)
+    got = mf.layer_norm_grad(dy.to(DEV), x.to(DEV), w.to(DEV), g, eps=0.0, centered=centered)
+    assert gref.worst(got, dx, bx + ref.half_step(F32) * dx.abs()) <= 1.0 and gref.worst(g, dw, bw + ref.U * dw.abs()) <= 1.0
 
 
 def test_norm_gradient_without_rows():
