@@ -247,11 +247,11 @@ mfsdp_status_t route_plan_impl(const int32_t* experts, int64_t tokens, int64_t k
   const dim3 grid(static_cast<unsigned>(p.blocks)), wg(kPlanThreads);
   hipError_t e;
   if (p.blocks == 1) {
-    e = launch(MFSDP_KERNEL_ROUTE, stream, [&] { plan_place_kernel<true><<<grid, wg, 0, stream>>>(a); });
+    e = launch(MFSDP_KERNEL_ROUTE, stream, [&] { plan_small_kernel<<<grid, wg, 0, stream>>>(a); });
   } else {
     e = launch(MFSDP_KERNEL_ROUTE, stream, [&] { plan_hist_kernel<<<grid, wg, 0, stream>>>(a); });
     if (e == hipSuccess)
-      e = launch(MFSDP_KERNEL_ROUTE, stream, [&] { plan_place_kernel<false><<<grid, wg, 0, stream>>>(a); });
+      e = launch(MFSDP_KERNEL_ROUTE, stream, [&] { plan_place_kernel<<<grid, wg, 0, stream>>>(a); });
   }
   return launched(e, "routing plan");
 }

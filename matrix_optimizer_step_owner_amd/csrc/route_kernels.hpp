@@ -11,8 +11,13 @@
 // and groups the order of scores is that of the logits, and no score is needed.
 // Otherwise keys are scores in fp32, and whatever they leave open -- neighbours
 // in the chosen order, the last chosen and any other, or the border between
-// groups, nearer than the rounding of both -- sends the token through the same choice in fp64.  That is one
-// token in some hundred; fp64 for all of them would double the time.
+// groups, nearer than the rounding of both -- sends the token through the same
+// choice in fp64: of 256 experts in eight groups, k = 8, normal logits, 6 tokens of
+// a thousand with sigmoid scores, 2 to 3 with softmax.
+//
+// Bound by the vector units, some 430 instructions of four cycles per token:
+// 32771 tokens of 256 experts, k = 8, 19 us by the logits alone, 24 with sigmoid
+// scores and a bias, 31 with eight groups; the bytes would take 7.
 #pragma once
 
 #include "common.hpp"
@@ -427,7 +432,8 @@ struct RouteGradArgs {
 //   ds_j = scale / D (g_j - sum_i g_i s_i / D)     (scale g_j if not renormalised)
 //   softmax  dx_e = p_e (ds_e - sum_j ds_j s_j)    ds_e = 0 where not chosen
 //   sigmoid  dx_e = ds_e s_e (1 - s_e)
-// Bound by HBM; the chosen experts' terms reach the lanes that hold them
+// Bound by HBM, 5.2 TB/s: 32771 tokens of 256 experts fp32, k = 8, 13.3 us.  The
+// chosen experts' terms reach the lanes that hold them
 // through LDS (a loop over them, which experts that are named twice still take,
 // was 40% of the instructions).
 template <class E, int PER>
@@ -507,12 +513,14 @@ __global__ __launch_bounds__(256) void route_grad_kernel(RouteGradArgs a) {
 }
 
 // ---------------------------------------------------------------------------
-// Plan: a stable counting sort of (token, choice) by expert
+// Plan: a stable counting sort of (token, choice) by expert.  Bound by latency: two
+// launches, each a few dependent trips to memory (262168 choices of 256 experts
+// 9.8 us, 2^21 of them 19).
 // ---------------------------------------------------------------------------
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanWaves = kPlanThreads / 64;
 constexpr int kPlanBinsMax = kRouteExpertsMax;
-constexpr int kPlanSmall = 4096;       // slots that one workgroup takes alone (16396 slots: 19 us, 10 with two launches)
+constexpr int kPlanSmall = 6 * kPlanThreads;    // slots that one workgroup takes alone: 4096 take 7.3 us, 16000 16.5; two launches 9.8
 
 struct PlanArgs {
   const int32_t* chosen;   // n slots; outside [0, experts): no row
@@ -544,23 +552,14 @@ __global__ __launch_bounds__(kPlanThreads) void plan_hist_kernel(PlanArgs a) {
     a.hist[static_cast<size_t>(blockIdx.x) * a.pitch + b] = h[b];
 }
 
-// Rows of this workgroup's slots.  base: first row of each expert's slots here.
-// Each wave takes a contiguous part; counts per wave give its own first rows,
-// and within 64 slots the lower lanes with the same expert are counted by
-// ballots over the bits of its number.  Counts are sums of whole numbers: the
-// order in which they are added does not show.
-__device__ __forceinline__ void plan_place(const PlanArgs& a, int i0, int i1, const uint32_t* base,
-                                           uint32_t (*cnt)[kPlanBinsMax]) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int per_wave = (i1 - i0 + kPlanThreads - 1) / kPlanThreads * 64;
-  const int w0 = min(i0 + wave * per_wave, i1), w1 = min(w0 + per_wave, i1);
-  for (int b = lane; b < a.experts; b += 64) cnt[wave][b] = 0;
-  __syncthreads();
-  for (int i = w0 + lane; i < w1; i += 64) {
-    const uint32_t e = plan_expert(a, i);
-    if (e != 0xffffffffu) atomicAdd(&cnt[wave][e], 1u);
-  }
-  __syncthreads();
+// Rows of a workgroup's slots: each wave takes a contiguous part, counts of each
+// wave's own give its first rows, and within 64 slots the lower lanes with the
+// same expert are counted by ballots over the bits of its number.  Counts are sums
+// of whole numbers: the order in which they are added does not show.
+__device__ __forceinline__ int plan_wave_slots(int slots) { return (slots + kPlanThreads - 1) / kPlanThreads * 64; }
+
+// cnt: from counts of each wave to its first rows; base: the workgroup's.
+__device__ __forceinline__ void plan_first_rows(const PlanArgs& a, const uint32_t* base, uint32_t (*cnt)[kPlanBinsMax]) {
   for (int b = threadIdx.x; b < a.experts; b += kPlanThreads) {
     uint32_t at = base[b];
 #pragma unroll
@@ -571,30 +570,28 @@ __device__ __forceinline__ void plan_place(const PlanArgs& a, int i0, int i1, co
     }
   }
   __syncthreads();
-  auto fetch = [&](int i) { return i + lane < w1 ? plan_expert(a, i + lane) : 0xffffffffu; };
-  uint32_t next = fetch(w0);
-  for (int i = w0; i < w1; i += 64) {
-    const bool in = i + lane < w1;
-    const uint32_t e = next;
-    next = fetch(i + 64);
-    const bool on = e != 0xffffffffu;
-    uint64_t same = __ballot(on);
-    for (int b = 0; b < a.bits; ++b) {
-      const uint64_t m = __ballot(e >> b & 1);
-      same &= e >> b & 1 ? m : ~m;
-    }
-    int row = -1;
-    if (on) {
-      const uint32_t rank = __popcll(same & ((uint64_t(1) << lane) - 1));
-      const uint32_t at = cnt[wave][e] + rank;
-      row = static_cast<int>(at);
-      // the highest lane of each expert moves the wave's place on, behind the
-      // reads above (one wave, LDS operations in order)
-      if (rank + 1 == static_cast<uint32_t>(__popcll(same))) cnt[wave][e] = at + 1;
-    }
-    if (in) a.place[i + lane] = row;
-    __builtin_amdgcn_wave_barrier();
+}
+
+// The 64 slots from i on, of experts e, the wave's part ending at w1.
+__device__ __forceinline__ void plan_round(const PlanArgs& a, int i, int w1, uint32_t e, uint32_t* cnt) {
+  const int lane = threadIdx.x & 63;
+  const bool on = e != 0xffffffffu;
+  uint64_t same = __ballot(on);
+  for (int b = 0; b < a.bits; ++b) {
+    const uint64_t m = __ballot(e >> b & 1);
+    same &= e >> b & 1 ? m : ~m;
   }
+  int row = -1;
+  if (on) {
+    const uint32_t rank = __popcll(same & ((uint64_t(1) << lane) - 1));
+    const uint32_t at = cnt[e] + rank;
+    row = static_cast<int>(at);
+    // the highest lane of each expert moves the wave's place on, behind the
+    // reads above (one wave, LDS operations in order)
+    if (rank + 1 == static_cast<uint32_t>(__popcll(same))) cnt[e] = at + 1;
+  }
+  if (i + lane < w1) a.place[i + lane] = row;
+  __builtin_amdgcn_wave_barrier();
 }
 
 // Exclusive scan of tot[0 .. experts) into base, plus add; one expert a thread.
@@ -624,56 +621,94 @@ __device__ __forceinline__ uint32_t plan_scan(const uint32_t* tot, const uint32_
 }
 static_assert(kPlanBinsMax <= kPlanThreads, "plan_scan takes one expert per thread");
 
-// One workgroup for all slots (SMALL), or the second of two launches.
-template <bool SMALL>
+// The second of two launches.
 __global__ __launch_bounds__(kPlanThreads) void plan_place_kernel(PlanArgs a) {
   __shared__ uint32_t base[kPlanBinsMax], tot[kPlanBinsMax], add[kPlanBinsMax];
   __shared__ uint32_t cnt[kPlanWaves][kPlanBinsMax];
   __shared__ uint32_t wave_sum[kPlanWaves];
-  if constexpr (SMALL) {
-    for (int b = threadIdx.x; b < a.experts; b += kPlanThreads) tot[b] = add[b] = 0;
-    __syncthreads();
-    for (int i = threadIdx.x; i < a.n; i += kPlanThreads) {
-      const uint32_t e = plan_expert(a, i);
-      if (e != 0xffffffffu) atomicAdd(&tot[e], 1u);
-    }
-  } else {
-    // every workgroup adds up all counts: four experts a thread, as many threads per
-    // four as there are, eight loads of each in flight
-    for (int b = threadIdx.x; b < a.experts; b += kPlanThreads) tot[b] = add[b] = 0;
-    __syncthreads();
-    const int wide = (a.pitch / 4 + 63) & ~63, slices = kPlanThreads / wide;
-    const int b = threadIdx.x % wide * 4, blocks = static_cast<int>(gridDim.x), here = static_cast<int>(blockIdx.x);
-    const int slice = __builtin_amdgcn_readfirstlane(threadIdx.x / wide);     // whole waves: addresses and ends are scalars
-    if (b < a.experts && slice < slices) {
-      uint32_t t[4] = {}, before[4] = {};
-      for (int w = slice; w < blocks; w += 8 * slices) {
-        uint4 c[8];
+  // every workgroup adds up all counts: four experts a thread, as many threads per
+  // four as there are, eight loads of each in flight
+  for (int b = threadIdx.x; b < a.experts; b += kPlanThreads) tot[b] = add[b] = 0;
+  __syncthreads();
+  const int wide = (a.pitch / 4 + 63) & ~63, slices = kPlanThreads / wide;
+  const int b = threadIdx.x % wide * 4, blocks = static_cast<int>(gridDim.x), here = static_cast<int>(blockIdx.x);
+  const int slice = __builtin_amdgcn_readfirstlane(threadIdx.x / wide);     // whole waves: addresses and ends are scalars
+  if (b < a.experts && slice < slices) {
+    uint32_t t[4] = {}, before[4] = {};
+    for (int w = slice; w < blocks; w += 8 * slices) {
+      uint4 c[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) c[i] = gld<uint4>(a.hist + static_cast<size_t>(min(w + i * slices, blocks - 1)) * a.pitch + b);
+      for (int i = 0; i < 8; ++i) c[i] = gld<uint4>(a.hist + static_cast<size_t>(min(w + i * slices, blocks - 1)) * a.pitch + b);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int at = w + i * slices;
-          const uint32_t v[4] = {c[i].x, c[i].y, c[i].z, c[i].w};
+      for (int i = 0; i < 8; ++i) {
+        const int at = w + i * slices;
+        const uint32_t v[4] = {c[i].x, c[i].y, c[i].z, c[i].w};
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            if (at < blocks) t[q] += v[q];
-            if (at < here) before[q] += v[q];
-          }
+        for (int q = 0; q < 4; ++q) {
+          if (at < blocks) t[q] += v[q];
+          if (at < here) before[q] += v[q];
         }
       }
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        if (b + q < a.experts) {
-          atomicAdd(&tot[b + q], t[q]);
-          atomicAdd(&add[b + q], before[q]);
-        }
     }
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      if (b + q < a.experts) {
+        atomicAdd(&tot[b + q], t[q]);
+        atomicAdd(&add[b + q], before[q]);
+      }
   }
   __syncthreads();
   plan_scan(tot, add, base, a.experts, wave_sum, blockIdx.x == 0 ? a.offsets : nullptr);
-  const int i0 = SMALL ? 0 : blockIdx.x * a.per_block;
-  plan_place(a, i0, SMALL ? a.n : min(i0 + a.per_block, a.n), base, cnt);
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int i0 = blockIdx.x * a.per_block, i1 = min(i0 + a.per_block, a.n), per_wave = plan_wave_slots(i1 - i0);
+  const int w0 = min(i0 + wave * per_wave, i1), w1 = min(w0 + per_wave, i1);
+  for (int b = lane; b < a.experts; b += 64) cnt[wave][b] = 0;
+  __syncthreads();
+  for (int i = w0 + lane; i < w1; i += 64) {
+    const uint32_t e = plan_expert(a, i);
+    if (e != 0xffffffffu) atomicAdd(&cnt[wave][e], 1u);
+  }
+  __syncthreads();
+  plan_first_rows(a, base, cnt);
+  auto fetch = [&](int i) { return i + lane < w1 ? plan_expert(a, i + lane) : 0xffffffffu; };
+  uint32_t next = fetch(w0);
+  for (int i = w0; i < w1; i += 64) {
+    const uint32_t e = next;
+    next = fetch(i + 64);
+    plan_round(a, i, w1, e, cnt[wave]);
+  }
+}
+
+// One workgroup for all slots, which stay in registers: read once, counted once.
+__global__ __launch_bounds__(kPlanThreads) void plan_small_kernel(PlanArgs a) {
+  constexpr int ROUNDS = kPlanSmall / kPlanThreads;
+  __shared__ uint32_t base[kPlanBinsMax], tot[kPlanBinsMax], add[kPlanBinsMax];
+  __shared__ uint32_t cnt[kPlanWaves][kPlanBinsMax];
+  __shared__ uint32_t wave_sum[kPlanWaves];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int per_wave = plan_wave_slots(a.n), w0 = min(wave * per_wave, a.n), w1 = min(w0 + per_wave, a.n);
+  uint32_t e[ROUNDS];
+#pragma unroll
+  for (int r = 0; r < ROUNDS; ++r) e[r] = w0 + 64 * r + lane < w1 ? plan_expert(a, w0 + 64 * r + lane) : 0xffffffffu;
+  for (int b = lane; b < a.experts; b += 64) cnt[wave][b] = 0;
+  __syncthreads();
+#pragma unroll
+  for (int r = 0; r < ROUNDS; ++r)
+    if (e[r] != 0xffffffffu) atomicAdd(&cnt[wave][e[r]], 1u);
+  __syncthreads();
+  for (int b = threadIdx.x; b < a.experts; b += kPlanThreads) {
+    uint32_t t = 0;
+#pragma unroll
+    for (int w = 0; w < kPlanWaves; ++w) t += cnt[w][b];
+    tot[b] = t;
+    add[b] = 0;
+  }
+  __syncthreads();
+  plan_scan(tot, add, base, a.experts, wave_sum, a.offsets);
+  plan_first_rows(a, base, cnt);
+#pragma unroll
+  for (int r = 0; r < ROUNDS; ++r)
+    if (w0 + 64 * r < w1) plan_round(a, w0 + 64 * r, w1, e[r], cnt[wave]);
 }
 
 // ---------------------------------------------------------------------------

@@ -182,7 +182,7 @@ def route_dispatch(x: torch.Tensor, place: torch.Tensor,
     x: (tokens, d) bf16 or fp32, rows contiguous at any stride; place: (tokens,
     k) int32, a row outside ``out`` is none.  ``out`` has tokens * k rows unless
     it is given; rows of no choice are left as they are in it (and undefined in
-    one made here).  Its gradient is ``route_combine`` without weights."""
+    one made here), and a row that two choices name gets either's values.  Its gradient is ``route_combine`` without weights."""
     device = _gpu(x, "x")
     _check(x, "x", device, _FLOATS, 2)
     tokens, d = x.shape

@@ -5,7 +5,7 @@ spills, and LDS for as many workgroups per CU as the tiles count on.
 
 from test_build_resources import device_build, kernel_usage, pytestmark  # noqa: F401
 
-KERNELS = {"route_kernel": 10, "route_grad_kernel": 10, "plan_hist_kernel": 1, "plan_place_kernel": 2, "route_balance_kernel": 1, "dispatch_kernel": 2,
+KERNELS = {"route_kernel": 10, "route_grad_kernel": 10, "plan_hist_kernel": 1, "plan_place_kernel": 1, "plan_small_kernel": 1, "route_balance_kernel": 1, "dispatch_kernel": 2,
            "combine_kernel": 4, "combine_grad_kernel": 4, "layer_norm_kernel": 20, "layer_norm_grad_kernel": 20, "layer_norm_wide_kernel": 4,
            "layer_norm_columns_kernel": 2, "layer_norm_sum_kernel": 1, "scaled_quantize_kernel": 2, "scaled_weight_kernel": 2, "scaled_tile_kernel": 4}
 
