@@ -15,7 +15,7 @@
 // choice in fp64: of 256 experts in eight groups, k = 8, normal logits, 6 tokens of
 // a thousand with sigmoid scores, 2 to 3 with softmax.
 //
-// Bound by the vector units, some 430 instructions of four cycles per token:
+// Bound by the vector units, some 450 instructions of four cycles per token:
 // 32771 tokens of 256 experts, k = 8, 19 us by the logits alone, 24 with sigmoid
 // scores and a bias, 31 with eight groups; the bytes would take 7.
 #pragma once
