@@ -607,9 +607,11 @@ mfsdp_status_t scaled_weight_impl(const void* w, int64_t experts, int64_t n, int
   a.nb = static_cast<int32_t>(nb);
   a.kb = static_cast<int32_t>(kb);
   hipError_t e = hipSuccess;
-  for (int64_t t = 0; t < static_cast<int64_t>(blocks) && e == hipSuccess; t += kBlocksMax) {
+  a.tiles = static_cast<int64_t>(blocks);
+  const int64_t most = kBlocksMax / kScaledBlocks * kScaledBlocks;    // blocks of one launch (under 2^32 threads)
+  for (int64_t t = 0; t < a.tiles && e == hipSuccess; t += most) {
     a.tile0 = t;
-    const dim3 grid(static_cast<unsigned>(std::min<int64_t>(kBlocksMax, static_cast<int64_t>(blocks) - t))), wg(256);
+    const dim3 grid(static_cast<unsigned>(ceil_div(std::min(most, a.tiles - t), kScaledBlocks))), wg(256 * kScaledBlocks);
     e = launch(MFSDP_KERNEL_SCALED, stream, [&] {
       if (dtype == MFSDP_DTYPE_BF16) scaled_weight_kernel<ElemBF16><<<grid, wg, 0, stream>>>(a);
       else scaled_weight_kernel<ElemF32><<<grid, wg, 0, stream>>>(a);

@@ -120,25 +120,33 @@ struct ScaledWeightArgs {
   uint8_t *codes, *scales;      // experts x n x kb * 128, experts x nb x kb; or null
   uint8_t *tcodes, *tscales;    // experts x k x nb * 128, experts x kb x nb; or null
   int32_t n, k, nb, kb;
-  int64_t tile0;                // first tile of this launch
+  int64_t tile0, tiles;         // first block of this launch, blocks in all
 };
 
-// One 128 x 128 block per workgroup: a thread holds four neighbouring rows of
+// A 128 x 128 block per 256 threads: a thread holds four neighbouring rows of
 // sixteen columns, so that four codes of a column are one word of the
-// transposed copy, which goes through LDS.  Bound by HBM: 256 x 512 x 1536 bf16 127
-// us (4.8 TB/s), with both copies 167.
+// transposed copy, which goes through LDS.  A
+// workgroup takes two neighbouring blocks, so that rows are read and written in
+// pieces of twice the length.  Bound by HBM: 256 x 512 x 1536 bf16 111 us (5.4 TB/s),
+// with both copies 151 (127 and 167 with a block per workgroup).
+constexpr int kScaledBlocks = 2;
+
 template <class E>
-__global__ __launch_bounds__(256) void scaled_weight_kernel(ScaledWeightArgs a) {
+__global__ __launch_bounds__(256 * kScaledBlocks) void scaled_weight_kernel(ScaledWeightArgs a) {
   using S = typename E::storage_t;
   constexpr int V = E::kVec;
   constexpr int PITCH = kScaledBlock + 4;
-  __shared__ uint32_t part[4];
-  __shared__ __align__(16) uint8_t turned[kScaledBlock * PITCH];
-  const int64_t tile = a.tile0 + blockIdx.x;
+  __shared__ uint32_t parts[kScaledBlocks][4];
+  __shared__ __align__(16) uint8_t turns[kScaledBlocks][kScaledBlock * PITCH];
+  const int mine = __builtin_amdgcn_readfirstlane(threadIdx.x >> 8), tid = threadIdx.x & 255;
+  uint32_t* part = parts[mine];
+  uint8_t* turned = turns[mine];
+  const int64_t tile = a.tile0 + static_cast<int64_t>(blockIdx.x) * kScaledBlocks + mine;
+  const bool there = tile < a.tiles;      // (the last workgroup's second may not be)
   const int per = a.nb * a.kb;
   const int64_t e = tile / per;
   const int rest = static_cast<int>(tile - e * per), tn = rest / a.kb, tk = rest - tn * a.kb;
-  const int r0 = (threadIdx.x >> 3) * 4, c0 = (threadIdx.x & 7) * 16;
+  const int r0 = (tid >> 3) * 4, c0 = (tid & 7) * 16;
   const int row = tn * kScaledBlock + r0, col = tk * kScaledBlock + c0;
   const S* src = static_cast<const S*>(a.w) + (e * a.n + row) * static_cast<int64_t>(a.k) + col;
   float v[4][16];
@@ -146,7 +154,7 @@ __global__ __launch_bounds__(256) void scaled_weight_kernel(ScaledWeightArgs a) 
   for (int i = 0; i < 4; ++i)
 #pragma unroll
     for (int h = 0; h < 16 / V; ++h) {
-      const int left = row + i < a.n ? a.k - col - h * V : 0;
+      const int left = there && row + i < a.n ? a.k - col - h * V : 0;
       const S* p = src + i * static_cast<int64_t>(a.k) + h * V;
       uint4 raw = make_uint4(0, 0, 0, 0);
       if (left >= V) {
@@ -169,7 +177,7 @@ __global__ __launch_bounds__(256) void scaled_weight_kernel(ScaledWeightArgs a) 
     for (int j = 0; j < 16; ++j) top = max(top, __float_as_uint(v[i][j]) & 0x7fffffffu);
 #pragma unroll
   for (int d = 32; d > 0; d >>= 1) top = max(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), d, 64)));
-  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = top;
+  if ((tid & 63) == 0) part[tid >> 6] = top;
   __syncthreads();
   top = max(max(part[0], part[1]), max(part[2], part[3]));
   const uint32_t be = scaled_exponent(top);
@@ -181,13 +189,13 @@ __global__ __launch_bounds__(256) void scaled_weight_kernel(ScaledWeightArgs a) 
     for (int q = 0; q < 4; ++q)
       w[i][q] = be == 255u ? kScaledNan
                            : scaled_codes(v[i][4 * q] * s, v[i][4 * q + 1] * s, v[i][4 * q + 2] * s, v[i][4 * q + 3] * s);
-  if (a.codes) {
+  if (a.codes && there) {
     uint8_t* out = a.codes + (e * a.n + row) * (static_cast<int64_t>(a.kb) * kScaledBlock) + col;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       if (row + i < a.n)
         gst<uint4>(out + i * (static_cast<int64_t>(a.kb) * kScaledBlock), make_uint4(w[i][0], w[i][1], w[i][2], w[i][3]));
-    if (threadIdx.x == 0) a.scales[tile] = static_cast<uint8_t>(be);
+    if (tid == 0) a.scales[tile] = static_cast<uint8_t>(be);
   }
   if (a.tcodes) {
 #pragma unroll
@@ -201,13 +209,13 @@ __global__ __launch_bounds__(256) void scaled_weight_kernel(ScaledWeightArgs a) 
     // eight lanes write one column of the block, 16 codes each
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int c = (threadIdx.x >> 3) + 32 * i, r = (threadIdx.x & 7) * 16;
-      if (tk * kScaledBlock + c >= a.k) continue;
+      const int c = (tid >> 3) + 32 * i, r = (tid & 7) * 16;
+      if (!there || tk * kScaledBlock + c >= a.k) continue;
       const uint32_t* p = reinterpret_cast<const uint32_t*>(turned + c * PITCH + r);
       gst<uint4>(a.tcodes + (e * a.k + tk * kScaledBlock + c) * (static_cast<int64_t>(a.nb) * kScaledBlock) + tn * kScaledBlock + r,
                  make_uint4(p[0], p[1], p[2], p[3]));
     }
-    if (threadIdx.x == 0) a.tscales[(e * a.kb + tk) * a.nb + tn] = static_cast<uint8_t>(be);
+    if (there && tid == 0) a.tscales[(e * a.kb + tk) * a.nb + tn] = static_cast<uint8_t>(be);
   }
 }
 
