@@ -279,19 +279,74 @@ __device__ __forceinline__ void lds_dma1_buf(uint32_t lds, uint32_t voff, u32x4s
                :: "s"(ulds), "v"(voff), "s"(buf) : "memory", "m0");
 }
 
-// group_find with an expert's row tiles in bands of equal height, five to eleven: a
-// last band of one or two rows reads all of a matrix for a few tiles (eight 14336 x
-// 4096 experts with about 2048 rows each, 957 -> 946 us).
-__device__ __forceinline__ bool scaled_find(const GroupArgs& g, int b, int bp, int nq, int& expert, int& ti, int& tj) {
-  GroupSpan s;
-  if (!group_span(g, b, bp, nq, s)) return false;
-  expert = s.expert;
-  const int bands = max(1, (s.rows + kGroupBand / 2) / kGroupBand), height = (s.rows + bands - 1) / bands;
-  const int band = s.local / (height * nq), r = s.local - band * (height * nq);
-  const int in_band = min(height, s.rows - band * height);
-  ti = band * height + r % in_band;
-  tj = r / in_band;
-  return true;
+// Sum over the lanes up to and with this one.
+__device__ __forceinline__ uint32_t wave_scan(uint32_t v) {
+  v += dpp_or0<0x111, 0xf>(v);   // row_shr:1, :2, :4, :8
+  v += dpp_or0<0x112, 0xf>(v);
+  v += dpp_or0<0x114, 0xf>(v);
+  v += dpp_or0<0x118, 0xf>(v);
+  v += dpp_or0<0x142, 0xa>(v);   // row_bcast:15, :31
+  v += dpp_or0<0x143, 0xc>(v);
+  return v;
+}
+
+// What group_find does, in fewer dependent steps, for tiles that take a few
+// microseconds: lane l sums the tiles of experts [l c, (l + 1) c) from loads that do
+// not wait for one another, the scan is six DPP steps, and the experts of the lane
+// that holds the tile are looked through by all lanes.  Sums stop at kScaledMany,
+// which only offsets that are not in order reach.
+// An expert's row tiles are in bands of equal height, five to eleven: a last band of
+// one or two rows reads all of a matrix for a few tiles (eight 14336 x 4096 experts
+// with about 2048 rows each, 957 -> 946 us).
+constexpr uint32_t kScaledMany = 1u << 24;    // more than a grid has
+
+template <int BP>
+__device__ __forceinline__ bool scaled_find(const GroupArgs& g, int b, int nq, int& expert, int& ti, int& tj, int& lo, int& hi) {
+  const int lane = threadIdx.x & 63;
+  const int c = (g.experts + 63) >> 6;
+  auto tiles = [](int from, int to) { return static_cast<uint32_t>(to - from + BP - 1) / BP; };
+  auto clamped = [&](int at) { return min(max(at, 0), g.rows); };
+  uint32_t sum = 0;
+  for (int i = 0; i < c; i += 4) {
+    int off[5];
+#pragma unroll
+    for (int q = 0; q < 5; ++q) off[q] = clamped(g.off[min(lane * c + i + q, g.experts)]);
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      if (i + q < c) sum = min(sum + tiles(off[q], max(off[q], off[q + 1])), kScaledMany);
+  }
+  const uint32_t upto = wave_scan(sum);
+  const int64_t all = static_cast<int64_t>(__builtin_amdgcn_readlane(static_cast<int>(upto), 63)) * nq;
+  // No more tiles than the grid has (the host bounds it by what ordered offsets
+  // can give; others give wrong results, not accesses outside).
+  const int total = static_cast<int>(min(all, static_cast<int64_t>(gridDim.x)));
+  if (b >= total) return false;
+  const int want = xcd_remap(b, total);
+  const int src = __builtin_ctzll(__ballot(want < static_cast<int64_t>(upto) * nq));
+  uint32_t at = static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(upto - sum), src));
+  for (int i = 0; i < c; i += 64) {
+    const int e = min(src * c + i + lane, g.experts);
+    const int from = clamped(g.off[e]), to = max(from, clamped(g.off[min(e + 1, g.experts)]));
+    const uint32_t n = i + lane < c ? min(tiles(from, to), kScaledMany) : 0;
+    const uint32_t end = at + wave_scan(n);
+    const uint64_t found = __ballot(want < static_cast<int64_t>(end) * nq);
+    if (found) {
+      const int l = __builtin_ctzll(found);
+      auto of = [&](int v) { return __builtin_amdgcn_readlane(v, l); };
+      expert = of(e);
+      lo = of(from);
+      hi = of(to);
+      const int rows = of(static_cast<int>(n)), local = want - of(static_cast<int>(end - n)) * nq;
+      const int bands = max(1, (rows + kGroupBand / 2) / kGroupBand), height = (rows + bands - 1) / bands;
+      const int band = local / (height * nq), r = local - band * (height * nq);
+      const int in_band = min(height, rows - band * height);
+      ti = band * height + r % in_band;
+      tj = r / in_band;
+      return true;
+    }
+    at = static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(end), 63));
+  }
+  return false;
 }
 
 template <class C>
@@ -309,8 +364,7 @@ __global__ __launch_bounds__(C::THREADS, C::OCC) void scaled_tile_kernel(ScaledA
   const int lrow = lane & 31, lhalf = lane >> 5;
 
   int e, ti, tj, lo, hi;
-  if (!scaled_find(g, blockIdx.x, C::BP, (g.n + C::BQ - 1) / C::BQ, e, ti, tj)) return;
-  group_segment(g, e, lo, hi);
+  if (!scaled_find<C::BP>(g, blockIdx.x, (g.n + C::BQ - 1) / C::BQ, e, ti, tj, lo, hi)) return;
   const int p0 = ti * C::BP, q0 = tj * C::BQ;
   const int prem = hi - lo - p0, qrem = g.n - q0;
   const char* pbase = static_cast<const char*>(g.p) + (static_cast<int64_t>(lo) + p0) * g.k;

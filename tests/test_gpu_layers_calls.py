@@ -56,6 +56,26 @@ def test_every_tile(shape, counts, n, k):
     assert (out[:, :8] == 7).all() and (out[:, 8 + n:] == 7).all()
 
 
+@pytest.mark.parametrize("experts", [63, 65, 300, 5000, 9000])
+def test_tiles_of_many_experts(experts):
+    # most of them without a row, some with several tiles
+    n, k = 40, 128
+    c = torch.where(torch.rand(experts, generator=torch.Generator().manual_seed(experts)) < 0.2, 3000 // experts + 1, 0)
+    c[0], c[experts // 2], c[-1] = 700, 130, 65
+    c = c.tolist()
+    rows = sum(c)
+    x, w = rand((rows, k), BF, 1).to(DEV), rand((experts, n, k), BF, 2, 0.05).to(DEV)
+    q, qw = mf.scaled_quantize(x), mf.scaled_quantize_weight(w)
+    y = mf.scaled_linear(*q, *qw, offsets_of(c).to(DEV))
+    e = torch.repeat_interleave(torch.arange(experts), torch.tensor(c)).to(DEV)
+    power = lambda s: torch.exp2(s.double() - 127)
+    xv = q[0].double() * power(q[1])
+    wv = (qw[0].double() * power(qw[1]).repeat_interleave(128, 1)[:, :n])[e]
+    want, mag = (wv * xv[:, None]).sum(2), (wv * xv[:, None]).abs().sum(2)
+    bound = ref.half_step(BF) * want.abs() + (1 + 2 ** -8) * (2 ** -10 + (k + 8) * ref.U) * mag + 1e-38
+    assert float(((y.double() - want).abs() / bound).max()) <= 1.0
+
+
 def test_wrong_offsets_stay_inside():
     # offsets that decrease or lie outside give wrong results, and touch nothing else
     x, w = rand((300, 256), BF, 1).to(DEV), rand((3, 200, 256), BF, 2, 0.05).to(DEV)
