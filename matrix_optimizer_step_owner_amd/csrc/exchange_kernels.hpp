@@ -8,7 +8,7 @@
 //
 // All of them go token by token, so that a token's own row is read or written
 // once whatever k is, and rows of no choice are neither read nor written.  They
-// are bound by HBM: 8192 tokens of 4096 bf16, k = 8, take 101 us to dispatch (6.0
+// are bound by HBM: 8192 tokens of 4096 bf16, k = 8, take 105 us to dispatch (5.8
 // TB/s), 113 to combine (5.3) and 206 for the combine's gradient (5.5).  A unit is
 // 16 bytes of a row, at any alignment of elements; the last of a row may hold fewer.
 #pragma once

@@ -515,12 +515,12 @@ __global__ __launch_bounds__(256) void route_grad_kernel(RouteGradArgs a) {
 // ---------------------------------------------------------------------------
 // Plan: a stable counting sort of (token, choice) by expert.  Bound by latency: two
 // launches, each a few dependent trips to memory (262168 choices of 256 experts
-// 9.8 us, 2^21 of them 19).
+// 9.8 us, 2^21 of them 18).
 // ---------------------------------------------------------------------------
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanWaves = kPlanThreads / 64;
 constexpr int kPlanBinsMax = kRouteExpertsMax;
-constexpr int kPlanSmall = 6 * kPlanThreads;    // slots that one workgroup takes alone: 4096 take 7.3 us, 16000 16.5; two launches 9.8
+constexpr int kPlanSmall = 8 * kPlanThreads;    // slots that one workgroup takes alone: 4096 take 5.9 us, 8192 9.5, 16396 14; two launches 10.1
 
 struct PlanArgs {
   const int32_t* chosen;   // n slots; outside [0, experts): no row
@@ -576,19 +576,22 @@ __device__ __forceinline__ void plan_first_rows(const PlanArgs& a, const uint32_
 __device__ __forceinline__ void plan_round(const PlanArgs& a, int i, int w1, uint32_t e, uint32_t* cnt) {
   const int lane = threadIdx.x & 63;
   const bool on = e != 0xffffffffu;
-  uint64_t same = __ballot(on);
+  const uint64_t there = __ballot(on);
+  uint32_t lo = static_cast<uint32_t>(there), hi = static_cast<uint32_t>(there >> 32);
   for (int b = 0; b < a.bits; ++b) {
-    const uint64_t m = __ballot(e >> b & 1);
-    same &= e >> b & 1 ? m : ~m;
+    const uint32_t bit = 0u - (e >> b & 1);       // all of it or none
+    const uint64_t m = __ballot(bit);
+    lo &= ~(bit ^ static_cast<uint32_t>(m));
+    hi &= ~(bit ^ static_cast<uint32_t>(m >> 32));
   }
   int row = -1;
   if (on) {
-    const uint32_t rank = __popcll(same & ((uint64_t(1) << lane) - 1));
+    const uint32_t rank = __builtin_amdgcn_mbcnt_hi(hi, __builtin_amdgcn_mbcnt_lo(lo, 0));
     const uint32_t at = cnt[e] + rank;
     row = static_cast<int>(at);
     // the highest lane of each expert moves the wave's place on, behind the
     // reads above (one wave, LDS operations in order)
-    if (rank + 1 == static_cast<uint32_t>(__popcll(same))) cnt[e] = at + 1;
+    if (rank + 1 == static_cast<uint32_t>(__popc(lo) + __popc(hi))) cnt[e] = at + 1;
   }
   if (i + lane < w1) a.place[i + lane] = row;
   __builtin_amdgcn_wave_barrier();

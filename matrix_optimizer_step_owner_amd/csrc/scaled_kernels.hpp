@@ -128,7 +128,7 @@ struct ScaledWeightArgs {
 // transposed copy, which goes through LDS.  A
 // workgroup takes two neighbouring blocks, so that rows are read and written in
 // pieces of twice the length.  Bound by HBM: 256 x 512 x 1536 bf16 111 us (5.4 TB/s),
-// with both copies 151 (127 and 167 with a block per workgroup).
+// with both copies 151 (127 and 167 with a block per workgroup, 118 and 165 with four).
 constexpr int kScaledBlocks = 2;
 
 template <class E>
@@ -247,7 +247,7 @@ __device__ __forceinline__ i32x8_t scaled_frag(const uint4& a, const uint4& b) {
 //
 // 256 x 256: bound by the MFMAs, two thirds of whose cycles are used, at the 1.8 GHz
 // that this load is given: one product of 8192^3 2.6 PFLOP/s, one expert of 16384 x
-// 14336 x 4096 2.46, eight of them with 2048 rows each 2.0 (947 us).  32 rows: bound
+// 14336 x 4096 2.46, eight of them with 2048 rows each 2.06 (934 us).  32 rows: bound
 // by HBM, 8 experts of 14336 x 4096 with 16 rows each 89 us, 5.3 TB/s.
 template <int BP_, int BQ_, int WP_, int WQ_, int U_, int STAGES_, int KS_ = 1, int OCC_ = 2>
 struct ScaledTile {
