@@ -16,7 +16,7 @@
 // a thousand with sigmoid scores, 2 to 3 with softmax.
 //
 // Bound by the vector units, some 450 instructions of four cycles per token:
-// 32771 tokens of 256 experts, k = 8, 19 us by the logits alone, 24 with sigmoid
+// 32771 tokens of 256 experts, k = 8, 19 us by the logits alone, 23 with sigmoid
 // scores and a bias, 31 with eight groups; the bytes would take 7.
 #pragma once
 
@@ -231,68 +231,70 @@ __device__ __forceinline__ uint32_t route_groups(const RouteArgs& a, const K (&v
   return mask;
 }
 
-// The k largest keys in order, lane j receiving expert j (others -1).  Lists of up
-// to four are sorted first, with their places, by rank, as the digits of one word
-// (of equal keys the lower place is first): a round then needs neither the
-// largest of a lane's own nor a search for it, and the winner's list moves up by
-// one.  (Lists of eight lose by it: 32768 x 512, k = 10, 64 and 42 us.)  On return
-// key[0] is the largest that a lane has left.
+// The k largest keys in order, lane j receiving expert j (others -1).  A lane's keys
+// are lists of up to four, each sorted first, with their places, by rank, as the
+// digits of one word (of equal keys the lower place is first): a round then compares
+// the lists' heads alone, and the list that the winner is of moves up by one.  (One
+// search per round over eight unsorted keys: 32768 x 512, k = 10, 40 us; one sorted
+// list of eight 64; two of four 34.)  On return key[0] is the largest that a lane
+// has left.
 template <int PER, class K>
 __device__ __forceinline__ int route_pick(K (&key)[PER], int k, int lane) {
+  constexpr int W = PER < 4 ? PER : 4, LISTS = PER / W;
   int mine = -1;
-  if constexpr (PER <= 4) {
-    int rank[PER];
+  uint32_t digits[LISTS];
 #pragma unroll
-    for (int i = 0; i < PER; ++i) rank[i] = i;
+  for (int l = 0; l < LISTS; ++l) {
+    K(&at)[W] = *reinterpret_cast<K(*)[W]>(&key[l * W]);
+    int rank[W];
 #pragma unroll
-    for (int i = 0; i < PER; ++i)
+    for (int i = 0; i < W; ++i) rank[i] = i;
 #pragma unroll
-      for (int q = i + 1; q < PER; ++q) {
-        const int after = key[i] < key[q] ? 1 : 0;
+    for (int i = 0; i < W; ++i)
+#pragma unroll
+      for (int q = i + 1; q < W; ++q) {
+        const int after = at[i] < at[q] ? 1 : 0;
         rank[i] += after;
         rank[q] -= after;
       }
-    uint32_t digits = 0;
+    digits[l] = 0;
 #pragma unroll
-    for (int i = 1; i < PER; ++i) digits |= static_cast<uint32_t>(i) << (4 * rank[i]);
+    for (int i = 0; i < W; ++i) digits[l] |= static_cast<uint32_t>(l * W + i) << (4 * rank[i]);
 #pragma unroll
-    for (int end = PER - 1; end > 0; --end)
+    for (int end = W - 1; end > 0; --end)
 #pragma unroll
       for (int i = 0; i < end; ++i) {
-        const K hi = max(key[i], key[i + 1]);
-        key[i + 1] = min(key[i], key[i + 1]);
-        key[i] = hi;
+        const K hi = max(at[i], at[i + 1]);
+        at[i + 1] = min(at[i], at[i + 1]);
+        at[i] = hi;
       }
-    for (int j = 0; j < k; ++j) {
-      const K m = wave_max(key[0]);
-      const int owner = __builtin_ctzll(__ballot(key[0] == m));
-      const int e = owner * PER + (__builtin_amdgcn_readlane(static_cast<int>(digits), owner) & 15);
-      const bool won = lane == owner;
-#pragma unroll
-      for (int i = 0; i < PER; ++i) key[i] = won ? (i + 1 < PER ? key[(i + 1) % PER] : K(0)) : key[i];
-      digits = won ? digits >> 4 : digits;
-      mine = lane == j ? e : mine;
-    }
-  } else {
-    for (int j = 0; j < k; ++j) {
-      K best = key[0];
-#pragma unroll
-      for (int i = 1; i < PER; ++i) best = max(best, key[i]);
-      const K m = wave_max(best);
-      const int owner = __builtin_ctzll(__ballot(best == m));
-      int at = 0;
-#pragma unroll
-      for (int i = PER - 1; i >= 0; --i)
-        if (key[i] == m) at = i;
-#pragma unroll
-      for (int i = 0; i < PER; ++i)
-        if (lane == owner && i == at) key[i] = 0;
-      const int e = __builtin_amdgcn_readlane(lane * PER + at, owner);
-      if (lane == j) mine = e;
-    }
-#pragma unroll
-    for (int i = 1; i < PER; ++i) key[0] = max(key[0], key[i]);
   }
+  auto head = [&] {
+    K h = key[0];
+#pragma unroll
+    for (int l = 1; l < LISTS; ++l) h = max(h, key[l * W]);
+    return h;
+  };
+  for (int j = 0; j < k; ++j) {
+    const K h = head(), m = wave_max(h);
+    const int owner = __builtin_ctzll(__ballot(h == m));
+    uint64_t left = uint64_t(1) << owner;     // of the owner's lists, the first with it
+    int place = 0;
+#pragma unroll
+    for (int l = 0; l < LISTS; ++l) {
+      const uint64_t of = LISTS == 1 ? left : left & __ballot(key[l * W] == m);
+      left &= ~of;
+      const bool won = __builtin_amdgcn_inverse_ballot_w64(of);    // no comparison per lane
+      const int digit = __builtin_amdgcn_readlane(static_cast<int>(digits[l]), owner) & 15;
+      if (LISTS == 1 || of) place = digit;
+#pragma unroll
+      for (int i = 0; i < W; ++i) key[l * W + i] = won ? (i + 1 < W ? key[l * W + (i + 1) % W] : K(0)) : key[l * W + i];
+      digits[l] = won ? digits[l] >> 4 : digits[l];
+    }
+    const int e = owner * PER + place;
+    mine = __builtin_amdgcn_inverse_ballot_w64(uint64_t(1) << j) ? e : mine;
+  }
+  key[0] = head();
   return mine;
 }
 

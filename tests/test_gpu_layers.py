@@ -66,6 +66,21 @@ def test_near_and_equal_keys(kind, groups, top):
             assert ref.f64(w)[told].sub(ww[told]).abs().le(bound[told]).all()
 
 
+@pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("n,k,groups,top", [(250, 20, 1, 1), (256, 32, 8, 3), (500, 32, 1, 1), (512, 20, 16, 4), (1000, 32, 1, 1), (1024, 9, 4, 1)])
+def test_equal_keys_of_a_lane(n, k, groups, top, kind):
+    # many equal keys in each lane's lists, whatever their order
+    g = torch.Generator().manual_seed(n)
+    x = torch.randint(-2, 3, (200, n), generator=g).float()
+    x[100:] = torch.where(torch.rand(100, n, generator=g) < 0.9, x[100:, :1], x[100:])
+    for bias in (None, torch.randint(0, 2, (n,), generator=g).float()):
+        e, w = mf.route(x.to(DEV), k, scores=kind, bias=None if bias is None else bias.to(DEV), groups=groups, top_groups=top)
+        want, ww, bound = ref.route(x, k, kind, bias, groups, top)
+        told = ~ref.undecided(x, kind, bias, groups, top)
+        assert torch.equal(e.cpu().long()[told], want[told]) and int(told.sum()) >= 100
+        assert ref.f64(w)[told].sub(ww[told]).abs().le(bound[told]).all()
+
+
 def test_trading_bias():
     # a bias that makes up for the score to the last bits of fp32: what the
     # scores round to would choose otherwise
