@@ -241,11 +241,15 @@ __device__ __forceinline__ double warp_sum(double v) {
   return v;
 }
 
-// Largest value in the wave, on every lane (as a scalar).
+// A lane's value from another lane, 0 from one that there is none or that is
+// switched off: behind a condition that lanes do not share (an if, but the right side of
+// &&, || and ?: as well) those that it left out count as 0.  So all functions from
+// here on are called where every lane of the wave is on, their results kept.
 template <int CTRL, int ROWS>
 __device__ __forceinline__ uint32_t dpp_or0(uint32_t v) {
   return static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), CTRL, ROWS, 0xf, false));
 }
+// Largest value in the wave, on every lane (as a scalar).
 __device__ __forceinline__ uint32_t wave_max(uint32_t v) {
   v = max(v, dpp_or0<0x111, 0xf>(v));   // row_shr:1, :2, :4, :8
   v = max(v, dpp_or0<0x112, 0xf>(v));
@@ -273,7 +277,7 @@ __device__ __forceinline__ float wave_sum(float v) {
   return __uint_as_float(static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(__float_as_uint(v)), 63)));
 }
 
-// The next lane's value (lane 63: 0).
+// The next lane's value (lane 63: 0); a lane that is switched off gives 0 too.
 __device__ __forceinline__ float wave_next(float v) { return __uint_as_float(dpp_or0<0x130, 0xf>(__float_as_uint(v))); }
 
 }  // namespace mfsdp

@@ -219,7 +219,7 @@ __device__ __forceinline__ uint32_t route_groups(const RouteArgs& a, const K (&v
     if (a.top < a.groups) {
       const float out = route_value(wave_max(group && !stays ? key : 0u));
       const float in = route_value(~wave_max(stays ? ~key : 0u));
-      close = !(in - out > 2.f * route_doubt(most, fabsf(in) + fabsf(out))) || __popcll(__ballot(stays)) != a.top * step;
+      close = __popcll(__ballot(stays)) != a.top * step || !(in - out > 2.f * route_doubt(most, fabsf(in) + fabsf(out)));
     }
   }
   if (a.lanes > 0) return stays ? 0xffffffffu : 0u;
@@ -397,10 +397,13 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
       const float mb = on ? gld<float>(a.bias + mine) : 0.f;
       const float mk = (a.sigmoid ? __builtin_amdgcn_rcpf(1.f + route_exp(-mx)) : route_exp(mx - top) * most) + mb;
       const float doubt = route_doubt(most, mk);
-      bool open = lane + 1 < a.k && !(mk - wave_next(mk) > doubt) && !(wave_next(mx) == mx && wave_next(mb) == mb);
+      // every lane takes part in these, before any of them can leave
+      const float nk = wave_next(mk), nx = wave_next(mx), nb = wave_next(mb);
       auto last = [&](float q) { return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(q), a.k - 1)); };
-      open = open || (vk[0] != 0 && !(last(mk) - route_value(vk[0]) > last(doubt)));
-      close = close || __ballot(open) != 0;
+      const float lk = last(mk), ld = last(doubt);
+      const bool order = (lane + 1 < a.k) & !(mk - nk > doubt) & !((nx == mx) & (nb == mb));
+      const bool rest = (vk[0] != 0) & !(lk - route_value(vk[0]) > ld);
+      close = __ballot(order | rest) != 0 || close;
     }
   }
   if (__builtin_expect(close, 0)) {
