@@ -87,21 +87,30 @@ __device__ __forceinline__ void route_load(const typename E::storage_t* p, int f
   }
 }
 
-// Score of one expert; top and inv are the row's largest logit and 1 / sum (softmax).
-__device__ __forceinline__ float route_score(float x, int sigmoid, float top, float inv) {
-  const float e = expf(sigmoid ? -x : x - top);
-  return sigmoid ? __builtin_amdgcn_rcpf(1.f + e) : e * inv;
+// n / d to little more than half a step, 1 where n == d: the hardware's reciprocal
+// (off by a step) and one Newton step.  For 1e-20 <= d < 2^20 and 0 <= n <= d.
+__device__ __forceinline__ float route_quotient(float n, float d) {
+  const float r = __builtin_amdgcn_rcpf(d), q = n * r;
+  return fmaf(fmaf(-q, d, n), r, q);
+}
+
+// Score of one expert; top and sum are the row's largest logit and the sum of its
+// exponentials (softmax).  A sigmoid by its smaller side's exponential, which has a
+// digit wherever the score has one.
+__device__ __forceinline__ float route_score(float x, int sigmoid, float top, float sum) {
+  const float e = expf(sigmoid ? -fabsf(x) : x - top);
+  return route_quotient(sigmoid && x >= 0.f ? 1.f : e, sigmoid ? 1.f + e : sum);
 }
 
 // exp(x) by the hardware's 2^x: relatively off by (|x| + 2) 2^-23, a fifth of the
 // instructions.  For keys, sums and gradients; the weights' scores are taken from
-// expf.  Quotients are products with the hardware's reciprocal, one step off.
+// expf.  Quotients in these are products with the hardware's reciprocal, one step off.
 __device__ __forceinline__ float route_exp(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504f); }
 
-// Largest logit and 1 / sum of exp(x - largest) of a row (softmax); x becomes the
+// Largest logit and sum of exp(x - largest) of a row (softmax); x becomes the
 // exponentials.
 template <int PER>
-__device__ __forceinline__ void route_softmax(float (&x)[PER], int first, int n, float& top, float& inv) {
+__device__ __forceinline__ void route_softmax(float (&x)[PER], int first, int n, float& top, float& sum) {
   uint32_t m = 0;
 #pragma unroll
   for (int i = 0; i < PER; ++i)
@@ -113,7 +122,7 @@ __device__ __forceinline__ void route_softmax(float (&x)[PER], int first, int n,
     x[i] = first + i < n ? route_exp(x[i] - top) : 0.f;
     s += x[i];
   }
-  inv = __builtin_amdgcn_rcpf(wave_sum(s));
+  sum = wave_sum(s);
 }
 
 // Distance within which fp32 keys do not decide, for keys of size `key`.  A
@@ -353,7 +362,7 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
   float x[PER];
   route_load<E, PER>(row, first, a.n, 0.f, x);
   const bool on = lane < a.k;
-  float top = 0.f, inv = 1.f;
+  float top = 0.f, sum = 1.f;
   uint32_t key[PER];
   int mine;
   float mx;
@@ -361,13 +370,13 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
 #pragma unroll
     for (int i = 0; i < PER; ++i) key[i] = first + i < a.n ? route_key(x[i]) : 0u;
   }
-  if (!a.sigmoid) route_softmax<PER>(x, first, a.n, top, inv);     // x: exponentials
+  if (!a.sigmoid) route_softmax<PER>(x, first, a.n, top, sum);     // x: exponentials
   bool close = false;
   if (!a.bias && a.groups == 1) {
     mine = route_pick<PER, uint32_t>(key, a.k, lane);
     mx = on ? E::to_f32(gld<S>(row + mine)) : 0.f;
   } else {
-    const float most = a.sigmoid ? 1.f : inv;
+    const float most = a.sigmoid ? 1.f : __builtin_amdgcn_rcpf(sum);
     float v[PER];
 #pragma unroll
     for (int i = 0; i < PER; ++i) v[i] = 0.f;
@@ -411,11 +420,11 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
     mx = on ? E::to_f32(gld<S>(row + mine)) : 0.f;
   }
 
-  const float s = on ? route_score(mx, a.sigmoid, top, inv) : 0.f;
-  const float factor = a.renorm ? a.scale * __builtin_amdgcn_rcpf(wave_sum(s) + kRouteTiny) : a.scale;
+  const float s = on ? route_score(mx, a.sigmoid, top, sum) : 0.f;
+  const float part = a.renorm ? route_quotient(s, wave_sum(s) + kRouteTiny) : s;
   if (on) {
     chosen[lane] = mine;
-    weights[lane] = s * factor;
+    weights[lane] = a.scale * part;
   }
 }
 
@@ -465,6 +474,7 @@ __global__ __launch_bounds__(256) void route_grad_kernel(RouteGradArgs a) {
     if (!a.sigmoid) {
       route_load<E, PER>(row, first, a.n, 0.f, x);
       route_softmax<PER>(x, first, a.n, top, inv);      // x: exponentials
+      inv = __builtin_amdgcn_rcpf(inv);
     }
     const float q = route_exp(a.sigmoid ? -fabsf(xe) : xe - top), r = __builtin_amdgcn_rcpf(1.f + q);
     const float s = !on ? 0.f : !a.sigmoid ? q * inv : xe >= 0.f ? r : q * r;
