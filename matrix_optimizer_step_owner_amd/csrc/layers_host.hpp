@@ -627,8 +627,8 @@ using ScaledRows = ScaledTile<32, 64, 1, 2, 4, 3, 4, 4>;     // two workgroups p
 using ScaledFew = ScaledTile<32, 32, 1, 1, 4, 3, 4, 4>;
 
 template <class C>
-hipError_t launch_scaled(const ScaledArgs& a, hipStream_t stream) {
-  const dim3 grid(static_cast<unsigned>(group_tiles_max(a.g.rows, a.g.experts, C::BP) * ceil_div(a.g.n, C::BQ)));
+hipError_t launch_scaled(const ScaledArgs& a, int64_t workgroups, hipStream_t stream) {
+  const dim3 grid(static_cast<unsigned>(workgroups));
   return launch(MFSDP_KERNEL_SCALED, stream, [&] { scaled_tile_kernel<C><<<grid, dim3(C::THREADS), 0, stream>>>(a); });
 }
 
@@ -669,23 +669,37 @@ GroupShape scaled_shape(ScaledKernel u) {
   return shape_of<ScaledFew>(true);
 }
 
+// The kernel that a product's sizes take and its workgroups (0: no launch), or why
+// they are refused.
+mfsdp_status_t scaled_choose(int64_t experts, int64_t rows, int64_t n, int64_t k, ScaledKernel* use, int64_t* workgroups) {
+  *workgroups = 0;
+  const mfsdp_status_t st = grouped_sizes(experts, rows, n, k, MFSDP_DTYPE_BF16);
+  if (st != MFSDP_OK) return st;
+  if (n > kScaledDimMax || k > kScaledDimMax) return too_large();
+  if (experts == 0 || rows == 0) return MFSDP_OK;
+  *use = scaled_kernel(experts, rows, n, round_up(k, kScaledBlock));
+  const GroupShape s = scaled_shape(*use);
+  const int64_t tiles = group_tiles_max(rows, experts, s.rows) * ceil_div(n, s.cols);
+  if (tiles > kGroupBlocksMax) return fail(MFSDP_ERR_UNSUPPORTED, "too many tiles");
+  *workgroups = tiles;
+  return MFSDP_OK;
+}
+
 mfsdp_status_t scaled_linear_impl(const uint8_t* codes, const uint8_t* scales, const uint8_t* wcodes,
                                   const uint8_t* wscales, const int32_t* offsets, int64_t experts, int64_t rows,
                                   int64_t n, int64_t k, void* y, int64_t ldy, hipStream_t stream) {
   g_last_error.clear();
-  mfsdp_status_t st = grouped_sizes(experts, rows, n, k, MFSDP_DTYPE_BF16);
+  ScaledKernel use{};
+  int64_t workgroups;
+  mfsdp_status_t st = scaled_choose(experts, rows, n, k, &use, &workgroups);
   if (st != MFSDP_OK) return st;
-  if (n > kScaledDimMax || k > kScaledDimMax || ldy > kGroupDimMax) return too_large();
+  if (ldy > kGroupDimMax) return too_large();
   if (ldy < n) return fail(MFSDP_ERR_INVALID_ARGUMENT, "a row stride is smaller than the row");
-  if (experts == 0 || rows == 0) return MFSDP_OK;
+  if (workgroups == 0) return MFSDP_OK;
   if (!codes || !scales || !wcodes || !wscales || !offsets || !y) return null_pointer();
   if (!aligned(y, 2) || !aligned(offsets, 4)) return misaligned();
   if (!aligned(codes, 16) || !aligned(wcodes, 16)) return fail(MFSDP_ERR_INVALID_ARGUMENT, "codes must be 16-byte aligned");
   const int64_t nb = ceil_div(n, kScaledBlock), kb = ceil_div(k, kScaledBlock), depth = kb * kScaledBlock;
-  const ScaledKernel use = scaled_kernel(experts, rows, n, depth);
-  const GroupShape shape = scaled_shape(use);
-  if (group_tiles_max(rows, experts, shape.rows) * ceil_div(n, shape.cols) > kGroupBlocksMax)
-    return fail(MFSDP_ERR_UNSUPPORTED, "too many tiles");
   Buffers b;
   b.rows(y, rows, n, ldy, 2, "y");
   b.outputs_end();
@@ -714,10 +728,10 @@ mfsdp_status_t scaled_linear_impl(const uint8_t* codes, const uint8_t* scales, c
   a.g.stream = aligned(y, 128) && ldy * 2 % 128 == 0;
   hipError_t e = hipErrorInvalidValue;
   switch (use) {
-    case kScaledLarge: e = launch_scaled<ScaledLarge>(a, stream); break;
-    case kScaledPair: e = launch_scaled<ScaledPair>(a, stream); break;
-    case kScaledRows: e = launch_scaled<ScaledRows>(a, stream); break;
-    case kScaledFew: e = launch_scaled<ScaledFew>(a, stream); break;
+    case kScaledLarge: e = launch_scaled<ScaledLarge>(a, workgroups, stream); break;
+    case kScaledPair: e = launch_scaled<ScaledPair>(a, workgroups, stream); break;
+    case kScaledRows: e = launch_scaled<ScaledRows>(a, workgroups, stream); break;
+    case kScaledFew: e = launch_scaled<ScaledFew>(a, workgroups, stream); break;
   }
   return launched(e, "8-bit float product");
 }
@@ -854,17 +868,19 @@ mfsdp_status_t mfsdp_scaled_linear_tile(int64_t n_experts, int64_t rows, int64_t
   return guarded([&]() -> mfsdp_status_t {
     g_last_error.clear();
     if (!out) return fail(MFSDP_ERR_INVALID_ARGUMENT, "out is null");
-    const mfsdp_status_t st = grouped_sizes(n_experts, rows, n, k, MFSDP_DTYPE_BF16);
+    ScaledKernel use{};
+    int64_t workgroups;
+    const mfsdp_status_t st = scaled_choose(n_experts, rows, n, k, &use, &workgroups);
     if (st != MFSDP_OK) return st;
     *out = mfsdp_grouped_tile_t{};
-    if (n_experts == 0 || rows == 0) return MFSDP_OK;   // no launch
-    const GroupShape s = scaled_shape(scaled_kernel(n_experts, rows, n, round_up(k, kScaledBlock)));
+    if (workgroups == 0) return MFSDP_OK;   // no launch
+    const GroupShape s = scaled_shape(use);
     out->rows = s.rows;
     out->cols = s.cols;
     out->threads = s.threads;
     out->wave_sets = s.wave_sets;
     out->lds_dma = 1;
-    out->workgroups = group_tiles_max(rows, n_experts, s.rows) * ceil_div(n, s.cols);
+    out->workgroups = workgroups;
     return MFSDP_OK;
   });
 }

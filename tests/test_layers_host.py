@@ -250,3 +250,19 @@ def test_reference_choice():
             stay = sorted(range(groups), key=lambda i: (-sums[i], i))[:top]
             order = sorted((e for e in range(24) if e // size in stay), key=lambda e: (-float(s[t, e]), e))
             assert got[t].tolist() == order[:5]
+
+
+SCALED_LINEAR = dict(c=P[0], s=P[1], wc=P[2], ws=P[3], off=P[4], e=3, rows=0, n=50, k=40, y=P[5], ldy=1 << 22)
+
+
+@pytest.mark.parametrize("e,rows,n,k,want", [
+    (3, 0, (1 << 22) - 128, 40, OK), (3, 0, (1 << 22) - 127, 40, UNSUPPORTED), (3, 0, 50, (1 << 22) - 127, UNSUPPORTED), (0, 5, 50, 1 << 22, UNSUPPORTED),
+    (1, 10, 1 << 22, 40, UNSUPPORTED), (1, 1 << 30, 4000000, 1, UNSUPPORTED), (1 << 20, 1 << 30, 128, 128, UNSUPPORTED), ((1 << 20) + 1, 0, 1, 1, UNSUPPORTED),
+    (3, -1, 50, 40, INVALID), (3, 0, 0, 40, INVALID),
+])
+def test_scaled_tile_query_refuses_what_the_product_does(e, rows, n, k, want):
+    assert tile(e, rows, n, k)[0] == want
+    assert call("mfsdp_scaled_linear", list(SCALED_LINEAR), SCALED_LINEAR, dict(e=e, rows=rows, n=n, k=k)) == want
+    if want != OK:      # and leaves what it was given
+        t = _lib.MfsdpGroupedTile(rows=7, workgroups=9)
+        assert _lib.load().mfsdp_scaled_linear_tile(e, rows, n, k, ctypes.byref(t)) == want and (t.rows, t.workgroups) == (7, 9)
