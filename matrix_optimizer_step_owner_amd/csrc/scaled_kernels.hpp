@@ -18,6 +18,7 @@
 // rows start on 128 bytes.
 #pragma once
 
+#include "bands.hpp"
 #include "common.hpp"
 #include "grouped_kernels.hpp"
 
@@ -295,9 +296,11 @@ __device__ __forceinline__ uint32_t wave_scan(uint32_t v) {
 // not wait for one another, the scan is six DPP steps, and the experts of the lane
 // that holds the tile are looked through by all lanes.  Sums stop at kScaledMany,
 // which only offsets that are not in order reach.
-// An expert's row tiles are in bands of equal height, five to eleven: a last band of
-// one or two rows reads all of a matrix for a few tiles (eight 14336 x 4096 experts
-// with about 2048 rows each, 957 -> 946 us).
+// An expert's row tiles are in bands of equal height (bands.hpp), six to eleven of them
+// where there are so many: a last band of one or two reads all of a matrix for a few
+// tiles (eight 14336 x 4096 experts with about 2048 rows each 957 us with bands of eight
+// and a rest, 946 with equal ones; one such expert of 73 row tiles 867 with nine bands
+// whose last is a single row, 864 with equal ones).
 constexpr uint32_t kScaledMany = 1u << 24;    // more than a grid has
 
 template <int BP>
@@ -337,11 +340,9 @@ __device__ __forceinline__ bool scaled_find(const GroupArgs& g, int b, int nq, i
       lo = of(from);
       hi = of(to);
       const int rows = of(static_cast<int>(n)), local = want - of(static_cast<int>(end - n)) * nq;
-      const int bands = max(1, (rows + kGroupBand / 2) / kGroupBand), height = (rows + bands - 1) / bands;
-      const int band = local / (height * nq), r = local - band * (height * nq);
-      const int in_band = min(height, rows - band * height);
-      ti = band * height + r % in_band;
-      tj = r / in_band;
+      const BandTile tile = band_tile(rows, nq, kGroupBand, local);
+      ti = tile.ti;
+      tj = tile.tj;
       return true;
     }
     at = static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(end), 63));
