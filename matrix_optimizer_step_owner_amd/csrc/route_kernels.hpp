@@ -171,7 +171,8 @@ __device__ __forceinline__ uint32_t route_groups(const RouteArgs& a, const K (&v
   int step;       // lanes between the first lanes of groups; group g's sum is with lane g * step
   V mine = V(0);
   if (a.lanes > 0) {
-    // a group is a.lanes lanes, a power of two: their two largest by exchanges
+    // a group is a.lanes lanes, a power of two up to 32 (there are two groups at least):
+    // their two largest by exchanges
     K one, two;
     route_two<PER, K>(vk, one, two);
     auto merge = [&](auto lanes_c) {
@@ -186,7 +187,6 @@ __device__ __forceinline__ uint32_t route_groups(const RouteArgs& a, const K (&v
     merge(std::integral_constant<int, 8>{});
     merge(std::integral_constant<int, 16>{});
     merge(std::integral_constant<int, 32>{});
-    merge(std::integral_constant<int, 64>{});
     mine = route_value(one);
     if (a.group_size > 1) mine += route_value(two);
     step = a.lanes;
@@ -613,8 +613,8 @@ __device__ __forceinline__ void plan_round(const PlanArgs& a, int i, int w1, uin
 }
 
 // Exclusive scan of tot[0 .. experts) into base, plus add; one expert a thread.
-__device__ __forceinline__ uint32_t plan_scan(const uint32_t* tot, const uint32_t* add, uint32_t* base, int experts,
-                                              uint32_t* wave_sum, int32_t* offsets) {
+__device__ __forceinline__ void plan_scan(const uint32_t* tot, const uint32_t* add, uint32_t* base, int experts,
+                                          uint32_t* wave_sum, int32_t* offsets) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, b = threadIdx.x;
   const uint32_t t = b < experts ? tot[b] : 0;
   uint32_t incl = t;
@@ -635,7 +635,6 @@ __device__ __forceinline__ uint32_t plan_scan(const uint32_t* tot, const uint32_
     }
   }
   __syncthreads();
-  return before;
 }
 static_assert(kPlanBinsMax <= kPlanThreads, "plan_scan takes one expert per thread");
 
