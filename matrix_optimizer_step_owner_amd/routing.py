@@ -78,12 +78,13 @@ def route(logits: torch.Tensor, k: int, *, scores: str = "softmax",
     ld = _rows(logits, "logits")
     b = None if bias is None else _whole(bias, "bias", device, _F32, (n,))
     m = None if mask is None else _whole(mask, "mask", device, (torch.bool,), (tokens,))
+    held = min(max(k, 0), n)    # a k outside is refused below, without room for it
     if experts is None:
-        experts = logits.new_empty((tokens, k), dtype=torch.int32)
+        experts = logits.new_empty((tokens, held), dtype=torch.int32)
     else:
         _whole(experts, "experts", device, _I32, (tokens, k))
     if weights is None:
-        weights = logits.new_empty((tokens, k), dtype=torch.float32)
+        weights = logits.new_empty((tokens, held), dtype=torch.float32)
     else:
         _whole(weights, "weights", device, _F32, (tokens, k))
     _call(device, "mfsdp_route", logits.data_ptr(), ld, b, m, tokens, n, k, _DTYPES[logits.dtype],
@@ -139,15 +140,15 @@ def route_plan(experts: torch.Tensor, n_experts: int, *, offsets: Optional[torch
     _check(experts, "experts", device, _I32, 2)
     _contiguous(experts, "experts")
     tokens, k = experts.shape
+    need = _plan_bytes(tokens, k, n_experts)    # refuses sizes before there is room for them
     if offsets is None:
-        offsets = experts.new_empty((max(n_experts, 0) + 1,))
+        offsets = experts.new_empty((n_experts + 1,))
     else:
         _whole(offsets, "offsets", device, _I32, (n_experts + 1,))
     if place is None:
         place = experts.new_empty((tokens, k))
     else:
         _whole(place, "place", device, _I32, (tokens, k))
-    need = _plan_bytes(tokens, k, n_experts)
     ws = None if need == 0 and workspace is None else _scratch(device, need, workspace)
     _call(device, "mfsdp_route_plan", experts.data_ptr(), tokens, k, n_experts, offsets.data_ptr(),
           place.data_ptr(), *_span(ws))
