@@ -523,8 +523,10 @@ mfsdp_status_t mfsdp_embedding_grad(const void* dy, int64_t ld_dy, mfsdp_dtype_t
  *           renormalize: the bias chooses and does not weigh
  * The choice is that of exact arithmetic on the logits and biases as stored, as
  * far as 64 bits tell it; ties go to the lowest index.  A NaN key is behind
- * -infinity; a row with a NaN or +infinity has NaN weights where its scores are
- * NaN, its experts are still k different ones.
+ * -infinity; a row with a NaN or +infinity (softmax: or of -infinity alone) has NaN
+ * weights where its scores are NaN, its experts are still k different ones.  Weights
+ * are rounded in fp32 by the score, its share and the factor in turn: one expert
+ * alone, renormalised, has exactly `scale` where its score is 2^-41 or more.
  *   logits   device, tokens x n_experts, row stride ld_logits, bf16 or fp32
  *   bias     device fp32, n_experts, or NULL
  *   mask     device, tokens bytes, or NULL: a token with 0 is padding, has experts

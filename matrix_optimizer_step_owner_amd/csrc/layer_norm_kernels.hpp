@@ -18,8 +18,9 @@
 // Bound by HBM, and close to it by the vector units: a value costs some 14
 // instructions of four cycles in the gradient, which 16 values per lane, their
 // deviations kept, and two sums of two values per row (instead of three) leave it.
-// 16384 rows of 5120 bf16 take 56 us forward (6.0 TB/s) and 97 for the gradients
-// (5.2, the partial sums' 21 MB among the bytes).
+// 16384 rows of 5120 bf16 take 56 us forward (6.0 TB/s) and 97 to 101 for the gradients
+// (5.2, the partial sums' 21 MB among the bytes), two launches in a row; one by one,
+// in a profile, 82 and 5.
 #pragma once
 
 #include "common.hpp"

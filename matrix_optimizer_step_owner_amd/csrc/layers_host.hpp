@@ -620,7 +620,8 @@ mfsdp_status_t scaled_weight_impl(const void* w, int64_t experts, int64_t n, int
   return launched(e, "8-bit float matrices");
 }
 
-// Tiles.  The rule below chooses among them; times in us, experts x rows x n x k:
+// Tiles.  scaled_kernel chooses among them; the times at its rule are in us, of
+// experts x rows x n x k.
 using ScaledLarge = ScaledTile<256, 256, 2, 4, 2, 2>;
 using ScaledPair = ScaledTile<128, 128, 2, 2, 2, 2>;         // two workgroups per CU
 using ScaledRows = ScaledTile<32, 64, 1, 2, 4, 3, 4, 4>;     // two workgroups per CU

@@ -13,11 +13,12 @@
 // in the chosen order, the last chosen and any other, or the border between
 // groups, nearer than the rounding of both -- sends the token through the same
 // choice in fp64: of 256 experts in eight groups, k = 8, normal logits, 6 tokens of
-// a thousand with sigmoid scores, 2 to 3 with softmax.
+// a thousand with sigmoid scores, 2 with softmax.
 //
-// Bound by the vector units, some 450 instructions of four cycles per token:
-// 32771 tokens of 256 experts, k = 8, 19 us by the logits alone, 23 with sigmoid
-// scores and a bias, 31 with eight groups; the bytes would take 7.
+// Bound by the vector units, some 470 instructions of four cycles per token:
+// 32771 tokens of 256 experts, k = 8, 18 us by the logits alone, 22 with sigmoid
+// scores and a bias, 29 with eight groups (single launches in a profile 32); the bytes
+// would take 7.
 #pragma once
 
 #include "common.hpp"

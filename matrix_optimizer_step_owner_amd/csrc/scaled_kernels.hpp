@@ -248,7 +248,8 @@ __device__ __forceinline__ i32x8_t scaled_frag(const uint4& a, const uint4& b) {
 //
 // 256 x 256: bound by the MFMAs, two thirds of whose cycles are used, at the 1.8 GHz
 // that this load is given: one product of 8192^3 2.6 PFLOP/s, one expert of 16384 x
-// 14336 x 4096 2.46, eight of them with 2048 rows each 2.0 (934 to 955 us).  32 rows: bound
+// 14336 x 4096 2.46, eight of them with 2048 rows each 2.0 to 2.15 (892 to 955 us by the
+// segments' lengths; 1030 to 1044 in a process's first ten passes).  32 rows: bound
 // by HBM, 8 experts of 14336 x 4096 with 16 rows each 89 us, 5.3 TB/s.
 template <int BP_, int BQ_, int WP_, int WQ_, int U_, int STAGES_, int KS_ = 1, int OCC_ = 2>
 struct ScaledTile {
